@@ -115,6 +115,24 @@ WsLayout ws_layout(const sffn_layer& L, int B) {
   return w;
 }
 
+sffn_status read_error_word(uint32_t* err, cudaStream_t st) {
+  cudaError_t e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(e, "check_error: synchronize");
+  uint32_t h = 0;
+  e = cudaMemcpy(&h, err, 4, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && h) e = cudaMemset(err, 0, 4);
+  if (e != cudaSuccess) return cuda_fail(e, "check_error: read error word");
+  if (h == SFFN_ERR_TIMEOUT) {
+    set_error("a bounded device-side wait ran out");
+    return SFFN_ERR_TIMEOUT;
+  }
+  if (h) {
+    set_error("the device flagged bad data");
+    return SFFN_ERR_DEVICE;
+  }
+  return SFFN_OK;
+}
+
 }  // namespace sffn
 
 using namespace sffn;
@@ -374,23 +392,6 @@ size_t sffn_workspace_bytes(const sffn_layer* L, int32_t B) {
   return ws_bytes_for(*L, B);
 }
 
-static sffn_status read_error_word(uint32_t* err, cudaStream_t st) {
-  cudaError_t e = cudaStreamSynchronize(st);
-  if (e != cudaSuccess) return cuda_fail(e, "check_error: synchronize");
-  uint32_t h = 0;
-  e = cudaMemcpy(&h, err, 4, cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && h) e = cudaMemset(err, 0, 4);
-  if (e != cudaSuccess) return cuda_fail(e, "check_error: read error word");
-  if (h == SFFN_ERR_TIMEOUT) {
-    set_error("a bounded device-side wait ran out");
-    return SFFN_ERR_TIMEOUT;
-  }
-  if (h) {
-    set_error("the device flagged bad data");
-    return SFFN_ERR_DEVICE;
-  }
-  return SFFN_OK;
-}
 
 sffn_status sffn_layer_check_error(const sffn_layer* L, sffn_stream stream) {
   if (!L) return invalid("layer is NULL");

@@ -126,6 +126,8 @@ cudaError_t launch_batch(const sffn_layer& L, const float* x, int B, float thres
 
 void set_error(const std::string& msg);
 sffn_status cuda_fail(cudaError_t e, const char* what);
+// Synchronizes the stream, reads and clears a device error word.
+sffn_status read_error_word(uint32_t* err, cudaStream_t st);
 
 // Launchers (each enqueues kernels on `st`; they return the launch status).
 cudaError_t launch_pred_hidden(const sffn_layer& L, const float* x, float* hid, cudaStream_t st);

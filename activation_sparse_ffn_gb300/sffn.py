@@ -63,6 +63,28 @@ class TraceC(ctypes.Structure):
     _fields_ = [("begin", _vp * 4), ("end", _vp * 4)]
 
 
+class RowsC(ctypes.Structure):
+    _fields_ = [("ptr", _vp), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", _i32), ("out_features", _i32), ("group", _i32), ("scale_dtype", _i32),
+                ("has_zero", _i32), ("max_batch", _i32)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("page_size", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("group", _i32)]
+
+
+class KvBatchC(ctypes.Structure):
+    _fields_ = [("table", _vp), ("kv_len", _vp), ("q_start", _vp), ("n_seq", _i32), ("n_tokens", _i32),
+                ("table_stride", _i32)]
+
+
+class RopeC(ctypes.Structure):
+    _fields_ = [("table", _vp), ("positions", _vp), ("length", _i32), ("dim", _i32), ("style", _i32)]
+
+
 class TamOutputsC(ctypes.Structure):
     _fields_ = [("cand", _vp), ("resident", _vp), ("load", _vp), ("evict", _vp), ("changed", _vp), ("topk", _vp),
                 ("n_cand", _vp), ("n_res", _vp)]
@@ -120,6 +142,23 @@ _sig("tam_get_shape", _c, _vp, _P(_i32), _P(_i32))
 _sig("tam_check_error", _c, _vp, _vp)
 _sig("tam_destroy", None, _vp)
 _sig("sffn_selftest_wait_timeout", _c, _vp, _i32, _vp)
+_sig("sffn_linear_validate", _c, _P(LinearDesc))
+_sig("sffn_linear_create", _c, _P(LinearDesc), _P(_vp))
+_sig("sffn_linear_pack", _c, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("sffn_linear_get_desc", _c, _vp, _P(LinearDesc))
+_sig("sffn_linear_workspace_bytes", _size, _vp, _i32)
+_sig("sffn_linear_forward", _c, _vp, RowsC, _i32, RowsC, RowsC, _i32, _vp, _size, _vp)
+_sig("sffn_linear_destroy", None, _vp)
+_sig("sffn_kv_validate", _c, _P(KvDesc))
+_sig("sffn_kv_bytes", _size, _P(KvDesc))
+_sig("sffn_kv_create", _c, _P(KvDesc), _P(_vp))
+_sig("sffn_kv_get_desc", _c, _vp, _P(KvDesc))
+_sig("sffn_kv_check_error", _c, _vp, _vp)
+_sig("sffn_kv_destroy", None, _vp)
+_sig("sffn_kv_append", _c, _vp, _P(KvBatchC), RowsC, _i32, RowsC, RowsC, RowsC, _P(RopeC), _i32, _vp)
+_sig("sffn_kv_gather", _c, _vp, _P(KvBatchC), RowsC, RowsC, _i32, _vp)
+_sig("sffn_attend_workspace_bytes", _size, _vp, _i32, _i32, _i32)
+_sig("sffn_attend", _c, _vp, _P(KvBatchC), RowsC, _i32, RowsC, _vp, _f32, _i32, _i32, _vp, _size, _vp)
 
 EXPORTS = [
     "sffn_status_string", "sffn_last_error", "sffn_version", "sffn_layer_validate", "sffn_layer_create",
@@ -132,6 +171,10 @@ EXPORTS = [
     "sffn_stack_destroy", "tam_create", "tam_update",
     "tam_adapt", "tam_get_state", "tam_set_state", "tam_get_shape", "tam_check_error", "tam_destroy",
     "sffn_selftest_wait_timeout",
+    "sffn_linear_validate", "sffn_linear_create", "sffn_linear_pack", "sffn_linear_get_desc",
+    "sffn_linear_workspace_bytes", "sffn_linear_forward", "sffn_linear_destroy",
+    "sffn_kv_validate", "sffn_kv_bytes", "sffn_kv_create", "sffn_kv_get_desc", "sffn_kv_check_error",
+    "sffn_kv_destroy", "sffn_kv_append", "sffn_kv_gather", "sffn_attend_workspace_bytes", "sffn_attend",
 ]
 
 
@@ -356,6 +399,156 @@ def sffn_stack_check_error(stack, stream=None) -> None:
 
 def sffn_stack_destroy(stack) -> None:
     _lib.sffn_stack_destroy(stack)
+
+
+# ----------------------------------------------------------------- attention half: projections, cache, attention
+
+def _rows(t, dtype=None, name="tensor") -> RowsC:
+    """RowsC of a (rows, width) or (rows, heads, width) tensor, or of None."""
+    if t is None:
+        return RowsC()
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype} given, {dtype} wanted (all arrays of a call have one type)")
+    if t.dim() not in (2, 3) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: two or three dimensions with a contiguous last one are wanted")
+    return RowsC(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+
+
+def _io_dtype(t) -> int:
+    if t.dtype not in TORCH_WDTYPE:
+        raise ValueError(f"{t.dtype}: float32, float16 or bfloat16 is wanted")
+    return DTYPE[TORCH_WDTYPE[t.dtype]]
+
+
+def _want(t, shape, name) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} given, {tuple(shape)} wanted")
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def make_linear_desc(in_features, out_features, group, scale_dtype, has_zero=False, max_batch=1) -> LinearDesc:
+    return LinearDesc(in_features, out_features, group,
+                      DTYPE[scale_dtype] if isinstance(scale_dtype, str) else scale_dtype, int(has_zero), max_batch)
+
+
+def sffn_linear_validate(desc: LinearDesc) -> int:
+    """Host-only check; returns the status code (no exception)."""
+    return _lib.sffn_linear_validate(ctypes.byref(desc))
+
+
+def sffn_linear_create(desc: LinearDesc) -> int:
+    h = _vp()
+    _check(_lib.sffn_linear_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_linear_create")
+    return h.value
+
+
+def sffn_linear_pack(linear, codes, scales, zeros=None, bias=None, stream=None) -> None:
+    _check(_lib.sffn_linear_pack(linear, _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _stream(stream)),
+           "sffn_linear_pack")
+
+
+def sffn_linear_get_desc(linear) -> LinearDesc:
+    out = LinearDesc()
+    _check(_lib.sffn_linear_get_desc(linear, ctypes.byref(out)), "sffn_linear_get_desc")
+    return out
+
+
+def sffn_linear_workspace_bytes(linear, B: int) -> int:
+    return int(_lib.sffn_linear_workspace_bytes(linear, B))
+
+
+def sffn_linear_forward(linear, x, y, residual=None, ws=None, stream=None) -> None:
+    """y (B, out) = x (B, in) through the layer, plus residual (B, out) if given (it may be y itself)."""
+    _want(residual, y.shape, "residual")
+    if y.shape[0] != x.shape[0]:
+        raise ValueError("x and y differ in their number of rows")
+    _check(_lib.sffn_linear_forward(linear, _rows(x, None, "x"), x.shape[0], _rows(residual, x.dtype, "residual"),
+                                    _rows(y, x.dtype, "y"), _io_dtype(x), *_ws_args(ws), _stream(stream)),
+           "sffn_linear_forward")
+
+
+def sffn_linear_destroy(linear) -> None:
+    _lib.sffn_linear_destroy(linear)
+
+
+def make_kv_desc(n_pages, page_size, n_kv_heads, head_dim, group) -> KvDesc:
+    return KvDesc(n_pages, page_size, n_kv_heads, head_dim, group)
+
+
+def sffn_kv_validate(desc: KvDesc) -> int:
+    """Host-only check; returns the status code (no exception)."""
+    return _lib.sffn_kv_validate(ctypes.byref(desc))
+
+
+def sffn_kv_bytes(desc: KvDesc) -> int:
+    return int(_lib.sffn_kv_bytes(ctypes.byref(desc)))
+
+
+def sffn_kv_create(desc: KvDesc) -> int:
+    h = _vp()
+    _check(_lib.sffn_kv_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_kv_create")
+    return h.value
+
+
+def sffn_kv_get_desc(kv) -> KvDesc:
+    out = KvDesc()
+    _check(_lib.sffn_kv_get_desc(kv, ctypes.byref(out)), "sffn_kv_get_desc")
+    return out
+
+
+def sffn_kv_check_error(kv, stream=None) -> None:
+    _check(_lib.sffn_kv_check_error(kv, _stream(stream)), "sffn_kv_check_error")
+
+
+def sffn_kv_destroy(kv) -> None:
+    _lib.sffn_kv_destroy(kv)
+
+
+def sffn_kv_append(kv, batch: "KvBatch", q, k, v, q_out=None, rope: "Rope | None" = None, stream=None) -> None:
+    """Append k, v (tokens, kv heads, dim); rotate q (tokens, heads, dim) into q_out if q is not None."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
+        if t is not None and t.shape[0] != batch.c.n_tokens:
+            raise ValueError(f"{name}: {t.shape[0]} rows given, {batch.c.n_tokens} wanted")
+    _want(v, k.shape, "v")
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q_out is required with q")
+        _want(q_out, q.shape, "q_out")
+    if rope is not None and rope.positions is not None:
+        _want(rope.positions, (batch.c.n_tokens,), "positions")
+    _check(_lib.sffn_kv_append(kv, ctypes.byref(batch.c), _rows(q, k.dtype, "q"), 0 if q is None else q.shape[1],
+                               _rows(k, k.dtype, "k"), _rows(v, k.dtype, "v"), _rows(q_out, k.dtype, "q_out"),
+                               None if rope is None else ctypes.byref(rope.c), _io_dtype(k), _stream(stream)),
+           "sffn_kv_append")
+
+
+def sffn_kv_gather(kv, batch: "KvBatch", k_out, v_out, stream=None) -> None:
+    """Values the cache holds for the batch's tokens; either output may be None."""
+    one = k_out if k_out is not None else v_out
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and t.shape[0] != batch.c.n_tokens:
+            raise ValueError(f"{name}: {t.shape[0]} rows given, {batch.c.n_tokens} wanted")
+    _check(_lib.sffn_kv_gather(kv, ctypes.byref(batch.c), _rows(k_out, one.dtype, "k_out"),
+                               _rows(v_out, one.dtype, "v_out"), _io_dtype(one), _stream(stream)), "sffn_kv_gather")
+
+
+def sffn_attend_workspace_bytes(kv, n_q_heads: int, n_seq: int, n_tokens: int) -> int:
+    return int(_lib.sffn_attend_workspace_bytes(kv, n_q_heads, n_seq, n_tokens))
+
+
+def sffn_attend(kv, batch: "KvBatch", q, out, lse, scale, window=0, ws=None, stream=None) -> None:
+    """out (tokens, heads, dim) = attention of q over the cache; lse (tokens, heads) float32 or None."""
+    if q.shape[0] != batch.c.n_tokens:
+        raise ValueError(f"q: {q.shape[0]} rows given, {batch.c.n_tokens} wanted")
+    _want(out, q.shape, "out")
+    _want(lse, q.shape[:2], "lse")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous float32 tensor is wanted")
+    _check(_lib.sffn_attend(kv, ctypes.byref(batch.c), _rows(q, None, "q"), q.shape[1], _rows(out, q.dtype, "out"),
+                            _ptr(lse), scale, window, _io_dtype(q), *_ws_args(ws), _stream(stream)), "sffn_attend")
 
 
 # ----------------------------------------------------------------- TAM calls
@@ -589,6 +782,123 @@ class Tam:
             self.close()
         except Exception:
             pass
+
+
+class Linear:
+    """Owns one sffn_linear handle: 4-bit codes with group scales."""
+
+    def __init__(self, in_features, out_features, group, scale_dtype="f16", has_zero=False, max_batch=1):
+        self.desc = make_linear_desc(in_features, out_features, group, scale_dtype, has_zero, max_batch)
+        self.handle = sffn_linear_create(self.desc)
+        self.in_features, self.out_features, self.max_batch = in_features, out_features, max_batch
+
+    @classmethod
+    def from_weights(cls, codes, scales, zeros=None, bias=None, max_batch=1, stream=None) -> "Linear":
+        """codes (out, in) int8 in [-8, 7]; scales and zeros (out, in / group); bias (out,) float32."""
+        out_features, in_features = codes.shape
+        group = in_features // scales.shape[1]
+        _want(scales, (out_features, in_features // group), "scales")
+        _want(zeros, scales.shape, "zeros")
+        _want(bias, (out_features,), "bias")
+        if codes.dtype != torch.int8 or (zeros is not None and zeros.dtype != scales.dtype):
+            raise ValueError("codes are int8, zeros have the scales' type")
+        if bias is not None and bias.dtype != torch.float32:
+            raise ValueError("bias is float32")
+        linear = cls(in_features, out_features, group, TORCH_WDTYPE[scales.dtype], zeros is not None, max_batch)
+        sffn_linear_pack(linear.handle, codes.contiguous(), scales.contiguous(),
+                         None if zeros is None else zeros.contiguous(), None if bias is None else bias.contiguous(),
+                         stream)
+        return linear
+
+    def workspace(self, B=1, device="cuda") -> torch.Tensor:
+        return torch.empty(max(256, sffn_linear_workspace_bytes(self.handle, B)), dtype=torch.uint8, device=device)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            sffn_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvCache:
+    """Owns one sffn_kv handle: the paged 4-bit cache of one layer."""
+
+    def __init__(self, n_pages, page_size, n_kv_heads, head_dim, group):
+        self.desc = make_kv_desc(n_pages, page_size, n_kv_heads, head_dim, group)
+        self.handle = sffn_kv_create(self.desc)
+        self.page_size, self.n_kv_heads, self.head_dim, self.group = page_size, n_kv_heads, head_dim, group
+
+    def workspace(self, batch: "KvBatch", n_q_heads: int, device="cuda") -> torch.Tensor:
+        n = sffn_attend_workspace_bytes(self.handle, n_q_heads, batch.c.n_seq, batch.c.n_tokens)
+        return torch.empty(max(256, n), dtype=torch.uint8, device=device)
+
+    def check_error(self, stream=None) -> None:
+        sffn_kv_check_error(self.handle, stream)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            sffn_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvBatch:
+    """The tokens of a call (sffn_kv_batch): table (n_seq, pages) int32, kv_len
+    (n_seq,) int32, q_start (n_seq + 1,) int32 or None for one token per
+    sequence, and the number of tokens. Keeps the tensors alive; the library
+    reads them on the device at every call, so their contents may change."""
+
+    def __init__(self, table, kv_len, q_start=None, n_tokens=None):
+        n_seq = kv_len.shape[0]
+        for t, name in ((table, "table"), (kv_len, "kv_len"), (q_start, "q_start")):
+            if t is not None and t.dtype != torch.int32:
+                raise ValueError(f"{name}: int32 is wanted")
+        _want(q_start, (n_seq + 1,), "q_start")
+        if table.dim() != 2 or table.shape[0] != n_seq or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table: (n_seq, pages) with contiguous rows is wanted")
+        if kv_len.stride(0) != 1 and n_seq > 1 or q_start is not None and q_start.stride(0) != 1:
+            raise ValueError("kv_len and q_start must be contiguous")
+        if q_start is not None and n_tokens is None:
+            raise ValueError("n_tokens is required with q_start")
+        self.table, self.kv_len, self.q_start = table, kv_len, q_start
+        stride = table.stride(0) if n_seq > 1 else table.shape[1]
+        if stride < table.shape[1]:
+            raise ValueError("table: rows must not overlap")
+        self.c = KvBatchC(_ptr(table), _ptr(kv_len), _ptr(q_start), n_seq, n_seq if n_tokens is None else n_tokens,
+                          stride)
+
+
+class Rope:
+    """A position rotation (sffn_rope): table (length, dim / 2, 2) float32 of
+    (cos, sin), style "halves" (channels j and j + dim/2) or "pairs" (2j and
+    2j + 1), and the tokens' positions if they are not those in the cache."""
+
+    STYLE = {"halves": 0, "pairs": 1}
+
+    def __init__(self, table, style="halves", positions=None):
+        if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+            raise ValueError("table: a contiguous float32 (length, dim / 2, 2) tensor is wanted")
+        if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
+            raise ValueError("positions: a contiguous int32 tensor is wanted")
+        self.table, self.positions = table, positions
+        self.c = RopeC(_ptr(table), _ptr(positions), table.shape[0], 2 * table.shape[1], self.STYLE[style])
+
+    @classmethod
+    def of_base(cls, length, dim, base=10000.0, style="halves", device="cuda") -> "Rope":
+        """The table of angles position * base^(-2j/dim), computed in 64 bits and rounded once."""
+        j = torch.arange(dim // 2, device=device, dtype=torch.float64)
+        angle = torch.arange(length, device=device, dtype=torch.float64)[:, None] * base ** (-2.0 * j / dim)
+        return cls(torch.stack((angle.cos(), angle.sin()), -1).float().contiguous(), style)
 
 
 class _DeviceArray:

@@ -485,6 +485,162 @@ sffn_status tam_get_shape(const tam_state* tam, int32_t* n_layers /* host */, in
 sffn_status tam_check_error(const tam_state* tam, sffn_stream stream);
 void tam_destroy(tam_state* tam);
 
+/* ------------------------------------------- 4-bit projections (attention) */
+
+/* The attention half of a decode step: the projections around it, the cache
+ * of keys and values, and the attention over that cache. A step of one layer
+ * is sffn_linear_forward (q, k and v), sffn_kv_append, sffn_attend,
+ * sffn_linear_forward (output), then the sparse FFN (sffn_decode_step). Hot
+ * calls: sffn_linear_forward, sffn_kv_append, sffn_kv_gather, sffn_attend
+ * (same rules as above: they allocate nothing, never synchronize, and may be
+ * captured in a CUDA graph). */
+
+/* Rows of a two- or three-dimensional device array: element (i, h, c) is at
+ * ptr + i*row_stride + h*head_stride + c (in elements; c contiguous, one h
+ * for two dimensions). ptr and both strides must be multiples of 16 bytes
+ * (a stride that is never stepped along is not looked at). */
+typedef struct {
+  void* ptr;
+  int64_t row_stride;
+  int64_t head_stride;
+} sffn_rows;
+
+/* A linear layer with 4-bit codes and group scales:
+ *   y[b][n] = sum_k scale[n][k/G] * (code[n][k] - zero[n][k/G]) * x[b][k]
+ *             + bias[n] + residual[b][n],
+ * codes in [-8, 7], zero = 0 if the layer has none.
+ *   in_features: multiple of group, at most 65536.
+ *   out_features: 1 .. 1048576.
+ *   group: 32, 64 or 128 consecutive inputs share a scale (and a zero).
+ *   scale_dtype: type of the scales and zeros as given and stored.
+ *   has_zero: nonzero if the layer has zeros.
+ *   max_batch: largest B the layer will be called with, 1..32. */
+typedef struct {
+  int32_t in_features, out_features, group, scale_dtype, has_zero, max_batch;
+} sffn_linear_desc;
+
+typedef struct sffn_linear sffn_linear;
+
+/* Host-only check of a description (no CUDA call). */
+sffn_status sffn_linear_validate(const sffn_linear_desc* desc);
+/* Allocates the packed arrays on the current device. Errors: INVALID_ARG, OOM, CUDA. */
+sffn_status sffn_linear_create(const sffn_linear_desc* desc, sffn_linear** out);
+/* Pack codes [out][in] int8 (each in [-8, 7]; another value fails with
+ * DEVICE and leaves the layer unpacked), scales and zeros [out][in/group] in
+ * scale_dtype (zeros NULL exactly if has_zero is 0) and bias [out] fp32 or
+ * NULL. Setup call: synchronizes the stream. Device pointers, 16-byte
+ * aligned. Errors: INVALID_ARG, DEVICE, CUDA. */
+sffn_status sffn_linear_pack(sffn_linear* linear, const int8_t* codes, const void* scales, const void* zeros,
+                             const float* bias, sffn_stream stream);
+sffn_status sffn_linear_get_desc(const sffn_linear* linear, sffn_linear_desc* out /* host */);
+/* Bytes of caller workspace for batch B (256-byte aligned, contents need no
+ * initialisation; 0 if the arguments are invalid or none is needed). */
+size_t sffn_linear_workspace_bytes(const sffn_linear* linear, int32_t B);
+/* x [B][in], y [B][out] and residual [B][out] (ptr NULL = none) in `dtype`;
+ * sums in fp32, y rounded once. residual may be y itself; x must not overlap
+ * y. A token with a non-finite x gives non-finite values in its own outputs only. y and
+ * residual need only be aligned to their elements, with any stride >= out.
+ * Errors: INVALID_ARG (also: not packed), CUDA. */
+sffn_status sffn_linear_forward(const sffn_linear* linear, sffn_rows x, int32_t B, sffn_rows residual, sffn_rows y,
+                                int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);
+void sffn_linear_destroy(sffn_linear* linear);
+
+/* ------------------------------------------------- paged 4-bit key/value cache */
+
+/* Pages of cached keys and values of one layer. A page holds page_size
+ * consecutive positions of one sequence for every key head. Keys and values
+ * are rounded per (position, head, group of channels) to sixteen levels
+ *   value = mid + step * (2u - 15),  u in 0..15,
+ * in fp32 arithmetic, one rounding per operation: lo, hi = least and largest
+ * value of the group, mid = f16(lo/2 + hi/2), step = f16(max(hi - mid,
+ * mid - lo) * f32(1/15)) (both limited to +-65504), u = floor((x - mid) *
+ * (1 / (2 step)) + 8) limited to 0..15, and u = 8 if step is 0. A group with
+ * a non-finite value is stored as NaN (mid = NaN).
+ *   n_pages: 1 .. 2^31 - 1.  page_size: 16, 32 or 64.  n_kv_heads: 1 .. 1024.
+ *   head_dim: 64, 128 or 256.  group: 32, 64 or 128, at most head_dim. */
+typedef struct {
+  int32_t n_pages, page_size, n_kv_heads, head_dim, group;
+} sffn_kv_desc;
+
+typedef struct sffn_kv sffn_kv;
+
+sffn_status sffn_kv_validate(const sffn_kv_desc* desc);
+/* Bytes of device memory the pages of a cache take (0 if desc is invalid). */
+size_t sffn_kv_bytes(const sffn_kv_desc* desc);
+/* Allocates the pages on the current device (contents undefined: a position
+ * is read only after a call appended it). Errors: INVALID_ARG, OOM, CUDA. */
+sffn_status sffn_kv_create(const sffn_kv_desc* desc, sffn_kv** out);
+sffn_status sffn_kv_get_desc(const sffn_kv* kv, sffn_kv_desc* out /* host */);
+/* Synchronize the stream, then read and clear the cache's device error word
+ * (DEVICE: a page id, length or rotation position out of range was seen). */
+sffn_status sffn_kv_check_error(const sffn_kv* kv, sffn_stream stream);
+void sffn_kv_destroy(sffn_kv* kv);
+
+/* The tokens of a call. Sequence s has the n_s = q_start[s+1] - q_start[s]
+ * rows q_start[s] .. q_start[s+1] - 1 of the call's arrays, and kv_len[s]
+ * cached positions, these tokens included: its row q_start[s] + i is at
+ * position kv_len[s] - n_s + i. Position p lives in page table[s][p /
+ * page_size], slot p % page_size. A row whose position is negative has no
+ * place in the cache (a sequence that is padded at its front).
+ *   table   [n_seq][table_stride] page ids, device
+ *   kv_len  [n_seq] device
+ *   q_start [n_seq + 1] device, ascending from 0, at most n_tokens; or NULL:
+ *           one token per sequence (n_tokens == n_seq)
+ * A length above table_stride * page_size is taken as that, and a page id
+ * outside [0, n_pages) as page 0 in reads and nowhere in writes; both set
+ * the cache's device error word. Rows outside every sequence are ignored. */
+typedef struct {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* q_start;
+  int32_t n_seq, n_tokens, table_stride;
+} sffn_kv_batch;
+
+/* Position rotation: channel pairs (a, b) of the first `dim` channels of a
+ * query or key head become (a cos - b sin, b cos + a sin) with (cos, sin) =
+ * table[position][pair], fp32, each product and sum rounded once. style 0:
+ * pair j is channels (j, j + dim/2); style 1: channels (2j, 2j + 1). dim is
+ * even, 0 < dim <= head_dim; table is 8-byte aligned. A position outside
+ * [0, length) is not rotated and sets the cache's device error word. */
+typedef struct {
+  const float* table;           /* [length][dim / 2][2], device */
+  const int32_t* positions;     /* [n_tokens] device, or NULL: the position in the cache */
+  int32_t length, dim, style;
+} sffn_rope;
+
+/* Append keys and values of the batch's tokens: k, v [n_tokens][n_kv_heads]
+ * [head_dim], rotating the keys on the way if `rope` is not NULL; and, if
+ * q.ptr is not NULL, write the rotated queries q [n_tokens][n_q_heads]
+ * [head_dim] to q_out (q_out may be q itself). All in `dtype`. Rows without a
+ * place in the cache only have their queries written. Two rows of one call
+ * must not share a place. Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_kv_append(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows q, int32_t n_q_heads,
+                           sffn_rows k, sffn_rows v, sffn_rows q_out, const sffn_rope* rope /* host, or NULL */,
+                           int32_t dtype, sffn_stream stream);
+
+/* Read back what the cache holds for the batch's tokens: k_out, v_out
+ * [n_tokens][n_kv_heads][head_dim] in `dtype` (either ptr may be NULL). Rows
+ * without a place in the cache give 0. Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows k_out, sffn_rows v_out,
+                           int32_t dtype, sffn_stream stream);
+
+/* Attention of the batch's tokens over the cache, after their keys and values
+ * were appended. Query head h reads key head h / (n_q_heads / n_kv_heads). The
+ * token at position p sees positions max(0, p - window + 1) .. p (window 0:
+ * all up to p):
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . K[j]) V[j],
+ *   lse[i][h] = log sum_j exp(scale * q[i][h] . K[j])  (fp32, or NULL),
+ * softmax statistics and sums in fp32. A token that sees nothing gives out =
+ * 0 and lse = -infinity. Positions a token does not see never reach its
+ * result, whatever is stored there. q, out in `dtype`; q and out must not
+ * overlap. The same arguments give the same bits at every call.
+ * n_q_heads: a multiple of n_kv_heads. scale: finite.
+ * ws: at least sffn_attend_workspace_bytes, 256-byte aligned. */
+size_t sffn_attend_workspace_bytes(const sffn_kv* kv, int32_t n_q_heads, int32_t n_seq, int32_t n_tokens);
+sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows q, int32_t n_q_heads,
+                        sffn_rows out, float* lse /* [n_tokens][n_q_heads] */, float scale, int32_t window,
+                        int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);
+
 /* ---------------------------------------------------------------- self-test */
 
 /* Exercise the bounded-wait path without any fault: one thread block waits
