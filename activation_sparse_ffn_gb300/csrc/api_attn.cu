@@ -53,12 +53,13 @@ sffn_status check_ws(const void* ws, size_t have, size_t need) {
   return SFFN_OK;
 }
 
-sffn_status check_batch(const sffn_kv_batch* b) {
+sffn_status check_batch(const sffn_kv_batch* b, int page_size) {
   if (!b) return invalid("batch is NULL");
   if (b->n_seq < 0 || b->n_tokens < 0) return invalid("n_seq and n_tokens must not be negative");
   if (b->n_tokens == 0) return SFFN_OK;
   if (b->n_seq < 1) return invalid("tokens without a sequence");
-  if (b->table_stride < 1) return invalid("table_stride must be positive");
+  if (b->table_stride < 1 || (long long)b->table_stride * page_size > (1 << 30))
+    return invalid("table_stride must be positive, and table_stride * page_size at most 2^30 positions");
   if (!b->table || !b->kv_len || !aligned(b->table, 4) || !aligned(b->kv_len, 4) || !aligned(b->q_start, 4))
     return invalid("table and kv_len are required; table, kv_len and q_start must be 4-byte aligned");
   if (!b->q_start && b->n_tokens != b->n_seq) return invalid("q_start may be NULL only for one token per sequence");
@@ -222,7 +223,7 @@ void sffn_kv_destroy(sffn_kv* C) {
 sffn_status sffn_kv_append(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows q, int32_t n_q_heads, sffn_rows k,
                            sffn_rows v, sffn_rows q_out, const sffn_rope* rope, int32_t dtype, sffn_stream stream) {
   if (!C) return invalid("kv is NULL");
-  sffn_status rc = check_batch(b);
+  sffn_status rc = check_batch(b, C->desc.page_size);
   if (rc != SFFN_OK) return rc;
   if (!is_dtype(dtype)) return invalid("dtype is not an sffn_dtype");
   const int D = C->desc.head_dim;
@@ -250,7 +251,7 @@ sffn_status sffn_kv_append(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows q
 sffn_status sffn_kv_gather(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows k_out, sffn_rows v_out, int32_t dtype,
                            sffn_stream stream) {
   if (!C) return invalid("kv is NULL");
-  sffn_status rc = check_batch(b);
+  sffn_status rc = check_batch(b, C->desc.page_size);
   if (rc != SFFN_OK) return rc;
   if (!is_dtype(dtype)) return invalid("dtype is not an sffn_dtype");
   if (b->n_tokens == 0) return SFFN_OK;
@@ -275,11 +276,12 @@ sffn_status sffn_attend(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows q, i
                         float* lse, float scale, int32_t window, int32_t dtype, void* ws, size_t ws_bytes,
                         sffn_stream stream) {
   if (!C) return invalid("kv is NULL");
-  sffn_status rc = check_batch(b);
+  sffn_status rc = check_batch(b, C->desc.page_size);
   if (rc != SFFN_OK) return rc;
   if (!is_dtype(dtype)) return invalid("dtype is not an sffn_dtype");
   if (n_q_heads < 1 || n_q_heads > 65536 || n_q_heads % C->desc.n_kv_heads)
     return invalid("n_q_heads must be a positive multiple of n_kv_heads, at most 65536");
+  if ((long long)b->n_tokens * n_q_heads > (1 << 30)) return invalid("n_tokens * n_q_heads must be at most 2^30");
   if (!std::isfinite(scale)) return invalid("scale must be finite");
   if (window < 0) return invalid("window must not be negative");
   if (b->n_tokens == 0) return SFFN_OK;

@@ -588,7 +588,8 @@ void sffn_kv_destroy(sffn_kv* kv);
  *           one token per sequence (n_tokens == n_seq)
  * A length above table_stride * page_size is taken as that, and a page id
  * outside [0, n_pages) as page 0 in reads and nowhere in writes; both set
- * the cache's device error word. Rows outside every sequence are ignored. */
+ * the cache's device error word. Rows outside every sequence are ignored.
+ * table_stride * page_size: at most 2^30. */
 typedef struct {
   const int32_t* table;
   const int32_t* kv_len;
@@ -634,7 +635,8 @@ sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host
  * 0 and lse = -infinity. Positions a token does not see never reach its
  * result, whatever is stored there. q, out in `dtype`; q and out must not
  * overlap. The same arguments give the same bits at every call.
- * n_q_heads: a multiple of n_kv_heads. scale: finite.
+ * n_q_heads: a multiple of n_kv_heads, n_q_heads * n_tokens at most 2^30.
+ * scale: finite.
  * ws: at least sffn_attend_workspace_bytes, 256-byte aligned. */
 size_t sffn_attend_workspace_bytes(const sffn_kv* kv, int32_t n_q_heads, int32_t n_seq, int32_t n_tokens);
 sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows q, int32_t n_q_heads,
