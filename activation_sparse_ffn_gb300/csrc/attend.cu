@@ -1,27 +1,34 @@
 // Attention of decode tokens over the paged 4-bit cache.
 //
 // Mathematics. For query row r (a token and one of the gq query heads of a key
-// head) and position j, in units of log2: S = q' . K_j with q' = q * scale *
-// log2(e). A cached key is mid + step * c per group of channels with c = 2u - 15
-// an odd integer, so S = sum over groups (step * (q'_g . c_g) + mid * sum(q'_g)):
-// the tensor cores multiply q' with the bare codes, exact as halves, and step
-// and mid are applied to eight positions at a time in fp32. In the same way
-// sum_j p_j V_j = sum_j (p_j step_j) c_j + sum_j p_j mid_j, with the running
-// maximum and sum of the softmax in fp32.
+// head) and position j, in units of log2: S = f q_r . K_j with f = scale *
+// log2(e). A cached key is mid + step * (2u - 15) per group of channels, so
+// S / f = sum over groups (step * (q_g . (2u - 15)) + mid * sum(q_g)): the
+// tensor cores multiply q with the bare codes, exact as halves, and step and
+// mid are applied once per group in fp32. In the same way sum_j p_j V_j = sum_j
+// (p_j step_j) (2u_j - 15) + sum_j p_j mid_j, with the running maximum and sum
+// of the softmax in fp32.
 //
-// Precision. q' and p * step are fp32 numbers carried by two halves each (22
-// bits): the eight query rows of a tile stand in rows 0-7 of the 16-row operand
-// and what the first halves leave in rows 8-15, so that the split costs no
-// products (the tile holds at most eight rows). Powers of two bring the row's
-// largest q' and the tile's largest step to 2^13 first, so that small numbers
-// keep their bits. The sums of 64 positions leave the tensor core and are added
-// to the running output in fp32: its own additions truncate, and over a long
-// history that would show.
+// Operands. Sixteen positions are the 16-row operand of the score product and
+// eight query rows its 8-column operand; for the values, sixteen channels and
+// again the eight rows. The weights change from the first product's result
+// layout to the second's operand layout by an 8 x 8 transpose in registers.
+//
+// Two arithmetics. 16-bit rows (Exact = false): q is exact as halves up to a
+// power of two per row; weights are rounded to halves (2^-11 relative, below
+// the result's own rounding, and at most 2^-39 of the unit's largest: they are
+// shifted up by 2^14); the denominator is summed in fp32 before. Codes go in as they stand in the word, u times 2^-23 or the
+// like: one mask per pair and no arithmetic; the sums of w are subtracted by
+// starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
+// p * step are carried by two halves each (22 bits) in two products, and the
+// codes are centred first, because the tensor core truncates its sums and a
+// sum of uncentred codes would show that over a long history. Either way the
+// sums of one unit's positions leave the tensor core and are added up in fp32.
 //
 // Work split. The visible blocks of U positions (`units`) of every (sequence,
 // key head, tile of eight rows) are numbered through, and each warp of the grid
 // takes an equal run of that list, whatever the lengths are. A warp streams its
-// units through a private ring in shared memory with one bulk copy per page for
+// units through a private ring in shared memory with bulk copies per page for
 // keys, values and params, so warps never wait for one another in the loop.
 // Rows whose units lie within one warp are finished by it; the others are
 // merged within the block at its end, and those cut by a block border by
@@ -35,21 +42,25 @@ namespace sffn {
 
 namespace {
 
-constexpr int kAttWarps = 8;
-constexpr int kAttThreads = kAttWarps * 32;
+constexpr int kMaxWarps = 16;
 constexpr int kRows = 8;   // query rows of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int D, int G>
+template <int D, int G, bool Exact>
 struct Att {
   static constexpr int NG = D / G;
   static constexpr int U = D == 256 ? 32 : 64;             // positions of a unit
   static constexpr int kStage = U * (D + 8 * NG);          // bytes
-  static constexpr int kStages = kStage * kAttWarps * 3 <= 212 * 1024 ? 3 : 2;
-  static constexpr int kRing = kStage * kStages * kAttWarps;
+  // as many warps as the registers of the inner loop and two stages each allow
+  static constexpr int kByRegs = Exact ? (D == 64 ? 12 : 8) : (D == 64 ? 16 : D == 128 ? 12 : 8);
+  static constexpr int kBudget = 224 * 1024;
+  static constexpr int kBySmem = kBudget / (2 * kStage);
+  static constexpr int kWarps = kByRegs < kBySmem ? kByRegs : kBySmem;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStages = kStage * kWarps * 3 <= kBudget ? 3 : 2;
   static constexpr int kPart = kRows * D + 2 * kRows;      // floats of a partial result: sums, maxima, totals
-  static constexpr int kParts = kPart * 4 * kAttWarps;
-  static constexpr int kSmem = kRing > kParts ? kRing : kParts;
+  static constexpr int kSmem = kStage * kStages * kWarps;
+  static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
 
 // What a block tells k_attend_join about the item its first unit lies in.
@@ -71,7 +82,7 @@ struct AttendArgs {
   int hq, gq, dtype, window;
   float scale;
   Border* borders;     // [blocks]
-  float* warp_parts;   // [blocks * kAttWarps][kPart]
+  float* warp_parts;   // [blocks * warps][kPart]
   float* block_parts;  // [blocks][2][kPart]
 };
 
@@ -156,7 +167,7 @@ struct Cursor {
   __device__ __forceinline__ bool empty(int U) const { return base0 + u * U > last; }
 };
 
-template <int D, int G>
+template <int D>
 __device__ __forceinline__ void write_row(const AttendArgs& a, int q0, int n, int kh, int row, int lane, const float* o,
                                           float m, float l) {
   // o: channels lane * (D/32) .. of the row
@@ -172,10 +183,10 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int q0, int n, in
     a.lse[(size_t)i * a.hq + h] = l == 0.f ? __int_as_float(0xff800000) : (m + log2f(l)) * kLn2;
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
-  using T = Att<D, G>;
-  constexpr int U = T::U, NG = T::NG, CPL = D / 32;
+template <int D, int G, bool Exact>
+__global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const AttendArgs a) {
+  using T = Att<D, G, Exact>;
+  constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[kAttWarps][T::kStages];
   __shared__ long long s_scan[kAttWarps + 1];
@@ -321,43 +332,52 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
   }
 
   const float ninf = __int_as_float(0xff800000);
-  uint32_t q[D / 16][4];
-  float qs[NG], mv[NG], o[D / 8][2];
-  float f = 1.f, m = ninf, l = 0.f;
-  int pos = 0, lo = 0;     // the row's position and the first it sees
-  int pos_min = 0, lo_max = 0;   // over the tile's rows
+  constexpr int QL = Exact ? 2 : 1;          // halves that carry a query element
+  uint32_t q[QL][D / 16][2];                 // column g of the operand
+  float qs[NG][2];                           // sums of q over a group, rows 2t and 2t + 1 as everything below
+  float o[D / 16][4];                        // channels 16x + g and 16x + 8 + g, each for both rows
+  float l[2] = {0.f, 0.f};                   // the lane's share of sum p
+  float mid_sum[Exact ? NG : 1][2];          // Exact: its share of sum p mid; else: the whole of group g's
+  float f[2] = {1.f, 1.f}, m[2] = {ninf, ninf};
+  int pos[2], lo[2];                         // position of the row and the first it sees
+  int pos_g = 0, lo_g = 0;                   // of row g
   bool dead = false, fresh = true;
   long long item_start = u0 - cur.u;
+  const int kt = kv_pos_of_col(g);           // position, of eight, of row g of a key operand
+  const int ta = kv_pos_of_col(2 * t), tb = kv_pos_of_col(2 * t + 1);  // of columns 2t, 2t + 1 of a value operand
 
   // after a wait that ran out: copies still under way must land before the ring is used for anything else
   auto drain = [&]() {
     if (dead)
       for (; taken < issued; ++taken) mbar_wait_bounded(&s_bar[warp][taken % T::kStages], (taken / T::kStages) & 1);
   };
-  // the end of a segment, the warp's units of one item (lane: row g, channels 8x + 2t, + 1); true: the item lies within the warp
+  // the end of a segment, the warp's units of one item; true: the whole item lies within the warp
   auto finish = [&](bool last) {
-    const float lt = quad_sum(l);
 #pragma unroll
-    for (int n = 0; n < NG; ++n) mv[n] = quad_sum(mv[n]);
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-    for (int x = 0; x < D / 8; ++x) {
-      o[x][0] += mv[x * 8 / G];
-      o[x][1] += mv[x * 8 / G];
-    }
+      for (int r = 0; r < 2; ++r) {
+        const float s = Exact ? row_sum(mid_sum[Exact ? n : 0][r]) : __shfl_sync(SFFN_FULL_MASK, mid_sum[0][r], 4 * n + t);
+#pragma unroll
+        for (int x = n * G / 16; x < (n + 1) * G / 16; ++x) o[x][r] += s, o[x][2 + r] += s;
+      }
+    const float lt[2] = {row_sum(l[0]), row_sum(l[1])};
+    const float mt[2] = {m[0] == ninf ? ninf : m[0] * f[0], m[1] == ninf ? ninf : m[1] * f[1]};
     const long long item_end = item_start + cur.units;
-    const float mt = m == ninf ? ninf : m * f;
     if (item_start >= u0 && item_end <= u1) {   // finish the rows here
-      const int row = cur.tile * kRows + g;
-      if (row < cur.n * a.gq) {
-        const int i = cur.q0 + row / a.gq, h = cur.kh * a.gq + row % a.gq;
-        const size_t at = (size_t)(i * a.out.row_stride + h * a.out.head_stride);
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) {
-          const float v[2] = {o[x][0] * inv, o[x][1] * inv};
-          st_run<2>(a.out.ptr, at + 8 * x + 2 * t, a.dtype, v);
+      for (int r = 0; r < 2; ++r) {
+        const int row = cur.tile * kRows + 2 * t + r;
+        if (row >= cur.n * a.gq) continue;
+        const int i = cur.q0 + row / a.gq, h = cur.kh * a.gq + row % a.gq;
+        const size_t at = (size_t)(i * a.out.row_stride + h * a.out.head_stride) + g;
+        const float inv = lt[r] == 0.f ? 0.f : 1.f / lt[r];
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          st_elem(a.out.ptr, at + 16 * x, o[x][r] * inv, a.dtype);
+          st_elem(a.out.ptr, at + 16 * x + 8, o[x][2 + r] * inv, a.dtype);
         }
-        if (a.lse && t == 0) a.lse[(size_t)i * a.hq + h] = lt == 0.f ? ninf : (mt + log2f(lt)) * kLn2;
+        if (a.lse && g == 0) a.lse[(size_t)i * a.hq + h] = lt[r] == 0.f ? ninf : (mt[r] + log2f(lt[r])) * kLn2;
       }
       return true;
     }
@@ -368,11 +388,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
     }
     float* dst = last ? reinterpret_cast<float*>(smem) + warp * T::kPart : a.warp_parts + gw * T::kPart;
 #pragma unroll
-    for (int x = 0; x < D / 8; ++x)
-      *reinterpret_cast<float2*>(dst + g * D + 8 * x + 2 * t) = make_float2(o[x][0], o[x][1]);
-    if (t == 0) {
-      dst[kRows * D + g] = mt;
-      dst[kRows * D + kRows + g] = lt;
+    for (int r = 0; r < 2; ++r) {
+      float* row = dst + (2 * t + r) * D + g;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) row[16 * x] = o[x][r], row[16 * x + 8] = o[x][2 + r];
+      if (g == 0) {
+        dst[kRows * D + 2 * t + r] = mt[r];
+        dst[kRows * D + kRows + 2 * t + r] = lt[r];
+      }
     }
     if (lane == 0) {
       Entry& e = s_entry[2 * warp + (last ? 1 : 0)];
@@ -388,46 +411,63 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
     if (fresh) {   // first unit of the warp in this item: query rows
       fresh = false;
       item_start = uu - cur.u;
-      const int rows = cur.n * a.gq, row = cur.tile * kRows + g, r = min(row, rows - 1);
-      pos = cur.len - cur.n + r / a.gq;
-      lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-      pos_min = cur.first;
-      lo_max = a.window > 0 ? max(0, cur.last - a.window + 1) : 0;
-      const size_t at = (size_t)((cur.q0 + r / a.gq) * a.q.row_stride + (cur.kh * a.gq + r % a.gq) * a.q.head_stride);
-      const float sc = row < rows ? a.scale * kLog2e : 0.f;
-      float big = 0.f;
-      // two passes over the row: its largest element, then the split
+      const int rows = cur.n * a.gq, row = cur.tile * kRows + g, rg = min(row, rows - 1);
+      pos_g = cur.len - cur.n + rg / a.gq;
+      lo_g = a.window > 0 ? max(0, pos_g - a.window + 1) : 0;
+      const size_t at = (size_t)((cur.q0 + rg / a.gq) * a.q.row_stride + (cur.kh * a.gq + rg % a.gq) * a.q.head_stride);
+      // the sign of the scale goes with q, its size with f; rows past the end are zero
+      const float sign = row >= rows || a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
+      float big = 0.f, fg, up, sum[NG];
+      // two passes over the row: its largest element, then the operand
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         float x[8];
         ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, a.dtype, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e] * sc));
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
       }
-      float up;
-      scale_to_half_range(quad_max(big), up, f);
+      scale_to_half_range(quad_max(big), up, fg);
+      fg = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e * fg, 1.1754944e-38f);
 #pragma unroll
-      for (int n = 0; n < NG; ++n) qs[n] = mv[n] = 0.f;
+      for (int n = 0; n < NG; ++n) sum[n] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         float x[8];
         ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, a.dtype, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] = row < rows ? x[e] * sc * up : 0.f;
-          qs[j * 32 / G] += x[e];
+          x[e] = sign == 0.f ? 0.f : x[e] * (up * sign);
+          sum[j * 32 / G] += x[e];
         }
-        split_f16(x[0], x[1], q[2 * j][0], q[2 * j][1]);
-        split_f16(x[2], x[3], q[2 * j][2], q[2 * j][3]);
-        split_f16(x[4], x[5], q[2 * j + 1][0], q[2 * j + 1][1]);
-        split_f16(x[6], x[7], q[2 * j + 1][2], q[2 * j + 1][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t* hi = &q[0][2 * j + (e >> 1)][e & 1];
+          if (Exact) {
+            split_f16(x[2 * e], x[2 * e + 1], *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
+          } else {   // odd pairs meet codes that are sixteen times as large
+            const float c = (e & 1) ? 0.0625f : 1.f;
+            *hi = h2_u32(__floats2half2_rn(x[2 * e] * c, x[2 * e + 1] * c));
+          }
+        }
+      }
+      if (!Exact) fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
+#pragma unroll
+      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * (Exact ? 1.f : 5.9604645e-8f);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int src = 4 * (2 * t + r);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) qs[n][r] = __shfl_sync(SFFN_FULL_MASK, sum[n], src);
+        f[r] = __shfl_sync(SFFN_FULL_MASK, fg, src);
+        pos[r] = __shfl_sync(SFFN_FULL_MASK, pos_g, src);
+        lo[r] = __shfl_sync(SFFN_FULL_MASK, lo_g, src);
+        m[r] = ninf;
+        l[r] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NG; ++n) qs[n] = quad_sum(qs[n]);
+      for (int n = 0; n < (Exact ? NG : 1); ++n) mid_sum[n][0] = mid_sum[n][1] = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = 0.f;
-      m = ninf;
-      l = 0.f;
+      for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
     }
     if (!cur.empty(U) && !dead) {
       issue();
@@ -441,93 +481,93 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
       const uint8_t* sv = sk + U * (D / 2);
       const uint8_t* sp = sk + U * D;
       const int base = cur.base(U);
-      const bool masked = base < lo_max || base + U - 1 > pos_min;
+      // whether some row does not see some position of the unit; positions that no row sees may be anything
+      const int lo_min = a.window > 0 ? max(0, cur.first - a.window + 1) : 0;
+      const bool masked = base + U - 1 > cur.first || (a.window > 0 && base < cur.last - a.window + 1);
+      auto param = [&](int tile, int n, int which, int slot) {   // (step, mid) of a slot of eight positions
+        return *reinterpret_cast<const uint32_t*>(sp + (tile * NG + n) * 64 + which * 32 + slot * 4);
+      };
 
-      // ---- scores of U positions
-      float s[U / 8][2];
-      const int kt = kv_pos_of_col(g);   // the position, of eight, that this lane's key words belong to
+      // ---- scores of U positions: s[i] rows 16i + slot g and 16i + 8 + slot g, each for both query rows
+      float s[U / 16][4];
 #pragma unroll
-      for (int i = 0; i < U / 8; ++i) {
-        const uint8_t* row = sk + (8 * i + kt) * (D / 2);
-        uint32_t w[D / 32];
-        if (D == 64) {
-          const uint2 v = *reinterpret_cast<const uint2*>(row + key_word_off<D>(kt, t, 0));
-          w[0] = v.x, w[1] = v.y;
-        } else {
+      for (int i = 0; i < U / 16; ++i) {
+        uint32_t w[2][D / 32];
 #pragma unroll
-          for (int j = 0; j < D / 32; j += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + key_word_off<D>(kt, t, j));
-            w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+        for (int k = 0; k < 2; ++k) {
+          const uint8_t* row = sk + (16 * i + 8 * k + kt) * (D / 2);
+          if (D == 64) {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + key_word_off<D>(kt, t, 0));
+            w[k][0] = v.x, w[k][1] = v.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 32; j += 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(row + key_word_off<D>(kt, t, j));
+              w[k][j] = v.x, w[k][j + 1] = v.y, w[k][j + 2] = v.z, w[k][j + 3] = v.w;
+            }
           }
         }
-        s[i][0] = s[i][1] = 0.f;
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
-            uint32_t p[4];
-            key_halves(w[j], p);
-            mma_f16(c, q[2 * j], p[0], p[1]);
-            mma_f16(c, q[2 * j + 1], p[2], p[3]);
+            uint32_t p0[4], p1[4];
+            if (Exact) {
+              key_halves(w[0][j], p0);
+              key_halves(w[1][j], p1);
+            } else {
+              key_bits(w[0][j], p0);
+              key_bits(w[1][j], p1);
+            }
+            const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
+#pragma unroll
+            for (int h = 0; h < QL; ++h) {
+              mma_f16(c, a0, q[h][2 * j][0], q[h][2 * j][1]);
+              mma_f16(c, a1, q[h][2 * j + 1][0], q[h][2 * j + 1][1]);
+            }
           }
-          const uint2 kp = *reinterpret_cast<const uint2*>(sp + ((i * NG + n) * 4 + t) * 16);
-          const float2 pa = __half22float2(u32_h2(kp.x)), pb = __half22float2(u32_h2(kp.y));
-          s[i][0] = fmaf(pa.x, c[0] + c[2], fmaf(pa.y, qs[n], s[i][0]));
-          s[i][1] = fmaf(pb.x, c[1] + c[3], fmaf(pb.y, qs[n], s[i][1]));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 0, g)));
+            const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
+            s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
+            s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
+          }
         }
       }
-      const int ta = kv_pos_of_col(2 * t), tb = kv_pos_of_col(2 * t + 1);  // positions of the lane's two columns
-      float mu = ninf;
+      if (masked) {
 #pragma unroll
-      for (int i = 0; i < U / 8; ++i) {
-        if (masked) {
-          const int ja = base + 8 * i + ta, jb = base + 8 * i + tb;
-          if (ja > pos || ja < lo) s[i][0] = ninf;
-          if (jb > pos || jb < lo) s[i][1] = ninf;
+        for (int i = 0; i < U / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = base + 16 * i + 8 * (e >> 1) + kt;
+            if (j > pos[e & 1] || j < lo[e & 1]) s[i][e] = ninf;
+          }
+      }
+      float mu[2] = {m[0], m[1]};
+#pragma unroll
+      for (int i = 0; i < U / 16; ++i) {
+        mu[0] = fmaxf(mu[0], fmaxf(s[i][0], s[i][2]));
+        mu[1] = fmaxf(mu[1], fmaxf(s[i][1], s[i][3]));
+      }
+      mu[0] = row_max(mu[0]);
+      mu[1] = row_max(mu[1]);
+      if (__any_sync(SFFN_FULL_MASK, mu[0] > m[0] || mu[1] > m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float back = mu[r] == m[r] ? 1.f : ex2((m[r] - mu[r]) * f[r]);   // m = -inf: 0
+          m[r] = mu[r];
+          l[r] *= back;
+#pragma unroll
+          for (int n = 0; n < (Exact ? NG : 1); ++n) mid_sum[n][r] *= back;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) o[x][r] *= back, o[x][2 + r] *= back;
         }
-        mu = fmaxf(mu, fmaxf(s[i][0], s[i][1]));
       }
-      mu = fmaxf(m, quad_max(mu));
-      if (__any_sync(SFFN_FULL_MASK, mu > m)) {
-        const float back = mu == m ? 1.f : ex2((m - mu) * f);   // m = -inf: 0
-        l *= back;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) mv[n] *= back;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) o[x][0] *= back, o[x][1] *= back;
-        m = mu;
-      }
-      const float mf = m == ninf ? 0.f : m * f;
-#pragma unroll
-      for (int i = 0; i < U / 8; ++i) {
-        s[i][0] = ex2(fmaf(s[i][0], f, -mf));
-        s[i][1] = ex2(fmaf(s[i][1], f, -mf));
-        l += s[i][0] + s[i][1];
-      }
+      float mf[2] = {m[0] == ninf ? 0.f : m[0] * f[0], m[1] == ninf ? 0.f : m[1] * f[1]};
 
-      // ---- weights times steps, and the sum over positions
-      auto value_params = [&](int i, int n, float2& va, float2& vb) {
-        const uint2 vp = *reinterpret_cast<const uint2*>(sp + ((i * NG + n) * 4 + t) * 16 + 8);
-        va = __half22float2(u32_h2(vp.x)), vb = __half22float2(u32_h2(vp.y));
-        if (masked) {   // what is not seen may be anything, NaN too
-          const int ja = base + 8 * i + ta, jb = base + 8 * i + tb;
-          if (ja > pos || ja < lo) va = make_float2(0.f, 0.f);
-          if (jb > pos || jb < lo) vb = make_float2(0.f, 0.f);
-        }
-      };
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < U / 8; ++i)
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          float2 va, vb;
-          value_params(i, n, va, vb);
-          top = fmaxf(top, fmaxf(va.x, vb.x));
-          mv[n] = fmaf(s[i][0], va.y, fmaf(s[i][1], vb.y, mv[n]));
-        }
-      float up, down;
-      scale_to_half_range(quad_max(top), up, down);
       uint32_t vw[U / 16][4][D / 64];   // the lane's words of four positions per 16
 #pragma unroll
       for (int k = 0; k < U / 16; ++k)
@@ -545,38 +585,185 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
             vw[k][r][0] = v.x, vw[k][r][1 % (D / 64)] = v.y, vw[k][r][2 % (D / 64)] = v.z, vw[k][r][3 % (D / 64)] = v.w;
           }
         }
+      constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the 64 channels of a word lie in
+
+      if (Exact) {
+        // weights in fp32; unseen steps and mids are cleared, weights of unseen positions are 0 already, and a
+        // seen NaN step meets only rows that see it
+        auto value_param = [&](int i, int k, int n) {
+          float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 1, g)));
+          if (masked) {
+            const int j = base + 16 * i + 8 * k + kt;
+            if (j > cur.last || j < lo_min) sm = make_float2(0.f, 0.f);
+          }
+          return sm;
+        };
+        float top = 0.f;
 #pragma unroll
-      for (int w = 0; w < D / 64; ++w) {
-        constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the word's 64 channels lie in
-        float acc[8][4];
+        for (int i = 0; i < U / 16; ++i) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+          for (int e = 0; e < 4; ++e) s[i][e] = ex2(fmaf(s[i][e], f[e & 1], -mf[e & 1]));
+          l[0] += s[i][0] + s[i][2];
+          l[1] += s[i][1] + s[i][3];
 #pragma unroll
-        for (int k = 0; k < U / 16; ++k) {
-          uint32_t pa[GW][4];
+          for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int n = 0; n < GW; ++n) {
-            float2 va, vb;
-            value_params(2 * k, w * 64 / G + n, va, vb);
-            split_f16(s[2 * k][0] * (va.x * up), s[2 * k][1] * (vb.x * up), pa[n][0], pa[n][1]);
-            value_params(2 * k + 1, w * 64 / G + n, va, vb);
-            split_f16(s[2 * k + 1][0] * (va.x * up), s[2 * k + 1][1] * (vb.x * up), pa[n][2], pa[n][3]);
+            for (int k = 0; k < 2; ++k) {
+              const float2 sm = value_param(i, k, n);
+              top = fmaxf(top, sm.x);
+              mid_sum[Exact ? n : 0][0] = fmaf(s[i][2 * k], sm.y, mid_sum[Exact ? n : 0][0]);
+              mid_sum[Exact ? n : 0][1] = fmaf(s[i][2 * k + 1], sm.y, mid_sum[Exact ? n : 0][1]);
+            }
+        }
+        float up, down;
+        scale_to_half_range(row_max(top), up, down);
+        uint32_t wh[GW][U / 16][2], wl[GW][U / 16][2];
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          if (w * 64 % G == 0) {
+#pragma unroll
+            for (int n = 0; n < GW; ++n)
+#pragma unroll
+              for (int i = 0; i < U / 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float st = value_param(i, k, w * 64 / G + n).x * up;
+                  float x0 = s[i][2 * k] * st, x1 = s[i][2 * k + 1] * st;
+                  if (masked) {
+                    if (s[i][2 * k] == 0.f) x0 = 0.f;
+                    if (s[i][2 * k + 1] == 0.f) x1 = 0.f;
+                  }
+                  uint32_t hi, lw;
+                  split_f16(x0, x1, hi, lw);
+                  wh[n][i][k] = transpose_8x8(hi);
+                  wl[n][i][k] = transpose_8x8(lw);
+                }
+          }
+          float acc[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < U / 16; ++k)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], hh ? 0x7632 : 0x5410);
+              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], hh ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next
+                const uint32_t y0 = e == 0 ? x0 << 4 : x0 >> 4, y1 = e == 0 ? x1 << 4 : x1 >> 4;
+                const uint32_t z0 = e == 0 ? x0 : x0 >> 8, z1 = e == 0 ? x1 : x1 >> 8;
+                const uint32_t av[4] = {value_halves(y0), value_halves(z0), value_halves(y1), value_halves(z1)};
+                const int n = (2 * hh + e) * 16 / G % GW;
+                mma_f16(acc[2 * hh + e], av, wh[n][k][0], wh[n][k][1]);
+                mma_f16(acc[2 * hh + e], av, wl[n][k][0], wl[n][k][1]);
+              }
+            }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * w + x][e] = fmaf(acc[x][e], down, o[4 * w + x][e]);
+        }
+      } else {
+        // what the lane's two slots of a tile may show: to any row, and to row g (all ones or zeros per half)
+        auto seen = [&](int tile, int first, int past) {
+          const int ja = base + 8 * tile + ta, jb = base + 8 * tile + tb;
+          return (ja >= first && ja <= past ? 0xffffu : 0u) | (jb >= first && jb <= past ? 0xffff0000u : 0u);
+        };
+        auto value_pair = [&](int tile, int n) { return *reinterpret_cast<const uint2*>(sp + (tile * NG + n) * 64 + 32 + 8 * t); };
+        auto value_steps = [&](int tile, int n) {
+          const uint2 v = value_pair(tile, n);
+          const uint32_t st = __byte_perm(v.x, v.y, 0x5410);
+          return masked ? st & seen(tile, lo_min, cur.last) : st;
+        };
+        __half2 big = u32_h2(0u);
+#pragma unroll
+        for (int i = 0; i < U / 8; ++i)
+#pragma unroll
+          for (int n = 0; n < NG; ++n) big = __hmax2(big, u32_h2(value_steps(i, n)));
+        // weights are 2^sh p with sh = 14 less the bits that the largest step needs above 1
+        const float top = quad_max(fmaxf(__low2float(big), __high2float(big)));
+        const int sh = min(14, 140 - (int)(__float_as_uint(top) >> 23));
+        const float down = __uint_as_float((uint32_t)(127 - sh) << 23);
+        mf[0] -= (float)sh;
+        mf[1] -= (float)sh;
+        uint32_t p[U / 16][2];
+        float mla[4] = {0.f, 0.f, 0.f, 0.f}, la[2] = {0.f, 0.f};
+        const uint32_t ones = 0x3c003c00u;
+#pragma unroll
+        for (int i = 0; i < U / 16; ++i) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = ex2(fmaf(s[i][2 * k], f[0], -mf[0])), p1 = ex2(fmaf(s[i][2 * k + 1], f[1], -mf[1]));
+            la[0] += p0;
+            la[1] += p1;
+            p[i][k] = transpose_8x8(h2_u32(__floats2half2_rn(p0, p1)));
+          }
+          // row n: the mids of group n
+          uint32_t mid[2] = {0u, 0u};
+          if (g < NG) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint2 v = value_pair(2 * i + k, g);
+              mid[k] = __byte_perm(v.x, v.y, 0x7632);
+              if (masked) mid[k] &= seen(2 * i + k, lo_min, cur.last);
+            }
+          }
+          const uint32_t am[4] = {mid[0], 0u, mid[1], 0u};
+          mma_f16(mla, am, p[i][0], p[i][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          l[r] = fmaf(la[r], down, l[r]);
+          mid_sum[0][r] = fmaf(mla[r], down, mid_sum[0][r]);
+        }
+        const float k0 = down * 33554432.f, k1 = down * 2097152.f;   // codes are u * 2^-24 and u * 2^-20
+        uint32_t wt[GW][U / 16][2];
+        float ws[GW][4];
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          if (w * 64 % G == 0) {
+#pragma unroll
+            for (int n = 0; n < GW; ++n) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < U / 16; ++i) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint32_t x = h2_u32(__hmul2(u32_h2(p[i][k]), u32_h2(value_steps(2 * i + k, w * 64 / G + n))));
+                  if (masked) x &= seen(2 * i + k, lo_g, pos_g);   // a step may be NaN
+                  wt[n][i][k] = x;
+                }
+                const uint32_t one[4] = {ones, 0u, ones, 0u};
+                mma_f16(c, one, wt[n][i][0], wt[n][i][1]);
+              }
+              // -15 sum(w) in units of the products
+              ws[n][0] = c[0] * -4.4703484e-7f, ws[n][1] = c[1] * -4.4703484e-7f;
+              ws[n][2] = ws[n][0] * 16.f, ws[n][3] = ws[n][1] * 16.f;
+            }
           }
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], hh ? 0x7632 : 0x5410);
-            const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], hh ? 0x7632 : 0x5410);
+            float acc[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t y0 = e == 0 ? x0 << 4 : x0 >> (4 * e - 4), y1 = e == 0 ? x1 << 4 : x1 >> (4 * e - 4);
-              mma_f16(acc[4 * hh + e], pa[(4 * hh + e) * 8 / G % GW], value_halves(y0), value_halves(y1));
+            for (int k = 0; k < U / 16; ++k)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next: the low and high nibble of a byte
+                const int n = (2 * hh + e) * 16 / G % GW;
+                const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
+                const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
+                const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
+                const uint32_t av[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u};
+                mma_f16_from(acc[e], av, wt[n][k][0], wt[n][k][1], k == 0 ? ws[n] : acc[e]);
+              }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float* ox = o[4 * w + 2 * hh + e];
+              ox[0] = fmaf(acc[e][0], k0, ox[0]);
+              ox[1] = fmaf(acc[e][1], k0, ox[1]);
+              ox[2] = fmaf(acc[e][2], k1, ox[2]);
+              ox[3] = fmaf(acc[e][3], k1, ox[3]);
             }
           }
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          o[8 * w + x][0] = fmaf(acc[x][0] + acc[x][2], down, o[8 * w + x][0]);
-          o[8 * w + x][1] = fmaf(acc[x][1] + acc[x][3], down, o[8 * w + x][1]);
         }
       }
       __syncwarp();
@@ -596,6 +783,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
   __syncthreads();
 
   // ---- partial results of the block: warp w merges row w of each item
+  if (warp >= kRows) return;
   const float* sm = reinterpret_cast<const float*>(smem);
   for (int e0 = 0; e0 < 2 * kAttWarps;) {
     if (s_entry[e0].where == 0) {
@@ -631,7 +819,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
       }
     }
     if (it.item_start >= block_u0 && it.item_end <= block_u1) {
-      write_row<D, G>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
+      write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
     } else {
       float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start <= block_u0 ? 0 : 1)) * T::kPart;
 #pragma unroll
@@ -648,10 +836,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_attend(const AttendArgs a) {
 // Rows cut by a block border: block c handles the item that the first unit of
 // attention block c + 1 lies in, if that item began before it and no earlier
 // border lies in it; warp w takes row w.
-template <int D, int G>
-__global__ void __launch_bounds__(kAttThreads) k_attend_join(const AttendArgs a, int blocks) {
-  using T = Att<D, G>;
-  constexpr int CPL = D / 32;
+template <int D>
+__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks) {
+  constexpr int CPL = D / 32, kPart = Att<D, 64, false>::kPart;
   pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -662,7 +849,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_join(const AttendArgs a,
   const float ninf = __int_as_float(0xff800000);
   int last = c;   // blocks c - 1 .. last hold a part
   while (last + 1 < blocks && start_at(last + 1) < item_end) ++last;
-  auto part = [&](int k) { return a.block_parts + ((long long)k * 2 + (k == c - 1 && prev < item_start ? 1 : 0)) * T::kPart; };
+  auto part = [&](int k) { return a.block_parts + ((long long)k * 2 + (k == c - 1 && prev < item_start ? 1 : 0)) * kPart; };
   auto has = [&](int k) { return k == c - 1 || (k + 1 < blocks ? start_at(k + 1) : item_end) > start_at(k); };
   float mt = ninf;
   for (int k = c - 1; k <= last; ++k)
@@ -681,7 +868,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend_join(const AttendArgs a,
   }
   const int q0 = __ldcg(&a.borders[c].q0), n = __ldcg(&a.borders[c].n), kh = __ldcg(&a.borders[c].kh),
             tile = __ldcg(&a.borders[c].tile);
-  write_row<D, G>(a, q0, n, kh, tile * kRows + warp, lane, ot, mt, lt);
+  write_row<D>(a, q0, n, kh, tile * kRows + warp, lane, ot, mt, lt);
 }
 
 template <typename F>
@@ -709,7 +896,7 @@ AttWs att_ws(const sffn_kv& C) {
   const size_t part = (size_t)(kRows * C.desc.head_dim + 2 * kRows) * 4, blocks = C.num_sms;
   AttWs w;
   w.warp_parts = up256(blocks * sizeof(Border));
-  w.block_parts = up256(w.warp_parts + blocks * kAttWarps * part);
+  w.block_parts = up256(w.warp_parts + blocks * kMaxWarps * part);
   w.total = up256(w.block_parts + blocks * 2 * part);
   return w;
 }
@@ -719,7 +906,11 @@ AttWs att_ws(const sffn_kv& C) {
 cudaError_t configure_attend_kernels(const sffn_kv& C) {
   return by_shape(C, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    return cudaFuncSetAttribute(k_attend<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, Att<D, G>::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(k_attend<D, G, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Att<D, G, false>::kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(k_attend<D, G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Att<D, G, true>::kSmem);
   });
 }
 
@@ -738,9 +929,15 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
   const int blocks = C.num_sms;
   return by_shape(C, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    cudaError_t e = launch_ex(k_attend<D, G>, dim3(blocks), dim3(kAttThreads), Att<D, G>::kSmem, st, true, 1, a);
-    if (e != cudaSuccess || blocks < 2) return e;
-    return launch_ex(k_attend_join<D, G>, dim3(blocks - 1), dim3(kAttThreads), 0, st, true, 1, a, blocks);
+    auto run = [&](auto* kern, int threads, int smem) {
+      const cudaError_t e = launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, 1, a);
+      if (e != cudaSuccess || blocks < 2) return e;
+      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks);
+    };
+    using E = Att<D, G, true>;
+    using N = Att<D, G, false>;
+    return dtype == SFFN_F32 ? run(k_attend<D, G, true>, E::kThreads, E::kSmem)
+                             : run(k_attend<D, G, false>, N::kThreads, N::kSmem);
   });
 }
 

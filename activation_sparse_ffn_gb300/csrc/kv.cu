@@ -108,13 +108,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
   const float midf = __half2float(mid);
   const float far = fmaxf(__fsub_rn(hi, midf), __fsub_rn(midf, lo));
   __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
-  if (bad) mid = __ushort_as_half(0x7fff), step = __ushort_as_half(0);
+  if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
   const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
   uint8_t* code = s_code[warp];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) {
     const float t = floorf(__fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f));
-    code[c0 + e] = stepf == 0.f ? 8 : (uint8_t)fminf(fmaxf(t, 0.f), 15.f);
+    code[c0 + e] = stepf == 0.f || bad ? 8 : (uint8_t)fminf(fmaxf(t, 0.f), 15.f);
   }
   __syncwarp();
   if (lane % lanes == 0) {

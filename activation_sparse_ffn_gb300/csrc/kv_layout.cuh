@@ -20,17 +20,19 @@
 // the position so that the four positions a warp reads together use different
 // banks.
 //
-// Params: for eight positions and one group, entry t holds the (step, mid)
-// pairs of positions T(2t) and T(2t + 1): keys first, then values; T(i) = i
-// for i < 4 and i ^ 1 above is the order in which the eight columns of a
-// score tile are assigned to positions.
+// Params: for eight positions and one group, the (step, mid) pairs of the keys
+// of the eight positions, then those of the values, each in the order T(0) ..
+// T(7); T(i) = i for i < 4 and i ^ 1 above is the order in which the eight
+// rows (keys) or columns (values) of a matrix operand are assigned to
+// positions. A group with a non-finite value has step = NaN and mid = 0: a
+// weight can be cleared before it meets a step, but not before it meets a mid.
 #pragma once
 
 #include "common.cuh"
 
 namespace sffn {
 
-// Column of a score tile <-> position within eight (its own inverse).
+// Row or column of a matrix operand <-> position within eight (its own inverse).
 __host__ __device__ constexpr int kv_pos_of_col(int c) { return c ^ (c >> 2); }
 
 template <int D>
@@ -66,16 +68,17 @@ __host__ __device__ constexpr int value_word_off(int pos, int g, int w) {
 
 // Byte offset, within the params, of the key (which = 0) or value (1) pair of a position and group.
 __host__ __device__ constexpr int param_off(int pos, int grp, int n_groups, int which) {
-  return (((pos >> 3) * n_groups + grp) * 4 + ((pos & 7) >> 1)) * 16 + which * 8 + ((pos ^ (pos >> 2)) & 1) * 4;
+  return ((pos >> 3) * n_groups + grp) * 64 + which * 32 + kv_pos_of_col(pos & 7) * 4;
 }
 
 // Key word: the codes of channel pairs e = 0..3 (channels 2e and 2e + 1 of the
 // eight) stand at bits 4 e of the two 16-bit halves; the whole word is then
 // rotated left by one bit. A code then lies at bits 1-4 or 5-8 of a half (after
 // a rotation by 8 for e = 2, 3), inside the ten mantissa bits with one bit to
-// spare below: with the exponent of 1024 put above it, the half-precision
-// number is 1024 + 2u (or 1024 + 32u) exactly, and one half-precision
-// operation makes it 2u - 15 exactly.
+// spare below: as a half-precision number the masked bits are u * 2^-23
+// (or u * 2^-19) exactly; with the exponent of 1024 put above them they are
+// 1024 + 2u (or 1024 + 32u), and one half-precision operation makes that 2u -
+// 15 exactly.
 __host__ __device__ __forceinline__ uint32_t key_word(const uint8_t* u) {
   uint32_t w = 0;
 #pragma unroll

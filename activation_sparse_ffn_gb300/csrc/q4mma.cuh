@@ -22,6 +22,21 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a b + c
+__device__ __forceinline__ void mma_f16_from(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const float* c) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Transpose of an 8 x 8 matrix of halves: lane 4 g + t gives row g, columns 2t, 2t + 1.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t h2_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u32_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
@@ -59,6 +74,16 @@ __device__ __forceinline__ void key_halves(uint32_t w, uint32_t* p) {
   p[3] = h2_u32(__hfma2(code_bits(r, 0x01e001e0u), k16, k79));
 }
 
+// The four pairs of a key word as they stand: u * 2^-23 for p[0] and p[2],
+// u * 2^-19 for p[1] and p[3] (subnormal halves, which the tensor cores take exactly).
+__device__ __forceinline__ void key_bits(uint32_t w, uint32_t* p) {
+  const uint32_t r = __funnelshift_r(w, w, 8);
+  p[0] = w & 0x001e001eu;
+  p[1] = w & 0x01e001e0u;
+  p[2] = r & 0x001e001eu;
+  p[3] = r & 0x01e001e0u;
+}
+
 // 2u - 15 for the code at bits 4-7 of both halves: (1024 + 16u) / 8 - 143.
 __device__ __forceinline__ uint32_t value_halves(uint32_t w) {
   return h2_u32(__hfma2(code_bits(w, 0x00f000f0u), u32_h2(0x30003000u), u32_h2(0xd878d878u)));
@@ -73,6 +98,17 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(SFFN_FULL_MASK, v, 1);
   return v + __shfl_xor_sync(SFFN_FULL_MASK, v, 2);
+}
+// Over the eight lanes that share t.
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor_sync(SFFN_FULL_MASK, v, 4);
+  v += __shfl_xor_sync(SFFN_FULL_MASK, v, 8);
+  return v + __shfl_xor_sync(SFFN_FULL_MASK, v, 16);
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(SFFN_FULL_MASK, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(SFFN_FULL_MASK, v, 8));
+  return fmaxf(v, __shfl_xor_sync(SFFN_FULL_MASK, v, 16));
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(SFFN_FULL_MASK, v, 1));

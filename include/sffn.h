@@ -555,7 +555,7 @@ void sffn_linear_destroy(sffn_linear* linear);
  * value of the group, mid = f16(lo/2 + hi/2), step = f16(max(hi - mid,
  * mid - lo) * f32(1/15)) (both limited to +-65504), u = floor((x - mid) *
  * (1 / (2 step)) + 8) limited to 0..15, and u = 8 if step is 0. A group with
- * a non-finite value is stored as NaN (mid = NaN).
+ * a non-finite value is stored as NaN (step = NaN).
  *   n_pages: 1 .. 2^31 - 1.  page_size: 16, 32 or 64.  n_kv_heads: 1 .. 1024.
  *   head_dim: 64, 128 or 256.  group: 32, 64 or 128, at most head_dim. */
 typedef struct {
