@@ -15,9 +15,10 @@
 // layout to the second's operand layout by an 8 x 8 transpose in registers.
 //
 // Two arithmetics. 16-bit rows (Exact = false): q is exact as halves up to a
-// power of two per row; weights are rounded to halves (2^-11 relative, below
-// the result's own rounding, and at most 2^-39 of the unit's largest: they are
-// shifted up by 2^14); the denominator is summed in fp32 before. Codes go in as they stand in the word, u times 2^-23 or the
+// power of two per row; a weight times its step is rounded to a half once
+// (2^-12 relative, below the result's own rounding; a power of two brings the
+// unit's largest step to 2^13 first, so that small ones keep their bits), the
+// denominator and the mids are summed in fp32. Codes go in as they stand in the word, u times 2^-23 or the
 // like: one mask per pair and no arithmetic; the sums of w are subtracted by
 // starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
 // p * step are carried by two halves each (22 bits) in two products, and the
@@ -74,7 +75,7 @@ static_assert(sizeof(Border) == 48, "");
 struct AttendArgs {
   const uint8_t* pages;
   size_t page_bytes, head_bytes;
-  int n_pages, P, hkv;
+  int n_pages, P, P_log2, hkv;
   uint32_t* err;
   sffn_kv_batch b;
   sffn_rows q, out;
@@ -285,12 +286,14 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   Cursor nxt = cur;
   long long nu = u0;       // next unit to copy
   int issued = 0, taken = 0;
+  auto slot_of = [](int k) { return k % T::kStages; };
+  auto phase_of = [](int k) { return (uint32_t)(k / T::kStages) & 1u; };
   int page = 0;            // lane i: page of run i of unit nu
   auto fetch_page = [&]() {
     if (nu < u1 && !nxt.empty(U)) {
       const int base = nxt.base(U);
       if (lane < parts && base + lane * RP <= nxt.last)
-        page = ld_dep(a.b.table + (size_t)nxt.s * a.b.table_stride + (base + lane * RP) / a.P);
+        page = ld_dep(a.b.table + (size_t)nxt.s * a.b.table_stride + ((base + lane * RP) >> a.P_log2));
     }
   };
   // copies the next unit that shows something; false: none left
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       fetch_page();
     }
     if (nu >= u1) return;
-    const int st = issued % T::kStages, base = nxt.base(U);
+    const int st = slot_of(issued), base = nxt.base(U);
     uint8_t* dst = ring + st * T::kStage;
     const int runs = min(parts, (nxt.last - base) / RP + 1);
     if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][st], (uint32_t)(runs * RP * (D + 8 * NG)));
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         page = 0;
       }
       const uint8_t* src = a.pages + (size_t)page * a.page_bytes + (size_t)nxt.kh * a.head_bytes;
-      const int slot = base % a.P;  // zero unless a page holds several units
+      const int slot = base & (a.P - 1);  // zero unless a page holds several units
       const uint64_t pol = l2_policy_evict_first();
       bulk_g2s(dst + lane * RP * (D / 2), src + slot * (D / 2), RP * (D / 2), &s_bar[warp][st], pol);
       bulk_g2s(dst + U * (D / 2) + lane * RP * (D / 2), src + kv_value_off(a.P, D) + slot * (D / 2), RP * (D / 2),
@@ -337,10 +340,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   float qs[NG][2];                           // sums of q over a group, rows 2t and 2t + 1 as everything below
   float o[D / 16][4];                        // channels 16x + g and 16x + 8 + g, each for both rows
   float l[2] = {0.f, 0.f};                   // the lane's share of sum p
-  float mid_sum[Exact ? NG : 1][2];          // Exact: its share of sum p mid; else: the whole of group g's
+  float mid_sum[NG][2];                      // and of sum p mid
   float f[2] = {1.f, 1.f}, m[2] = {ninf, ninf};
   int pos[2], lo[2];                         // position of the row and the first it sees
-  int pos_g = 0, lo_g = 0;                   // of row g
   bool dead = false, fresh = true;
   long long item_start = u0 - cur.u;
   const int kt = kv_pos_of_col(g);           // position, of eight, of row g of a key operand
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   // after a wait that ran out: copies still under way must land before the ring is used for anything else
   auto drain = [&]() {
     if (dead)
-      for (; taken < issued; ++taken) mbar_wait_bounded(&s_bar[warp][taken % T::kStages], (taken / T::kStages) & 1);
+      for (; taken < issued; ++taken) mbar_wait_bounded(&s_bar[warp][slot_of(taken)], phase_of(taken));
   };
   // the end of a segment, the warp's units of one item; true: the whole item lies within the warp
   auto finish = [&](bool last) {
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float s = Exact ? row_sum(mid_sum[Exact ? n : 0][r]) : __shfl_sync(SFFN_FULL_MASK, mid_sum[0][r], 4 * n + t);
+        const float s = row_sum(mid_sum[n][r]);
 #pragma unroll
         for (int x = n * G / 16; x < (n + 1) * G / 16; ++x) o[x][r] += s, o[x][2 + r] += s;
       }
@@ -406,14 +408,229 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     return false;
   };
 
+  // one unit of positions, from its copy in shared memory
+  auto unit = [&](auto masked, const uint8_t* sk, int base) {
+    constexpr bool Masked = decltype(masked)::value;   // some row does not see some of the positions
+    const uint8_t* sv = sk + U * (D / 2);
+    const uint8_t* sp = sk + U * D;
+    const int lo_min = a.window > 0 ? max(0, cur.first - a.window + 1) : 0;   // before it nothing is seen
+    auto param = [&](int tile, int n, int which, int slot) {   // (step, mid) of a slot of eight positions
+      return *reinterpret_cast<const uint32_t*>(sp + (tile * NG + n) * 64 + which * 32 + slot * 4);
+    };
+
+    // ---- scores of U positions: s[i] rows 16i + slot g and 16i + 8 + slot g, each for both query rows
+    float s[U / 16][4];
+#pragma unroll
+    for (int i = 0; i < U / 16; ++i) {
+      uint32_t w[2][D / 32];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint8_t* row = sk + (16 * i + 8 * k + kt) * (D / 2);
+        if (D == 64) {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + key_word_off<D>(kt, t, 0));
+          w[k][0] = v.x, w[k][1] = v.y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; j += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + key_word_off<D>(kt, t, j));
+            w[k][j] = v.x, w[k][j + 1] = v.y, w[k][j + 2] = v.z, w[k][j + 3] = v.w;
+          }
+        }
+      }
+      s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
+          uint32_t p0[4], p1[4];
+          if (Exact) {
+            key_halves(w[0][j], p0);
+            key_halves(w[1][j], p1);
+          } else {
+            key_bits(w[0][j], p0);
+            key_bits(w[1][j], p1);
+          }
+          const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
+#pragma unroll
+          for (int h = 0; h < QL; ++h) {
+            mma_f16(c, a0, q[h][2 * j][0], q[h][2 * j][1]);
+            mma_f16(c, a1, q[h][2 * j + 1][0], q[h][2 * j + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 0, g)));
+          const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
+          s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
+          s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
+        }
+      }
+    }
+    if (Masked) {
+#pragma unroll
+      for (int i = 0; i < U / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = base + 16 * i + 8 * (e >> 1) + kt;
+          if (j > pos[e & 1] || j < lo[e & 1]) s[i][e] = ninf;
+        }
+    }
+    float mu[2] = {m[0], m[1]};
+#pragma unroll
+    for (int i = 0; i < U / 16; ++i) {
+      mu[0] = fmaxf(mu[0], fmaxf(s[i][0], s[i][2]));
+      mu[1] = fmaxf(mu[1], fmaxf(s[i][1], s[i][3]));
+    }
+    mu[0] = row_max(mu[0]);
+    mu[1] = row_max(mu[1]);
+    if (__any_sync(SFFN_FULL_MASK, mu[0] > m[0] || mu[1] > m[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float back = mu[r] == m[r] ? 1.f : ex2((m[r] - mu[r]) * f[r]);   // m = -inf: 0
+        m[r] = mu[r];
+        l[r] *= back;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) mid_sum[n][r] *= back;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) o[x][r] *= back, o[x][2 + r] *= back;
+      }
+    }
+    const float mf[2] = {m[0] == ninf ? 0.f : m[0] * f[0], m[1] == ninf ? 0.f : m[1] * f[1]};
+
+    uint32_t vw[U / 16][4][D / 64];   // the lane's words of four positions per 16
+#pragma unroll
+    for (int k = 0; k < U / 16; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int p8 = (r & 1) ? tb : ta;
+        const uint8_t* c = sv + (16 * k + 8 * (r >> 1) + p8) * (D / 2) + value_word_off<D>(p8, g, 0);
+        if (D == 64) {
+          vw[k][r][0] = *reinterpret_cast<const uint32_t*>(c);
+        } else if (D == 128) {
+          const uint2 v = *reinterpret_cast<const uint2*>(c);
+          vw[k][r][0] = v.x, vw[k][r][1 % (D / 64)] = v.y;
+        } else {
+          const uint4 v = *reinterpret_cast<const uint4*>(c);
+          vw[k][r][0] = v.x, vw[k][r][1 % (D / 64)] = v.y, vw[k][r][2 % (D / 64)] = v.z, vw[k][r][3 % (D / 64)] = v.w;
+        }
+      }
+    constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the 64 channels of a word lie in
+
+    // what no row sees is cleared; the weights of rows that do not see it are 0 already
+    auto value_param = [&](int i, int k, int n) {
+      float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 1, g)));
+      if (Masked) {
+        const int j = base + 16 * i + 8 * k + kt;
+        if (j > cur.last || j < lo_min) sm = make_float2(0.f, 0.f);
+      }
+      return sm;
+    };
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < U / 16; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = ex2(fmaf(s[i][e], f[e & 1], -mf[e & 1]));
+      l[0] += s[i][0] + s[i][2];
+      l[1] += s[i][1] + s[i][3];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 sm = value_param(i, k, n);
+          top = fmaxf(top, sm.x);
+          mid_sum[n][0] = fmaf(s[i][2 * k], sm.y, mid_sum[n][0]);
+          mid_sum[n][1] = fmaf(s[i][2 * k + 1], sm.y, mid_sum[n][1]);
+        }
+    }
+    float up, down;
+    scale_to_half_range(row_max(top), up, down);
+    const float k0 = Exact ? down : down * 33554432.f, k1 = Exact ? down : down * 2097152.f;  // bare codes: u * 2^-24, 2^-20
+    uint32_t wt[QL][GW][U / 16][2];
+    float ws[GW][4];
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+      if (w * 64 % G == 0) {
+#pragma unroll
+        for (int n = 0; n < GW; ++n) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < U / 16; ++i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float st = value_param(i, k, w * 64 / G + n).x * up;
+              float x0 = s[i][2 * k] * st, x1 = s[i][2 * k + 1] * st;
+              if (Masked) {   // a step may be NaN for the rows that see it
+                if (s[i][2 * k] == 0.f) x0 = 0.f;
+                if (s[i][2 * k + 1] == 0.f) x1 = 0.f;
+              }
+              if (Exact) {
+                uint32_t hi, lw;
+                split_f16(x0, x1, hi, lw);
+                wt[0][n][i][k] = transpose_8x8(hi);
+                wt[QL - 1][n][i][k] = transpose_8x8(lw);
+              } else {
+                wt[0][n][i][k] = transpose_8x8(h2_u32(__floats2half2_rn(x0, x1)));
+              }
+            }
+            if (!Exact) {
+              const uint32_t one[4] = {0x3c003c00u, 0u, 0x3c003c00u, 0u};
+              mma_f16(c, one, wt[0][n][i][0], wt[0][n][i][1]);
+            }
+          }
+          // -15 sum(w) in units of the products of bare codes
+          ws[n][0] = c[0] * -4.4703484e-7f, ws[n][1] = c[1] * -4.4703484e-7f;
+          ws[n][2] = ws[n][0] * 16.f, ws[n][3] = ws[n][1] * 16.f;
+        }
+      }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float acc[2][4];
+#pragma unroll
+        for (int k = 0; k < U / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next
+            const int n = (2 * hh + e) * 16 / G % GW;
+            uint32_t av[4];
+            if (Exact) {
+              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], hh ? 0x7632 : 0x5410);
+              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], hh ? 0x7632 : 0x5410);
+              av[0] = value_halves(e == 0 ? x0 << 4 : x0 >> 4);
+              av[1] = value_halves(e == 0 ? x0 : x0 >> 8);
+              av[2] = value_halves(e == 0 ? x1 << 4 : x1 >> 4);
+              av[3] = value_halves(e == 0 ? x1 : x1 >> 8);
+              if (k == 0) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+              mma_f16(acc[e], av, wt[0][n][k][0], wt[0][n][k][1]);
+              mma_f16(acc[e], av, wt[QL - 1][n][k][0], wt[QL - 1][n][k][1]);
+            } else {                      // the low and high nibble of a byte
+              const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
+              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
+              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
+              av[0] = x0 & 0x000f000fu, av[1] = x0 & 0x00f000f0u;
+              av[2] = x1 & 0x000f000fu, av[3] = x1 & 0x00f000f0u;
+              mma_f16_from(acc[e], av, wt[0][n][k][0], wt[0][n][k][1], k == 0 ? ws[n] : acc[e]);
+            }
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* ox = o[4 * w + 2 * hh + e];
+          ox[0] = fmaf(acc[e][0], k0, ox[0]);
+          ox[1] = fmaf(acc[e][1], k0, ox[1]);
+          ox[2] = fmaf(acc[e][2], k1, ox[2]);
+          ox[3] = fmaf(acc[e][3], k1, ox[3]);
+        }
+      }
+    }
+  };
+
   bool at_barrier = false;
   for (long long uu = u0; uu < u1; ++uu) {
     if (fresh) {   // first unit of the warp in this item: query rows
       fresh = false;
       item_start = uu - cur.u;
       const int rows = cur.n * a.gq, row = cur.tile * kRows + g, rg = min(row, rows - 1);
-      pos_g = cur.len - cur.n + rg / a.gq;
-      lo_g = a.window > 0 ? max(0, pos_g - a.window + 1) : 0;
+      const int pos_g = cur.len - cur.n + rg / a.gq;
+      const int lo_g = a.window > 0 ? max(0, pos_g - a.window + 1) : 0;
       const size_t at = (size_t)((cur.q0 + rg / a.gq) * a.q.row_stride + (cur.kh * a.gq + rg % a.gq) * a.q.head_stride);
       // the sign of the scale goes with q, its size with f; rows past the end are zero
       const float sign = row >= rows || a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
@@ -465,307 +682,24 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         l[r] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < (Exact ? NG : 1); ++n) mid_sum[n][0] = mid_sum[n][1] = 0.f;
+      for (int n = 0; n < NG; ++n) mid_sum[n][0] = mid_sum[n][1] = 0.f;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
     }
     if (!cur.empty(U) && !dead) {
       issue();
-      const int st = taken % T::kStages;
-      if (!mbar_wait_bounded(&s_bar[warp][st], (taken / T::kStages) & 1)) {
+      const int st = slot_of(taken);
+      if (!mbar_wait_bounded(&s_bar[warp][st], phase_of(taken))) {
         set_device_error(a.err, SFFN_ERR_TIMEOUT);
         dead = true;
       }
       ++taken;
       const uint8_t* sk = ring + st * T::kStage;
-      const uint8_t* sv = sk + U * (D / 2);
-      const uint8_t* sp = sk + U * D;
       const int base = cur.base(U);
-      // whether some row does not see some position of the unit; positions that no row sees may be anything
-      const int lo_min = a.window > 0 ? max(0, cur.first - a.window + 1) : 0;
-      const bool masked = base + U - 1 > cur.first || (a.window > 0 && base < cur.last - a.window + 1);
-      auto param = [&](int tile, int n, int which, int slot) {   // (step, mid) of a slot of eight positions
-        return *reinterpret_cast<const uint32_t*>(sp + (tile * NG + n) * 64 + which * 32 + slot * 4);
-      };
-
-      // ---- scores of U positions: s[i] rows 16i + slot g and 16i + 8 + slot g, each for both query rows
-      float s[U / 16][4];
-#pragma unroll
-      for (int i = 0; i < U / 16; ++i) {
-        uint32_t w[2][D / 32];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint8_t* row = sk + (16 * i + 8 * k + kt) * (D / 2);
-          if (D == 64) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + key_word_off<D>(kt, t, 0));
-            w[k][0] = v.x, w[k][1] = v.y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < D / 32; j += 4) {
-              const uint4 v = *reinterpret_cast<const uint4*>(row + key_word_off<D>(kt, t, j));
-              w[k][j] = v.x, w[k][j + 1] = v.y, w[k][j + 2] = v.z, w[k][j + 3] = v.w;
-            }
-          }
-        }
-        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
-            uint32_t p0[4], p1[4];
-            if (Exact) {
-              key_halves(w[0][j], p0);
-              key_halves(w[1][j], p1);
-            } else {
-              key_bits(w[0][j], p0);
-              key_bits(w[1][j], p1);
-            }
-            const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
-#pragma unroll
-            for (int h = 0; h < QL; ++h) {
-              mma_f16(c, a0, q[h][2 * j][0], q[h][2 * j][1]);
-              mma_f16(c, a1, q[h][2 * j + 1][0], q[h][2 * j + 1][1]);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 0, g)));
-            const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
-            s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
-            s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
-          }
-        }
-      }
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < U / 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = base + 16 * i + 8 * (e >> 1) + kt;
-            if (j > pos[e & 1] || j < lo[e & 1]) s[i][e] = ninf;
-          }
-      }
-      float mu[2] = {m[0], m[1]};
-#pragma unroll
-      for (int i = 0; i < U / 16; ++i) {
-        mu[0] = fmaxf(mu[0], fmaxf(s[i][0], s[i][2]));
-        mu[1] = fmaxf(mu[1], fmaxf(s[i][1], s[i][3]));
-      }
-      mu[0] = row_max(mu[0]);
-      mu[1] = row_max(mu[1]);
-      if (__any_sync(SFFN_FULL_MASK, mu[0] > m[0] || mu[1] > m[1])) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float back = mu[r] == m[r] ? 1.f : ex2((m[r] - mu[r]) * f[r]);   // m = -inf: 0
-          m[r] = mu[r];
-          l[r] *= back;
-#pragma unroll
-          for (int n = 0; n < (Exact ? NG : 1); ++n) mid_sum[n][r] *= back;
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) o[x][r] *= back, o[x][2 + r] *= back;
-        }
-      }
-      float mf[2] = {m[0] == ninf ? 0.f : m[0] * f[0], m[1] == ninf ? 0.f : m[1] * f[1]};
-
-      uint32_t vw[U / 16][4][D / 64];   // the lane's words of four positions per 16
-#pragma unroll
-      for (int k = 0; k < U / 16; ++k)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int p8 = (r & 1) ? tb : ta;
-          const uint8_t* c = sv + (16 * k + 8 * (r >> 1) + p8) * (D / 2) + value_word_off<D>(p8, g, 0);
-          if (D == 64) {
-            vw[k][r][0] = *reinterpret_cast<const uint32_t*>(c);
-          } else if (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(c);
-            vw[k][r][0] = v.x, vw[k][r][1 % (D / 64)] = v.y;
-          } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(c);
-            vw[k][r][0] = v.x, vw[k][r][1 % (D / 64)] = v.y, vw[k][r][2 % (D / 64)] = v.z, vw[k][r][3 % (D / 64)] = v.w;
-          }
-        }
-      constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the 64 channels of a word lie in
-
-      if (Exact) {
-        // weights in fp32; unseen steps and mids are cleared, weights of unseen positions are 0 already, and a
-        // seen NaN step meets only rows that see it
-        auto value_param = [&](int i, int k, int n) {
-          float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 1, g)));
-          if (masked) {
-            const int j = base + 16 * i + 8 * k + kt;
-            if (j > cur.last || j < lo_min) sm = make_float2(0.f, 0.f);
-          }
-          return sm;
-        };
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < U / 16; ++i) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] = ex2(fmaf(s[i][e], f[e & 1], -mf[e & 1]));
-          l[0] += s[i][0] + s[i][2];
-          l[1] += s[i][1] + s[i][3];
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float2 sm = value_param(i, k, n);
-              top = fmaxf(top, sm.x);
-              mid_sum[Exact ? n : 0][0] = fmaf(s[i][2 * k], sm.y, mid_sum[Exact ? n : 0][0]);
-              mid_sum[Exact ? n : 0][1] = fmaf(s[i][2 * k + 1], sm.y, mid_sum[Exact ? n : 0][1]);
-            }
-        }
-        float up, down;
-        scale_to_half_range(row_max(top), up, down);
-        uint32_t wh[GW][U / 16][2], wl[GW][U / 16][2];
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          if (w * 64 % G == 0) {
-#pragma unroll
-            for (int n = 0; n < GW; ++n)
-#pragma unroll
-              for (int i = 0; i < U / 16; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float st = value_param(i, k, w * 64 / G + n).x * up;
-                  float x0 = s[i][2 * k] * st, x1 = s[i][2 * k + 1] * st;
-                  if (masked) {
-                    if (s[i][2 * k] == 0.f) x0 = 0.f;
-                    if (s[i][2 * k + 1] == 0.f) x1 = 0.f;
-                  }
-                  uint32_t hi, lw;
-                  split_f16(x0, x1, hi, lw);
-                  wh[n][i][k] = transpose_8x8(hi);
-                  wl[n][i][k] = transpose_8x8(lw);
-                }
-          }
-          float acc[4][4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
-#pragma unroll
-          for (int k = 0; k < U / 16; ++k)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], hh ? 0x7632 : 0x5410);
-              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], hh ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next
-                const uint32_t y0 = e == 0 ? x0 << 4 : x0 >> 4, y1 = e == 0 ? x1 << 4 : x1 >> 4;
-                const uint32_t z0 = e == 0 ? x0 : x0 >> 8, z1 = e == 0 ? x1 : x1 >> 8;
-                const uint32_t av[4] = {value_halves(y0), value_halves(z0), value_halves(y1), value_halves(z1)};
-                const int n = (2 * hh + e) * 16 / G % GW;
-                mma_f16(acc[2 * hh + e], av, wh[n][k][0], wh[n][k][1]);
-                mma_f16(acc[2 * hh + e], av, wl[n][k][0], wl[n][k][1]);
-              }
-            }
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * w + x][e] = fmaf(acc[x][e], down, o[4 * w + x][e]);
-        }
-      } else {
-        // what the lane's two slots of a tile may show: to any row, and to row g (all ones or zeros per half)
-        auto seen = [&](int tile, int first, int past) {
-          const int ja = base + 8 * tile + ta, jb = base + 8 * tile + tb;
-          return (ja >= first && ja <= past ? 0xffffu : 0u) | (jb >= first && jb <= past ? 0xffff0000u : 0u);
-        };
-        auto value_pair = [&](int tile, int n) { return *reinterpret_cast<const uint2*>(sp + (tile * NG + n) * 64 + 32 + 8 * t); };
-        auto value_steps = [&](int tile, int n) {
-          const uint2 v = value_pair(tile, n);
-          const uint32_t st = __byte_perm(v.x, v.y, 0x5410);
-          return masked ? st & seen(tile, lo_min, cur.last) : st;
-        };
-        __half2 big = u32_h2(0u);
-#pragma unroll
-        for (int i = 0; i < U / 8; ++i)
-#pragma unroll
-          for (int n = 0; n < NG; ++n) big = __hmax2(big, u32_h2(value_steps(i, n)));
-        // weights are 2^sh p with sh = 14 less the bits that the largest step needs above 1
-        const float top = quad_max(fmaxf(__low2float(big), __high2float(big)));
-        const int sh = min(14, 140 - (int)(__float_as_uint(top) >> 23));
-        const float down = __uint_as_float((uint32_t)(127 - sh) << 23);
-        mf[0] -= (float)sh;
-        mf[1] -= (float)sh;
-        uint32_t p[U / 16][2];
-        float mla[4] = {0.f, 0.f, 0.f, 0.f}, la[2] = {0.f, 0.f};
-        const uint32_t ones = 0x3c003c00u;
-#pragma unroll
-        for (int i = 0; i < U / 16; ++i) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float p0 = ex2(fmaf(s[i][2 * k], f[0], -mf[0])), p1 = ex2(fmaf(s[i][2 * k + 1], f[1], -mf[1]));
-            la[0] += p0;
-            la[1] += p1;
-            p[i][k] = transpose_8x8(h2_u32(__floats2half2_rn(p0, p1)));
-          }
-          // row n: the mids of group n
-          uint32_t mid[2] = {0u, 0u};
-          if (g < NG) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint2 v = value_pair(2 * i + k, g);
-              mid[k] = __byte_perm(v.x, v.y, 0x7632);
-              if (masked) mid[k] &= seen(2 * i + k, lo_min, cur.last);
-            }
-          }
-          const uint32_t am[4] = {mid[0], 0u, mid[1], 0u};
-          mma_f16(mla, am, p[i][0], p[i][1]);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          l[r] = fmaf(la[r], down, l[r]);
-          mid_sum[0][r] = fmaf(mla[r], down, mid_sum[0][r]);
-        }
-        const float k0 = down * 33554432.f, k1 = down * 2097152.f;   // codes are u * 2^-24 and u * 2^-20
-        uint32_t wt[GW][U / 16][2];
-        float ws[GW][4];
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          if (w * 64 % G == 0) {
-#pragma unroll
-            for (int n = 0; n < GW; ++n) {
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int i = 0; i < U / 16; ++i) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  uint32_t x = h2_u32(__hmul2(u32_h2(p[i][k]), u32_h2(value_steps(2 * i + k, w * 64 / G + n))));
-                  if (masked) x &= seen(2 * i + k, lo_g, pos_g);   // a step may be NaN
-                  wt[n][i][k] = x;
-                }
-                const uint32_t one[4] = {ones, 0u, ones, 0u};
-                mma_f16(c, one, wt[n][i][0], wt[n][i][1]);
-              }
-              // -15 sum(w) in units of the products
-              ws[n][0] = c[0] * -4.4703484e-7f, ws[n][1] = c[1] * -4.4703484e-7f;
-              ws[n][2] = ws[n][0] * 16.f, ws[n][3] = ws[n][1] * 16.f;
-            }
-          }
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float acc[2][4];
-#pragma unroll
-            for (int k = 0; k < U / 16; ++k)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next: the low and high nibble of a byte
-                const int n = (2 * hh + e) * 16 / G % GW;
-                const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
-                const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
-                const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
-                const uint32_t av[4] = {x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u};
-                mma_f16_from(acc[e], av, wt[n][k][0], wt[n][k][1], k == 0 ? ws[n] : acc[e]);
-              }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float* ox = o[4 * w + 2 * hh + e];
-              ox[0] = fmaf(acc[e][0], k0, ox[0]);
-              ox[1] = fmaf(acc[e][1], k0, ox[1]);
-              ox[2] = fmaf(acc[e][2], k1, ox[2]);
-              ox[3] = fmaf(acc[e][3], k1, ox[3]);
-            }
-          }
-        }
-      }
+      if (base + U - 1 > cur.first || (a.window > 0 && base < cur.last - a.window + 1))
+        unit(std::true_type(), sk, base);
+      else
+        unit(std::false_type(), sk, base);
       __syncwarp();
     }
     const bool last = uu + 1 == u1;
@@ -922,8 +856,8 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
   if ((long long)window >= (long long)b.table_stride * C.desc.page_size) window = 0;   // no position is that far back
   const AttWs w = att_ws(C);
   uint8_t* p = static_cast<uint8_t*>(ws);
-  const AttendArgs a{C.pages, C.page_bytes, C.head_bytes, C.desc.n_pages, C.desc.page_size, C.desc.n_kv_heads, C.err,
-                     b, q, out, lse, n_q_heads, n_q_heads / C.desc.n_kv_heads, dtype, window, scale,
+  const AttendArgs a{C.pages, C.page_bytes, C.head_bytes, C.desc.n_pages, C.desc.page_size,
+                     C.desc.page_size == 16 ? 4 : C.desc.page_size == 32 ? 5 : 6, C.desc.n_kv_heads, C.err, b, q, out, lse, n_q_heads, n_q_heads / C.desc.n_kv_heads, dtype, window, scale,
                      reinterpret_cast<Border*>(p), reinterpret_cast<float*>(p + w.warp_parts),
                      reinterpret_cast<float*>(p + w.block_parts)};
   const int blocks = C.num_sms;

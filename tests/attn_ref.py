@@ -14,9 +14,9 @@ absolute terms that the bounds are made of:
 * attention: a score is off by at most 2^-20 of scale * sum |q||k| (the same
   terms, and its own rounding), a weight by that and 2^-20 relative, the
   weighted sum of values by a further 2^-19 of sum p|V|; the normalisation at
-  most doubles the first part. With 16-bit rows a weight, and its product with
-  a step, are rounded to a half each (2^-11): with step |2u - 15| <= |V| + |mid|
-  at most 2^-10 of sum p (|V| + 2 |mid|) more.
+  most doubles the first part. With 16-bit rows the product of a weight and a
+  step is rounded to a half (2^-11 relative): with step |2u - 15| <= |V| + |mid|
+  at most 2^-11 of sum p (|V| + |mid|) more.
 * a result rounded to 16 bits is off by a further half unit in the last place.
 """
 
@@ -63,7 +63,7 @@ def rotate(x: np.ndarray, cs: np.ndarray, style: str) -> np.ndarray:
 
 def attention(q, k, v, n_new: int, scale: float, window: int, vsize=None):
     """One sequence: q (n_new, Hq, D), k, v (len, Hkv, D); vsize (len, Hkv, D),
-    |V| + 2 |mid|, if the rows have 16 bits. Returns out, lse and the bound on
+    |V| + |mid|, if the rows have 16 bits. Returns out, lse and the bound on
     the error of out, all float64."""
     q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
     n, hq = k.shape[0], q.shape[1]
@@ -84,7 +84,7 @@ def attention(q, k, v, n_new: int, scale: float, window: int, vsize=None):
         out[i] = np.einsum("hl,lhd->hd", w, vv)
         tol[i] = (2 * (es + 2.0 ** -20) + 2.0 ** -19)[:, None] * np.einsum("hl,lhd->hd", w, abs(vv))
         if vsize is not None:
-            tol[i] += 2.0 ** -10 * np.einsum("hl,lhd->hd", w, np.repeat(vsize[a:p + 1], rep, axis=1))
+            tol[i] += 2.0 ** -11 * np.einsum("hl,lhd->hd", w, np.repeat(vsize[a:p + 1], rep, axis=1))
     return out, lse, tol
 
 
