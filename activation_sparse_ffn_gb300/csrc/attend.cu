@@ -64,9 +64,17 @@ struct Att {
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
 
+// Equal runs of a list of `total` units: run w of `runs` starts at floor(w * total / runs).
+struct Runs {
+  long long total, per, rest, runs;
+  __device__ __forceinline__ Runs(long long total_, long long runs_)
+      : total(total_), per(total_ / runs_), rest(total_ % runs_), runs(runs_) {}
+  __device__ __forceinline__ long long start(long long w) const { return per * w + rest * w / runs; }
+};
+
 // What a block tells k_attend_join about the item its first unit lies in.
 struct Border {
-  long long start, item_start, item_end;
+  long long total, item_start, item_end;   // item_end 0: the block has no unit behind its start
   int q0, n, kh, tile;
   int pad[2];
 };
@@ -190,9 +198,10 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[kAttWarps][T::kStages];
-  __shared__ long long s_scan[kAttWarps + 1];
+  __shared__ long long s_scan[kAttWarps];
   __shared__ int s_seq[kAttWarps];
   __shared__ long long s_off[kAttWarps];
+  __shared__ Seq s_rows[kAttWarps];
   struct Entry {
     long long item_start, item_end;
     int q0, n, kh, tile, where;  // where: 0 none, 1 shared memory, 2 the warp's global slot
@@ -205,27 +214,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the block's and the warp's run of units
-  long long total = 0;
-  for (int s = threadIdx.x; s < a.b.n_seq; s += kAttThreads) total += total_of(a, load_seq(a, s), U);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(SFFN_FULL_MASK, total, o);
-  if (lane == 0) s_scan[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttWarps; ++w) total += s_scan[w];
-  const long long n_warps = (long long)gridDim.x * kAttWarps, gw = (long long)blockIdx.x * kAttWarps + warp;
-  // start of warp w's run: floor(w * total / n_warps), without overflow
-  const long long per = total / n_warps, rest = total % n_warps;
-  auto start_of = [&](long long w) { return per * w + rest * w / n_warps; };
-  const long long u0 = start_of(gw), u1 = start_of(gw + 1), block_u0 = start_of((long long)blockIdx.x * kAttWarps);
-  const long long block_u1 = start_of((long long)(blockIdx.x + 1) * kAttWarps);
-  // sequence of every warp's first unit
-  long long before = 0;
-  for (int s0 = 0; s0 < a.b.n_seq; s0 += kAttThreads) {
-    const int s = s0 + threadIdx.x;
-    const long long mine = s < a.b.n_seq ? total_of(a, load_seq(a, s), U) : 0;
+  // ---- the block's and the warp's run of units, and the sequence of every warp's first unit. Up to a block's
+  // worth of sequences is looked at in one pass (its counts stay in registers), more in two.
+  auto scan = [&](long long mine, long long& sum) {   // sum over earlier threads; over all of them
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,22 +226,63 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     __syncthreads();
     if (lane == 31) s_scan[warp] = upto;
     __syncthreads();
-    long long chunk = 0, below = 0;
+    long long below = 0;
+    sum = 0;
 #pragma unroll
     for (int w = 0; w < kAttWarps; ++w) {
       if (w < warp) below += s_scan[w];
-      chunk += s_scan[w];
+      sum += s_scan[w];
     }
-    const long long lo = before + below + upto - mine;
-#pragma unroll
+    return below + upto - mine;
+  };
+  Seq sq{0, 0, 0};
+  long long mine = 0, total = 0, lo_u = 0;
+  auto look = [&](int s) {
+    if (s < a.b.n_seq) {
+      sq = load_seq(a, s);
+      mine = total_of(a, sq, U);
+    } else {
+      mine = 0;
+    }
+  };
+  if (a.b.n_seq <= kAttThreads) {
+    look(threadIdx.x);
+    lo_u = scan(mine, total);
+  } else {
+    for (int s = threadIdx.x; s < a.b.n_seq; s += kAttThreads) {
+      look(s);
+      lo_u += mine;
+    }
+    scan(lo_u, total);
+  }
+  const Runs runs(total, (long long)gridDim.x * kAttWarps);
+  const long long gw = (long long)blockIdx.x * kAttWarps + warp, w0 = (long long)blockIdx.x * kAttWarps;
+  const long long u0 = runs.start(gw), u1 = runs.start(gw + 1);
+  const long long block_u0 = runs.start(w0), block_u1 = runs.start(w0 + kAttWarps);
+  // the warps whose first unit lies in sequence s, known by its thread (a block without units needs its start too)
+  const long long block_past = block_u1 > block_u0 ? block_u1 : block_u0 + 1;
+  auto find = [&](int s) {
+#pragma unroll 1
     for (int w = 0; w < kAttWarps; ++w) {
-      const long long want = start_of((long long)blockIdx.x * kAttWarps + w);
-      if (want >= lo && want < lo + mine) {
+      const long long want = runs.start(w0 + w);
+      if (want >= lo_u && want < lo_u + mine) {
         s_seq[w] = s;
-        s_off[w] = want - lo;
+        s_off[w] = want - lo_u;
+        s_rows[w] = sq;
       }
     }
-    before += chunk;
+  };
+  if (a.b.n_seq <= kAttThreads) {
+    if (mine > 0 && lo_u < block_past && lo_u + mine > block_u0) find(threadIdx.x);
+  } else {
+    long long before = 0;
+    for (int s0 = 0; s0 < a.b.n_seq; s0 += kAttThreads) {
+      look(s0 + threadIdx.x);
+      long long sum;
+      lo_u = before + scan(mine, sum);
+      if (mine > 0 && lo_u < block_past && lo_u + mine > block_u0) find(s0 + threadIdx.x);
+      before += sum;
+    }
   }
   __syncthreads();
 
@@ -259,7 +291,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   if (any || (warp == 0 && block_u0 < total)) {
     const long long off = s_off[warp];
     cur.s = s_seq[warp];
-    cur.set_seq(a, load_seq(a, cur.s), U);
+    cur.set_seq(a, s_rows[warp], U);
     const long long item = off / cur.units;
     cur.u = (int)(off % cur.units);
     cur.kh = (int)(item / cur.tiles);
@@ -267,7 +299,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     cur.set_tile(a, U);
     if (warp == 0 && lane == 0) {
       Border bd;
-      bd.start = u0;
+      bd.total = total;
       bd.item_start = u0 - cur.u;
       bd.item_end = bd.item_start + cur.units;
       bd.q0 = cur.q0, bd.n = cur.n, bd.kh = cur.kh, bd.tile = cur.tile;
@@ -276,12 +308,14 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     }
   } else if (warp == 0 && lane == 0) {
     Border bd{};
-    bd.start = total;
+    bd.total = total;
     a.borders[blockIdx.x] = bd;
   }
 
   // ---- copies: the warp's ring
-  const int RP = min(a.P, U), parts = U / RP;   // positions of a unit that share a page, and how many such runs
+  // 2^rp_log2 positions of a unit share a page; `parts` such runs make up the unit
+  const int rp_log2 = min(a.P_log2, U == 32 ? 5 : 6), RP = 1 << rp_log2, parts = U >> rp_log2;
+  const uint64_t pol = l2_policy_evict_first();
   uint8_t* ring = smem + (size_t)warp * T::kStages * T::kStage;
   Cursor nxt = cur;
   long long nu = u0;       // next unit to copy
@@ -306,17 +340,16 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     if (nu >= u1) return;
     const int st = slot_of(issued), base = nxt.base(U);
     uint8_t* dst = ring + st * T::kStage;
-    const int runs = min(parts, (nxt.last - base) / RP + 1);
-    if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][st], (uint32_t)(runs * RP * (D + 8 * NG)));
+    const int n_runs = min(parts, ((nxt.last - base) >> rp_log2) + 1);
+    if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][st], (uint32_t)((n_runs << rp_log2) * (D + 8 * NG)));
     __syncwarp();
-    if (lane < runs) {
+    if (lane < n_runs) {
       if (page < 0 || page >= a.n_pages) {
         set_device_error(a.err, SFFN_ERR_DEVICE);
         page = 0;
       }
       const uint8_t* src = a.pages + (size_t)page * a.page_bytes + (size_t)nxt.kh * a.head_bytes;
       const int slot = base & (a.P - 1);  // zero unless a page holds several units
-      const uint64_t pol = l2_policy_evict_first();
       bulk_g2s(dst + lane * RP * (D / 2), src + slot * (D / 2), RP * (D / 2), &s_bar[warp][st], pol);
       bulk_g2s(dst + U * (D / 2) + lane * RP * (D / 2), src + kv_value_off(a.P, D) + slot * (D / 2), RP * (D / 2),
                &s_bar[warp][st], pol);
@@ -769,40 +802,61 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 
 // Rows cut by a block border: block c handles the item that the first unit of
 // attention block c + 1 lies in, if that item began before it and no earlier
-// border lies in it; warp w takes row w.
+// border lies in it; warp w takes row w. Lane k looks at the k-th part.
 template <int D>
-__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks) {
-  constexpr int CPL = D / 32, kPart = Att<D, 64, false>::kPart;
+__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks, int warps) {
+  constexpr int CPL = D / 32, kPart = Att<D, 64, false>::kPart, kAhead = 8;
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto start_at = [&](int k) { return __ldcg(&a.borders[k].start); };
-  const long long start = start_at(c), item_start = __ldcg(&a.borders[c].item_start),
-                  item_end = __ldcg(&a.borders[c].item_end), prev = start_at(c - 1);
-  if (item_end == 0 || item_start >= start || item_start < prev) return;
+  const int c = blockIdx.x + 1, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Border* bp = a.borders + c;
+  const long long total = __ldcg(&bp->total), item_start = __ldcg(&bp->item_start), item_end = __ldcg(&bp->item_end);
+  const int q0 = __ldcg(&bp->q0), n = __ldcg(&bp->n), kh = __ldcg(&bp->kh), tile = __ldcg(&bp->tile);
+  const Runs runs(total, (long long)blocks * warps);
+  auto start = [&](int k) { return runs.start((long long)k * warps); };
+  if (item_end == 0 || item_start >= start(c) || item_start < start(c - 1)) return;
   const float ninf = __int_as_float(0xff800000);
-  int last = c;   // blocks c - 1 .. last hold a part
-  while (last + 1 < blocks && start_at(last + 1) < item_end) ++last;
-  auto part = [&](int k) { return a.block_parts + ((long long)k * 2 + (k == c - 1 && prev < item_start ? 1 : 0)) * kPart; };
-  auto has = [&](int k) { return k == c - 1 || (k + 1 < blocks ? start_at(k + 1) : item_end) > start_at(k); };
-  float mt = ninf;
-  for (int k = c - 1; k <= last; ++k)
-    if (has(k)) mt = fmaxf(mt, __ldcg(part(k) + kRows * D + warp));
-  float lt = 0.f, ot[CPL];
+  // parts: the last item of block c - 1 (its first if it begins with it), the first items of c, c + 1, ...
+  int count = 2;
+  while (c + count - 1 < blocks && start(c + count - 1) < item_end) ++count;
+  auto part = [&](int k) {
+    return a.block_parts + ((long long)(c - 1 + k) * 2 + (k == 0 && start(c - 1) < item_start ? 1 : 0)) * kPart;
+  };
+  float mt = ninf, lt = 0.f, ot[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) ot[e] = 0.f;
-  for (int k = c - 1; k <= last; ++k) {
-    if (!has(k)) continue;
-    const float* p = part(k);
-    const float me = __ldcg(p + kRows * D + warp), le = __ldcg(p + kRows * D + kRows + warp);
-    const float w = me == mt ? 1.f : ex2(me - mt);
-    lt = fmaf(le, w, lt);
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    const int k = k0 + lane;
+    const bool has = k < count && (k == 0 || start(c + k) > start(c - 1 + k));   // an empty block has no part
+    const float me = has ? __ldcg(part(k) + kRows * D + row) : ninf;
+    const float le = has ? __ldcg(part(k) + kRows * D + kRows + row) : 0.f;
+    float mn = me;
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) ot[e] = fmaf(__ldcg(p + warp * D + lane * CPL + e), w, ot[e]);
+    for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(SFFN_FULL_MASK, mn, o));
+    mn = fmaxf(mn, mt);
+    const float back = mt == mn ? 1.f : ex2(mt - mn), w = !has ? 0.f : me == mn ? 1.f : ex2(me - mn);
+    mt = mn;
+    lt = lt * back + warp_sum(le * w);
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) ot[e] *= back;
+    const unsigned mask = __ballot_sync(SFFN_FULL_MASK, has);
+    const int here = min(32, count - k0);
+    for (int i0 = 0; i0 < here; i0 += kAhead) {
+      float x[kAhead][CPL];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int e = 0; e < CPL; ++e)
+          x[i][e] = (mask >> (i0 + i)) & 1 ? __ldcg(part(k0 + i0 + i) + row * D + lane * CPL + e) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float wi = __shfl_sync(SFFN_FULL_MASK, w, i0 + i);
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) ot[e] = fmaf(x[i][e], wi, ot[e]);
+      }
+    }
   }
-  const int q0 = __ldcg(&a.borders[c].q0), n = __ldcg(&a.borders[c].n), kh = __ldcg(&a.borders[c].kh),
-            tile = __ldcg(&a.borders[c].tile);
-  write_row<D>(a, q0, n, kh, tile * kRows + warp, lane, ot, mt, lt);
+  write_row<D>(a, q0, n, kh, tile * kRows + row, lane, ot, mt, lt);
 }
 
 template <typename F>
@@ -866,7 +920,7 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
     auto run = [&](auto* kern, int threads, int smem) {
       const cudaError_t e = launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, 1, a);
       if (e != cudaSuccess || blocks < 2) return e;
-      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks);
+      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks, threads / 32);
     };
     using E = Att<D, G, true>;
     using N = Att<D, G, false>;
