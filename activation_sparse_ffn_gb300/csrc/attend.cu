@@ -22,9 +22,10 @@
 // like: one mask per pair and no arithmetic; the sums of w are subtracted by
 // starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
 // p * step are carried by two halves each (22 bits) in two products, and the
-// codes are centred first, because the tensor core truncates its sums and a
-// sum of uncentred codes would show that over a long history. Either way the
-// sums of one unit's positions leave the tensor core and are added up in fp32.
+// value codes are centred first, because the tensor core truncates its sums and
+// a sum of uncentred codes, all weights being positive, would show that over a
+// long history. Either way the sums of one unit's positions leave the tensor
+// core and are added up in fp32.
 //
 // Work split. The visible blocks of U positions (`units`) of every (sequence,
 // key head, tile of eight rows) are numbered through, and each warp of the grid
@@ -53,7 +54,7 @@ struct Att {
   static constexpr int U = D == 256 ? 32 : 64;             // positions of a unit
   static constexpr int kStage = U * (D + 8 * NG);          // bytes
   // as many warps as the registers of the inner loop and two stages each allow
-  static constexpr int kByRegs = Exact ? (D == 64 ? 12 : 8) : (D == 64 ? 16 : D == 128 ? 12 : 8);
+  static constexpr int kByRegs = D == 64 ? (Exact ? 12 : 16) : D == 128 && !Exact && NG < 4 ? 12 : 8;
   static constexpr int kBudget = 224 * 1024;
   static constexpr int kBySmem = kBudget / (2 * kStage);
   static constexpr int kWarps = kByRegs < kBySmem ? kByRegs : kBySmem;
@@ -64,21 +65,26 @@ struct Att {
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
 
-// Equal runs of a list of `total` units: run w of `runs` starts at floor(w * total / runs).
+// Equal runs of a list of `total` units: block b of `blocks` takes those from
+// floor(b * total / blocks), and so on for the warps of a block.
 struct Runs {
-  long long total, per, rest, runs;
-  __device__ __forceinline__ Runs(long long total_, long long runs_)
-      : total(total_), per(total_ / runs_), rest(total_ % runs_), runs(runs_) {}
-  __device__ __forceinline__ long long start(long long w) const { return per * w + rest * w / runs; }
+  int total, per, rest, blocks;
+  __device__ __forceinline__ Runs(int total_, int blocks_)
+      : total(total_), per(total_ / blocks_), rest(total_ % blocks_), blocks(blocks_) {}
+  __device__ __forceinline__ int start(int b) const { return per * b + rest * b / blocks; }
 };
+template <int W>
+__device__ __forceinline__ int warp_start(int u0, int u1, int w) {
+  const int n = u1 - u0;
+  return u0 + n / W * w + n % W * w / W;
+}
 
 // What a block tells k_attend_join about the item its first unit lies in.
 struct Border {
-  long long total, item_start, item_end;   // item_end 0: the block has no unit behind its start
-  int q0, n, kh, tile;
-  int pad[2];
+  int total, item_start, item_end;   // item_end 0: the block has no unit behind its start
+  int q0, n, kh, tile, pad;
 };
-static_assert(sizeof(Border) == 48, "");
+static_assert(sizeof(Border) == 32, "");
 
 struct AttendArgs {
   const uint8_t* pages;
@@ -131,8 +137,8 @@ __device__ __forceinline__ int units_of(const AttendArgs& a, const Seq& q, int U
   }
   return max(units, 1);
 }
-__device__ __forceinline__ long long total_of(const AttendArgs& a, const Seq& q, int U) {
-  return q.n > 0 ? (long long)a.hkv * tiles_of(a, q) * units_of(a, q, U) : 0;
+__device__ __forceinline__ int total_of(const AttendArgs& a, const Seq& q, int U) {
+  return q.n > 0 ? a.hkv * tiles_of(a, q) * units_of(a, q, U) : 0;
 }
 
 // A place in the list of units.
@@ -198,13 +204,10 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[kAttWarps][T::kStages];
-  __shared__ long long s_scan[kAttWarps];
-  __shared__ int s_seq[kAttWarps];
-  __shared__ long long s_off[kAttWarps];
+  __shared__ int s_scan[kAttWarps], s_seq[kAttWarps], s_off[kAttWarps];
   __shared__ Seq s_rows[kAttWarps];
   struct Entry {
-    long long item_start, item_end;
-    int q0, n, kh, tile, where;  // where: 0 none, 1 shared memory, 2 the warp's global slot
+    int item_start, item_end, q0, n, kh, tile, where;  // where: 0 none, 1 shared memory, 2 the warp's global slot
   };
   __shared__ Entry s_entry[2 * kAttWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -214,96 +217,100 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the block's and the warp's run of units, and the sequence of every warp's first unit. Up to a block's
-  // worth of sequences is looked at in one pass (its counts stay in registers), more in two.
-  auto scan = [&](long long mine, long long& sum) {   // sum over earlier threads; over all of them
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(SFFN_FULL_MASK, upto, o);
-      if (lane >= o) upto += v;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
-    long long below = 0;
-    sum = 0;
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      if (w < warp) below += s_scan[w];
-      sum += s_scan[w];
-    }
-    return below + upto - mine;
-  };
-  Seq sq{0, 0, 0};
-  long long mine = 0, total = 0, lo_u = 0;
+  // ---- the block's and the warp's run of units, and the sequence of the warp's first unit
+  Seq sq{0, 0, 0};       // that sequence's rows; before that, of the sequence a thread looks at
+  int mine = 0, total, lo_u = 0, first_seq = 0, first_off = 0;
   auto look = [&](int s) {
+    mine = 0;
     if (s < a.b.n_seq) {
       sq = load_seq(a, s);
       mine = total_of(a, sq, U);
-    } else {
-      mine = 0;
     }
   };
-  if (a.b.n_seq <= kAttThreads) {
-    look(threadIdx.x);
-    lo_u = scan(mine, total);
-  } else {
+  auto warp_scan = [&](int v) {   // sum over this and earlier lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(SFFN_FULL_MASK, v, o);
+      if (lane >= o) v += w;
+    }
+    return v;
+  };
+  int block_u0, block_u1, u0, u1;
+  auto runs_of = [&]() {
+    const Runs runs(total, gridDim.x);
+    block_u0 = runs.start(blockIdx.x), block_u1 = runs.start(blockIdx.x + 1);
+    u0 = warp_start<kAttWarps>(block_u0, block_u1, warp), u1 = warp_start<kAttWarps>(block_u0, block_u1, warp + 1);
+  };
+  if (a.b.n_seq <= 32) {   // each warp on its own, lane s for sequence s
+    look(lane);
+    const int upto = warp_scan(mine);
+    total = __shfl_sync(SFFN_FULL_MASK, upto, 31);
+    runs_of();
+    const int src = __ffs(__ballot_sync(SFFN_FULL_MASK, u0 < upto)) - 1;
+    if (src >= 0) {
+      first_seq = src;
+      first_off = u0 - __shfl_sync(SFFN_FULL_MASK, upto - mine, src);
+      sq.q0 = __shfl_sync(SFFN_FULL_MASK, sq.q0, src);
+      sq.n = __shfl_sync(SFFN_FULL_MASK, sq.n, src);
+      sq.len = __shfl_sync(SFFN_FULL_MASK, sq.len, src);
+    }
+  } else {                 // the block together, once for the total and once for the places
+    auto block_scan = [&](int v, int& sum) {   // sum over earlier threads; over all of them
+      const int upto = warp_scan(v);
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = upto;
+      __syncthreads();
+      int below = 0;
+      sum = 0;
+#pragma unroll 1
+      for (int w = 0; w < kAttWarps; ++w) {
+        if (w < warp) below += s_scan[w];
+        sum += s_scan[w];
+      }
+      return below + upto - v;
+    };
     for (int s = threadIdx.x; s < a.b.n_seq; s += kAttThreads) {
       look(s);
       lo_u += mine;
     }
-    scan(lo_u, total);
-  }
-  const Runs runs(total, (long long)gridDim.x * kAttWarps);
-  const long long gw = (long long)blockIdx.x * kAttWarps + warp, w0 = (long long)blockIdx.x * kAttWarps;
-  const long long u0 = runs.start(gw), u1 = runs.start(gw + 1);
-  const long long block_u0 = runs.start(w0), block_u1 = runs.start(w0 + kAttWarps);
-  // the warps whose first unit lies in sequence s, known by its thread (a block without units needs its start too)
-  const long long block_past = block_u1 > block_u0 ? block_u1 : block_u0 + 1;
-  auto find = [&](int s) {
-#pragma unroll 1
-    for (int w = 0; w < kAttWarps; ++w) {
-      const long long want = runs.start(w0 + w);
-      if (want >= lo_u && want < lo_u + mine) {
-        s_seq[w] = s;
-        s_off[w] = want - lo_u;
-        s_rows[w] = sq;
-      }
-    }
-  };
-  if (a.b.n_seq <= kAttThreads) {
-    if (mine > 0 && lo_u < block_past && lo_u + mine > block_u0) find(threadIdx.x);
-  } else {
-    long long before = 0;
+    block_scan(lo_u, total);
+    runs_of();
+    int before = 0;
     for (int s0 = 0; s0 < a.b.n_seq; s0 += kAttThreads) {
       look(s0 + threadIdx.x);
-      long long sum;
-      lo_u = before + scan(mine, sum);
-      if (mine > 0 && lo_u < block_past && lo_u + mine > block_u0) find(s0 + threadIdx.x);
+      int sum;
+      lo_u = before + block_scan(mine, sum);
       before += sum;
+#pragma unroll 1
+      for (int w = 0; w < kAttWarps; ++w) {
+        const int want = warp_start<kAttWarps>(block_u0, block_u1, w);
+        if (want >= lo_u && want < lo_u + mine) {
+          s_seq[w] = s0 + threadIdx.x;
+          s_off[w] = want - lo_u;
+          s_rows[w] = sq;
+        }
+      }
     }
+    __syncthreads();
+    first_seq = s_seq[warp], first_off = s_off[warp], sq = s_rows[warp];   // of use if the warp's start is below total
   }
-  __syncthreads();
 
   const bool any = u0 < u1;
   Cursor cur{};
   if (any || (warp == 0 && block_u0 < total)) {
-    const long long off = s_off[warp];
-    cur.s = s_seq[warp];
-    cur.set_seq(a, s_rows[warp], U);
-    const long long item = off / cur.units;
-    cur.u = (int)(off % cur.units);
-    cur.kh = (int)(item / cur.tiles);
-    cur.tile = (int)(item % cur.tiles);
+    cur.s = first_seq;
+    cur.set_seq(a, sq, U);
+    const int item = first_off / cur.units;
+    cur.u = first_off - item * cur.units;
+    cur.kh = item / cur.tiles;
+    cur.tile = item - cur.kh * cur.tiles;
     cur.set_tile(a, U);
     if (warp == 0 && lane == 0) {
       Border bd;
       bd.total = total;
       bd.item_start = u0 - cur.u;
       bd.item_end = bd.item_start + cur.units;
-      bd.q0 = cur.q0, bd.n = cur.n, bd.kh = cur.kh, bd.tile = cur.tile;
-      bd.pad[0] = bd.pad[1] = 0;
+      bd.q0 = cur.q0, bd.n = cur.n, bd.kh = cur.kh, bd.tile = cur.tile, bd.pad = 0;
       a.borders[blockIdx.x] = bd;
     }
   } else if (warp == 0 && lane == 0) {
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   const uint64_t pol = l2_policy_evict_first();
   uint8_t* ring = smem + (size_t)warp * T::kStages * T::kStage;
   Cursor nxt = cur;
-  long long nu = u0;       // next unit to copy
+  int nu = u0;             // next unit to copy
   int issued = 0, taken = 0;
   auto slot_of = [](int k) { return k % T::kStages; };
   auto phase_of = [](int k) { return (uint32_t)(k / T::kStages) & 1u; };
@@ -367,6 +374,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     for (int i = 0; i < T::kStages - 1; ++i) issue();
   }
 
+  const int dtype = Exact ? (int)SFFN_F32 : a.dtype;
   const float ninf = __int_as_float(0xff800000);
   constexpr int QL = Exact ? 2 : 1;          // halves that carry a query element
   uint32_t q[QL][D / 16][2];                 // column g of the operand
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   float f[2] = {1.f, 1.f}, m[2] = {ninf, ninf};
   int pos[2], lo[2];                         // position of the row and the first it sees
   bool dead = false, fresh = true;
-  long long item_start = u0 - cur.u;
+  int item_start = u0 - cur.u;
   const int kt = kv_pos_of_col(g);           // position, of eight, of row g of a key operand
   const int ta = kv_pos_of_col(2 * t), tb = kv_pos_of_col(2 * t + 1);  // of columns 2t, 2t + 1 of a value operand
 
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       }
     const float lt[2] = {row_sum(l[0]), row_sum(l[1])};
     const float mt[2] = {m[0] == ninf ? ninf : m[0] * f[0], m[1] == ninf ? ninf : m[1] * f[1]};
-    const long long item_end = item_start + cur.units;
+    const int item_end = item_start + cur.units;
     if (item_start >= u0 && item_end <= u1) {   // finish the rows here
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -409,8 +417,8 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         const float inv = lt[r] == 0.f ? 0.f : 1.f / lt[r];
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          st_elem(a.out.ptr, at + 16 * x, o[x][r] * inv, a.dtype);
-          st_elem(a.out.ptr, at + 16 * x + 8, o[x][2 + r] * inv, a.dtype);
+          st_elem(a.out.ptr, at + 16 * x, o[x][r] * inv, dtype);
+          st_elem(a.out.ptr, at + 16 * x + 8, o[x][2 + r] * inv, dtype);
         }
         if (a.lse && g == 0) a.lse[(size_t)i * a.hq + h] = lt[r] == 0.f ? ninf : (mt[r] + log2f(lt[r])) * kLn2;
       }
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       drain();
       __syncthreads();
     }
-    float* dst = last ? reinterpret_cast<float*>(smem) + warp * T::kPart : a.warp_parts + gw * T::kPart;
+    float* dst = last ? reinterpret_cast<float*>(smem) + warp * T::kPart : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + warp) * T::kPart;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float* row = dst + (2 * t + r) * D + g;
@@ -447,8 +455,21 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     const uint8_t* sv = sk + U * (D / 2);
     const uint8_t* sp = sk + U * D;
     const int lo_min = a.window > 0 ? max(0, cur.first - a.window + 1) : 0;   // before it nothing is seen
-    auto param = [&](int tile, int n, int which, int slot) {   // (step, mid) of a slot of eight positions
-      return *reinterpret_cast<const uint32_t*>(sp + (tile * NG + n) * 64 + which * 32 + slot * 4);
+    // the (step, mid) pairs of slot g of eight positions, all groups
+    auto params = [&](int tile, int which, uint32_t* v) {
+      const uint8_t* at = sp + tile * NG * 64 + which * NG * 32 + g * NG * 4;
+      if (NG == 1) {
+        v[0] = *reinterpret_cast<const uint32_t*>(at);
+      } else if (NG == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        v[0] = x.x, v[1 % NG] = x.y;
+      } else {
+#pragma unroll
+        for (int n = 0; n < NG; n += 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(at + 4 * n);
+          v[n] = x.x, v[(n + 1) % NG] = x.y, v[(n + 2) % NG] = x.z, v[(n + 3) % NG] = x.w;
+        }
+      }
     };
 
     // ---- scores of U positions: s[i] rows 16i + slot g and 16i + 8 + slot g, each for both query rows
@@ -471,19 +492,17 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         }
       }
       s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      uint32_t kp[2][NG];
+      params(2 * i, 0, kp[0]);
+      params(2 * i + 1, 0, kp[1]);
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
           uint32_t p0[4], p1[4];
-          if (Exact) {
-            key_halves(w[0][j], p0);
-            key_halves(w[1][j], p1);
-          } else {
-            key_bits(w[0][j], p0);
-            key_bits(w[1][j], p1);
-          }
+          key_bits(w[0][j], p0);
+          key_bits(w[1][j], p1);
           const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
 #pragma unroll
           for (int h = 0; h < QL; ++h) {
@@ -493,8 +512,8 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 0, g)));
-          const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
+          const float2 sm = __half22float2(u32_h2(kp[k][n]));
+          const float off = fmaf(-15.f, sm.x, sm.y);
           s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
           s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
         }
@@ -550,16 +569,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       }
     constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the 64 channels of a word lie in
 
-    // what no row sees is cleared; the weights of rows that do not see it are 0 already
-    auto value_param = [&](int i, int k, int n) {
-      float2 sm = __half22float2(u32_h2(param(2 * i + k, n, 1, g)));
-      if (Masked) {
-        const int j = base + 16 * i + 8 * k + kt;
-        if (j > cur.last || j < lo_min) sm = make_float2(0.f, 0.f);
-      }
-      return sm;
-    };
-    float top = 0.f;
+    float top = 0.f, step[U / 16][2][NG];
 #pragma unroll
     for (int i = 0; i < U / 16; ++i) {
 #pragma unroll
@@ -567,18 +577,29 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       l[0] += s[i][0] + s[i][2];
       l[1] += s[i][1] + s[i][3];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int k = 0; k < 2; ++k) {
+        uint32_t vp[NG];
+        params(2 * i + k, 1, vp);
+        if (Masked) {   // what no row sees is cleared; the weights of rows that do not see it are 0 already
+          const int j = base + 16 * i + 8 * k + kt;
+          if (j > cur.last || j < lo_min) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 sm = value_param(i, k, n);
+            for (int n = 0; n < NG; ++n) vp[n] = 0u;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const float2 sm = __half22float2(u32_h2(vp[n]));
+          step[i][k][n] = sm.x;
           top = fmaxf(top, sm.x);
           mid_sum[n][0] = fmaf(s[i][2 * k], sm.y, mid_sum[n][0]);
           mid_sum[n][1] = fmaf(s[i][2 * k + 1], sm.y, mid_sum[n][1]);
         }
+      }
     }
     float up, down;
     scale_to_half_range(row_max(top), up, down);
-    const float k0 = Exact ? down : down * 33554432.f, k1 = Exact ? down : down * 2097152.f;  // bare codes: u * 2^-24, 2^-20
+    const float k0 = Exact ? down : down * 16777216.f, k1 = Exact ? down : down * 1048576.f;  // bare codes: u * 2^-23, 2^-19
     uint32_t wt[QL][GW][U / 16][2];
     float ws[GW][4];
 #pragma unroll
@@ -591,7 +612,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
           for (int i = 0; i < U / 16; ++i) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float st = value_param(i, k, w * 64 / G + n).x * up;
+              const float st = step[i][k][w * 64 / G + n] * up;
               float x0 = s[i][2 * k] * st, x1 = s[i][2 * k + 1] * st;
               if (Masked) {   // a step may be NaN for the rows that see it
                 if (s[i][2 * k] == 0.f) x0 = 0.f;
@@ -612,7 +633,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
             }
           }
           // -15 sum(w) in units of the products of bare codes
-          ws[n][0] = c[0] * -4.4703484e-7f, ws[n][1] = c[1] * -4.4703484e-7f;
+          ws[n][0] = c[0] * -8.940697e-7f, ws[n][1] = c[1] * -8.940697e-7f;
           ws[n][2] = ws[n][0] * 16.f, ws[n][3] = ws[n][1] * 16.f;
         }
       }
@@ -624,23 +645,17 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next
             const int n = (2 * hh + e) * 16 / G % GW;
-            uint32_t av[4];
+            // the low and the high nibble of a byte
+            const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
+            const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
+            const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
             if (Exact) {
-              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], hh ? 0x7632 : 0x5410);
-              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], hh ? 0x7632 : 0x5410);
-              av[0] = value_halves(e == 0 ? x0 << 4 : x0 >> 4);
-              av[1] = value_halves(e == 0 ? x0 : x0 >> 8);
-              av[2] = value_halves(e == 0 ? x1 << 4 : x1 >> 4);
-              av[3] = value_halves(e == 0 ? x1 : x1 >> 8);
+              const uint32_t av[4] = {value_low(x0), value_high(x0), value_low(x1), value_high(x1)};
               if (k == 0) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
               mma_f16(acc[e], av, wt[0][n][k][0], wt[0][n][k][1]);
               mma_f16(acc[e], av, wt[QL - 1][n][k][0], wt[QL - 1][n][k][1]);
-            } else {                      // the low and high nibble of a byte
-              const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
-              const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
-              const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
-              av[0] = x0 & 0x000f000fu, av[1] = x0 & 0x00f000f0u;
-              av[2] = x1 & 0x000f000fu, av[3] = x1 & 0x00f000f0u;
+            } else {
+              const uint32_t av[4] = {x0 & 0x001e001eu, x0 & 0x01e001e0u, x1 & 0x001e001eu, x1 & 0x01e001e0u};
               mma_f16_from(acc[e], av, wt[0][n][k][0], wt[0][n][k][1], k == 0 ? ws[n] : acc[e]);
             }
           }
@@ -657,7 +672,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   };
 
   bool at_barrier = false;
-  for (long long uu = u0; uu < u1; ++uu) {
+  for (int uu = u0; uu < u1; ++uu) {
     if (fresh) {   // first unit of the warp in this item: query rows
       fresh = false;
       item_start = uu - cur.u;
@@ -667,42 +682,37 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       const size_t at = (size_t)((cur.q0 + rg / a.gq) * a.q.row_stride + (cur.kh * a.gq + rg % a.gq) * a.q.head_stride);
       // the sign of the scale goes with q, its size with f; rows past the end are zero
       const float sign = row >= rows || a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
-      float big = 0.f, fg, up, sum[NG];
-      // two passes over the row: its largest element, then the operand
+      float big = 0.f, fg, up, sum[NG], x[D / 32][8];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        float x[8];
-        ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, a.dtype, x);
+      for (int j = 0; j < D / 32; ++j) ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, dtype, x[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
-      }
+      for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[j][e]));
       scale_to_half_range(quad_max(big), up, fg);
       fg = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e * fg, 1.1754944e-38f);
 #pragma unroll
       for (int n = 0; n < NG; ++n) sum[n] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        float x[8];
-        ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, a.dtype, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] = sign == 0.f ? 0.f : x[e] * (up * sign);
-          sum[j * 32 / G] += x[e];
+          x[j][e] = sign == 0.f ? 0.f : x[j][e] * (up * sign);
+          sum[j * 32 / G] += x[j][e];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          const float c = (e & 1) ? 0.0625f : 1.f;   // odd pairs meet codes that are sixteen times as large
           uint32_t* hi = &q[0][2 * j + (e >> 1)][e & 1];
-          if (Exact) {
-            split_f16(x[2 * e], x[2 * e + 1], *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
-          } else {   // odd pairs meet codes that are sixteen times as large
-            const float c = (e & 1) ? 0.0625f : 1.f;
-            *hi = h2_u32(__floats2half2_rn(x[2 * e] * c, x[2 * e + 1] * c));
-          }
+          if (Exact)
+            split_f16(x[j][2 * e] * c, x[j][2 * e + 1] * c, *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
+          else
+            *hi = h2_u32(__floats2half2_rn(x[j][2 * e] * c, x[j][2 * e + 1] * c));
         }
       }
-      if (!Exact) fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
+      fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
 #pragma unroll
-      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * (Exact ? 1.f : 5.9604645e-8f);
+      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * 5.9604645e-8f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int src = 4 * (2 * t + r);
@@ -764,7 +774,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     for (int e = e0; e < e1; ++e) {
       if (s_entry[e].where == 0) continue;
       const float* p = s_entry[e].where == 1 ? sm + (e >> 1) * T::kPart
-                                             : a.warp_parts + ((long long)blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
+                                             : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
       mt = fmaxf(mt, s_entry[e].where == 1 ? p[kRows * D + warp] : __ldcg(p + kRows * D + warp));
     }
     float lt = 0.f, ot[CPL];
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       if (s_entry[e].where == 0) continue;
       const bool in_smem = s_entry[e].where == 1;
       const float* p = in_smem ? sm + (e >> 1) * T::kPart
-                               : a.warp_parts + ((long long)blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
+                               : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
       const float me = in_smem ? p[kRows * D + warp] : __ldcg(p + kRows * D + warp);
       const float le = in_smem ? p[kRows * D + kRows + warp] : __ldcg(p + kRows * D + kRows + warp);
       const float w = me == mt ? 1.f : ex2(me - mt);
@@ -804,16 +814,16 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 // attention block c + 1 lies in, if that item began before it and no earlier
 // border lies in it; warp w takes row w. Lane k looks at the k-th part.
 template <int D>
-__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks, int warps) {
+__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks) {
   constexpr int CPL = D / 32, kPart = Att<D, 64, false>::kPart, kAhead = 8;
   pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x + 1, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Border* bp = a.borders + c;
-  const long long total = __ldcg(&bp->total), item_start = __ldcg(&bp->item_start), item_end = __ldcg(&bp->item_end);
+  const int total = __ldcg(&bp->total), item_start = __ldcg(&bp->item_start), item_end = __ldcg(&bp->item_end);
   const int q0 = __ldcg(&bp->q0), n = __ldcg(&bp->n), kh = __ldcg(&bp->kh), tile = __ldcg(&bp->tile);
-  const Runs runs(total, (long long)blocks * warps);
-  auto start = [&](int k) { return runs.start((long long)k * warps); };
+  const Runs runs(total, blocks);
+  auto start = [&](int k) { return runs.start(k); };
   if (item_end == 0 || item_start >= start(c) || item_start < start(c - 1)) return;
   const float ninf = __int_as_float(0xff800000);
   // parts: the last item of block c - 1 (its first if it begins with it), the first items of c, c + 1, ...
@@ -920,7 +930,7 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
     auto run = [&](auto* kern, int threads, int smem) {
       const cudaError_t e = launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, 1, a);
       if (e != cudaSuccess || blocks < 2) return e;
-      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks, threads / 32);
+      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks);
     };
     using E = Att<D, G, true>;
     using N = Att<D, G, false>;

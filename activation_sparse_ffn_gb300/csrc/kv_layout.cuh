@@ -20,9 +20,9 @@
 // the position so that the four positions a warp reads together use different
 // banks.
 //
-// Params: for eight positions and one group, the (step, mid) pairs of the keys
-// of the eight positions, then those of the values, each in the order T(0) ..
-// T(7); T(i) = i for i < 4 and i ^ 1 above is the order in which the eight
+// Params: for eight positions, the (step, mid) pairs of the keys, then those of
+// the values, each position by position in the order T(0) .. T(7) with its D/G
+// groups beside each other; T(i) = i for i < 4 and i ^ 1 above is the order in which the eight
 // rows (keys) or columns (values) of a matrix operand are assigned to
 // positions. A group with a non-finite value has step = NaN and mid = 0: a
 // weight can be cleared before it meets a step, but not before it meets a mid.
@@ -68,17 +68,14 @@ __host__ __device__ constexpr int value_word_off(int pos, int g, int w) {
 
 // Byte offset, within the params, of the key (which = 0) or value (1) pair of a position and group.
 __host__ __device__ constexpr int param_off(int pos, int grp, int n_groups, int which) {
-  return ((pos >> 3) * n_groups + grp) * 64 + which * 32 + kv_pos_of_col(pos & 7) * 4;
+  return (pos >> 3) * n_groups * 64 + which * n_groups * 32 + (kv_pos_of_col(pos & 7) * n_groups + grp) * 4;
 }
 
 // Key word: the codes of channel pairs e = 0..3 (channels 2e and 2e + 1 of the
 // eight) stand at bits 4 e of the two 16-bit halves; the whole word is then
-// rotated left by one bit. A code then lies at bits 1-4 or 5-8 of a half (after
-// a rotation by 8 for e = 2, 3), inside the ten mantissa bits with one bit to
-// spare below: as a half-precision number the masked bits are u * 2^-23
-// (or u * 2^-19) exactly; with the exponent of 1024 put above them they are
-// 1024 + 2u (or 1024 + 32u), and one half-precision operation makes that 2u -
-// 15 exactly.
+// rotated left by one bit. A code lies at bits 1-4 or 5-8 of a half (after a
+// rotation by 8 for e = 2, 3): as a half-precision number the masked bits are
+// u * 2^-23 (or u * 2^-19), exactly.
 __host__ __device__ __forceinline__ uint32_t key_word(const uint8_t* u) {
   uint32_t w = 0;
 #pragma unroll
@@ -90,12 +87,21 @@ __host__ __device__ __forceinline__ int key_code(uint32_t w, int i) {
   return (w >> ((i & 1) * 16 + (i >> 1) * 4)) & 15;
 }
 
-// Value word: code i (channel 64 w + 8 i + g) at bits 4 i.
+// Value word: codes i = 0..3 (channels 64 w + 8 i + g) at bits 4 i of the low
+// half, i = 4..7 likewise of the high half, each half then rotated left by one
+// bit. A code lies at bits 1-4 or 5-8 of a half, or does so once its two bytes
+// are swapped, which the byte selection that pairs two positions does on the
+// way: with the exponent of 1024 put above it, it is the half-precision number
+// 1024 + 2u (or 1024 + 32u), and one operation makes that 2u - 15 exactly.
 __host__ __device__ __forceinline__ uint32_t value_word(const uint8_t* u) {
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w |= (uint32_t)u[i] << (4 * i);
-  return w;
+  return ((w << 1) & 0xfffefffeu) | ((w >> 15) & 0x00010001u);
+}
+__host__ __device__ __forceinline__ int value_code(uint32_t w, int i) {
+  w = ((w >> 1) & 0x7fff7fffu) | ((w << 15) & 0x80008000u);
+  return (w >> (4 * i)) & 15;
 }
 
 // One stored value, decoded on its own: (2u - 15) * step + mid, the product
@@ -107,7 +113,7 @@ __device__ __forceinline__ float kv_value(const uint8_t* block, int P, int n_gro
   if (which == 0)
     u = key_code(__ldcg(reinterpret_cast<const uint32_t*>(row + key_word_off<D>(pos, (c & 31) >> 3, c >> 5))), c & 7);
   else
-    u = (__ldcg(reinterpret_cast<const uint32_t*>(row + value_word_off<D>(pos, c & 7, c >> 6))) >> (4 * ((c & 63) >> 3))) & 15;
+    u = value_code(__ldcg(reinterpret_cast<const uint32_t*>(row + value_word_off<D>(pos, c & 7, c >> 6))), (c & 63) >> 3);
   const uint32_t pw = __ldcg(reinterpret_cast<const uint32_t*>(
       block + kv_param_off(P, D) + param_off(pos, c / (D / n_groups), n_groups, which)));
   const float2 pm = __half22float2(*reinterpret_cast<const __half2*>(&pw));

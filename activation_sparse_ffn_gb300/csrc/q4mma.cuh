@@ -61,20 +61,7 @@ __device__ __forceinline__ __half2 code_bits(uint32_t w, uint32_t mask) {
   return u32_h2((w & mask) | 0x64006400u);
 }
 
-// The four pairs 2u - 15 of a key word (kv_layout.cuh): 1024 + 2u - 1039 and
-// (1024 + 32u) / 16 - 79, both exact.
-__device__ __forceinline__ void key_halves(uint32_t w, uint32_t* p) {
-  const __half2 k1 = u32_h2(0xe40fe40fu);     // -1039
-  const __half2 k16 = u32_h2(0x2c002c00u);    // 1/16
-  const __half2 k79 = u32_h2(0xd4f0d4f0u);    // -79
-  const uint32_t r = __funnelshift_r(w, w, 8);
-  p[0] = h2_u32(__hadd2(code_bits(w, 0x001e001eu), k1));
-  p[1] = h2_u32(__hfma2(code_bits(w, 0x01e001e0u), k16, k79));
-  p[2] = h2_u32(__hadd2(code_bits(r, 0x001e001eu), k1));
-  p[3] = h2_u32(__hfma2(code_bits(r, 0x01e001e0u), k16, k79));
-}
-
-// The four pairs of a key word as they stand: u * 2^-23 for p[0] and p[2],
+// The four pairs of a key word (kv_layout.cuh) as they stand: u * 2^-23 for p[0] and p[2],
 // u * 2^-19 for p[1] and p[3] (subnormal halves, which the tensor cores take exactly).
 __device__ __forceinline__ void key_bits(uint32_t w, uint32_t* p) {
   const uint32_t r = __funnelshift_r(w, w, 8);
@@ -84,9 +71,13 @@ __device__ __forceinline__ void key_bits(uint32_t w, uint32_t* p) {
   p[3] = r & 0x01e001e0u;
 }
 
-// 2u - 15 for the code at bits 4-7 of both halves: (1024 + 16u) / 8 - 143.
-__device__ __forceinline__ uint32_t value_halves(uint32_t w) {
-  return h2_u32(__hfma2(code_bits(w, 0x00f000f0u), u32_h2(0x30003000u), u32_h2(0xd878d878u)));
+// 2u - 15 for the codes at bits 1-4 of both halves, and at bits 5-8:
+// 1024 + 2u - 1039 and (1024 + 32u) / 16 - 79.
+__device__ __forceinline__ uint32_t value_low(uint32_t w) {
+  return h2_u32(__hadd2(code_bits(w, 0x001e001eu), u32_h2(0xe40fe40fu)));
+}
+__device__ __forceinline__ uint32_t value_high(uint32_t w) {
+  return h2_u32(__hfma2(code_bits(w, 0x01e001e0u), u32_h2(0x2c002c00u), u32_h2(0xd4f0d4f0u)));
 }
 
 __device__ __forceinline__ float ex2(float x) {
