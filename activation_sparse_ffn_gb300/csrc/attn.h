@@ -16,6 +16,8 @@ struct sffn_linear {
   void* zeros = nullptr;       // the same shape, or null
   float* bias = nullptr;       // [tiles * 16], zeros if none was given
   uint32_t* err = nullptr;
+  // clusters of 1, 2, 4 and 8 blocks that the GPU holds, by column tiles (1, 2, 4, 8) and shared memory (linear.cuh)
+  int fit_small[4][4] = {}, fit_large[4][4] = {};
 };
 
 struct sffn_kv {
@@ -32,7 +34,7 @@ namespace sffn {
 
 sffn_status pack_linear(sffn_linear& L, const int8_t* codes, const void* scales, const void* zeros, const float* bias,
                         cudaStream_t st);
-cudaError_t configure_linear_kernels(const sffn_linear& L);
+cudaError_t configure_linear_kernels(sffn_linear& L);
 size_t linear_ws_bytes(const sffn_linear& L, int B);
 cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const sffn_rows& residual,
                           const sffn_rows& y, int dtype, void* ws, cudaStream_t st);

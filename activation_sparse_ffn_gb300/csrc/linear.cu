@@ -4,11 +4,14 @@
 // that a warp (lane = 4 g + t) takes a block with one 16-byte load per lane:
 // words (row g, inputs 8t..8t+7 of the first 32), (row g + 8, the same),
 // (row g, of the second 32), (row g + 8, the same). In a word, the codes of
-// inputs 2e and 2e + 1 of its eight stand at bits 4e of the two halves. Rows and
+// inputs 2e and 2e + 1 of its eight stand at bits 4e of the two halves
+// (e = 0, 1 as they are, e = 2, 3 after a shift by 8: two bits of a half apart by
+// four, which is all that linear.cuh has to undo). Rows and
 // inputs are padded with code 0 (stored as 8). Scales (and zeros) stand as
 // [tile][group][8][2], rows g and g + 8 beside each other.
-#include "attn.h"
-#include "rows_io.cuh"
+#include <algorithm>
+
+#include "linear.cuh"
 
 namespace sffn {
 
@@ -54,41 +57,13 @@ __global__ void k_pack_bias(const float* in, float* out, int n, int np) {
   if (i < np) out[i] = in && i < n ? in[i] : 0.f;
 }
 
-struct LinearArgs {
-  const uint32_t* codes;
-  const void* scales;
-  const void* zeros;
-  const float* bias;
-  int n, k, kp, group, sdtype, B, dtype;
-  sffn_rows x, residual, y;
-};
+int column_tiles(int B, int dtype) {   // of eight columns, rounded up to a power of two
+  const int cols = dtype == SFFN_F32 ? 2 * B : B;
+  return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
+}
 
-// One warp per (output, token).
-__global__ void __launch_bounds__(128) k_linear(const LinearArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, n = blockIdx.x * 4 + (threadIdx.x >> 5), b = blockIdx.y;
-  if (n >= a.n) return;
-  const int tile = n / 16, r = n % 16, g = r % 8, half = r / 8, ngk = a.kp / a.group;
-  float y = 0.f;
-  for (int w = lane; w < a.k / 8; w += 32) {  // word: inputs 8w .. 8w + 7
-    const int kb = w / 8, t = w % 4, second = (w / 4) & 1;
-    const uint32_t c = __ldg(a.codes + ((size_t)tile * (a.kp / 64) + kb) * 128 + (g * 4 + t) * 4 + second * 2 + half);
-    const size_t gi = (((size_t)tile * ngk + 8 * w / a.group) * 8 + g) * 2 + half;
-    const float s = ld_elem(a.scales, gi, a.sdtype), z = a.zeros ? ld_elem(a.zeros, gi, a.sdtype) : 0.f;
-    float v = 0.f;
-    for (int e = 0; e < 8; ++e) {
-      const float code = (float)((int)(c >> ((e & 1) * 16 + (e >> 1) * 4) & 15) - 8);
-      v = fmaf(code - z, ld_elem(a.x.ptr, (size_t)(b * a.x.row_stride) + 8 * w + e, a.dtype), v);
-    }
-    y = fmaf(s, v, y);
-  }
-  y = warp_sum(y);
-  if (lane == 0) {
-    y += a.bias[n];
-    if (a.residual.ptr) y += ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n, a.dtype);
-    st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n, y, a.dtype);
-  }
+int scale_format(const sffn_linear& L) {
+  return L.desc.scale_dtype == SFFN_F32 ? kScale32 : L.desc.has_zero ? kScale16Zero : kScale16;
 }
 
 }  // namespace
@@ -125,16 +100,62 @@ sffn_status pack_linear(sffn_linear& L, const int8_t* codes, const void* scales,
   return SFFN_OK;
 }
 
-cudaError_t configure_linear_kernels(const sffn_linear&) { return cudaSuccess; }
+cudaError_t configure_linear_kernels(sffn_linear& L) {
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    LinearFit fit = {};
+    const int nt = 1 << i, fmt = scale_format(L);
+    e = L.desc.group == 32 ? prepare_linear_g32(nt, fmt, &fit)
+                           : L.desc.group == 64 ? prepare_linear_g64(nt, fmt, &fit) : prepare_linear_g128(nt, fmt, &fit);
+    for (int c = 0; c < 4; ++c) L.fit_small[i][c] = fit.small[c], L.fit_large[i][c] = fit.large[c];
+  }
+  return e;
+}
 
 size_t linear_ws_bytes(const sffn_linear&, int) { return 0; }
 
 cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const sffn_rows& residual,
                           const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
   (void)ws;
-  const LinearArgs a{L.codes, L.scales, L.zeros, L.bias, L.desc.out_features, L.desc.in_features, L.kp,
-                     L.desc.group, L.desc.scale_dtype, B, dtype, x, residual, y};
-  return launch_ex(k_linear, dim3((a.n + 3) / 4, B), dim3(128), 0, st, true, 1, a);
+  LinearArgs a = {};
+  a.codes = L.codes, a.scales = L.scales, a.zeros = L.zeros, a.bias = L.bias;
+  a.n = L.desc.out_features, a.k = L.desc.in_features, a.kp = L.kp, a.B = B, a.dtype = dtype;
+  a.sdtype = L.desc.scale_dtype, a.tiles = L.tiles, a.x = x, a.residual = residual, a.y = y;
+  const int G = L.desc.group, S = std::max(G, 64), steps = a.kp / S;
+  const int nt = column_tiles(B, dtype), nti = nt == 1 ? 0 : nt == 2 ? 1 : nt == 4 ? 2 : 3;
+  const int cols = dtype == SFFN_F32 ? 2 * B : B, elems = 16 * B;
+  // a block has at least 512 inputs, so that converting x and adding sums stay small beside its steps
+  int ci = 3;
+  while (ci > 0 && (steps * S) >> ci < 512) --ci;
+  const int cs = 1 << ci, own = (steps + cs - 1) / cs * S;   // inputs of a block
+  auto up16 = [](int v) { return (v + 15) & ~15; };
+  // Two small blocks per SM hide each other's latencies; a large one holds more of x at a time. Sums of at most
+  // 40 KB of tiles are kept, which bounds the tiles of a cluster.
+  const int most = std::max(1, 40 * 1024 / (elems * 4));
+  int smem = 0, blocks = 0;
+  for (int large = 0; large < 2; ++large) {
+    const int fit = std::max(1, large ? L.fit_large[nti][ci] : L.fit_small[nti][ci]);
+    a.clusters = std::max(std::min(a.tiles, fit), (a.tiles + most - 1) / most);
+    a.max_tiles = (a.tiles + a.clusters - 1) / a.clusters;
+    const int fixed = a.max_tiles * elems * 4 + 2 * kLinWarps * elems * 4;
+    const int room = (large ? kLinLarge : kLinSmall) - fixed - 64;
+    // halves of x and its (scale, sum) pairs per 128 inputs, and the rows' padding
+    const int per128 = cols * 256 + 128 / G * 8 * nt * 8, pad = cols * 64;
+    const int runs = std::min((own + 127) / 128, (room - pad) / per128);
+    if (runs < 1 || (!large && runs < std::min(4, (own + 127) / 128))) continue;
+    a.chunk = runs * 128;
+    a.chunk_stride = a.chunk + 32;
+    a.off_xg = up16(cols * a.chunk_stride * 2);
+    a.off_acc = up16(a.off_xg + a.chunk / G * 8 * nt * 8);
+    a.off_part = up16(a.off_acc + a.max_tiles * elems * 4);
+    smem = a.off_part + 2 * kLinWarps * elems * 4;
+    blocks = a.clusters * cs;
+    break;
+  }
+  const int fmt = scale_format(L);
+  return G == 32 ? run_linear_g32(nt, fmt, cs, a, blocks, smem, st)
+                 : G == 64 ? run_linear_g64(nt, fmt, cs, a, blocks, smem, st)
+                           : run_linear_g128(nt, fmt, cs, a, blocks, smem, st);
 }
 
 }  // namespace sffn

@@ -1,0 +1,413 @@
+// The product kernel of the 4-bit linear layer, one instantiation per group
+// size, number of 8-column tiles and scale format (linear_g*.cu).
+//
+// Mathematics. y[b][n] = sum over groups of s * (sum_k c x[b][k] - z sum_k
+// x[b][k]). Weights are the 16-row operand of the tensor-core product: a code c
+// = u - 8 becomes a half with one mask and one operation per pair (1024 + u -
+// 1032 or (1024 + 16u) / 16 - 72, both exact), and scales and zeros are applied
+// to the sums of a group in fp32. Codes go in centred although bare ones would
+// cost nothing: the tensor core cuts its addends off at 2^-24 of the largest,
+// and activations have large elements. Tokens are the 8-column operand,
+// as halves: 16-bit activations exactly, up to a power of two per token and run
+// of 128 inputs that brings the largest to 2^13; fp32 activations as two
+// columns, the nearest half and the nearest half of what is left (22 bits).
+//
+// Work split. The codes are read once, straight to registers, and everything
+// else is small: for up to 8 tokens this is a stream of N K / 2 bytes. A cluster
+// of blocks takes a run of 16-row tiles and its blocks split the inputs, so
+// that a block converts only its share of x; the blocks' sums are added through
+// distributed shared memory in rank order. Within a block the (tile, run of
+// inputs) steps are numbered through and each warp takes an equal run of them,
+// with kAhead steps' loads in flight, begun before the wait for the kernel
+// that produces x.
+#pragma once
+
+#include <type_traits>
+
+#include "attn.h"
+#include "q4mma.cuh"
+#include "rows_io.cuh"
+
+namespace sffn {
+
+struct LinearArgs {
+  const uint32_t* codes;
+  const void* scales;
+  const void* zeros;
+  const float* bias;
+  int n, k, kp, B, dtype, sdtype;
+  int tiles;        // 16-row tiles
+  int clusters, chunk, chunk_stride;   // inputs of x held at a time (a multiple of 128), halves of a row of xs
+  int max_tiles;    // of a cluster
+  int off_xg, off_acc, off_part;       // bytes in shared memory
+  sffn_rows x, residual, y;
+};
+
+constexpr int kLinWarps = 8;
+constexpr int kLinThreads = kLinWarps * 32;
+
+// Scale formats: 16-bit scales, 16-bit scales and zeros, 32-bit scales (and zeros if given).
+enum { kScale16 = 0, kScale16Zero = 1, kScale32 = 2 };
+
+// Shared-memory limits of the kernels of one number of column tiles, and how
+// many clusters of 1, 2, 4 and 8 blocks the GPU holds with `small` and with
+// `large` bytes each.
+struct LinearFit {
+  int small[4], large[4];
+};
+constexpr int kLinSmall = 100 * 1024, kLinLarge = 216 * 1024;
+
+cudaError_t prepare_linear_g32(int nt, int fmt, LinearFit* fit);
+cudaError_t prepare_linear_g64(int nt, int fmt, LinearFit* fit);
+cudaError_t prepare_linear_g128(int nt, int fmt, LinearFit* fit);
+cudaError_t run_linear_g32(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st);
+cudaError_t run_linear_g64(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st);
+cudaError_t run_linear_g128(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st);
+
+#ifdef SFFN_LINEAR_GROUP
+
+namespace {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t smem_addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The code pairs u - 8 at bits 0-3 and 4-7 of both halves of a word.
+__device__ __forceinline__ uint32_t weight_low(uint32_t w) {
+  return h2_u32(__hadd2(code_bits(w, 0x000f000fu), u32_h2(0xe408e408u)));
+}
+__device__ __forceinline__ uint32_t weight_high(uint32_t w) {
+  return h2_u32(__hfma2(code_bits(w, 0x00f000f0u), u32_h2(0x2c002c00u), u32_h2(0xd480d480u)));
+}
+
+template <int FMT>
+struct ScaleWord {   // the scales (and zeros) of rows g and g + 8 as loaded
+  uint32_t w[FMT == kScale16 ? 1 : FMT == kScale16Zero ? 2 : 4];
+};
+
+template <int G, int NT, int FMT>
+__global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const LinearArgs a, int cs) {
+  constexpr int S = G > 64 ? G : 64;        // inputs of a step
+  constexpr int BL = S / 64, GS = S / G;    // 64-input blocks and groups of a step
+  constexpr int kAhead = FMT == kScale32 && G == 32 ? 4 : 8 / BL;   // by registers
+  extern __shared__ __align__(16) uint8_t smem[];
+  __half* xs = reinterpret_cast<__half*>(smem);                  // [columns][chunk_stride]
+  float2* xg = reinterpret_cast<float2*>(smem + a.off_xg);       // [groups of a chunk][8 NT]: down, down * sum(x)
+  float* acc_s = reinterpret_cast<float*>(smem + a.off_acc);     // [tiles of the cluster][B][16]
+  float* part = reinterpret_cast<float*>(smem + a.off_part);     // [warp][2][B][16]
+  __shared__ int s_tile[kLinWarps][2];                           // tile of a part, -1: none
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
+  const int tile0 = (int)((long long)cluster * a.tiles / a.clusters);
+  const int nt = (int)((long long)(cluster + 1) * a.tiles / a.clusters) - tile0;
+  // this block's inputs, in steps
+  const int all_steps = (a.kp + S - 1) / S;
+  const int k_step0 = all_steps * rank / cs, k_step1 = all_steps * (rank + 1) / cs;
+  const bool split = a.dtype == SFFN_F32;
+  const int cols = split ? 2 * a.B : a.B, elems = a.B * 16;
+  const int chunk_steps = a.chunk / S;
+  const int groups = a.kp / G, blocks64 = a.kp / 64;
+
+  for (int c0 = k_step0; c0 < k_step1 || c0 == k_step0; c0 += chunk_steps) {
+    const int spt = min(chunk_steps, k_step1 - c0);   // steps of a tile in this chunk
+    const int steps = nt * max(spt, 0);
+    const int s0 = steps * warp / kLinWarps, s1 = steps * (warp + 1) / kLinWarps;
+
+    // ---- the first loads of codes and scales: these do not depend on an earlier kernel
+    uint4 cw[kAhead][BL];
+    ScaleWord<FMT> sw[kAhead][GS];
+    int ld_tile = spt > 0 ? s0 / spt : 0, ld_k = spt > 0 ? s0 % spt : 0, ld_s = s0;
+    auto load = [&](uint4* c, ScaleWord<FMT>* s) {
+      if (ld_s < s1) {
+        const size_t tile = tile0 + ld_tile;
+        const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + (tile * blocks64 + (size_t)(c0 + ld_k) * BL) * 32 + lane;
+#pragma unroll
+        for (int b = 0; b < BL; ++b) c[b] = ldg_stream(cp + b * 32);   // kp is a multiple of S
+        const size_t at = (tile * groups + (size_t)(c0 + ld_k) * GS) * 8 + g;
+#pragma unroll
+        for (int q = 0; q < GS; ++q) {
+          if (FMT == kScale32) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.scales) + at + q * 8);
+            s[q].w[0] = v.x, s[q].w[1 % (sizeof(s[q].w) / 4)] = v.y;
+            uint2 z = make_uint2(0u, 0u);
+            if (a.zeros) z = __ldg(reinterpret_cast<const uint2*>(a.zeros) + at + q * 8);
+            s[q].w[2 % (sizeof(s[q].w) / 4)] = z.x, s[q].w[3 % (sizeof(s[q].w) / 4)] = z.y;
+          } else {
+            s[q].w[0] = __ldg(reinterpret_cast<const uint32_t*>(a.scales) + at + q * 8);
+            if (FMT == kScale16Zero) s[q].w[1 % (sizeof(s[q].w) / 4)] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros) + at + q * 8);
+          }
+        }
+        if (++ld_k == spt) ld_k = 0, ++ld_tile;
+        ++ld_s;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(cw[i], sw[i]);
+
+    if (c0 == k_step0) {
+      pdl_launch_dependents();
+      pdl_wait();
+      for (int i = threadIdx.x; i < nt * elems; i += kLinThreads) acc_s[i] = 0.f;
+      if (threadIdx.x < 2 * kLinWarps) (&s_tile[0][0])[threadIdx.x] = -1;
+    } else {
+      __syncthreads();   // every warp is done with the chunk before
+    }
+
+    // ---- x of the chunk: one warp per token and run of 128 inputs, four inputs per lane
+    const int k0 = c0 * S, kn = spt * S, runs = (kn + 127) / 128;
+    for (int task = warp; task < a.B * runs; task += kLinWarps) {
+      const int b = task / runs, run = task % runs, kk = run * 128 + lane * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kk < kn && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v);
+      float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
+      float up, down;
+      scale_to_half_range(big, up, down);
+      uint32_t hi[2], lo[2];
+      float sh = 0.f, sl = 0.f;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
+        const float2 fh = __half22float2(u32_h2(hi[p])), fl = __half22float2(u32_h2(lo[p]));
+        sh += fh.x + fh.y;
+        sl += fl.x + fl.y;
+      }
+#pragma unroll
+      for (int o = 1; o < (G > 128 ? 32 : G / 4); o <<= 1) {
+        sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
+        sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
+      }
+      if (kk < kn) {
+        const int col = split ? 2 * b : b;
+        *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
+        if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
+        if (lane % (G / 4) == 0) {
+          float2* at = xg + (size_t)(kk / G) * (8 * NT) + col;
+          at[0] = make_float2(down, down * sh);
+          if (split) at[1] = make_float2(down, down * sl);
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- the warp's steps
+    float y[NT][4];
+    int tile = spt > 0 ? s0 / spt : 0, kk = spt > 0 ? s0 % spt : 0;
+    const int first_k = kk;
+    bool fresh = true, first = true;
+    const __half* xcol[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int c = 8 * n + g;   // columns past the end repeat the last one; their results are not used
+      xcol[n] = xs + (size_t)min(c, cols - 1) * a.chunk_stride + 8 * t;
+    }
+    auto store = [&](float* dst, bool add) {   // sums of a tile, [B][16]
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (split) {
+            const int b = 4 * n + t;
+            if (b < a.B) {
+              float* p = dst + b * 16 + g + 8 * r;
+              const float v = y[n][2 * r] + y[n][2 * r + 1];
+              *p = add ? *p + v : v;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int b = 8 * n + 2 * t + c;
+              if (b < a.B) {
+                float* p = dst + b * 16 + g + 8 * r;
+                *p = add ? *p + y[n][2 * r + c] : y[n][2 * r + c];
+              }
+            }
+          }
+        }
+      }
+    };
+    auto step = [&](const uint4* c, const ScaleWord<FMT>* s) {
+      if (fresh) {
+        fresh = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
+      }
+      float d[NT][4];
+#pragma unroll
+      for (int b = 0; b < BL; ++b) {
+        const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 32 inputs
+          const uint32_t wa = w[2 * h], wb = w[2 * h + 1], ra = wa >> 8, rb = wb >> 8;
+          const uint32_t a0[4] = {weight_low(wa), weight_low(wb), weight_high(wa), weight_high(wb)};
+          const uint32_t a1[4] = {weight_low(ra), weight_low(rb), weight_high(ra), weight_high(rb)};
+          const bool begin = (b * 64 + h * 32) % G == 0;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + kk * S + b * 64 + h * 32);
+            if (begin) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+            mma_f16(d[n], a0, xv.x, xv.y);
+            mma_f16(d[n], a1, xv.z, xv.w);
+          }
+          if ((b * 64 + h * 32 + 32) % G == 0) {   // end of a group: scales
+            const int q = (b * 64 + h * 32) / G;
+            float sc[2], z[2] = {0.f, 0.f};
+            if (FMT == kScale32) {
+              sc[0] = __uint_as_float(s[q].w[0]), sc[1] = __uint_as_float(s[q].w[1 % (sizeof(s[q].w) / 4)]);
+              z[0] = __uint_as_float(s[q].w[2 % (sizeof(s[q].w) / 4)]);
+              z[1] = __uint_as_float(s[q].w[3 % (sizeof(s[q].w) / 4)]);
+            } else {
+              auto two = [&](uint32_t v, float& lo, float& hi) {
+                if (a.sdtype == SFFN_F16) {
+                  const float2 f = __half22float2(u32_h2(v));
+                  lo = f.x, hi = f.y;
+                } else {
+                  lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xffff0000u);
+                }
+              };
+              two(s[q].w[0], sc[0], sc[1]);
+              if (FMT == kScale16Zero) two(s[q].w[1 % (sizeof(s[q].w) / 4)], z[0], z[1]);
+            }
+            const float2* xq = xg + (size_t)(kk * GS + q) * (8 * NT) + 2 * t;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float4 v = *reinterpret_cast<const float4*>(xq + 8 * n);   // (down, sum) of columns 2t, 2t + 1
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                if (FMT == kScale16) {
+                  y[n][2 * r] = fmaf(sc[r], d[n][2 * r] * v.x, y[n][2 * r]);
+                  y[n][2 * r + 1] = fmaf(sc[r], d[n][2 * r + 1] * v.z, y[n][2 * r + 1]);
+                } else {
+                  y[n][2 * r] = fmaf(sc[r], fmaf(d[n][2 * r], v.x, -z[r] * v.y), y[n][2 * r]);
+                  y[n][2 * r + 1] = fmaf(sc[r], fmaf(d[n][2 * r + 1], v.z, -z[r] * v.w), y[n][2 * r + 1]);
+                }
+              }
+            }
+          }
+        }
+      }
+      if (++kk == spt) {
+        // a tile that began in this warp's run is complete; the tail of an earlier warp's tile is a part
+        if (first && first_k != 0) {
+          store(part + (size_t)(warp * 2) * elems, false);
+          if (lane == 0) s_tile[warp][0] = tile;
+        } else {
+          store(acc_s + (size_t)tile * elems, true);
+        }
+        first = false;
+        fresh = true;
+        kk = 0;
+        ++tile;
+      }
+    };
+    for (int s = s0; s < s1;) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s < s1) {
+          step(cw[i], sw[i]);
+          load(cw[i], sw[i]);
+          ++s;
+        }
+      }
+    }
+    if (!fresh) {   // the head of a tile that a later warp completes
+      store(part + (size_t)(warp * 2 + 1) * elems, false);
+      if (lane == 0) s_tile[warp][1] = tile;
+    }
+    __syncthreads();
+    // parts in warp order; a thread keeps to its elements, so no barrier is needed between them
+    for (int e = threadIdx.x; e < elems; e += kLinThreads)
+      for (int p = 0; p < 2 * kLinWarps; ++p) {
+        const int pt = (&s_tile[0][0])[p];
+        if (pt >= 0) acc_s[(size_t)pt * elems + e] += part[(size_t)p * elems + e];
+      }
+    __syncthreads();
+    if (threadIdx.x < 2 * kLinWarps) (&s_tile[0][0])[threadIdx.x] = -1;
+    if (spt <= 0) break;
+  }
+
+  // ---- the cluster's blocks add their sums; each writes its share of the outputs
+  if (cs > 1) cluster_barrier();
+  else __syncthreads();
+  const int all = nt * elems;
+  const uint32_t base = smem_u32(acc_s);
+  for (int e = threadIdx.x * cs + rank; e < all; e += kLinThreads * cs) {
+    const int tile = e / elems, b = (e % elems) / 16, n = (tile0 + tile) * 16 + e % 16;
+    float v = 0.f;
+    if (cs > 1) {
+      for (int r = 0; r < cs; ++r) v += ld_cluster(base + 4u * e, r);
+    } else {
+      v = acc_s[e];
+    }
+    if (n < a.n) {
+      v += a.bias[n];
+      if (a.residual.ptr) v += ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n, a.dtype);
+      st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n, v, a.dtype);
+    }
+  }
+  if (cs > 1) cluster_barrier();
+}
+
+// Calls f with the kernel of a number of column tiles and a scale format.
+template <int G, typename F>
+cudaError_t with_kernel(int nt, int fmt, F&& f) {
+  auto by_fmt = [&](auto n) {
+    constexpr int NT = decltype(n)::value;
+    return fmt == kScale16 ? f(k_linear<G, NT, kScale16>)
+                           : fmt == kScale16Zero ? f(k_linear<G, NT, kScale16Zero>) : f(k_linear<G, NT, kScale32>);
+  };
+  switch (nt) {
+    case 1: return by_fmt(std::integral_constant<int, 1>());
+    case 2: return by_fmt(std::integral_constant<int, 2>());
+    case 4: return by_fmt(std::integral_constant<int, 4>());
+    default: return by_fmt(std::integral_constant<int, 8>());
+  }
+}
+
+template <int G>
+cudaError_t prepare(int nt, int fmt, LinearFit* fit) {
+  return with_kernel<G>(nt, fmt, [&](auto* kern) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinLarge);
+    for (int i = 0; i < 8 && e == cudaSuccess; ++i) {
+      const int c = 1 << (i / 2);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(kLinThreads);
+      cfg.dynamicSmemBytes = i % 2 ? kLinLarge : kLinSmall;
+      cudaLaunchAttribute at;
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = c;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(i % 2 ? &fit->large[i / 2] : &fit->small[i / 2], kern, &cfg);
+    }
+    return e;
+  });
+}
+
+template <int G>
+cudaError_t run(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st) {
+  return with_kernel<G>(nt, fmt, [&](auto* kern) {
+    return launch_ex(kern, dim3(blocks), dim3(kLinThreads), smem, st, true, cluster, a, cluster);
+  });
+}
+
+}  // namespace
+
+#endif  // SFFN_LINEAR_GROUP
+
+}  // namespace sffn

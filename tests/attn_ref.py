@@ -11,8 +11,8 @@ absolute terms that the bounds are made of:
   of a tensor core, each off by at most 2^-22 of the terms' absolute sum; the
   K/G group sums are added in fp32. Together at most (40 + K/G) 2^-24 of
   sum |w||x|.
-* attention: a score is off by at most 2^-20 of scale * sum |q||k| (the same
-  terms, and its own rounding), a weight by that and 2^-20 relative, the
+* attention: a score is a sum of q times bare codes 0..15, so it is off by at
+  most 2^-20 of scale * sum |q| (|mid| + 30 step), its own rounding included; a weight by that and 2^-20 relative, the
   weighted sum of values by a further 2^-19 of sum p|V|; the normalisation at
   most doubles the first part. With 16-bit rows the product of a weight and a
   step is rounded to a half (2^-11 relative): with step |2u - 15| <= |V| + |mid|
@@ -61,9 +61,10 @@ def rotate(x: np.ndarray, cs: np.ndarray, style: str) -> np.ndarray:
     return x
 
 
-def attention(q, k, v, n_new: int, scale: float, window: int, vsize=None):
-    """One sequence: q (n_new, Hq, D), k, v (len, Hkv, D); vsize (len, Hkv, D),
-    |V| + |mid|, if the rows have 16 bits. Returns out, lse and the bound on
+def attention(q, k, v, n_new: int, scale: float, window: int, ksize=None, vsize=None):
+    """One sequence: q (n_new, Hq, D), k, v (len, Hkv, D); ksize
+    (len, Hkv, D) |mid| + 30 step of the keys; vsize (len, Hkv, D) |V| + |mid|
+    if the rows have 16 bits. Returns out, lse and the bound on
     the error of out, all float64."""
     q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
     n, hq = k.shape[0], q.shape[1]
@@ -76,7 +77,8 @@ def attention(q, k, v, n_new: int, scale: float, window: int, vsize=None):
         a = max(0, p - window + 1) if window else 0
         kk, vv = (np.repeat(t[a:p + 1], rep, axis=1) for t in (k, v))
         s = np.einsum("hd,lhd->hl", q[i], kk) * scale
-        es = 2.0 ** -20 * abs(scale) * np.einsum("hd,lhd->hl", abs(q[i]), abs(kk)).max(1)
+        ks = abs(kk) if ksize is None else np.repeat(ksize[a:p + 1], rep, axis=1)
+        es = 2.0 ** -20 * abs(scale) * np.einsum("hd,lhd->hl", abs(q[i]), ks).max(1)
         m = s.max(1)
         w = np.exp(s - m[:, None])
         lse[i] = m + np.log(w.sum(1))

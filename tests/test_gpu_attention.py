@@ -198,6 +198,8 @@ class Case:
         v = self.randn(self.total, self.hkv, self.D)
         sffn.sffn_kv_append(self.cache.handle, self.all, None, k, v)
         self.k, self.v = (R.stored(t.float().cpu().numpy(), self.G) for t in (k, v))
+        step, mid, _ = R.group_params(k.float().cpu().numpy(), self.G)
+        self.ksize = np.repeat(abs(mid.astype(np.float64)) + 30 * step.astype(np.float64), self.G, axis=-1)
         mid = R.group_params(v.float().cpu().numpy(), self.G)[1].astype(np.float64)
         self.vsize = None if self.dtype == torch.float32 else abs(self.v) + np.repeat(abs(mid), self.G, axis=-1)
         return k, v
@@ -340,7 +342,7 @@ def check_attention(sffn, lens, hq, hkv, D, G, P, dtype="f32", window=0, scale=N
     qh, oh = host(q), host(out)
     at = row = 0
     for n, m in lens:
-        want, wlse, tol = R.attention(qh[row:row + m], c.k[at:at + n], c.v[at:at + n], m, scale, window,
+        want, wlse, tol = R.attention(qh[row:row + m], c.k[at:at + n], c.v[at:at + n], m, scale, window, c.ksize[at:at + n],
                                       None if c.vsize is None else c.vsize[at:at + n])
         R.assert_close(oh[row:row + m], want, tol, dtype, f"attention len {n} new {m}")
         if with_lse:
