@@ -124,34 +124,61 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
   const int G = L.desc.group, S = std::max(G, 64), steps = a.kp / S;
   const int nt = column_tiles(B, dtype), nti = nt == 1 ? 0 : nt == 2 ? 1 : nt == 4 ? 2 : 3;
   const int cols = dtype == SFFN_F32 ? 2 * B : B, elems = 16 * B;
-  // a block has at least 512 inputs, so that converting x and adding sums stay small beside its steps
-  int ci = 3;
-  while (ci > 0 && (steps * S) >> ci < 512) --ci;
-  const int cs = 1 << ci, own = (steps + cs - 1) / cs * S;   // inputs of a block
   auto up16 = [](int v) { return (v + 15) & ~15; };
-  // Two small blocks per SM hide each other's latencies; a large one holds more of x at a time. Sums of at most
-  // 40 KB of tiles are kept, which bounds the tiles of a cluster.
-  const int most = std::max(1, 40 * 1024 / (elems * 4));
-  int smem = 0, blocks = 0;
-  for (int large = 0; large < 2; ++large) {
-    const int fit = std::max(1, large ? L.fit_large[nti][ci] : L.fit_small[nti][ci]);
-    a.clusters = std::max(std::min(a.tiles, fit), (a.tiles + most - 1) / most);
-    a.max_tiles = (a.tiles + a.clusters - 1) / a.clusters;
-    const int fixed = a.max_tiles * elems * 4 + 2 * kLinWarps * elems * 4;
-    const int room = (large ? kLinLarge : kLinSmall) - fixed - 64;
-    // halves of x and its (scale, sum) pairs per 128 inputs, and the rows' padding
-    const int per128 = cols * 256 + 128 / G * 8 * nt * 8, pad = cols * 64;
-    const int runs = std::min((own + 127) / 128, (room - pad) / per128);
-    if (runs < 1 || (!large && runs < std::min(4, (own + 127) / 128))) continue;
-    a.chunk = runs * 128;
-    a.chunk_stride = a.chunk + 32;
-    a.off_xg = up16(cols * a.chunk_stride * 2);
-    a.off_acc = up16(a.off_xg + a.chunk / G * 8 * nt * 8);
-    a.off_part = up16(a.off_acc + a.max_tiles * elems * 4);
-    smem = a.off_part + 2 * kLinWarps * elems * 4;
-    blocks = a.clusters * cs;
-    break;
+  const int xpair = 8 * nt * 8;   // bytes of the (scale, sum) pairs of a group of inputs
+  int smem = 0, ci = 3;
+  if (nt == 1) {
+    // The split of the inputs that gives a block the least to read; a cluster costs two barriers and a pass over
+    // its sums, about what 64 KB take.
+    long long best = -1;
+    for (int c = 0; c < 4; ++c) {
+      const int slices = kLinWarps << c;
+      const int own = (steps + slices - 1) / slices * S, own128 = (own + 127) / 128 * 128;
+      const int xbytes = up16(kLinWarps * cols * (own128 + 32) * 2) + kLinWarps * (own128 / G) * xpair;
+      const int per_tile = (kLinWarps + 1) * elems * 4;
+      for (int large = 0; large < 2; ++large) {
+        const int room = (large ? kLinLarge : kLinSmall) - xbytes - 64;
+        if (room < per_tile || (!large && room < 8 * per_tile)) continue;
+        const int fit = std::max(1, large ? L.fit_large[0][c] : L.fit_small[0][c]);
+        const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + room / per_tile - 1) / (room / per_tile));
+        const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
+        const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + (c ? 64 * 1024 : 0);
+        if (best >= 0 && cost >= best) break;
+        best = cost, ci = c;
+        a.clusters = clusters, a.chunk = own128, a.chunk_stride = own128 + 32, a.max_tiles = most;
+        a.off_xg = up16(kLinWarps * cols * a.chunk_stride * 2);
+        a.off_part = up16(a.off_xg + kLinWarps * (own128 / G) * xpair);
+        a.off_acc = a.off_part + most * kLinWarps * elems * 4;
+        smem = a.off_acc + most * elems * 4;
+        break;
+      }
+    }
+  } else {
+    // a block has at least 512 inputs, so that converting x and adding sums stay small beside its steps
+    while (ci > 0 && (steps * S) >> ci < 512) --ci;
+    const int cs = 1 << ci, own = (steps + cs - 1) / cs * S;   // inputs of a block
+    // Two small blocks per SM hide each other's latencies; a large one holds more of x at a time. Sums of at most
+    // 40 KB of tiles are kept, which bounds the tiles of a cluster.
+    const int most = std::max(1, 40 * 1024 / (elems * 4));
+    for (int large = 0; large < 2; ++large) {
+      const int fit = std::max(1, large ? L.fit_large[nti][ci] : L.fit_small[nti][ci]);
+      a.clusters = std::max(std::min(a.tiles, fit), (a.tiles + most - 1) / most);
+      a.max_tiles = (a.tiles + a.clusters - 1) / a.clusters;
+      const int fixed = a.max_tiles * elems * 4 + 2 * kLinWarps * elems * 4;
+      const int room = (large ? kLinLarge : kLinSmall) - fixed - 64;
+      const int per128 = cols * 256 + 128 / G * xpair, pad = cols * 64;
+      const int runs = std::min((own + 127) / 128, (room - pad) / per128);
+      if (runs < 1 || (!large && runs < std::min(4, (own + 127) / 128))) continue;
+      a.chunk = runs * 128;
+      a.chunk_stride = a.chunk + 32;
+      a.off_xg = up16(cols * a.chunk_stride * 2);
+      a.off_acc = up16(a.off_xg + a.chunk / G * xpair);
+      a.off_part = up16(a.off_acc + a.max_tiles * elems * 4);
+      smem = a.off_part + 2 * kLinWarps * elems * 4;
+      break;
+    }
   }
+  const int cs = 1 << ci, blocks = a.clusters * cs;
   const int fmt = scale_format(L);
   return G == 32 ? run_linear_g32(nt, fmt, cs, a, blocks, smem, st)
                  : G == 64 ? run_linear_g64(nt, fmt, cs, a, blocks, smem, st)

@@ -12,14 +12,16 @@
 // of 128 inputs that brings the largest to 2^13; fp32 activations as two
 // columns, the nearest half and the nearest half of what is left (22 bits).
 //
-// Work split. The codes are read once, straight to registers, and everything
-// else is small: for up to 8 tokens this is a stream of N K / 2 bytes. A cluster
-// of blocks takes a run of 16-row tiles and its blocks split the inputs, so
-// that a block converts only its share of x; the blocks' sums are added through
-// distributed shared memory in rank order. Within a block the (tile, run of
-// inputs) steps are numbered through and each warp takes an equal run of them,
-// with kAhead steps' loads in flight, begun before the wait for the kernel
-// that produces x.
+// Work split. The codes are read once, straight to registers, with kAhead steps'
+// loads in flight per warp, begun before the wait for the kernel that produces
+// x. A cluster of blocks takes a run of 16-row tiles and its blocks split the
+// inputs, so that a block converts only its share of x; their sums are added
+// through distributed shared memory in rank order.
+//   Up to eight columns (k_linear_few): the warps of a block split its inputs
+// too, each goes over all tiles with the same share of x, which it converts for
+// itself, and leaves one sum per tile and warp: no barrier before the end.
+//   More columns (k_linear): those sums would not fit, so the (tile, run of
+// inputs) steps are numbered through and each warp takes an equal run of them.
 #pragma once
 
 #include <type_traits>
@@ -94,8 +96,280 @@ __device__ __forceinline__ uint32_t weight_high(uint32_t w) {
 
 template <int FMT>
 struct ScaleWord {   // the scales (and zeros) of rows g and g + 8 as loaded
-  uint32_t w[FMT == kScale16 ? 1 : FMT == kScale16Zero ? 2 : 4];
+  static constexpr int N = FMT == kScale16 ? 1 : FMT == kScale16Zero ? 2 : 4;
+  uint32_t w[N];
+  // entry `at` of [..][8][2] arrays
+  __device__ __forceinline__ void load(const LinearArgs& a, size_t at) {
+    if (FMT == kScale32) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.scales) + at);
+      uint2 z = make_uint2(0u, 0u);
+      if (a.zeros) z = __ldg(reinterpret_cast<const uint2*>(a.zeros) + at);
+      w[0] = v.x, w[1 % N] = v.y, w[2 % N] = z.x, w[3 % N] = z.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(a.scales) + at);
+      if (FMT == kScale16Zero) w[1 % N] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros) + at);
+    }
+  }
+  __device__ __forceinline__ void get(int sdtype, float* sc, float* z) const {
+    z[0] = z[1] = 0.f;
+    if (FMT == kScale32) {
+      sc[0] = __uint_as_float(w[0]), sc[1] = __uint_as_float(w[1 % N]);
+      z[0] = __uint_as_float(w[2 % N]), z[1] = __uint_as_float(w[3 % N]);
+    } else {
+      two(w[0], sdtype, sc);
+      if (FMT == kScale16Zero) two(w[1 % N], sdtype, z);
+    }
+  }
+  __device__ __forceinline__ static void two(uint32_t v, int sdtype, float* o) {
+    if (sdtype == SFFN_F16) {
+      const float2 f = __half22float2(u32_h2(v));
+      o[0] = f.x, o[1] = f.y;
+    } else {
+      o[0] = __uint_as_float(v << 16), o[1] = __uint_as_float(v & 0xffff0000u);
+    }
+  }
 };
+
+// y += one step: S inputs of a tile's codes c with their scales s, times the
+// columns xcol[n] (this lane's column of each eight) at halves `at`, with the
+// (down, down * sum) pairs of columns 2t, 2t + 1 of the step's groups at xq
+// (xq_stride pairs from group to group).
+template <int G, int NT, int FMT>
+__device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4* c, const ScaleWord<FMT>* s,
+                                            const __half* const* xcol, int at, const float2* xq, float (*y)[4]) {
+  constexpr int S = G > 64 ? G : 64, BL = S / 64;
+  float d[NT][4];
+#pragma unroll
+  for (int b = 0; b < BL; ++b) {
+    const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // 32 inputs
+      const uint32_t wa = w[2 * h], wb = w[2 * h + 1], ra = wa >> 8, rb = wb >> 8;
+      const uint32_t a0[4] = {weight_low(wa), weight_low(wb), weight_high(wa), weight_high(wb)};
+      const uint32_t a1[4] = {weight_low(ra), weight_low(rb), weight_high(ra), weight_high(rb)};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + at + b * 64 + h * 32);
+        if ((b * 64 + h * 32) % G == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+        mma_f16(d[n], a0, xv.x, xv.y);
+        mma_f16(d[n], a1, xv.z, xv.w);
+      }
+      if ((b * 64 + h * 32 + 32) % G == 0) {   // end of a group: scales
+        const int q = (b * 64 + h * 32) / G;
+        float sc[2], z[2];
+        s[q].get(a.sdtype, sc, z);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 v = *reinterpret_cast<const float4*>(xq + q * (8 * NT) + 8 * n);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (FMT == kScale16) {
+              y[n][2 * r] = fmaf(sc[r], d[n][2 * r] * v.x, y[n][2 * r]);
+              y[n][2 * r + 1] = fmaf(sc[r], d[n][2 * r + 1] * v.z, y[n][2 * r + 1]);
+            } else {
+              y[n][2 * r] = fmaf(sc[r], fmaf(d[n][2 * r], v.x, -z[r] * v.y), y[n][2 * r]);
+              y[n][2 * r + 1] = fmaf(sc[r], fmaf(d[n][2 * r + 1], v.z, -z[r] * v.w), y[n][2 * r + 1]);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// Four inputs of a lane (of a run of 128 that one warp converts together) as
+// halves: the nearest in hi, what is left in lo, both times a power of two; sums
+// over a group of G of either; `down` undoes the power of two.
+template <int G>
+__device__ __forceinline__ void convert_run(const float* v, uint32_t* hi, uint32_t* lo, float& sh, float& sl, float& down) {
+  float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
+  float up;
+  scale_to_half_range(big, up, down);
+  sh = sl = 0.f;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
+    const float2 fh = __half22float2(u32_h2(hi[p])), fl = __half22float2(u32_h2(lo[p]));
+    sh += fh.x + fh.y;
+    sl += fl.x + fl.y;
+  }
+#pragma unroll
+  for (int o = 1; o < G / 4; o <<= 1) {
+    sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
+    sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
+  }
+}
+
+// The sums of a tile ([B][16]) from the fragments of one warp.
+template <int NT>
+__device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], int B, bool split, bool add, int g, int t) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (split) {
+        const int b = 4 * n + t;
+        if (b < B) {
+          float* p = dst + b * 16 + g + 8 * r;
+          const float v = y[n][2 * r] + y[n][2 * r + 1];
+          *p = add ? *p + v : v;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int b = 8 * n + 2 * t + c;
+          if (b < B) {
+            float* p = dst + b * 16 + g + 8 * r;
+            *p = add ? *p + y[n][2 * r + c] : y[n][2 * r + c];
+          }
+        }
+      }
+    }
+}
+
+// Adds the sums acc_s (nt tiles, [B][16] each) of the cluster's blocks; every
+// block writes its share of the outputs.
+__device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* acc_s, int tile0, int nt, int cs, int rank) {
+  const int elems = a.B * 16, all = nt * elems;
+  const uint32_t base = smem_u32(acc_s);
+  if (cs > 1) cluster_barrier();
+  for (int e = threadIdx.x * cs + rank; e < all; e += kLinThreads * cs) {
+    const int tile = e / elems, in = e - tile * elems, b = in >> 4, n = (tile0 + tile) * 16 + (in & 15);
+    float v = 0.f;
+    if (cs > 1) {
+      float p[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) p[r] = r < cs ? ld_cluster(base + 4u * e, r) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v += p[r];
+    } else {
+      v = acc_s[e];
+    }
+    if (n < a.n) {
+      v += a.bias[n];
+      if (a.residual.ptr) v += ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n, a.dtype);
+      st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n, v, a.dtype);
+    }
+  }
+  if (cs > 1) cluster_barrier();
+}
+
+// At most eight columns. Shared memory: per warp its columns of x and their
+// (down, down * sum) pairs; [tile][warp][B][16] sums; for clusters [tile][B][16].
+template <int G, int FMT>
+__global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs a, int cs) {
+  constexpr int S = G > 64 ? G : 64, BL = S / 64, GS = S / G;
+  constexpr int kAhead = FMT == kScale32 && G == 32 ? 4 : 8 / BL;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
+  const bool split = a.dtype == SFFN_F32;
+  const int cols = split ? 2 * a.B : a.B, elems = a.B * 16;
+  // tiles of the cluster and steps of the warp: equal shares up to one
+  const int tper = a.tiles / a.clusters, trest = a.tiles % a.clusters;
+  const int tile0 = tper * cluster + min(cluster, trest), nt = tper + (cluster < trest);
+  const int slices = cs * kLinWarps, slice = rank * kLinWarps + warp, all_steps = a.kp / S;
+  const int sper = all_steps / slices, srest = all_steps % slices;
+  const int k_first = sper * slice + min(slice, srest), spt = sper + (slice < srest);
+  float* part = reinterpret_cast<float*>(smem + a.off_part);   // [tile][warp][elems]
+
+  const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + ((size_t)tile0 * (a.kp / 64) + (size_t)k_first * BL) * 32 + lane;
+  size_t sp = ((size_t)tile0 * (a.kp / G) + (size_t)k_first * GS) * 8 + g;
+  const size_t cp_skip = (size_t)(a.kp / 64 - spt * BL) * 32, sp_skip = (size_t)(a.kp / G - spt * GS) * 8;
+  const int steps = nt * spt;
+  uint4 cw[kAhead][BL];
+  ScaleWord<FMT> sw[kAhead][GS];
+  int left = steps, ld_k = 0;
+  auto load = [&](uint4* c, ScaleWord<FMT>* s) {
+    if (left > 0) {
+      --left;
+#pragma unroll
+      for (int b = 0; b < BL; ++b) c[b] = ldg_stream(cp + b * 32);
+#pragma unroll
+      for (int q = 0; q < GS; ++q) s[q].load(a, sp + q * 8);
+      cp += BL * 32;
+      sp += GS * 8;
+      if (++ld_k == spt) ld_k = 0, cp += cp_skip, sp += sp_skip;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(cw[i], sw[i]);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- the warp's share of x: runs of 128 inputs, the next one loaded while one is converted
+  __half* xs = reinterpret_cast<__half*>(smem) + (size_t)warp * cols * a.chunk_stride;
+  float2* xg = reinterpret_cast<float2*>(smem + a.off_xg) + (size_t)warp * (a.chunk / G) * 8;
+  const int k0 = k_first * S, kn = spt * S, runs = (kn + 127) / 128, tasks = runs * a.B;
+  auto fetch = [&](int b, int run, float* v) {
+    const int kk = run * 128 + lane * 4;
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+    if (kk < kn && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v);
+  };
+  float v[4], vn[4];
+  int b = 0, run = 0;
+  if (tasks > 0) fetch(0, 0, v);
+  for (int i = 0; i < tasks; ++i) {
+    const int b1 = run + 1 < runs ? b : b + 1, run1 = run + 1 < runs ? run + 1 : 0;
+    if (i + 1 < tasks) fetch(b1, run1, vn);
+    uint32_t hi[2], lo[2];
+    float sh, sl, down;
+    convert_run<G>(v, hi, lo, sh, sl, down);
+    const int kk = run * 128 + lane * 4, col = split ? 2 * b : b;
+    if (kk < kn) {
+      *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
+      if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
+      if (lane % (G / 4) == 0) {
+        float2* at = xg + (kk / G) * 8 + col;
+        at[0] = make_float2(down, down * sh);
+        if (split) at[1] = make_float2(down, down * sl);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = vn[e];
+    b = b1, run = run1;
+  }
+  __syncwarp();
+
+  // ---- steps
+  const __half* xcol[1] = {xs + (size_t)min(g, cols - 1) * a.chunk_stride + 8 * t};   // columns past the end: not used
+  float y[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  float* dst = part + (size_t)warp * elems;
+  int kk = 0;
+  for (int s = 0; s < steps;) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s < steps) {
+        linear_step<G, 1, FMT>(a, cw[i], sw[i], xcol, kk * S, xg + kk * GS * 8 + 2 * t, y);
+        load(cw[i], sw[i]);
+        ++s;
+        if (++kk == spt) {
+          store_tile<1>(dst, y, a.B, split, false, g, t);
+          y[0][0] = y[0][1] = y[0][2] = y[0][3] = 0.f;
+          dst += kLinWarps * elems;
+          kk = 0;
+        }
+      }
+    }
+  }
+  if (spt == 0)   // a warp without inputs
+    for (int i = 0; i < nt; ++i, dst += kLinWarps * elems) store_tile<1>(dst, y, a.B, split, false, g, t);
+  __syncthreads();
+
+  // ---- the block's sums, in warp order
+  float* acc_s = reinterpret_cast<float*>(smem + a.off_acc);
+  for (int e = threadIdx.x; e < nt * elems; e += kLinThreads) {
+    const int tile = e / elems;
+    const float* p = part + (size_t)tile * (kLinWarps - 1) * elems + e;
+    float r = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLinWarps; ++w) r += p[w * elems];
+    acc_s[e] = r;
+  }
+  write_outputs(a, acc_s, tile0, nt, cs, rank);
+}
 
 template <int G, int NT, int FMT>
 __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const LinearArgs a, int cs) {
@@ -137,18 +411,7 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
         for (int b = 0; b < BL; ++b) c[b] = ldg_stream(cp + b * 32);   // kp is a multiple of S
         const size_t at = (tile * groups + (size_t)(c0 + ld_k) * GS) * 8 + g;
 #pragma unroll
-        for (int q = 0; q < GS; ++q) {
-          if (FMT == kScale32) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.scales) + at + q * 8);
-            s[q].w[0] = v.x, s[q].w[1 % (sizeof(s[q].w) / 4)] = v.y;
-            uint2 z = make_uint2(0u, 0u);
-            if (a.zeros) z = __ldg(reinterpret_cast<const uint2*>(a.zeros) + at + q * 8);
-            s[q].w[2 % (sizeof(s[q].w) / 4)] = z.x, s[q].w[3 % (sizeof(s[q].w) / 4)] = z.y;
-          } else {
-            s[q].w[0] = __ldg(reinterpret_cast<const uint32_t*>(a.scales) + at + q * 8);
-            if (FMT == kScale16Zero) s[q].w[1 % (sizeof(s[q].w) / 4)] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros) + at + q * 8);
-          }
-        }
+        for (int q = 0; q < GS; ++q) s[q].load(a, at + q * 8);
         if (++ld_k == spt) ld_k = 0, ++ld_tile;
         ++ld_s;
       }
@@ -165,39 +428,33 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
       __syncthreads();   // every warp is done with the chunk before
     }
 
-    // ---- x of the chunk: one warp per token and run of 128 inputs, four inputs per lane
-    const int k0 = c0 * S, kn = spt * S, runs = (kn + 127) / 128;
-    for (int task = warp; task < a.B * runs; task += kLinWarps) {
-      const int b = task / runs, run = task % runs, kk = run * 128 + lane * 4;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (kk < kn && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v);
-      float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+    // ---- x of the chunk: one warp per token and run of 128 inputs, kBatch of them at a time
+    constexpr int kBatch = 4;
+    const int k0 = c0 * S, kn = spt * S, runs = (kn + 127) / 128, tasks = a.B * runs;
+    for (int task0 = warp; task0 < tasks; task0 += kLinWarps * kBatch) {
+      float v[kBatch][4];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
-      float up, down;
-      scale_to_half_range(big, up, down);
-      uint32_t hi[2], lo[2];
-      float sh = 0.f, sl = 0.f;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
-        const float2 fh = __half22float2(u32_h2(hi[p])), fl = __half22float2(u32_h2(lo[p]));
-        sh += fh.x + fh.y;
-        sl += fl.x + fl.y;
+      for (int i = 0; i < kBatch; ++i) {
+        const int task = task0 + i * kLinWarps, b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
+        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+        if (task < tasks && kk < kn && k0 + kk < a.k)
+          ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
       }
 #pragma unroll
-      for (int o = 1; o < (G > 128 ? 32 : G / 4); o <<= 1) {
-        sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
-        sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
-      }
-      if (kk < kn) {
-        const int col = split ? 2 * b : b;
-        *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
-        if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
-        if (lane % (G / 4) == 0) {
-          float2* at = xg + (size_t)(kk / G) * (8 * NT) + col;
-          at[0] = make_float2(down, down * sh);
-          if (split) at[1] = make_float2(down, down * sl);
+      for (int i = 0; i < kBatch; ++i) {
+        const int task = task0 + i * kLinWarps, b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
+        uint32_t hi[2], lo[2];
+        float sh, sl, down;
+        convert_run<G>(v[i], hi, lo, sh, sl, down);
+        if (task < tasks && kk < kn) {
+          const int col = split ? 2 * b : b;
+          *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
+          if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
+          if (lane % (G / 4) == 0) {
+            float2* at = xg + (size_t)(kk / G) * (8 * NT) + col;
+            at[0] = make_float2(down, down * sh);
+            if (split) at[1] = make_float2(down, down * sl);
+          }
         }
       }
     }
@@ -214,91 +471,14 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
       const int c = 8 * n + g;   // columns past the end repeat the last one; their results are not used
       xcol[n] = xs + (size_t)min(c, cols - 1) * a.chunk_stride + 8 * t;
     }
-    auto store = [&](float* dst, bool add) {   // sums of a tile, [B][16]
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (split) {
-            const int b = 4 * n + t;
-            if (b < a.B) {
-              float* p = dst + b * 16 + g + 8 * r;
-              const float v = y[n][2 * r] + y[n][2 * r + 1];
-              *p = add ? *p + v : v;
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int b = 8 * n + 2 * t + c;
-              if (b < a.B) {
-                float* p = dst + b * 16 + g + 8 * r;
-                *p = add ? *p + y[n][2 * r + c] : y[n][2 * r + c];
-              }
-            }
-          }
-        }
-      }
-    };
+    auto store = [&](float* dst, bool add) { store_tile<NT>(dst, y, a.B, split, add, g, t); };
     auto step = [&](const uint4* c, const ScaleWord<FMT>* s) {
       if (fresh) {
         fresh = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
       }
-      float d[NT][4];
-#pragma unroll
-      for (int b = 0; b < BL; ++b) {
-        const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 32 inputs
-          const uint32_t wa = w[2 * h], wb = w[2 * h + 1], ra = wa >> 8, rb = wb >> 8;
-          const uint32_t a0[4] = {weight_low(wa), weight_low(wb), weight_high(wa), weight_high(wb)};
-          const uint32_t a1[4] = {weight_low(ra), weight_low(rb), weight_high(ra), weight_high(rb)};
-          const bool begin = (b * 64 + h * 32) % G == 0;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + kk * S + b * 64 + h * 32);
-            if (begin) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-            mma_f16(d[n], a0, xv.x, xv.y);
-            mma_f16(d[n], a1, xv.z, xv.w);
-          }
-          if ((b * 64 + h * 32 + 32) % G == 0) {   // end of a group: scales
-            const int q = (b * 64 + h * 32) / G;
-            float sc[2], z[2] = {0.f, 0.f};
-            if (FMT == kScale32) {
-              sc[0] = __uint_as_float(s[q].w[0]), sc[1] = __uint_as_float(s[q].w[1 % (sizeof(s[q].w) / 4)]);
-              z[0] = __uint_as_float(s[q].w[2 % (sizeof(s[q].w) / 4)]);
-              z[1] = __uint_as_float(s[q].w[3 % (sizeof(s[q].w) / 4)]);
-            } else {
-              auto two = [&](uint32_t v, float& lo, float& hi) {
-                if (a.sdtype == SFFN_F16) {
-                  const float2 f = __half22float2(u32_h2(v));
-                  lo = f.x, hi = f.y;
-                } else {
-                  lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xffff0000u);
-                }
-              };
-              two(s[q].w[0], sc[0], sc[1]);
-              if (FMT == kScale16Zero) two(s[q].w[1 % (sizeof(s[q].w) / 4)], z[0], z[1]);
-            }
-            const float2* xq = xg + (size_t)(kk * GS + q) * (8 * NT) + 2 * t;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float4 v = *reinterpret_cast<const float4*>(xq + 8 * n);   // (down, sum) of columns 2t, 2t + 1
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                if (FMT == kScale16) {
-                  y[n][2 * r] = fmaf(sc[r], d[n][2 * r] * v.x, y[n][2 * r]);
-                  y[n][2 * r + 1] = fmaf(sc[r], d[n][2 * r + 1] * v.z, y[n][2 * r + 1]);
-                } else {
-                  y[n][2 * r] = fmaf(sc[r], fmaf(d[n][2 * r], v.x, -z[r] * v.y), y[n][2 * r]);
-                  y[n][2 * r + 1] = fmaf(sc[r], fmaf(d[n][2 * r + 1], v.z, -z[r] * v.w), y[n][2 * r + 1]);
-                }
-              }
-            }
-          }
-        }
-      }
+      linear_step<G, NT, FMT>(a, c, s, xcol, kk * S, xg + (size_t)kk * GS * (8 * NT) + 2 * t, y);
       if (++kk == spt) {
         // a tile that began in this warp's run is complete; the tail of an earlier warp's tile is a part
         if (first && first_k != 0) {
@@ -339,26 +519,7 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
     if (spt <= 0) break;
   }
 
-  // ---- the cluster's blocks add their sums; each writes its share of the outputs
-  if (cs > 1) cluster_barrier();
-  else __syncthreads();
-  const int all = nt * elems;
-  const uint32_t base = smem_u32(acc_s);
-  for (int e = threadIdx.x * cs + rank; e < all; e += kLinThreads * cs) {
-    const int tile = e / elems, b = (e % elems) / 16, n = (tile0 + tile) * 16 + e % 16;
-    float v = 0.f;
-    if (cs > 1) {
-      for (int r = 0; r < cs; ++r) v += ld_cluster(base + 4u * e, r);
-    } else {
-      v = acc_s[e];
-    }
-    if (n < a.n) {
-      v += a.bias[n];
-      if (a.residual.ptr) v += ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n, a.dtype);
-      st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n, v, a.dtype);
-    }
-  }
-  if (cs > 1) cluster_barrier();
+  write_outputs(a, acc_s, tile0, nt, cs, rank);
 }
 
 // Calls f with the kernel of a number of column tiles and a scale format.
@@ -369,8 +530,10 @@ cudaError_t with_kernel(int nt, int fmt, F&& f) {
     return fmt == kScale16 ? f(k_linear<G, NT, kScale16>)
                            : fmt == kScale16Zero ? f(k_linear<G, NT, kScale16Zero>) : f(k_linear<G, NT, kScale32>);
   };
+  if (nt == 1)
+    return fmt == kScale16 ? f(k_linear_few<G, kScale16>)
+                           : fmt == kScale16Zero ? f(k_linear_few<G, kScale16Zero>) : f(k_linear_few<G, kScale32>);
   switch (nt) {
-    case 1: return by_fmt(std::integral_constant<int, 1>());
     case 2: return by_fmt(std::integral_constant<int, 2>());
     case 4: return by_fmt(std::integral_constant<int, 4>());
     default: return by_fmt(std::integral_constant<int, 8>());
