@@ -199,8 +199,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (2.9 us a call), where this torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -403,30 +410,40 @@ def sffn_stack_destroy(stack) -> None:
 
 # ----------------------------------------------------------------- attention half: projections, cache, attention
 
+# These calls are launched once per layer and token and take a few microseconds on the device, so the marshalling
+# below asks each tensor for each property once.
+
+_NO_ROWS = RowsC()
+_IO_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
 def _rows(t, dtype=None, name="tensor") -> RowsC:
     """RowsC of a (rows, width) or (rows, heads, width) tensor, or of None."""
     if t is None:
-        return RowsC()
-    if dtype is not None and t.dtype != dtype:
+        return _NO_ROWS
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype} given, {dtype} wanted (all arrays of a call have one type)")
-    if t.dim() not in (2, 3) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    st = t.stride()
+    n = len(st)
+    if n != 3 and n != 2 or st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: two or three dimensions with a contiguous last one are wanted")
-    return RowsC(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+    return RowsC(t.data_ptr(), st[0], st[1] if n == 3 else 0)
 
 
-def _io_dtype(t) -> int:
-    if t.dtype not in TORCH_WDTYPE:
-        raise ValueError(f"{t.dtype}: float32, float16 or bfloat16 is wanted")
-    return DTYPE[TORCH_WDTYPE[t.dtype]]
+def _io_dtype(dtype) -> int:
+    d = _IO_DTYPE.get(dtype)
+    if d is None:
+        raise ValueError(f"{dtype}: float32, float16 or bfloat16 is wanted")
+    return d
 
 
 def _want(t, shape, name) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} given, {tuple(shape)} wanted")
 
 
 def _ws_args(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def make_linear_desc(in_features, out_features, group, scale_dtype, has_zero=False, max_batch=1) -> LinearDesc:
@@ -462,12 +479,16 @@ def sffn_linear_workspace_bytes(linear, B: int) -> int:
 
 def sffn_linear_forward(linear, x, y, residual=None, ws=None, stream=None) -> None:
     """y (B, out) = x (B, in) through the layer, plus residual (B, out) if given (it may be y itself)."""
-    _want(residual, y.shape, "residual")
-    if y.shape[0] != x.shape[0]:
+    B, dtype, shape = x.shape[0], x.dtype, y.shape
+    if shape[0] != B:
         raise ValueError("x and y differ in their number of rows")
-    _check(_lib.sffn_linear_forward(linear, _rows(x, None, "x"), x.shape[0], _rows(residual, x.dtype, "residual"),
-                                    _rows(y, x.dtype, "y"), _io_dtype(x), *_ws_args(ws), _stream(stream)),
-           "sffn_linear_forward")
+    if residual is not None and residual.shape != shape:
+        _want(residual, shape, "residual")
+    ws_ptr, ws_bytes = _ws_args(ws)
+    rc = _lib.sffn_linear_forward(linear, _rows(x, None, "x"), B, _rows(residual, dtype, "residual"),
+                                  _rows(y, dtype, "y"), _io_dtype(dtype), ws_ptr, ws_bytes, _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_linear_forward")
 
 
 def sffn_linear_destroy(linear) -> None:
@@ -507,32 +528,47 @@ def sffn_kv_destroy(kv) -> None:
     _lib.sffn_kv_destroy(kv)
 
 
+def _token_rows(t, n, name) -> None:
+    if t.shape[0] != n:
+        raise ValueError(f"{name}: {t.shape[0]} rows given, {n} wanted")
+
+
 def sffn_kv_append(kv, batch: "KvBatch", q, k, v, q_out=None, rope: "Rope | None" = None, stream=None) -> None:
     """Append k, v (tokens, kv heads, dim); rotate q (tokens, heads, dim) into q_out if q is not None."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
-        if t is not None and t.shape[0] != batch.c.n_tokens:
-            raise ValueError(f"{name}: {t.shape[0]} rows given, {batch.c.n_tokens} wanted")
-    _want(v, k.shape, "v")
+    n, dtype, shape, n_q_heads = batch.n_tokens, k.dtype, k.shape, 0
+    if shape[0] != n:
+        _token_rows(k, n, "k")
+    if v.shape != shape:
+        _want(v, shape, "v")
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is required with q")
-        _want(q_out, q.shape, "q_out")
+        q_shape = q.shape
+        if q_shape[0] != n:
+            _token_rows(q, n, "q")
+        if q_out.shape != q_shape:
+            _want(q_out, q_shape, "q_out")
+        n_q_heads = q_shape[1]
     if rope is not None and rope.positions is not None:
-        _want(rope.positions, (batch.c.n_tokens,), "positions")
-    _check(_lib.sffn_kv_append(kv, ctypes.byref(batch.c), _rows(q, k.dtype, "q"), 0 if q is None else q.shape[1],
-                               _rows(k, k.dtype, "k"), _rows(v, k.dtype, "v"), _rows(q_out, k.dtype, "q_out"),
-                               None if rope is None else ctypes.byref(rope.c), _io_dtype(k), _stream(stream)),
-           "sffn_kv_append")
+        _want(rope.positions, (n,), "positions")
+    rc = _lib.sffn_kv_append(kv, batch.ref, _rows(q, dtype, "q"), n_q_heads, _rows(k, None, "k"),
+                             _rows(v, dtype, "v"), _rows(q_out, dtype, "q_out"), None if rope is None else rope.ref,
+                             _io_dtype(dtype), _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_kv_append")
 
 
 def sffn_kv_gather(kv, batch: "KvBatch", k_out, v_out, stream=None) -> None:
     """Values the cache holds for the batch's tokens; either output may be None."""
-    one = k_out if k_out is not None else v_out
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.shape[0] != batch.c.n_tokens:
-            raise ValueError(f"{name}: {t.shape[0]} rows given, {batch.c.n_tokens} wanted")
-    _check(_lib.sffn_kv_gather(kv, ctypes.byref(batch.c), _rows(k_out, one.dtype, "k_out"),
-                               _rows(v_out, one.dtype, "v_out"), _io_dtype(one), _stream(stream)), "sffn_kv_gather")
+    dtype = (k_out if k_out is not None else v_out).dtype
+    if k_out is not None:
+        _token_rows(k_out, batch.n_tokens, "k_out")
+    if v_out is not None:
+        _token_rows(v_out, batch.n_tokens, "v_out")
+    rc = _lib.sffn_kv_gather(kv, batch.ref, _rows(k_out, dtype, "k_out"), _rows(v_out, dtype, "v_out"),
+                             _io_dtype(dtype), _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_kv_gather")
 
 
 def sffn_attend_workspace_bytes(kv, n_q_heads: int, n_seq: int, n_tokens: int) -> int:
@@ -541,14 +577,23 @@ def sffn_attend_workspace_bytes(kv, n_q_heads: int, n_seq: int, n_tokens: int) -
 
 def sffn_attend(kv, batch: "KvBatch", q, out, lse, scale, window=0, ws=None, stream=None) -> None:
     """out (tokens, heads, dim) = attention of q over the cache; lse (tokens, heads) float32 or None."""
-    if q.shape[0] != batch.c.n_tokens:
-        raise ValueError(f"q: {q.shape[0]} rows given, {batch.c.n_tokens} wanted")
-    _want(out, q.shape, "out")
-    _want(lse, q.shape[:2], "lse")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse: a contiguous float32 tensor is wanted")
-    _check(_lib.sffn_attend(kv, ctypes.byref(batch.c), _rows(q, None, "q"), q.shape[1], _rows(out, q.dtype, "out"),
-                            _ptr(lse), scale, window, _io_dtype(q), *_ws_args(ws), _stream(stream)), "sffn_attend")
+    shape, dtype = q.shape, q.dtype
+    if shape[0] != batch.n_tokens:
+        _token_rows(q, batch.n_tokens, "q")
+    if out.shape != shape:
+        _want(out, shape, "out")
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != shape[:2]:
+            _want(lse, shape[:2], "lse")
+        if lse.dtype is not torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse: a contiguous float32 tensor is wanted")
+        lse_ptr = lse.data_ptr()
+    ws_ptr, ws_bytes = _ws_args(ws)
+    rc = _lib.sffn_attend(kv, batch.ref, _rows(q, None, "q"), shape[1], _rows(out, dtype, "out"), lse_ptr, scale,
+                          window, _io_dtype(dtype), ws_ptr, ws_bytes, _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_attend")
 
 
 # ----------------------------------------------------------------- TAM calls
@@ -874,8 +919,9 @@ class KvBatch:
         stride = table.stride(0) if n_seq > 1 else table.shape[1]
         if stride < table.shape[1]:
             raise ValueError("table: rows must not overlap")
-        self.c = KvBatchC(_ptr(table), _ptr(kv_len), _ptr(q_start), n_seq, n_seq if n_tokens is None else n_tokens,
-                          stride)
+        self.n_tokens = n_seq if n_tokens is None else n_tokens
+        self.c = KvBatchC(_ptr(table), _ptr(kv_len), _ptr(q_start), n_seq, self.n_tokens, stride)
+        self.ref = ctypes.byref(self.c)
 
 
 class Rope:
@@ -892,6 +938,7 @@ class Rope:
             raise ValueError("positions: a contiguous int32 tensor is wanted")
         self.table, self.positions = table, positions
         self.c = RopeC(_ptr(table), _ptr(positions), table.shape[0], 2 * table.shape[1], self.STYLE[style])
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def of_base(cls, length, dim, base=10000.0, style="halves", device="cuda") -> "Rope":
