@@ -100,6 +100,7 @@ sffn_status sffn_linear_create(const sffn_linear_desc* d, sffn_linear** out) {
   if (e == cudaSuccess && d->has_zero) e = cudaMalloc(&L->zeros, vals);
   if (e == cudaSuccess) e = cudaMalloc(&L->bias, (size_t)L->tiles * 16 * 4);
   if (e == cudaSuccess) e = cudaMalloc(&L->err, 256);
+  if (e == cudaSuccess) e = cudaMemset(L->err, 0, 256);
   if (e == cudaSuccess) e = configure_linear_kernels(*L);
   if (e != cudaSuccess) {
     rc = cuda_fail(e, "sffn_linear_create");
@@ -150,6 +151,11 @@ sffn_status sffn_linear_forward(const sffn_linear* L, sffn_rows x, int32_t B, sf
   rc = check_device(L->device);
   if (rc != SFFN_OK) return rc;
   return launched(launch_linear(*L, x, B, residual, y, dtype, ws, (cudaStream_t)stream), "sffn_linear_forward");
+}
+
+sffn_status sffn_linear_check_error(const sffn_linear* L, sffn_stream stream) {
+  if (!L) return invalid("linear is NULL");
+  return read_error_word(L->err, (cudaStream_t)stream);
 }
 
 void sffn_linear_destroy(sffn_linear* L) {

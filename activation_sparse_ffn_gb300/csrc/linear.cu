@@ -112,13 +112,31 @@ cudaError_t configure_linear_kernels(sffn_linear& L) {
   return e;
 }
 
-size_t linear_ws_bytes(const sffn_linear&, int) { return 0; }
+namespace {
+
+// x as halves and its pairs, for the kernel of more than eight columns.
+struct LinearWs {
+  size_t pairs, total;
+};
+LinearWs linear_ws(const sffn_linear& L, int B, int dtype) {
+  const int nt = column_tiles(B, dtype), cols = dtype == SFFN_F32 ? 2 * B : B;
+  if (nt == 1) return LinearWs{0, 0};
+  LinearWs w;
+  w.pairs = ((size_t)cols * L.kp * 2 + 255) / 256 * 256;
+  w.total = w.pairs + (size_t)(L.kp / L.desc.group) * 8 * nt * sizeof(float2);
+  return w;
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(const sffn_linear& L, int B) { return linear_ws(L, B, SFFN_F32).total; }
 
 cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const sffn_rows& residual,
                           const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
-  (void)ws;
   LinearArgs a = {};
-  a.codes = L.codes, a.scales = L.scales, a.zeros = L.zeros, a.bias = L.bias;
+  a.codes = L.codes, a.scales = L.scales, a.zeros = L.zeros, a.bias = L.bias, a.err = L.err;
+  a.ws_x = static_cast<const __half*>(ws);
+  a.ws_xg = reinterpret_cast<const float2*>(static_cast<const uint8_t*>(ws) + linear_ws(L, B, dtype).pairs);
   a.n = L.desc.out_features, a.k = L.desc.in_features, a.kp = L.kp, a.B = B, a.dtype = dtype;
   a.sdtype = L.desc.scale_dtype, a.tiles = L.tiles, a.x = x, a.residual = residual, a.y = y;
   const int G = L.desc.group, S = std::max(G, 64), steps = a.kp / S;
@@ -128,8 +146,8 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
   const int xpair = 8 * nt * 8;   // bytes of the (scale, sum) pairs of a group of inputs
   int smem = 0, ci = 3;
   if (nt == 1) {
-    // The split of the inputs that gives a block the least to read; a cluster costs two barriers and a pass over
-    // its sums, about what 64 KB take.
+    // The split of the inputs that gives a block the least to do, in bytes of codes that take as long: a cluster
+    // costs two barriers and a pass over its sums, about 64 KB; a run of 128 inputs of a token costs its warp 4 KB.
     long long best = -1;
     for (int c = 0; c < 4; ++c) {
       const int slices = kLinWarps << c;
@@ -142,10 +160,11 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
         const int fit = std::max(1, large ? L.fit_large[0][c] : L.fit_small[0][c]);
         const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + room / per_tile - 1) / (room / per_tile));
         const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
-        const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + (c ? 64 * 1024 : 0);
+        const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + (c ? 64 * 1024 : 0) +
+                               (long long)(own128 / 128) * B * 4 * 1024;
         if (best >= 0 && cost >= best) break;
         best = cost, ci = c;
-        a.clusters = clusters, a.chunk = own128, a.chunk_stride = own128 + 32, a.max_tiles = most;
+        a.clusters = clusters, a.chunk = own128, a.chunk_stride = own128 + 32;
         a.off_xg = up16(kLinWarps * cols * a.chunk_stride * 2);
         a.off_part = up16(a.off_xg + kLinWarps * (own128 / G) * xpair);
         a.off_acc = a.off_part + most * kLinWarps * elems * 4;
@@ -154,28 +173,27 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
       }
     }
   } else {
-    // a block has at least 512 inputs, so that converting x and adding sums stay small beside its steps
-    while (ci > 0 && (steps * S) >> ci < 512) --ci;
-    const int cs = 1 << ci, own = (steps + cs - 1) / cs * S;   // inputs of a block
-    // Two small blocks per SM hide each other's latencies; a large one holds more of x at a time. Sums of at most
-    // 40 KB of tiles are kept, which bounds the tiles of a cluster.
-    const int most = std::max(1, 40 * 1024 / (elems * 4));
-    for (int large = 0; large < 2; ++large) {
-      const int fit = std::max(1, large ? L.fit_large[nti][ci] : L.fit_small[nti][ci]);
-      a.clusters = std::max(std::min(a.tiles, fit), (a.tiles + most - 1) / most);
-      a.max_tiles = (a.tiles + a.clusters - 1) / a.clusters;
-      const int fixed = a.max_tiles * elems * 4 + 2 * kLinWarps * elems * 4;
-      const int room = (large ? kLinLarge : kLinSmall) - fixed - 64;
+    // The split that gives an SM the least to read, among those that keep 40 KB of sums; chunks of x as large as
+    // fit, a barrier between them costs about 8 KB.
+    const int warps = linear_warps(nt), most_tiles = std::max(1, 40 * 1024 / (elems * 4));
+    long long best = -1;
+    for (int c = 0; c < 4; ++c) {
+      const int own = (steps + (1 << c) - 1) / (1 << c) * S, fit = std::max(1, L.fit_large[nti][c]);
+      const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + most_tiles - 1) / most_tiles);
+      const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
+      const int room = kLinLarge - (most + 2 * warps) * elems * 4 - 64;
       const int per128 = cols * 256 + 128 / G * xpair, pad = cols * 64;
       const int runs = std::min((own + 127) / 128, (room - pad) / per128);
-      if (runs < 1 || (!large && runs < std::min(4, (own + 127) / 128))) continue;
-      a.chunk = runs * 128;
-      a.chunk_stride = a.chunk + 32;
+      if (runs < 1) continue;
+      const int chunks = (own + runs * 128 - 1) / (runs * 128);
+      const long long cost = ((long long)most * 8 * own + chunks * 8 * 1024) * waves + (c ? 64 * 1024 : 0);
+      if (best >= 0 && cost >= best) continue;
+      best = cost, ci = c;
+      a.clusters = clusters, a.chunk = runs * 128, a.chunk_stride = a.chunk + 32;
       a.off_xg = up16(cols * a.chunk_stride * 2);
       a.off_acc = up16(a.off_xg + a.chunk / G * xpair);
-      a.off_part = up16(a.off_acc + a.max_tiles * elems * 4);
-      smem = a.off_part + 2 * kLinWarps * elems * 4;
-      break;
+      a.off_part = up16(a.off_acc + most * elems * 4);
+      smem = a.off_part + 2 * warps * elems * 4;
     }
   }
   const int cs = 1 << ci, blocks = a.clusters * cs;

@@ -21,7 +21,9 @@
 // too, each goes over all tiles with the same share of x, which it converts for
 // itself, and leaves one sum per tile and warp: no barrier before the end.
 //   More columns (k_linear): those sums would not fit, so the (tile, run of
-// inputs) steps are numbered through and each warp takes an equal run of them.
+// inputs) steps are numbered through and each warp takes an equal run of them;
+// x is converted once for all blocks by a small kernel before (k_linear_x),
+// because every cluster would convert the same numbers again.
 #pragma once
 
 #include <type_traits>
@@ -37,16 +39,20 @@ struct LinearArgs {
   const void* scales;
   const void* zeros;
   const float* bias;
+  uint32_t* err;
   int n, k, kp, B, dtype, sdtype;
   int tiles;        // 16-row tiles
   int clusters, chunk, chunk_stride;   // inputs of x held at a time (a multiple of 128), halves of a row of xs
-  int max_tiles;    // of a cluster
   int off_xg, off_acc, off_part;       // bytes in shared memory
+  const __half* ws_x;    // k_linear: x as halves [columns][kp], and
+  const float2* ws_xg;   // its (down, down * sum) pairs [groups][8 NT]
   sffn_rows x, residual, y;
 };
 
-constexpr int kLinWarps = 8;
+constexpr int kLinWarps = 8;                   // of a block of k_linear_few
 constexpr int kLinThreads = kLinWarps * 32;
+// Of a block of k_linear: one block per SM, as many warps as 64 accumulators per thread leave registers for.
+constexpr int linear_warps(int nt) { return nt == 8 ? 8 : 16; }
 
 // Scale formats: 16-bit scales, 16-bit scales and zeros, 32-bit scales (and zeros if given).
 enum { kScale16 = 0, kScale16Zero = 1, kScale32 = 2 };
@@ -78,11 +84,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t smem_addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster(uint32_t smem_addr, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
 
@@ -177,28 +183,51 @@ __device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4* c,
   }
 }
 
-// Four inputs of a lane (of a run of 128 that one warp converts together) as
-// halves: the nearest in hi, what is left in lo, both times a power of two; sums
-// over a group of G of either; `down` undoes the power of two.
-template <int G>
-__device__ __forceinline__ void convert_run(const float* v, uint32_t* hi, uint32_t* lo, float& sh, float& sl, float& down) {
-  float big = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+// N runs of 128 inputs that one warp converts together, four inputs of each per
+// lane, as halves: the nearest in hi, what is left in lo (fp32 rows only), both
+// times a power of two that `down` undoes; f16 rows are taken as they are. With
+// Sums, the sums of hi and lo over a group of G.
+template <int G, int N, bool Sums>
+__device__ __forceinline__ void convert_runs(const float (*v)[4], int dtype, uint32_t (*hi)[2], uint32_t (*lo)[2],
+                                             float* sh, float* sl, float* down) {
+  float up[N];
+  if (dtype == SFFN_F16) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
-  float up;
-  scale_to_half_range(big, up, down);
-  sh = sl = 0.f;
+    for (int i = 0; i < N; ++i) up[i] = down[i] = 1.f;
+  } else {
+    float big[N];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
-    const float2 fh = __half22float2(u32_h2(hi[p])), fl = __half22float2(u32_h2(lo[p]));
-    sh += fh.x + fh.y;
-    sl += fl.x + fl.y;
+    for (int i = 0; i < N; ++i)
+      big[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) big[i] = fmaxf(big[i], __shfl_xor_sync(SFFN_FULL_MASK, big[i], o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) scale_to_half_range(big[i], up[i], down[i]);
   }
 #pragma unroll
-  for (int o = 1; o < G / 4; o <<= 1) {
-    sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
-    sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) split_f16(v[i][2 * p] * up[i], v[i][2 * p + 1] * up[i], hi[i][p], lo[i][p]);
+  if (Sums) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 a = __half22float2(u32_h2(hi[i][0])), b = __half22float2(u32_h2(hi[i][1]));
+      const float2 c = __half22float2(u32_h2(lo[i][0])), d = __half22float2(u32_h2(lo[i][1]));
+      sh[i] = (a.x + a.y) + (b.x + b.y);
+      sl[i] = (c.x + c.y) + (d.x + d.y);
+    }
+#pragma unroll
+    for (int o = 1; o < G / 4; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        sh[i] += __shfl_xor_sync(SFFN_FULL_MASK, sh[i], o);
+        sl[i] += __shfl_xor_sync(SFFN_FULL_MASK, sl[i], o);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh[i] = sl[i] = 0.f;
   }
 }
 
@@ -230,28 +259,35 @@ __device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], int 
 }
 
 // Adds the sums acc_s (nt tiles, [B][16] each) of the cluster's blocks; every
-// block writes its share of the outputs.
-__device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* acc_s, int tile0, int nt, int cs, int rank) {
-  const int elems = a.B * 16, all = nt * elems;
+// block writes a contiguous share of the outputs, four rows per thread.
+__device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* acc_s, int tile0, int nt, int cs, int rank,
+                                              int threads) {
+  const int quads = a.B * 4, all = nt * quads, share = (all + cs - 1) / cs;
   const uint32_t base = smem_u32(acc_s);
   if (cs > 1) cluster_barrier();
-  for (int e = threadIdx.x * cs + rank; e < all; e += kLinThreads * cs) {
-    const int tile = e / elems, in = e - tile * elems, b = in >> 4, n = (tile0 + tile) * 16 + (in & 15);
-    float v = 0.f;
+  for (int e = rank * share + threadIdx.x; e < min(all, (rank + 1) * share); e += threads) {
+    const int tile = e / quads, in = e - tile * quads, b = in >> 2, n = (tile0 + tile) * 16 + (in & 3) * 4;
+    float4 v = *reinterpret_cast<const float4*>(a.bias + n);   // padded to whole tiles
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.residual.ptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.n) r[i] = ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n + i, a.dtype);
+    }
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (cs > 1) {
-      float p[8];
+      float4 p[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) p[r] = r < cs ? ld_cluster(base + 4u * e, r) : 0.f;
+      for (int k = 0; k < 8; ++k) p[k] = k < cs ? ld_cluster(base + 16u * e, k) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) v += p[r];
+      for (int k = 0; k < 8; ++k) s.x += p[k].x, s.y += p[k].y, s.z += p[k].z, s.w += p[k].w;
     } else {
-      v = acc_s[e];
+      s = *reinterpret_cast<const float4*>(acc_s + 4 * e);
     }
-    if (n < a.n) {
-      v += a.bias[n];
-      if (a.residual.ptr) v += ld_elem(a.residual.ptr, (size_t)(b * a.residual.row_stride) + n, a.dtype);
-      st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n, v, a.dtype);
-    }
+    const float o[4] = {s.x + v.x + r[0], s.y + v.y + r[1], s.z + v.z + r[2], s.w + v.w + r[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.n) st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n + i, o[i], a.dtype);
   }
   if (cs > 1) cluster_barrier();
 }
@@ -299,37 +335,37 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the warp's share of x: runs of 128 inputs, the next one loaded while one is converted
+  // ---- the warp's share of x, kBatch runs of 128 inputs at a time
+  constexpr int kBatch = 4;
   __half* xs = reinterpret_cast<__half*>(smem) + (size_t)warp * cols * a.chunk_stride;
   float2* xg = reinterpret_cast<float2*>(smem + a.off_xg) + (size_t)warp * (a.chunk / G) * 8;
   const int k0 = k_first * S, kn = spt * S, runs = (kn + 127) / 128, tasks = runs * a.B;
-  auto fetch = [&](int b, int run, float* v) {
-    const int kk = run * 128 + lane * 4;
-    v[0] = v[1] = v[2] = v[3] = 0.f;
-    if (kk < kn && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v);
-  };
-  float v[4], vn[4];
-  int b = 0, run = 0;
-  if (tasks > 0) fetch(0, 0, v);
-  for (int i = 0; i < tasks; ++i) {
-    const int b1 = run + 1 < runs ? b : b + 1, run1 = run + 1 < runs ? run + 1 : 0;
-    if (i + 1 < tasks) fetch(b1, run1, vn);
-    uint32_t hi[2], lo[2];
-    float sh, sl, down;
-    convert_run<G>(v, hi, lo, sh, sl, down);
-    const int kk = run * 128 + lane * 4, col = split ? 2 * b : b;
-    if (kk < kn) {
-      *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
-      if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
+  for (int task = 0, b = 0, run = 0; task < tasks; task += kBatch) {
+    float v[kBatch][4], sh[kBatch], sl[kBatch], down[kBatch];
+    uint32_t hi[kBatch][2], lo[kBatch][2];
+    int at[kBatch], bs[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int kk = run * 128 + lane * 4;
+      at[i] = task + i < tasks && kk < kn ? kk : -1;
+      bs[i] = b;
+      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+      if (at[i] >= 0 && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
+      if (++run == runs) run = 0, ++b;
+    }
+    convert_runs<G, kBatch, FMT != kScale16>(v, a.dtype, hi, lo, sh, sl, down);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (at[i] < 0) continue;
+      const int col = split ? 2 * bs[i] : bs[i];
+      *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + at[i]) = make_uint2(hi[i][0], hi[i][1]);
+      if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + at[i]) = make_uint2(lo[i][0], lo[i][1]);
       if (lane % (G / 4) == 0) {
-        float2* at = xg + (kk / G) * 8 + col;
-        at[0] = make_float2(down, down * sh);
-        if (split) at[1] = make_float2(down, down * sl);
+        float2* p = xg + (at[i] / G) * 8 + col;
+        p[0] = make_float2(down[i], down[i] * sh[i]);
+        if (split) p[1] = make_float2(down[i], down[i] * sl[i]);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = vn[e];
-    b = b1, run = run1;
   }
   __syncwarp();
 
@@ -368,11 +404,37 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
     for (int w = 0; w < kLinWarps; ++w) r += p[w * elems];
     acc_s[e] = r;
   }
-  write_outputs(a, acc_s, tile0, nt, cs, rank);
+  __syncthreads();
+  write_outputs(a, acc_s, tile0, nt, cs, rank, kLinThreads);
+}
+
+// x of a call as halves, and its pairs, for k_linear: one warp per token and run of 128 inputs.
+template <int G, int FMT>
+__global__ void __launch_bounds__(256) k_linear_x(const LinearArgs a, int pairs, __half* xh, float2* xg) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, runs = (a.kp + 127) / 128, task = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (task >= a.B * runs) return;
+  const int b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
+  float v[1][4] = {{0.f, 0.f, 0.f, 0.f}}, sh[1], sl[1], down[1];
+  uint32_t hi[1][2], lo[1][2];
+  if (kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + kk, a.dtype, v[0]);
+  convert_runs<G, 1, FMT != kScale16>(v, a.dtype, hi, lo, sh, sl, down);
+  if (kk >= a.kp) return;
+  const bool split = a.dtype == SFFN_F32;
+  const int col = split ? 2 * b : b;
+  *reinterpret_cast<uint2*>(xh + (size_t)col * a.kp + kk) = make_uint2(hi[0][0], hi[0][1]);
+  if (split) *reinterpret_cast<uint2*>(xh + (size_t)(col + 1) * a.kp + kk) = make_uint2(lo[0][0], lo[0][1]);
+  if (lane % (G / 4) == 0) {
+    float2* p = xg + (size_t)(kk / G) * pairs + col;
+    p[0] = make_float2(down[0], down[0] * sh[0]);
+    if (split) p[1] = make_float2(down[0], down[0] * sl[0]);
+  }
 }
 
 template <int G, int NT, int FMT>
-__global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const LinearArgs a, int cs) {
+__global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const LinearArgs a, int cs) {
+  constexpr int kWarps = linear_warps(NT), kThreads = kWarps * 32;
   constexpr int S = G > 64 ? G : 64;        // inputs of a step
   constexpr int BL = S / 64, GS = S / G;    // 64-input blocks and groups of a step
   constexpr int kAhead = FMT == kScale32 && G == 32 ? 4 : 8 / BL;   // by registers
@@ -381,7 +443,8 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
   float2* xg = reinterpret_cast<float2*>(smem + a.off_xg);       // [groups of a chunk][8 NT]: down, down * sum(x)
   float* acc_s = reinterpret_cast<float*>(smem + a.off_acc);     // [tiles of the cluster][B][16]
   float* part = reinterpret_cast<float*>(smem + a.off_part);     // [warp][2][B][16]
-  __shared__ int s_tile[kLinWarps][2];                           // tile of a part, -1: none
+  __shared__ int s_tile[kWarps][2];                              // tile of a part, -1: none
+  __shared__ uint64_t s_bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
   const int tile0 = (int)((long long)cluster * a.tiles / a.clusters);
@@ -394,10 +457,11 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
   const int chunk_steps = a.chunk / S;
   const int groups = a.kp / G, blocks64 = a.kp / 64;
 
+  uint32_t phase = 0;
   for (int c0 = k_step0; c0 < k_step1 || c0 == k_step0; c0 += chunk_steps) {
     const int spt = min(chunk_steps, k_step1 - c0);   // steps of a tile in this chunk
     const int steps = nt * max(spt, 0);
-    const int s0 = steps * warp / kLinWarps, s1 = steps * (warp + 1) / kLinWarps;
+    const int s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;
 
     // ---- the first loads of codes and scales: these do not depend on an earlier kernel
     uint4 cw[kAhead][BL];
@@ -420,45 +484,30 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
     for (int i = 0; i < kAhead; ++i) load(cw[i], sw[i]);
 
     if (c0 == k_step0) {
+      if (threadIdx.x == 0) mbar_init(&s_bar, 1);
+      fence_mbar_init();
       pdl_launch_dependents();
       pdl_wait();
-      for (int i = threadIdx.x; i < nt * elems; i += kLinThreads) acc_s[i] = 0.f;
-      if (threadIdx.x < 2 * kLinWarps) (&s_tile[0][0])[threadIdx.x] = -1;
-    } else {
-      __syncthreads();   // every warp is done with the chunk before
+      for (int i = threadIdx.x; i < nt * elems; i += kThreads) acc_s[i] = 0.f;
+      if (threadIdx.x < 2 * kWarps) (&s_tile[0][0])[threadIdx.x] = -1;
     }
+    __syncthreads();   // every warp is done with the chunk before
 
-    // ---- x of the chunk: one warp per token and run of 128 inputs, kBatch of them at a time
-    constexpr int kBatch = 4;
-    const int k0 = c0 * S, kn = spt * S, runs = (kn + 127) / 128, tasks = a.B * runs;
-    for (int task0 = warp; task0 < tasks; task0 += kLinWarps * kBatch) {
-      float v[kBatch][4];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int task = task0 + i * kLinWarps, b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
-        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-        if (task < tasks && kk < kn && k0 + kk < a.k)
-          ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int task = task0 + i * kLinWarps, b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
-        uint32_t hi[2], lo[2];
-        float sh, sl, down;
-        convert_run<G>(v[i], hi, lo, sh, sl, down);
-        if (task < tasks && kk < kn) {
-          const int col = split ? 2 * b : b;
-          *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
-          if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
-          if (lane % (G / 4) == 0) {
-            float2* at = xg + (size_t)(kk / G) * (8 * NT) + col;
-            at[0] = make_float2(down, down * sh);
-            if (split) at[1] = make_float2(down, down * sl);
-          }
-        }
-      }
+    // ---- x of the chunk: a bulk copy per column, and one for the pairs
+    if (warp == 0 && spt > 0) {
+      const uint32_t row = (uint32_t)spt * S * 2, pair = (uint32_t)spt * GS * 8 * NT * 8;
+      if (lane == 0) mbar_arrive_expect_tx(&s_bar, row * cols + pair);
+      __syncwarp();
+      const uint64_t pol = l2_policy_keep();
+      for (int c = lane; c < cols; c += 32)
+        bulk_g2s(xs + (size_t)c * a.chunk_stride, a.ws_x + (size_t)c * a.kp + (size_t)c0 * S, row, &s_bar, pol);
+      if (lane == 0) bulk_g2s(xg, a.ws_xg + (size_t)c0 * GS * 8 * NT, pair, &s_bar, pol);
     }
-    __syncthreads();
+    if (spt > 0 && !mbar_wait_bounded(&s_bar, phase)) {
+      set_device_error(a.err, SFFN_ERR_TIMEOUT);
+      mbar_wait_bounded(&s_bar, phase);   // the copies must land before the block ends
+    }
+    phase ^= 1;
 
     // ---- the warp's steps
     float y[NT][4];
@@ -509,17 +558,17 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 4 ? 2 : 1) k_linear(const L
     }
     __syncthreads();
     // parts in warp order; a thread keeps to its elements, so no barrier is needed between them
-    for (int e = threadIdx.x; e < elems; e += kLinThreads)
-      for (int p = 0; p < 2 * kLinWarps; ++p) {
+    for (int e = threadIdx.x; e < elems; e += kThreads)
+      for (int p = 0; p < 2 * kWarps; ++p) {
         const int pt = (&s_tile[0][0])[p];
         if (pt >= 0) acc_s[(size_t)pt * elems + e] += part[(size_t)p * elems + e];
       }
     __syncthreads();
-    if (threadIdx.x < 2 * kLinWarps) (&s_tile[0][0])[threadIdx.x] = -1;
+    if (threadIdx.x < 2 * kWarps) (&s_tile[0][0])[threadIdx.x] = -1;
     if (spt <= 0) break;
   }
 
-  write_outputs(a, acc_s, tile0, nt, cs, rank);
+  write_outputs(a, acc_s, tile0, nt, cs, rank, kThreads);
 }
 
 // Calls f with the kernel of a number of column tiles and a scale format.
@@ -548,7 +597,7 @@ cudaError_t prepare(int nt, int fmt, LinearFit* fit) {
       const int c = 1 << (i / 2);
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(c);
-      cfg.blockDim = dim3(kLinThreads);
+      cfg.blockDim = dim3(nt == 1 ? kLinThreads : linear_warps(nt) * 32);
       cfg.dynamicSmemBytes = i % 2 ? kLinLarge : kLinSmall;
       cudaLaunchAttribute at;
       at.id = cudaLaunchAttributeClusterDimension;
@@ -564,8 +613,15 @@ cudaError_t prepare(int nt, int fmt, LinearFit* fit) {
 
 template <int G>
 cudaError_t run(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st) {
+  if (nt > 1) {
+    auto* kx = fmt == kScale16 ? k_linear_x<G, kScale16> : k_linear_x<G, kScale32>;   // sums only where there are zeros
+    const cudaError_t e = launch_ex(kx, dim3((a.B * ((a.kp + 127) / 128) + 7) / 8), dim3(256), 0, st, true, 1, a, 8 * nt,
+                                    const_cast<__half*>(a.ws_x), const_cast<float2*>(a.ws_xg));
+    if (e != cudaSuccess) return e;
+  }
   return with_kernel<G>(nt, fmt, [&](auto* kern) {
-    return launch_ex(kern, dim3(blocks), dim3(kLinThreads), smem, st, true, cluster, a, cluster);
+    return launch_ex(kern, dim3(blocks), dim3(nt == 1 ? kLinThreads : linear_warps(nt) * 32), smem, st, true, cluster, a,
+                     cluster);
   });
 }
 

@@ -148,6 +148,7 @@ _sig("sffn_linear_pack", _c, _vp, _vp, _vp, _vp, _vp, _vp)
 _sig("sffn_linear_get_desc", _c, _vp, _P(LinearDesc))
 _sig("sffn_linear_workspace_bytes", _size, _vp, _i32)
 _sig("sffn_linear_forward", _c, _vp, RowsC, _i32, RowsC, RowsC, _i32, _vp, _size, _vp)
+_sig("sffn_linear_check_error", _c, _vp, _vp)
 _sig("sffn_linear_destroy", None, _vp)
 _sig("sffn_kv_validate", _c, _P(KvDesc))
 _sig("sffn_kv_bytes", _size, _P(KvDesc))
@@ -172,7 +173,7 @@ EXPORTS = [
     "tam_adapt", "tam_get_state", "tam_set_state", "tam_get_shape", "tam_check_error", "tam_destroy",
     "sffn_selftest_wait_timeout",
     "sffn_linear_validate", "sffn_linear_create", "sffn_linear_pack", "sffn_linear_get_desc",
-    "sffn_linear_workspace_bytes", "sffn_linear_forward", "sffn_linear_destroy",
+    "sffn_linear_workspace_bytes", "sffn_linear_forward", "sffn_linear_check_error", "sffn_linear_destroy",
     "sffn_kv_validate", "sffn_kv_bytes", "sffn_kv_create", "sffn_kv_get_desc", "sffn_kv_check_error",
     "sffn_kv_destroy", "sffn_kv_append", "sffn_kv_gather", "sffn_attend_workspace_bytes", "sffn_attend",
 ]
@@ -489,6 +490,10 @@ def sffn_linear_forward(linear, x, y, residual=None, ws=None, stream=None) -> No
                                   _rows(y, dtype, "y"), _io_dtype(dtype), ws_ptr, ws_bytes, _stream(stream))
     if rc:
         raise SffnError(rc, "sffn_linear_forward")
+
+
+def sffn_linear_check_error(linear, stream=None) -> None:
+    _check(_lib.sffn_linear_check_error(linear, _stream(stream)), "sffn_linear_check_error")
 
 
 def sffn_linear_destroy(linear) -> None:
@@ -857,6 +862,9 @@ class Linear:
 
     def workspace(self, B=1, device="cuda") -> torch.Tensor:
         return torch.empty(max(256, sffn_linear_workspace_bytes(self.handle, B)), dtype=torch.uint8, device=device)
+
+    def check_error(self, stream=None) -> None:
+        sffn_linear_check_error(self.handle, stream)
 
     def close(self) -> None:
         if getattr(self, "handle", None):

@@ -543,6 +543,9 @@ size_t sffn_linear_workspace_bytes(const sffn_linear* linear, int32_t B);
  * Errors: INVALID_ARG (also: not packed), CUDA. */
 sffn_status sffn_linear_forward(const sffn_linear* linear, sffn_rows x, int32_t B, sffn_rows residual, sffn_rows y,
                                 int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);
+/* Synchronize the stream, then read and clear the layer's device error word
+ * (TIMEOUT: a bounded wait ran out). */
+sffn_status sffn_linear_check_error(const sffn_linear* linear, sffn_stream stream);
 void sffn_linear_destroy(sffn_linear* linear);
 
 /* ------------------------------------------------- paged 4-bit key/value cache */

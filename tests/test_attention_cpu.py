@@ -67,7 +67,7 @@ def test_null_arguments_are_rejected_on_the_host(lib):
     assert L.sffn_kv_gather(None, ctypes.byref(batch), rows, rows, 0, None) == bad
     assert L.sffn_attend(None, ctypes.byref(batch), rows, 1, rows, None, 1.0, 0, 0, None, 0, None) == bad
     assert L.sffn_attend_workspace_bytes(None, 1, 1, 1) == 0
-    assert L.sffn_kv_check_error(None, None) == bad
+    assert L.sffn_kv_check_error(None, None) == bad and L.sffn_linear_check_error(None, None) == bad
     assert L.sffn_kv_bytes(None) == 0
     assert "NULL" in lib.last_error()
     L.sffn_linear_destroy(None)

@@ -57,6 +57,7 @@ def check_linear(sffn, n, k, group, B, dtype, zeros=False, bias=False, residual=
     want, tol = R.linear(host(x), codes.cpu().numpy(), host(scales), None if z is None else host(z),
                          None if b is None else host(b), None if r is None else host(r), group)
     R.assert_close(host(y), want, tol, dtype, f"linear {n}x{k} G{group} B{B} {dtype}")
+    lin.check_error()
     return lin, x, y, r
 
 
