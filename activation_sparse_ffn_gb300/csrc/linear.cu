@@ -62,6 +62,11 @@ int column_tiles(int B, int dtype) {   // of eight columns, rounded up to a powe
   return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
 }
 
+// What a cluster of 1, 2, 4 or 8 blocks costs, in bytes of codes an SM reads in that time: fitted to 10240 x 8192 at
+// one token (17.1, 15.5, 15.5 and 19.8 us), and the order found at 32 tokens (42.2, 37.4, 34.4, 57.5) and at 4099 x
+// 11008 with five (36.3, 25.8, 19.8, 20.6) is the same.
+constexpr long long kClusterCost[4] = {0, 16 * 1024, 56 * 1024, 224 * 1024};
+
 int scale_format(const sffn_linear& L) {
   return L.desc.scale_dtype == SFFN_F32 ? kScale32 : L.desc.has_zero ? kScale16Zero : kScale16;
 }
@@ -147,7 +152,7 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
   int smem = 0, ci = 3;
   if (nt == 1) {
     // The split of the inputs that gives a block the least to do, in bytes of codes that take as long: a cluster
-    // costs two barriers and a pass over its sums, about 64 KB; a run of 128 inputs of a token costs its warp 4 KB.
+    // costs two barriers and a pass over its sums; a run of 128 inputs of a token costs its warp 4 KB.
     long long best = -1;
     for (int c = 0; c < 4; ++c) {
       const int slices = kLinWarps << c;
@@ -160,7 +165,7 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
         const int fit = std::max(1, large ? L.fit_large[0][c] : L.fit_small[0][c]);
         const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + room / per_tile - 1) / (room / per_tile));
         const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
-        const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + (c ? 64 * 1024 : 0) +
+        const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + kClusterCost[c] +
                                (long long)(own128 / 128) * B * 4 * 1024;
         if (best >= 0 && cost >= best) break;
         best = cost, ci = c;
@@ -186,7 +191,7 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
       const int runs = std::min((own + 127) / 128, (room - pad) / per128);
       if (runs < 1) continue;
       const int chunks = (own + runs * 128 - 1) / (runs * 128);
-      const long long cost = ((long long)most * 8 * own + chunks * 8 * 1024) * waves + (c ? 64 * 1024 : 0);
+      const long long cost = ((long long)most * 8 * own + chunks * 8 * 1024) * waves + kClusterCost[c];
       if (best >= 0 && cost >= best) continue;
       best = cost, ci = c;
       a.clusters = clusters, a.chunk = runs * 128, a.chunk_stride = a.chunk + 32;

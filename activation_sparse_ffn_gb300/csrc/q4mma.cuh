@@ -56,9 +56,12 @@ __device__ __forceinline__ void scale_to_half_range(float m, float& up, float& d
   down = __uint_as_float((uint32_t)(e - 13) << 23);
 }
 
-// (w & mask) | 0x6400 in both halves: the exponent of 1024 over the selected bits.
+// (w & mask) | 0x6400 in both halves, the exponent of 1024 over the selected
+// bits, as the one three-input logic operation that it is.
 __device__ __forceinline__ __half2 code_bits(uint32_t w, uint32_t mask) {
-  return u32_h2((w & mask) | 0x64006400u);
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+  return u32_h2(r);
 }
 
 // The four pairs of a key word (kv_layout.cuh) as they stand: u * 2^-23 for p[0] and p[2],
