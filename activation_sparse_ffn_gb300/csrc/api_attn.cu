@@ -1,5 +1,6 @@
 // The extern "C" entry points of the attention half of a decode step: argument
 // checks, handles, and the launches.
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <string>
@@ -243,6 +244,8 @@ sffn_status sffn_kv_append(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows q
   if (b->n_tokens == 0) return SFFN_OK;
   if (!rows_ok(k, b->n_tokens, C->desc.n_kv_heads, D, dtype) || !rows_ok(v, b->n_tokens, C->desc.n_kv_heads, D, dtype))
     return invalid("k, v: need a pointer and strides of at least head_dim, multiples of 16 bytes");
+  if ((long long)b->n_tokens * (2 * C->desc.n_kv_heads + (q.ptr ? std::max(n_q_heads, 0) : 0)) > (1 << 30))
+    return invalid("n_tokens * (n_q_heads + 2 * n_kv_heads) must be at most 2^30");
   if (q.ptr) {
     if (n_q_heads < 1 || n_q_heads > 65536) return invalid("n_q_heads must be in [1, 65536]");
     if (!rows_ok(q, b->n_tokens, n_q_heads, D, dtype) || !rows_ok(q_out, b->n_tokens, n_q_heads, D, dtype))
@@ -265,6 +268,8 @@ sffn_status sffn_kv_gather(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows k
   for (const sffn_rows* r : rows)
     if (r->ptr && !rows_ok(*r, b->n_tokens, C->desc.n_kv_heads, C->desc.head_dim, dtype))
       return invalid("k_out, v_out: need strides of at least head_dim, multiples of 16 bytes");
+  if ((long long)b->n_tokens * 2 * C->desc.n_kv_heads > (1 << 30))
+    return invalid("n_tokens * 2 * n_kv_heads must be at most 2^30");
   if (!k_out.ptr && !v_out.ptr) return invalid("one of k_out and v_out is required");
   rc = check_device(C->device);
   if (rc != SFFN_OK) return rc;

@@ -22,10 +22,11 @@
 // like: one mask per pair and no arithmetic; the sums of w are subtracted by
 // starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
 // p * step are carried by two halves each (22 bits) in two products, and the
-// value codes are centred first, because the tensor core truncates its sums and
-// a sum of uncentred codes, all weights being positive, would show that over a
-// long history. Either way the sums of one unit's positions leave the tensor
-// core and are added up in fp32.
+// codes are centred first, because the tensor core truncates its sums: with bare
+// key codes the result is off by 1.3e-6 instead of 0.5e-6 (131072 positions),
+// and with bare value codes, all weights being positive, by far more over a long
+// history. Either way the sums of one unit's positions leave the tensor core
+// and are added up in fp32.
 //
 // Work split. The visible blocks of U positions (`units`) of every (sequence,
 // key head, tile of eight rows) are numbered through, and each warp of the grid
@@ -501,8 +502,13 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 #pragma unroll
         for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
           uint32_t p0[4], p1[4];
-          key_bits(w[0][j], p0);
-          key_bits(w[1][j], p1);
+          if (Exact) {
+            key_halves(w[0][j], p0);
+            key_halves(w[1][j], p1);
+          } else {
+            key_bits(w[0][j], p0);
+            key_bits(w[1][j], p1);
+          }
           const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
 #pragma unroll
           for (int h = 0; h < QL; ++h) {
@@ -513,7 +519,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 sm = __half22float2(u32_h2(kp[k][n]));
-          const float off = fmaf(-15.f, sm.x, sm.y);
+          const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
           s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
           s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
         }
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float c = (e & 1) ? 0.0625f : 1.f;   // odd pairs meet codes that are sixteen times as large
+          const float c = !Exact && (e & 1) ? 0.0625f : 1.f;   // odd pairs meet bare codes sixteen times as large
           uint32_t* hi = &q[0][2 * j + (e >> 1)][e & 1];
           if (Exact)
             split_f16(x[j][2 * e] * c, x[j][2 * e + 1] * c, *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
@@ -710,9 +716,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
             *hi = h2_u32(__floats2half2_rn(x[j][2 * e] * c, x[j][2 * e + 1] * c));
         }
       }
-      fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
+      if (!Exact) fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
 #pragma unroll
-      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * 5.9604645e-8f;
+      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * (Exact ? 1.f : 5.9604645e-8f);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int src = 4 * (2 * t + r);

@@ -76,15 +76,21 @@ __host__ __device__ constexpr int param_off(int pos, int grp, int n_groups, int 
 // rotated left by one bit. A code lies at bits 1-4 or 5-8 of a half (after a
 // rotation by 8 for e = 2, 3): as a half-precision number the masked bits are
 // u * 2^-23 (or u * 2^-19), exactly.
-__host__ __device__ __forceinline__ uint32_t key_word(const uint8_t* u) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w |= (uint32_t)u[2 * e] << (4 * e) | (uint32_t)u[2 * e + 1] << (16 + 4 * e);
+// From the codes in channel order, four bits each:
+__host__ __device__ __forceinline__ uint32_t key_word(uint32_t nat) {
+  uint32_t e = nat & 0x0f0f0f0fu, o = (nat >> 4) & 0x0f0f0f0fu;
+  e = (e | e >> 4) & 0x00ff00ffu, o = (o | o >> 4) & 0x00ff00ffu;
+  e = (e | e >> 8) & 0xffffu, o = (o | o >> 8) & 0xffffu;
+  const uint32_t w = e | o << 16;
   return w << 1 | w >> 31;
 }
-__host__ __device__ __forceinline__ int key_code(uint32_t w, int i) {
+// and back.
+__host__ __device__ __forceinline__ uint32_t key_codes(uint32_t w) {
   w = w >> 1 | w << 31;
-  return (w >> ((i & 1) * 16 + (i >> 1) * 4)) & 15;
+  uint32_t e = w & 0xffffu, o = w >> 16;
+  e = (e | e << 8) & 0x00ff00ffu, o = (o | o << 8) & 0x00ff00ffu;
+  e = (e | e << 4) & 0x0f0f0f0fu, o = (o | o << 4) & 0x0f0f0f0fu;
+  return e | o << 4;
 }
 
 // Value word: codes i = 0..3 (channels 64 w + 8 i + g) at bits 4 i of the low
@@ -93,31 +99,25 @@ __host__ __device__ __forceinline__ int key_code(uint32_t w, int i) {
 // are swapped, which the byte selection that pairs two positions does on the
 // way: with the exponent of 1024 put above it, it is the half-precision number
 // 1024 + 2u (or 1024 + 32u), and one operation makes that 2u - 15 exactly.
-__host__ __device__ __forceinline__ uint32_t value_word(const uint8_t* u) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (uint32_t)u[i] << (4 * i);
-  return ((w << 1) & 0xfffefffeu) | ((w >> 15) & 0x00010001u);
+// From the codes in order, four bits each, and back.
+__host__ __device__ __forceinline__ uint32_t value_word(uint32_t nat) {
+  return ((nat << 1) & 0xfffefffeu) | ((nat >> 15) & 0x00010001u);
 }
-__host__ __device__ __forceinline__ int value_code(uint32_t w, int i) {
-  w = ((w >> 1) & 0x7fff7fffu) | ((w << 15) & 0x80008000u);
-  return (w >> (4 * i)) & 15;
+__host__ __device__ __forceinline__ uint32_t value_codes(uint32_t w) {
+  return ((w >> 1) & 0x7fff7fffu) | ((w << 15) & 0x80008000u);
 }
 
-// One stored value, decoded on its own: (2u - 15) * step + mid, the product
-// exact in fp32 (an 11-bit by a 4-bit number).
-template <int D>
-__device__ __forceinline__ float kv_value(const uint8_t* block, int P, int n_groups, int pos, int c, int which) {
-  const uint8_t* row = block + (which ? kv_value_off(P, D) : 0) + pos * (D / 2);
-  int u;
-  if (which == 0)
-    u = key_code(__ldcg(reinterpret_cast<const uint32_t*>(row + key_word_off<D>(pos, (c & 31) >> 3, c >> 5))), c & 7);
-  else
-    u = value_code(__ldcg(reinterpret_cast<const uint32_t*>(row + value_word_off<D>(pos, c & 7, c >> 6))), (c & 63) >> 3);
-  const uint32_t pw = __ldcg(reinterpret_cast<const uint32_t*>(
-      block + kv_param_off(P, D) + param_off(pos, c / (D / n_groups), n_groups, which)));
-  const float2 pm = __half22float2(*reinterpret_cast<const __half2*>(&pw));
-  return __fmaf_rn((float)(2 * u - 15), pm.x, pm.y);
+// Eight lanes hold eight 4-bit codes each; afterwards code i of lane g is what
+// code g of lane i was. Its own inverse: it turns eight channels of a lane into
+// the codes of a value word and back.
+__device__ __forceinline__ uint32_t transpose_codes(uint32_t w, int lane) {
+#pragma unroll
+  for (int s = 4; s; s >>= 1) {
+    const uint32_t m = s == 4 ? 0x0000ffffu : s == 2 ? 0x00ff00ffu : 0x0f0f0f0fu;   // codes whose index has bit s clear
+    const uint32_t p = __shfl_xor_sync(SFFN_FULL_MASK, w, s);
+    w = (lane & s) ? (w & ~m) | ((p & ~m) >> (4 * s)) : (w & m) | ((p & m) << (4 * s));
+  }
+  return w;
 }
 
 // ----------------------------------------------------------------- places

@@ -74,6 +74,16 @@ __device__ __forceinline__ void key_bits(uint32_t w, uint32_t* p) {
   p[3] = r & 0x01e001e0u;
 }
 
+// The same as 2u - 15: 1024 + 2u - 1039 and (1024 + 32u) / 16 - 79, both exact.
+__device__ __forceinline__ void key_halves(uint32_t w, uint32_t* p) {
+  const uint32_t r = __funnelshift_r(w, w, 8);
+  const __half2 k1 = u32_h2(0xe40fe40fu), k16 = u32_h2(0x2c002c00u), k79 = u32_h2(0xd4f0d4f0u);  // -1039, 1/16, -79
+  p[0] = h2_u32(__hadd2(code_bits(w, 0x001e001eu), k1));
+  p[1] = h2_u32(__hfma2(code_bits(w, 0x01e001e0u), k16, k79));
+  p[2] = h2_u32(__hadd2(code_bits(r, 0x001e001eu), k1));
+  p[3] = h2_u32(__hfma2(code_bits(r, 0x01e001e0u), k16, k79));
+}
+
 // 2u - 15 for the codes at bits 1-4 of both halves, and at bits 5-8:
 // 1024 + 2u - 1039 and (1024 + 32u) / 16 - 79.
 __device__ __forceinline__ uint32_t value_low(uint32_t w) {

@@ -617,7 +617,8 @@ typedef struct {
  * q.ptr is not NULL, write the rotated queries q [n_tokens][n_q_heads]
  * [head_dim] to q_out (q_out may be q itself). All in `dtype`. Rows without a
  * place in the cache only have their queries written. Two rows of one call
- * must not share a place. Errors: INVALID_ARG, CUDA. */
+ * must not share a place. n_tokens * (n_q_heads + 2 n_kv_heads) is at most
+ * 2^30. Errors: INVALID_ARG, CUDA. */
 sffn_status sffn_kv_append(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows q, int32_t n_q_heads,
                            sffn_rows k, sffn_rows v, sffn_rows q_out, const sffn_rope* rope /* host, or NULL */,
                            int32_t dtype, sffn_stream stream);

@@ -11,8 +11,10 @@ absolute terms that the bounds are made of:
   of a tensor core, each off by at most 2^-22 of the terms' absolute sum; the
   K/G group sums are added in fp32. Together at most (40 + K/G) 2^-24 of
   sum |w||x|.
-* attention: a score is a sum of q times bare codes 0..15, so it is off by at
-  most 2^-20 of scale * sum |q| (|mid| + 30 step), its own rounding included; a weight by that and 2^-20 relative, the
+* attention: a score is a sum of q * mid and q * step * (2u - 15), or with
+  16-bit rows of q * step * 2u and a sum taken off again, so it is off by at most
+  2^-20 of scale * sum |q| (|mid| + 15 step), twice the step with 16-bit rows,
+  its own rounding included; a weight by that and 2^-20 relative, the
   weighted sum of values by a further 2^-19 of sum p|V|; the normalisation at
   most doubles the first part. With 16-bit rows the product of a weight and a
   step is rounded to a half (2^-11 relative): with step |2u - 15| <= |V| + |mid|
@@ -63,7 +65,7 @@ def rotate(x: np.ndarray, cs: np.ndarray, style: str) -> np.ndarray:
 
 def attention(q, k, v, n_new: int, scale: float, window: int, ksize=None, vsize=None):
     """One sequence: q (n_new, Hq, D), k, v (len, Hkv, D); ksize
-    (len, Hkv, D) |mid| + 30 step of the keys; vsize (len, Hkv, D) |V| + |mid|
+    (len, Hkv, D) |mid| + 15 step of the keys (30 with 16-bit rows); vsize (len, Hkv, D) |V| + |mid|
     if the rows have 16 bits. Returns out, lse and the bound on
     the error of out, all float64."""
     q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))

@@ -200,7 +200,7 @@ class Case:
         sffn.sffn_kv_append(self.cache.handle, self.all, None, k, v)
         self.k, self.v = (R.stored(t.float().cpu().numpy(), self.G) for t in (k, v))
         step, mid, _ = R.group_params(k.float().cpu().numpy(), self.G)
-        self.ksize = np.repeat(abs(mid.astype(np.float64)) + 30 * step.astype(np.float64), self.G, axis=-1)
+        self.ksize = np.repeat(abs(mid.astype(np.float64)) + (15 if self.dtype == torch.float32 else 30) * step.astype(np.float64), self.G, axis=-1)
         mid = R.group_params(v.float().cpu().numpy(), self.G)[1].astype(np.float64)
         self.vsize = None if self.dtype == torch.float32 else abs(self.v) + np.repeat(abs(mid), self.G, axis=-1)
         return k, v
