@@ -65,7 +65,10 @@ struct Turn {
         kind = c0 < half ? 1 : 2;
         partner = kind == 1 ? lane + half / 8 : lane - half / 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cs[e] = __ldg(table + (kind == 1 ? c0 : c0 - half) + e);
+        for (int e = 0; e < 8; ++e) {
+          cs[e] = __ldg(table + (kind == 1 ? c0 : c0 - half) + e);
+          if (kind == 1) cs[e].y = -cs[e].y;   // a cos - b sin and b cos + a sin become one formula, the same bits
+        }
       }
     } else if (r.style == 1 && r.dim % 8 == 0) {
       if (c0 < r.dim) {
@@ -84,10 +87,7 @@ struct Turn {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float y = __shfl_sync(SFFN_FULL_MASK, x[e], partner);
-        if (on && (kind == 1 || kind == 2)) {
-          const float u = __fmul_rn(x[e], cs[e].x), w = __fmul_rn(y, cs[e].y);
-          x[e] = kind == 1 ? __fsub_rn(u, w) : __fadd_rn(u, w);
-        }
+        if (on && kind != 0) x[e] = __fadd_rn(__fmul_rn(x[e], cs[e].x), __fmul_rn(y, cs[e].y));
       }
     } else if (on && kind == 3) {
 #pragma unroll
@@ -117,7 +117,7 @@ struct Turn {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 8) k_kv_append(const AppendArgs a) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows;
   pdl_launch_dependents();
   pdl_wait();
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
   }
   const int slot = query ? 0 : at.pos % a.c.P;
   const int glanes = LR / a.c.n_groups, grp = lr / glanes;
+  const unsigned group_mask = (glanes == 32 ? 0xffffffffu : (1u << glanes) - 1u) << (lane / glanes * glanes);
 
   for (int r = r0 + sub; r - sub < r1; r += RI) {
     float x[8];
@@ -180,20 +181,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
       continue;
     }
     // least and largest value of the group, over the lanes that share it
-    float lo = x[0], hi = x[0];
-    int bad = 0;
+    float lo = x[0], hi = x[0], nan = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       lo = fminf(lo, x[e]);
       hi = fmaxf(hi, x[e]);
-      bad |= !(fabsf(x[e]) < __int_as_float(0x7f800000));
+      nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
     }
-#pragma unroll 4
     for (int o = 1; o < glanes; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
       hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
-      bad |= __shfl_xor_sync(SFFN_FULL_MASK, bad, o);
     }
+    const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
     const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
     __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
     const float midf = __half2float(mid);
@@ -201,14 +200,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
     __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
     if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
     const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
-    const bool flat = stepf == 0.f || bad;
+    // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
+    // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
     uint32_t codes = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = floorf(__fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f));
-      const uint32_t u = flat ? 8u : (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
-      codes |= u << (4 * e);
+      const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
+      codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
     }
+    codes -= 0x4b000000u * 0x11111111u;
+    if (stepf == 0.f || bad) codes = 0x88888888u;
     const bool value = r >= a.c.hkv;
     const uint32_t turned = __any_sync(SFFN_FULL_MASK, value) ? transpose_codes(codes, lane) : 0u;
     if (in) {
@@ -265,14 +266,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
     for (int k = 0; k < kBatch; ++k) {
       const int r = rb + k * RI + sub;
       const bool value = r >= a.c.hkv;
-      const uint32_t turned = transpose_codes(value_codes(w[k]), lane);
+      const uint32_t turned = __any_sync(SFFN_FULL_MASK, value) ? transpose_codes(value_codes(w[k]), lane) : 0u;
       const uint32_t codes = value ? turned : key_codes(w[k]);
       const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pm[k]));
       float x[8];
-      // (2u - 15) * step is exact in fp32 (a 4-bit by an 11-bit number), so one rounding either way
+      // 2u - 15 from the bit pattern of 2^23 + 2u; its product with step is exact in fp32 (a 4-bit by an 11-bit
+      // number), so there is one rounding
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = at.pos < 0 ? 0.f : __fmaf_rn((float)(2 * (int)(codes >> (4 * e) & 15) - 15), sm.x, sm.y);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u2 = e == 0 ? codes << 1 : codes >> (4 * e - 1);
+        x[e] = __fmaf_rn(__uint_as_float((u2 & 30u) | 0x4b000000u) - 8388623.f, sm.x, sm.y);
+        if (at.pos < 0) x[e] = 0.f;
+      }
       const sffn_rows& dst = value ? a.v : a.k;
       if (r < r1 && dst.ptr)
         st_run<8>(dst.ptr, (size_t)(i * dst.row_stride + (value ? r - a.c.hkv : r) * dst.head_stride) + lr * 8, a.dtype, x);
