@@ -34,12 +34,32 @@ struct RowLanes {
   static constexpr int kLanes = D / 8, kRows = 32 / kLanes;
 };
 
+// Eight consecutive elements as loaded, and as fp32.
+template <typename T>
+struct Raw {
+  static constexpr int N = sizeof(T) / 2;   // 16-byte pieces
+  uint4 v[N];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) WType<T>::unpack(v[i], x + i * WType<T>::kPerChunk);
+  }
+};
+
+template <typename T>
+constexpr int dtype_of() {
+  return std::is_same<T, float>::value ? SFFN_F32 : std::is_same<T, __half>::value ? SFFN_F16 : SFFN_BF16;
+}
+
 struct AppendArgs {
   CacheView c;
   sffn_kv_batch b;
   sffn_rows q, k, v, q_out;
   int hq, dtype;
-  int per, q_tasks, kv_tasks;   // rows of a task (one warp), tasks of a token's query rows and of its key and value rows
+  int per, q_tasks, kv_tasks;   // rows of a task (one warp), tasks of a token's query rows, of its key rows and of its value rows
   sffn_rope rope;               // table null: no rotation
 };
 
@@ -80,9 +100,8 @@ struct Turn {
       kind = 4;
     }
   }
-  // x: the lane's channels of a row whose channel 0 is element `at` of src
-  __device__ __forceinline__ void apply(const sffn_rope& r, float* x, const void* src, size_t at, int dtype, int lane,
-                                        bool on) const {
+  // x: the lane's channels of a row of elements of type dtype
+  __device__ __forceinline__ void apply(const sffn_rope& r, float* x, const void* row, int dtype, int lane, bool on) const {
     if (shuffles) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -105,7 +124,7 @@ struct Turn {
         const bool first = r.style == 0 ? c < half : (c & 1) == 0;
         const int p = r.style == 0 ? (first ? c + half : c - half) : c ^ 1;
         const float2 t = __ldg(table + (r.style == 0 ? (first ? c : c - half) : c >> 1));
-        const float u = __fmul_rn(ld_elem(src, at + c, dtype), t.x), w = __fmul_rn(ld_elem(src, at + p, dtype), t.y);
+        const float u = __fmul_rn(ld_elem(row, c, dtype), t.x), w = __fmul_rn(ld_elem(row, p, dtype), t.y);
         const float v = first ? __fsub_rn(u, w) : __fadd_rn(u, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -116,112 +135,121 @@ struct Turn {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 8) k_kv_append(const AppendArgs a) {
-  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, sub = lane / LR, lr = lane % LR, c0 = lr * 8;
-  const int tasks = a.q_tasks + a.kv_tasks;
-  const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (task >= a.b.n_tokens * tasks) return;
-  const int i = task / tasks, part = task - i * tasks;
-  const bool query = part < a.q_tasks;
-  const int r0 = (query ? part : part - a.q_tasks) * a.per, rows = query ? a.hq : 2 * a.c.hkv;
-  const int r1 = min(r0 + a.per, rows);
-  auto where = [&](int r, const void*& src) {   // element of channel 0
-    const bool key = r < a.c.hkv;
-    const sffn_rows& s = query ? a.q : key ? a.k : a.v;
-    src = s.ptr;
-    return (size_t)(i * s.row_stride + (query ? r : key ? r : r - a.c.hkv) * s.head_stride);
-  };
-  float nx[8];
-  const void* nsrc = nullptr;
-  size_t nat = 0;
-  auto fetch = [&](int r) {
-    if (r < r1) {
-      nat = where(r, nsrc);
-      ld_run<8>(nsrc, nat + c0, a.dtype, nx);
-    }
-  };
+// Rows r0 .. r1 - 1 of one kind (0 queries, 1 keys, 2 values) of token i.
+template <int D, typename T, int KIND>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
+  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kAhead = 3, dtype = dtype_of<T>();
+  const int sub = lane / LR, lr = lane % LR, c0 = lr * 8;
+  const sffn_rows& rows = KIND == 0 ? a.q : KIND == 1 ? a.k : a.v;
+  const T* p = static_cast<const T*>(rows.ptr) + i * rows.row_stride + (r0 + sub) * rows.head_stride + c0;
+  const int64_t hop = RI * rows.head_stride;
+  Raw<T> next[kAhead] = {};
+  const T* ahead = p;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) nx[e] = 0.f;
-  fetch(r0 + sub);
+  for (int k = 0; k < kAhead; ++k, ahead += hop)
+    if (r0 + sub + k * RI < r1) next[k].load(ahead);
   const KvPlace at = kv_place(a.b, i, lane, a.c.P, a.c.err);
   if (at.seq < 0) return;
   Turn<D> turn;
-  if (a.rope.table && (query || r0 < a.c.hkv)) {
+  if (KIND != 2 && a.rope.table) {
     const int pos = a.rope.positions ? ld_dep(a.rope.positions + i) : at.pos;
     if (pos >= 0 && pos < a.rope.length)
       turn.set(a.rope, pos, lane);
     else if (a.rope.positions || pos >= 0)
       set_device_error(a.c.err, SFFN_ERR_DEVICE);
   }
-  int page = -1;
-  if (!query) {
-    if (at.pos < 0) return;
-    page = kv_page(a.b, at.seq, at.pos / a.c.P, a.c.n_pages, a.c.err);
-    if (page < 0) return;
-  }
-  const int slot = query ? 0 : at.pos % a.c.P;
-  const int glanes = LR / a.c.n_groups, grp = lr / glanes;
+  const int glanes = LR / a.c.n_groups;
   const unsigned group_mask = (glanes == 32 ? 0xffffffffu : (1u << glanes) - 1u) << (lane / glanes * glanes);
+  uint8_t* word = nullptr;     // of the lane's codes, and of its group's params, in the block of head r0 + sub
+  uint8_t* param = nullptr;
+  T* out = nullptr;
+  if (KIND == 0) {
+    out = static_cast<T*>(a.q_out.ptr) + i * a.q_out.row_stride + (r0 + sub) * a.q_out.head_stride + c0;
+  } else {
+    if (at.pos < 0) return;
+    const int page = kv_page(a.b, at.seq, at.pos / a.c.P, a.c.n_pages, a.c.err);
+    if (page < 0) return;
+    const int slot = at.pos % a.c.P;
+    uint8_t* block = a.c.pages + (size_t)page * a.c.page_bytes + (size_t)(r0 + sub) * a.c.head_bytes;
+    word = block + (KIND == 2 ? kv_value_off(a.c.P, D) : 0) + slot * (D / 2) +
+           (KIND == 2 ? value_word_off<D>(slot, lr & 7, lr >> 3) : key_word_off<D>(slot, lr & 3, lr >> 2));
+    param = block + kv_param_off(a.c.P, D) + param_off(slot, lr / glanes, a.c.n_groups, KIND == 2);
+  }
 
-  for (int r = r0 + sub; r - sub < r1; r += RI) {
-    float x[8];
-    const void* src = nsrc;
-    const size_t elem = nat;
+  for (int rb = r0; rb < r1;) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = nx[e];
-    fetch(r + RI);
-    const bool in = r < r1;
-    turn.apply(a.rope, x, src, elem, a.dtype, lane, in && (query || r < a.c.hkv));
-    if (query) {
-      if (in) st_run<8>(a.q_out.ptr, (size_t)(i * a.q_out.row_stride + r * a.q_out.head_stride) + c0, a.dtype, x);
-      continue;
-    }
-    // least and largest value of the group, over the lanes that share it
-    float lo = x[0], hi = x[0], nan = 0.f;
+    for (int k = 0; k < kAhead; ++k) {
+      if (rb >= r1) break;
+      const bool in = rb + sub < r1;
+      float x[8];
+      next[k].get(x);
+      if (rb + sub + kAhead * RI < r1) next[k].load(ahead);
+      ahead += hop;
+      if (KIND != 2) turn.apply(a.rope, x, p - c0, dtype, lane, in);
+      p += hop;
+      rb += RI;
+      if (KIND == 0) {
+        if (in) st_run<8>(out, 0, dtype, x);
+        out += RI * a.q_out.head_stride;
+        continue;
+      }
+      // least and largest value of the group, over the lanes that share it
+      float lo = x[0], hi = x[0], nan = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
-    }
-    for (int o = 1; o < glanes; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
-    }
-    const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
-    const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
-    __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
-    const float midf = __half2float(mid);
-    const float far = fmaxf(__fsub_rn(hi, midf), __fsub_rn(midf, lo));
-    __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
-    if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
-    const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
-    // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
-    // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
-    uint32_t codes = 0;
+      for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
+        nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
+      }
+      for (int o = 1; o < glanes; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
+      }
+      const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
+      const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
+      __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
+      const float midf = __half2float(mid);
+      const float far = fmaxf(__fsub_rn(hi, midf), __fsub_rn(midf, lo));
+      __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
+      if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
+      const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
+      // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
+      // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
+      uint32_t codes = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
-      codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+      for (int e = 0; e < 8; ++e) {
+        const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
+        codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+      }
+      codes -= 0x4b000000u * 0x11111111u;
+      if (stepf == 0.f || bad) codes = 0x88888888u;
+      const uint32_t w = KIND == 2 ? value_word(transpose_codes(codes, lane)) : key_word(codes);
+      if (in) {
+        *reinterpret_cast<uint32_t*>(word) = w;
+        if (lr % glanes == 0) *reinterpret_cast<__half2*>(param) = __halves2half2(step, mid);
+      }
+      word += RI * a.c.head_bytes;
+      param += RI * a.c.head_bytes;
     }
-    codes -= 0x4b000000u * 0x11111111u;
-    if (stepf == 0.f || bad) codes = 0x88888888u;
-    const bool value = r >= a.c.hkv;
-    const uint32_t turned = __any_sync(SFFN_FULL_MASK, value) ? transpose_codes(codes, lane) : 0u;
-    if (in) {
-      const int h = value ? r - a.c.hkv : r;
-      uint8_t* block = a.c.pages + (size_t)page * a.c.page_bytes + (size_t)h * a.c.head_bytes;
-      uint8_t* row = block + (value ? kv_value_off(a.c.P, D) : 0) + slot * (D / 2);
-      const int off = value ? value_word_off<D>(slot, lr & 7, lr >> 3) : key_word_off<D>(slot, lr & 3, lr >> 2);
-      *reinterpret_cast<uint32_t*>(row + off) = value ? value_word(turned) : key_word(codes);
-      if (lr % glanes == 0)
-        *reinterpret_cast<__half2*>(block + kv_param_off(a.c.P, D) + param_off(slot, grp, a.c.n_groups, value)) =
-            __halves2half2(step, mid);
-    }
+  }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, tasks = a.q_tasks + 2 * a.kv_tasks;
+  const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (task >= a.b.n_tokens * tasks) return;
+  const int i = task / tasks, part = task - i * tasks;
+  if (part < a.q_tasks) {
+    append_rows<D, T, 0>(a, i, part * a.per, min((part + 1) * a.per, a.hq), lane);
+  } else {
+    const int n = part - a.q_tasks, r0 = (n >> 1) * a.per, r1 = min(r0 + a.per, a.c.hkv);
+    if (n & 1)
+      append_rows<D, T, 2>(a, i, r0, r1, lane);
+    else
+      append_rows<D, T, 1>(a, i, r0, r1, lane);
   }
 }
 
@@ -230,44 +258,40 @@ struct GatherArgs {
   sffn_kv_batch b;
   sffn_rows k, v;
   int dtype;
-  int per, tasks;   // rows of a task, tasks of a token
+  int per, tasks;   // rows of a task, tasks of a token's key rows and of its value rows
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
+template <int D, typename T, bool VALUE>
+__device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kBatch = 4;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, sub = lane / LR, lr = lane % LR;
-  const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (task >= a.b.n_tokens * a.tasks) return;
-  const int i = task / a.tasks, r0 = (task - i * a.tasks) * a.per, r1 = min(r0 + a.per, 2 * a.c.hkv);
+  const sffn_rows& rows = VALUE ? a.v : a.k;
+  if (!rows.ptr) return;
+  const int sub = lane / LR, lr = lane % LR;
   const KvPlace at = kv_place(a.b, i, lane, a.c.P, a.c.err);
   if (at.seq < 0) return;
-  const int page = at.pos >= 0 ? max(0, kv_page(a.b, at.seq, at.pos / a.c.P, a.c.n_pages, a.c.err)) : 0;
-  const int slot = at.pos >= 0 ? at.pos % a.c.P : 0, grp = lr / (LR / a.c.n_groups);
+  const bool placed = at.pos >= 0;
+  const int page = placed ? max(0, kv_page(a.b, at.seq, at.pos / a.c.P, a.c.n_pages, a.c.err)) : 0;
+  const int slot = placed ? at.pos % a.c.P : 0;
+  const uint8_t* block = a.c.pages + (size_t)page * a.c.page_bytes + (size_t)(r0 + sub) * a.c.head_bytes;
+  const uint8_t* word = block + (VALUE ? kv_value_off(a.c.P, D) : 0) + slot * (D / 2) +
+                        (VALUE ? value_word_off<D>(slot, lr & 7, lr >> 3) : key_word_off<D>(slot, lr & 3, lr >> 2));
+  const uint8_t* param = block + kv_param_off(a.c.P, D) + param_off(slot, lr / (LR / a.c.n_groups), a.c.n_groups, VALUE);
+  T* out = static_cast<T*>(rows.ptr) + i * rows.row_stride + (r0 + sub) * rows.head_stride + lr * 8;
   for (int rb = r0; rb < r1; rb += RI * kBatch) {
     uint32_t w[kBatch], pm[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int r = rb + k * RI + sub;
       w[k] = pm[k] = 0u;
-      if (r < r1 && at.pos >= 0) {
-        const bool value = r >= a.c.hkv;
-        const uint8_t* block = a.c.pages + (size_t)page * a.c.page_bytes + (size_t)(value ? r - a.c.hkv : r) * a.c.head_bytes;
-        const uint8_t* row = block + (value ? kv_value_off(a.c.P, D) : 0) + slot * (D / 2);
-        const int off = value ? value_word_off<D>(slot, lr & 7, lr >> 3) : key_word_off<D>(slot, lr & 3, lr >> 2);
-        w[k] = __ldcg(reinterpret_cast<const uint32_t*>(row + off));
-        pm[k] = __ldcg(reinterpret_cast<const uint32_t*>(block + kv_param_off(a.c.P, D) +
-                                                         param_off(slot, grp, a.c.n_groups, value)));
+      if (placed && rb + sub + k * RI < r1) {
+        w[k] = __ldcg(reinterpret_cast<const uint32_t*>(word));
+        pm[k] = __ldcg(reinterpret_cast<const uint32_t*>(param));
       }
+      word += RI * a.c.head_bytes;
+      param += RI * a.c.head_bytes;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int r = rb + k * RI + sub;
-      const bool value = r >= a.c.hkv;
-      const uint32_t turned = __any_sync(SFFN_FULL_MASK, value) ? transpose_codes(value_codes(w[k]), lane) : 0u;
-      const uint32_t codes = value ? turned : key_codes(w[k]);
+      const uint32_t codes = VALUE ? transpose_codes(value_codes(w[k]), lane) : key_codes(w[k]);
       const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pm[k]));
       float x[8];
       // 2u - 15 from the bit pattern of 2^23 + 2u; its product with step is exact in fp32 (a 4-bit by an 11-bit
@@ -276,13 +300,25 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
       for (int e = 0; e < 8; ++e) {
         const uint32_t u2 = e == 0 ? codes << 1 : codes >> (4 * e - 1);
         x[e] = __fmaf_rn(__uint_as_float((u2 & 30u) | 0x4b000000u) - 8388623.f, sm.x, sm.y);
-        if (at.pos < 0) x[e] = 0.f;
       }
-      const sffn_rows& dst = value ? a.v : a.k;
-      if (r < r1 && dst.ptr)
-        st_run<8>(dst.ptr, (size_t)(i * dst.row_stride + (value ? r - a.c.hkv : r) * dst.head_stride) + lr * 8, a.dtype, x);
+      if (rb + sub + k * RI < r1) st_run<8>(out, 0, dtype_of<T>(), x);   // no place: step and mid are 0
+      out += RI * rows.head_stride;
     }
   }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, task = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (task >= a.b.n_tokens * 2 * a.tasks) return;
+  const int i = task / (2 * a.tasks), part = task - i * 2 * a.tasks;
+  const int r0 = (part >> 1) * a.per, r1 = min(r0 + a.per, a.c.hkv);
+  if (part & 1)
+    gather_rows<D, T, true>(a, i, r0, r1, lane);
+  else
+    gather_rows<D, T, false>(a, i, r0, r1, lane);
 }
 
 // Rows that a task takes: all of a token's where there are tokens enough to fill
@@ -309,27 +345,33 @@ cudaError_t launch_kv_append(const sffn_kv& C, const sffn_kv_batch& b, const sff
                              const sffn_rows& k, const sffn_rows& v, const sffn_rows& q_out, const sffn_rope& rope,
                              int dtype, cudaStream_t st) {
   AppendArgs a{view_of(C), b, q, k, v, q_out, q.ptr ? n_q_heads : 0, dtype, 0, 0, 0, rope};
-  const int kv = 2 * a.c.hkv, at_once = 32 / (C.desc.head_dim / 8);
-  a.per = rows_per_task((long long)b.n_tokens * (a.hq + kv), std::max(a.hq, kv), at_once, C.num_sms);
+  const int at_once = 32 / (C.desc.head_dim / 8);
+  a.per = rows_per_task((long long)b.n_tokens * (a.hq + 2 * a.c.hkv), std::max(a.hq, a.c.hkv), at_once, C.num_sms);
   a.q_tasks = (a.hq + a.per - 1) / a.per;
-  a.kv_tasks = (kv + a.per - 1) / a.per;
-  const long long tasks = (long long)b.n_tokens * (a.q_tasks + a.kv_tasks);
+  a.kv_tasks = (a.c.hkv + a.per - 1) / a.per;
+  const long long tasks = (long long)b.n_tokens * (a.q_tasks + 2 * a.kv_tasks);
+  const dim3 grid((unsigned)((tasks + kWarps - 1) / kWarps));
   return by_dim(C.desc.head_dim, [&](auto d) {
-    return launch_ex(k_kv_append<decltype(d)::value>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), dim3(kWarps * 32),
-                     0, st, true, 1, a);
+    constexpr int D = decltype(d)::value;
+    auto run = [&](auto* kern) { return launch_ex(kern, grid, dim3(kWarps * 32), 0, st, true, 1, a); };
+    return dtype == SFFN_F32 ? run(k_kv_append<D, float>)
+                             : dtype == SFFN_F16 ? run(k_kv_append<D, __half>) : run(k_kv_append<D, __nv_bfloat16>);
   });
 }
 
 cudaError_t launch_kv_gather(const sffn_kv& C, const sffn_kv_batch& b, const sffn_rows& k_out, const sffn_rows& v_out,
                              int dtype, cudaStream_t st) {
   GatherArgs a{view_of(C), b, k_out, v_out, dtype, 0, 0};
-  const int kv = 2 * a.c.hkv, at_once = 32 / (C.desc.head_dim / 8);
-  a.per = rows_per_task((long long)b.n_tokens * kv, kv, at_once, C.num_sms);
-  a.tasks = (kv + a.per - 1) / a.per;
-  const long long tasks = (long long)b.n_tokens * a.tasks;
+  const int at_once = 32 / (C.desc.head_dim / 8);
+  a.per = rows_per_task((long long)b.n_tokens * 2 * a.c.hkv, a.c.hkv, at_once, C.num_sms);
+  a.tasks = (a.c.hkv + a.per - 1) / a.per;
+  const long long tasks = (long long)b.n_tokens * 2 * a.tasks;
+  const dim3 grid((unsigned)((tasks + kWarps - 1) / kWarps));
   return by_dim(C.desc.head_dim, [&](auto d) {
-    return launch_ex(k_kv_gather<decltype(d)::value>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), dim3(kWarps * 32),
-                     0, st, true, 1, a);
+    constexpr int D = decltype(d)::value;
+    auto run = [&](auto* kern) { return launch_ex(kern, grid, dim3(kWarps * 32), 0, st, true, 1, a); };
+    return dtype == SFFN_F32 ? run(k_kv_gather<D, float>)
+                             : dtype == SFFN_F16 ? run(k_kv_gather<D, __half>) : run(k_kv_gather<D, __nv_bfloat16>);
   });
 }
 
