@@ -138,7 +138,7 @@ struct Turn {
 // Rows r0 .. r1 - 1 of one kind (0 queries, 1 keys, 2 values) of token i.
 template <int D, typename T, int KIND>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
-  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kAhead = 3, dtype = dtype_of<T>();
+  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kAhead = 1, dtype = dtype_of<T>();
   const int sub = lane / LR, lr = lane % LR, c0 = lr * 8;
   const sffn_rows& rows = KIND == 0 ? a.q : KIND == 1 ? a.k : a.v;
   const T* p = static_cast<const T*>(rows.ptr) + i * rows.row_stride + (r0 + sub) * rows.head_stride + c0;
@@ -241,12 +241,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
   const int lane = threadIdx.x & 31, tasks = a.q_tasks + 2 * a.kv_tasks;
   const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (task >= a.b.n_tokens * tasks) return;
-  const int i = task / tasks, part = task - i * tasks;
+  // neighbouring warps take neighbouring tokens, so that those of an SM mostly run the same of the three loops
+  const int part = task / a.b.n_tokens, i = task - part * a.b.n_tokens;
   if (part < a.q_tasks) {
     append_rows<D, T, 0>(a, i, part * a.per, min((part + 1) * a.per, a.hq), lane);
   } else {
-    const int n = part - a.q_tasks, r0 = (n >> 1) * a.per, r1 = min(r0 + a.per, a.c.hkv);
-    if (n & 1)
+    const int n = part - a.q_tasks, value = n >= a.kv_tasks, r0 = (n - value * a.kv_tasks) * a.per;
+    const int r1 = min(r0 + a.per, a.c.hkv);
+    if (value)
       append_rows<D, T, 2>(a, i, r0, r1, lane);
     else
       append_rows<D, T, 1>(a, i, r0, r1, lane);
@@ -313,9 +315,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, task = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (task >= a.b.n_tokens * 2 * a.tasks) return;
-  const int i = task / (2 * a.tasks), part = task - i * 2 * a.tasks;
-  const int r0 = (part >> 1) * a.per, r1 = min(r0 + a.per, a.c.hkv);
-  if (part & 1)
+  const int part = task / a.b.n_tokens, i = task - part * a.b.n_tokens, value = part >= a.tasks;
+  const int r0 = (part - value * a.tasks) * a.per, r1 = min(r0 + a.per, a.c.hkv);
+  if (value)
     gather_rows<D, T, true>(a, i, r0, r1, lane);
   else
     gather_rows<D, T, false>(a, i, r0, r1, lane);
