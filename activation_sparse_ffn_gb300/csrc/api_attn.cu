@@ -91,8 +91,8 @@ sffn_status sffn_linear_create(const sffn_linear_desc* d, sffn_linear** out) {
   sffn_linear* L = new (std::nothrow) sffn_linear();
   if (!L) return invalid("host allocation failed");
   L->desc = *d;
-  L->kp = (d->in_features + 63) / 64 * 64;
-  L->tiles = (d->out_features + 15) / 16;
+  L->kp = (d->in_features + 127) / 128 * 128;
+  L->tiles = (d->out_features + 31) / 32 * 2;
   const size_t vals = (size_t)L->tiles * (L->kp / d->group) * 16 * elem_bytes(d->scale_dtype);
   cudaError_t e = cudaGetDevice(&L->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);

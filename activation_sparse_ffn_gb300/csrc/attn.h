@@ -9,10 +9,10 @@ struct sffn_linear {
   int device = 0;
   int num_sms = 0;
   bool packed = false;
-  int kp = 0;            // in_features rounded up to 64
-  int tiles = 0;         // 16-row tiles of out_features
+  int kp = 0;            // in_features rounded up to 128
+  int tiles = 0;         // 16-row tiles of out_features, an even number
   uint32_t* codes = nullptr;   // [tiles][kp / 64][128 words], see linear.cu
-  void* scales = nullptr;      // [tiles][kp / group][16] in scale_dtype
+  void* scales = nullptr;      // [tiles][kp / 128][8][128 / group][2] in scale_dtype
   void* zeros = nullptr;       // the same shape, or null
   float* bias = nullptr;       // [tiles * 16], zeros if none was given
   uint32_t* err = nullptr;

@@ -7,8 +7,8 @@
 // inputs 2e and 2e + 1 of its eight stand at bits 4e of the two halves
 // (e = 0, 1 as they are, e = 2, 3 after a shift by 8: two bits of a half apart by
 // four, which is all that linear.cuh has to undo). Rows and
-// inputs are padded with code 0 (stored as 8). Scales (and zeros) stand as
-// [tile][group][8][2], rows g and g + 8 beside each other.
+// inputs are padded with code 0 (stored as 8), to an even number of tiles and to
+// 128 inputs.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -42,13 +42,14 @@ __global__ void k_pack_codes(const int8_t* codes, uint32_t* out, int n, int k, i
   out[w] = weight_word(u);
 }
 
-// Scales or zeros as 16- or 32-bit words.
+// Scales or zeros, 16- or 32-bit words: [tile][step of 128 inputs][8][128 / G][2], rows g and g + 8 beside each other.
 template <typename T>
-__global__ void k_pack_groups(const T* in, T* out, int n, int groups, int groups_p, int tiles) {
+__global__ void k_pack_groups(const T* in, T* out, int n, int groups, int per_step, int steps, int tiles) {
   const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (size_t)tiles * groups_p * 16) return;
-  const int half = (int)(i % 2), g = (int)(i / 2 % 8), grp = (int)(i / 16 % groups_p), tile = (int)(i / 16 / groups_p);
-  const int row = tile * 16 + g + 8 * half;
+  if (i >= (size_t)tiles * steps * per_step * 16) return;
+  const int half = (int)(i % 2), q = (int)(i / 2 % per_step), g = (int)(i / 2 / per_step % 8);
+  const size_t st = i / 16 / per_step;
+  const int step = (int)(st % steps), tile = (int)(st / steps), row = tile * 16 + g + 8 * half, grp = step * per_step + q;
   out[i] = row < n && grp < groups ? in[(size_t)row * groups + grp] : T(0);
 }
 
@@ -75,8 +76,8 @@ int scale_format(const sffn_linear& L) {
 
 sffn_status pack_linear(sffn_linear& L, const int8_t* codes, const void* scales, const void* zeros, const float* bias,
                         cudaStream_t st) {
-  const int n = L.desc.out_features, k = L.desc.in_features, groups = k / L.desc.group, gp = L.kp / L.desc.group;
-  const size_t words = (size_t)L.tiles * (L.kp / 64) * 128, vals = (size_t)L.tiles * gp * 16;
+  const int n = L.desc.out_features, k = L.desc.in_features, groups = k / L.desc.group, per_step = 128 / L.desc.group;
+  const size_t words = (size_t)L.tiles * (L.kp / 64) * 128, vals = (size_t)L.tiles * (L.kp / 128) * per_step * 16;
   L.packed = false;
   cudaError_t e = cudaMemsetAsync(L.err, 0, 4, st);
   if (e != cudaSuccess) return cuda_fail(e, "sffn_linear_pack");
@@ -87,9 +88,11 @@ sffn_status pack_linear(sffn_linear& L, const int8_t* codes, const void* scales,
     if (!in) continue;
     const unsigned blocks = (unsigned)((vals + 255) / 256);
     if (L.desc.scale_dtype == SFFN_F32)
-      k_pack_groups<uint32_t><<<blocks, 256, 0, st>>>((const uint32_t*)in, (uint32_t*)out, n, groups, gp, L.tiles);
+      k_pack_groups<uint32_t><<<blocks, 256, 0, st>>>((const uint32_t*)in, (uint32_t*)out, n, groups, per_step, L.kp / 128,
+                                                 L.tiles);
     else
-      k_pack_groups<uint16_t><<<blocks, 256, 0, st>>>((const uint16_t*)in, (uint16_t*)out, n, groups, gp, L.tiles);
+      k_pack_groups<uint16_t><<<blocks, 256, 0, st>>>((const uint16_t*)in, (uint16_t*)out, n, groups, per_step, L.kp / 128,
+                                                 L.tiles);
   }
   k_pack_bias<<<(L.tiles * 16 + 255) / 256, 256, 0, st>>>(bias, L.bias, n, L.tiles * 16);
   e = cudaGetLastError();
@@ -119,16 +122,17 @@ cudaError_t configure_linear_kernels(sffn_linear& L) {
 
 namespace {
 
-// x as halves and its pairs, for the kernel of more than eight columns.
+// x as halves, its scales and its sums over groups, for the kernel of more than eight columns.
 struct LinearWs {
-  size_t pairs, total;
+  size_t down, sum, total;
 };
 LinearWs linear_ws(const sffn_linear& L, int B, int dtype) {
   const int nt = column_tiles(B, dtype), cols = dtype == SFFN_F32 ? 2 * B : B;
-  if (nt == 1) return LinearWs{0, 0};
+  if (nt == 1) return LinearWs{0, 0, 0};
   LinearWs w;
-  w.pairs = ((size_t)cols * L.kp * 2 + 255) / 256 * 256;
-  w.total = w.pairs + (size_t)(L.kp / L.desc.group) * 8 * nt * sizeof(float2);
+  w.down = (size_t)cols * L.kp * 2;   // kp is a multiple of 128
+  w.sum = w.down + 256;
+  w.total = w.sum + (size_t)(L.kp / L.desc.group) * 8 * nt * sizeof(float);
   return w;
 }
 
@@ -140,24 +144,25 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
                           const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
   LinearArgs a = {};
   a.codes = L.codes, a.scales = L.scales, a.zeros = L.zeros, a.bias = L.bias, a.err = L.err;
+  const LinearWs w = linear_ws(L, B, dtype);
   a.ws_x = static_cast<const __half*>(ws);
-  a.ws_xg = reinterpret_cast<const float2*>(static_cast<const uint8_t*>(ws) + linear_ws(L, B, dtype).pairs);
+  a.ws_down = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws) + w.down);
+  a.ws_sum = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws) + w.sum);
   a.n = L.desc.out_features, a.k = L.desc.in_features, a.kp = L.kp, a.B = B, a.dtype = dtype;
   a.sdtype = L.desc.scale_dtype, a.tiles = L.tiles, a.x = x, a.residual = residual, a.y = y;
-  const int G = L.desc.group, S = std::max(G, 64), steps = a.kp / S;
+  const int G = L.desc.group, steps = a.kp / 128;
   const int nt = column_tiles(B, dtype), nti = nt == 1 ? 0 : nt == 2 ? 1 : nt == 4 ? 2 : 3;
   const int cols = dtype == SFFN_F32 ? 2 * B : B, elems = 16 * B;
   auto up16 = [](int v) { return (v + 15) & ~15; };
-  const int xpair = 8 * nt * 8;   // bytes of the (scale, sum) pairs of a group of inputs
-  int smem = 0, ci = 3;
+  const int sum = 8 * nt * 4;   // bytes of the sums of a group of inputs
+  int smem = 0, ci = 0;
+  long long best = -1;
   if (nt == 1) {
     // The split of the inputs that gives a block the least to do, in bytes of codes that take as long: a cluster
     // costs two barriers and a pass over its sums; a run of 128 inputs of a token costs its warp 4 KB.
-    long long best = -1;
     for (int c = 0; c < 4; ++c) {
-      const int slices = kLinWarps << c;
-      const int own = (steps + slices - 1) / slices * S, own128 = (own + 127) / 128 * 128;
-      const int xbytes = up16(kLinWarps * cols * (own128 + 32) * 2) + kLinWarps * (own128 / G) * xpair;
+      const int slices = kLinWarps << c, own = (steps + slices - 1) / slices * 128;
+      const int xbytes = up16(kLinWarps * cols * (own + 32) * 2) + kLinWarps * (own / G + 1) * sum;
       const int per_tile = (kLinWarps + 1) * elems * 4;
       for (int large = 0; large < 2; ++large) {
         const int room = (large ? kLinLarge : kLinSmall) - xbytes - 64;
@@ -166,12 +171,12 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
         const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + room / per_tile - 1) / (room / per_tile));
         const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
         const long long cost = (long long)most * waves * own * kLinWarps * 8 * (large ? 1 : 2) + kClusterCost[c] +
-                               (long long)(own128 / 128) * B * 4 * 1024;
+                               (long long)(own / 128) * B * 4 * 1024;
         if (best >= 0 && cost >= best) break;
         best = cost, ci = c;
-        a.clusters = clusters, a.chunk = own128, a.chunk_stride = own128 + 32;
-        a.off_xg = up16(kLinWarps * cols * a.chunk_stride * 2);
-        a.off_part = up16(a.off_xg + kLinWarps * (own128 / G) * xpair);
+        a.clusters = clusters, a.chunk = own, a.chunk_stride = own + 32;
+        a.off_sum = up16(kLinWarps * cols * a.chunk_stride * 2);
+        a.off_part = up16(a.off_sum + kLinWarps * (own / G + 1) * sum);
         a.off_acc = a.off_part + most * kLinWarps * elems * 4;
         smem = a.off_acc + most * elems * 4;
         break;
@@ -180,25 +185,25 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
   } else {
     // The split that gives an SM the least to read, among those that keep 40 KB of sums; chunks of x as large as
     // fit, a barrier between them costs about 8 KB.
-    const int warps = linear_warps(nt), most_tiles = std::max(1, 40 * 1024 / (elems * 4));
-    long long best = -1;
+    const int warps = linear_warps(nt), rt = linear_tiles(nt), units = a.tiles / rt, uelems = rt * elems;
+    const int most_units = std::max(1, 40 * 1024 / (uelems * 4));
     for (int c = 0; c < 4; ++c) {
-      const int own = (steps + (1 << c) - 1) / (1 << c) * S, fit = std::max(1, L.fit_large[nti][c]);
-      const int clusters = std::max(std::min(a.tiles, fit), (a.tiles + most_tiles - 1) / most_tiles);
-      const int most = (a.tiles + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
-      const int room = kLinLarge - (most + 2 * warps) * elems * 4 - 64;
-      const int per128 = cols * 256 + 128 / G * xpair, pad = cols * 64;
-      const int runs = std::min((own + 127) / 128, (room - pad) / per128);
+      const int own = (steps + (1 << c) - 1) / (1 << c) * 128, fit = std::max(1, L.fit_large[nti][c]);
+      const int clusters = std::max(std::min(units, fit), (units + most_units - 1) / most_units);
+      const int most = (units + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
+      const int room = kLinLarge - (most + 2 * warps) * uelems * 4 - 64;
+      const int per128 = cols * 256 + 128 / G * sum, pad = cols * 64;
+      const int runs = std::min(own / 128, (room - pad) / per128);
       if (runs < 1) continue;
       const int chunks = (own + runs * 128 - 1) / (runs * 128);
-      const long long cost = ((long long)most * 8 * own + chunks * 8 * 1024) * waves + kClusterCost[c];
+      const long long cost = ((long long)most * rt * 8 * own + chunks * 8 * 1024) * waves + kClusterCost[c];
       if (best >= 0 && cost >= best) continue;
       best = cost, ci = c;
       a.clusters = clusters, a.chunk = runs * 128, a.chunk_stride = a.chunk + 32;
-      a.off_xg = up16(cols * a.chunk_stride * 2);
-      a.off_acc = up16(a.off_xg + a.chunk / G * xpair);
-      a.off_part = up16(a.off_acc + most * elems * 4);
-      smem = a.off_part + 2 * warps * elems * 4;
+      a.off_sum = up16(cols * a.chunk_stride * 2);
+      a.off_acc = up16(a.off_sum + a.chunk / G * sum);
+      a.off_part = up16(a.off_acc + most * uelems * 4);
+      smem = a.off_part + 2 * warps * uelems * 4;
     }
   }
   const int cs = 1 << ci, blocks = a.clusters * cs;

@@ -8,8 +8,8 @@
 // to the sums of a group in fp32. Codes go in centred although bare ones would
 // cost nothing: the tensor core cuts its addends off at 2^-24 of the largest,
 // and activations have large elements. Tokens are the 8-column operand,
-// as halves: 16-bit activations exactly, up to a power of two per token and run
-// of 128 inputs that brings the largest to 2^13; fp32 activations as two
+// as halves: 16-bit activations exactly, up to a power of two per token (and
+// share of the inputs) that brings the largest to 2^13; fp32 activations as two
 // columns, the nearest half and the nearest half of what is left (22 bits).
 //
 // Work split. The codes are read once, straight to registers, with kAhead steps'
@@ -23,7 +23,8 @@
 //   More columns (k_linear): those sums would not fit, so the (tile, run of
 // inputs) steps are numbered through and each warp takes an equal run of them;
 // x is converted once for all blocks by a small kernel before (k_linear_x),
-// because every cluster would convert the same numbers again.
+// because every cluster would convert the same numbers again. A warp takes two
+// tiles at a time with the same columns of x from shared memory.
 #pragma once
 
 #include <type_traits>
@@ -43,16 +44,19 @@ struct LinearArgs {
   int n, k, kp, B, dtype, sdtype;
   int tiles;        // 16-row tiles
   int clusters, chunk, chunk_stride;   // inputs of x held at a time (a multiple of 128), halves of a row of xs
-  int off_xg, off_acc, off_part;       // bytes in shared memory
-  const __half* ws_x;    // k_linear: x as halves [columns][kp], and
-  const float2* ws_xg;   // its (down, down * sum) pairs [groups][8 NT]
+  int off_sum, off_acc, off_part;      // bytes in shared memory
+  const __half* ws_x;    // k_linear: x as halves [columns][kp], scaled;
+  const float* ws_down;  // what undoes the scale, [8 NT];
+  const float* ws_sum;   // sums over groups [groups][8 NT] (layers with zeros)
   sffn_rows x, residual, y;
 };
 
 constexpr int kLinWarps = 8;                   // of a block of k_linear_few
 constexpr int kLinThreads = kLinWarps * 32;
-// Of a block of k_linear: one block per SM, as many warps as 64 accumulators per thread leave registers for.
-constexpr int linear_warps(int nt) { return nt == 8 ? 8 : 16; }
+// Of a block of k_linear, one per SM: tiles that a warp takes at a time, and as many warps as 64 sums per thread leave
+// registers for.
+constexpr int linear_tiles(int nt) { return nt == 8 ? 1 : 2; }
+constexpr int linear_warps(int nt) { return nt == 8 ? 8 : 12; }
 
 // Scale formats: 16-bit scales, 16-bit scales and zeros, 32-bit scales (and zeros if given).
 enum { kScale16 = 0, kScale16Zero = 1, kScale32 = 2 };
@@ -100,82 +104,95 @@ __device__ __forceinline__ uint32_t weight_high(uint32_t w) {
   return h2_u32(__hfma2(code_bits(w, 0x00f000f0u), u32_h2(0x2c002c00u), u32_h2(0xd480d480u)));
 }
 
-template <int FMT>
-struct ScaleWord {   // the scales (and zeros) of rows g and g + 8 as loaded
-  static constexpr int N = FMT == kScale16 ? 1 : FMT == kScale16Zero ? 2 : 4;
-  uint32_t w[N];
-  // entry `at` of [..][8][2] arrays
-  __device__ __forceinline__ void load(const LinearArgs& a, size_t at) {
-    if (FMT == kScale32) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.scales) + at);
-      uint2 z = make_uint2(0u, 0u);
-      if (a.zeros) z = __ldg(reinterpret_cast<const uint2*>(a.zeros) + at);
-      w[0] = v.x, w[1 % N] = v.y, w[2 % N] = z.x, w[3 % N] = z.y;
+// The scales (and zeros) of rows g and g + 8 for the groups of one step, as loaded: [tile][step][8][GS] words of two
+// 16-bit numbers, or pairs of 32-bit ones.
+template <int G, int FMT>
+struct StepScales {
+  static constexpr int GS = 128 / G, N = FMT == kScale32 ? 2 * GS : GS;   // words of each array
+  uint32_t sc[N], zr[FMT == kScale16 ? 1 : N];
+  __device__ __forceinline__ static void words(const void* p, size_t at, uint32_t* w) {
+    const uint32_t* q = static_cast<const uint32_t*>(p) + at * N;
+    if (N == 1) {
+      w[0] = __ldg(q);
+    } else if (N == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+      w[0] = v.x, w[1 % N] = v.y;
     } else {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(a.scales) + at);
-      if (FMT == kScale16Zero) w[1 % N] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros) + at);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + i));
+        w[i] = v.x, w[(i + 1) % N] = v.y, w[(i + 2) % N] = v.z, w[(i + 3) % N] = v.w;
+      }
     }
   }
-  __device__ __forceinline__ void get(int sdtype, float* sc, float* z) const {
-    z[0] = z[1] = 0.f;
+  __device__ __forceinline__ void load(const LinearArgs& a, size_t at) {   // at: (tile * steps + step) * 8 + g
+    words(a.scales, at, sc);
+    if (FMT == kScale16Zero) words(a.zeros, at, zr);
     if (FMT == kScale32) {
-      sc[0] = __uint_as_float(w[0]), sc[1] = __uint_as_float(w[1 % N]);
-      z[0] = __uint_as_float(w[2 % N]), z[1] = __uint_as_float(w[3 % N]);
-    } else {
-      two(w[0], sdtype, sc);
-      if (FMT == kScale16Zero) two(w[1 % N], sdtype, z);
+      if (a.zeros) {
+        words(a.zeros, at, zr);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) zr[i % (sizeof(zr) / 4)] = 0u;
+      }
     }
   }
-  __device__ __forceinline__ static void two(uint32_t v, int sdtype, float* o) {
-    if (sdtype == SFFN_F16) {
-      const float2 f = __half22float2(u32_h2(v));
+  __device__ __forceinline__ static void two(const uint32_t* w, int q, int sdtype, float* o) {
+    if (FMT == kScale32) {
+      o[0] = __uint_as_float(w[2 * q % N]), o[1] = __uint_as_float(w[(2 * q + 1) % N]);
+    } else if (sdtype == SFFN_F16) {
+      const float2 f = __half22float2(u32_h2(w[q % N]));
       o[0] = f.x, o[1] = f.y;
     } else {
-      o[0] = __uint_as_float(v << 16), o[1] = __uint_as_float(v & 0xffff0000u);
+      o[0] = __uint_as_float(w[q % N] << 16), o[1] = __uint_as_float(w[q % N] & 0xffff0000u);
     }
   }
 };
 
-// y += one step: S inputs of a tile's codes c with their scales s, times the
-// columns xcol[n] (this lane's column of each eight) at halves `at`, with the
-// (down, down * sum) pairs of columns 2t, 2t + 1 of the step's groups at xq
-// (xq_stride pairs from group to group).
-template <int G, int NT, int FMT>
-__device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4* c, const ScaleWord<FMT>* s,
-                                            const __half* const* xcol, int at, const float2* xq, float (*y)[4]) {
-  constexpr int S = G > 64 ? G : 64, BL = S / 64;
-  float d[NT][4];
+// y[r] += one step of 128 inputs of RT tiles: codes c[r] with scales s[r], times
+// the columns xcol[n] (this lane's column of each eight) from half `at` on, whose
+// sums over the step's groups stand at sums (rows of 8 NT).
+template <int G, int NT, int RT, int FMT>
+__device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4 (*c)[2], const StepScales<G, FMT>* s,
+                                            const __half* const* xcol, int at, const float* sums, float (*y)[NT][4]) {
+  float d[RT][NT][4];
 #pragma unroll
-  for (int b = 0; b < BL; ++b) {
-    const uint32_t w[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+  for (int h = 0; h < 4; ++h) {   // 32 inputs
+    uint32_t a0[RT][4], a1[RT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // 32 inputs
-      const uint32_t wa = w[2 * h], wb = w[2 * h + 1], ra = wa >> 8, rb = wb >> 8;
-      const uint32_t a0[4] = {weight_low(wa), weight_low(wb), weight_high(wa), weight_high(wb)};
-      const uint32_t a1[4] = {weight_low(ra), weight_low(rb), weight_high(ra), weight_high(rb)};
+    for (int r = 0; r < RT; ++r) {
+      const uint4& v = c[r][h >> 1];
+      const uint32_t wa = h & 1 ? v.z : v.x, wb = h & 1 ? v.w : v.y, ra = wa >> 8, rb = wb >> 8;
+      a0[r][0] = weight_low(wa), a0[r][1] = weight_low(wb), a0[r][2] = weight_high(wa), a0[r][3] = weight_high(wb);
+      a1[r][0] = weight_low(ra), a1[r][1] = weight_low(rb), a1[r][2] = weight_high(ra), a1[r][3] = weight_high(rb);
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + at + b * 64 + h * 32);
-        if ((b * 64 + h * 32) % G == 0) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-        mma_f16(d[n], a0, xv.x, xv.y);
-        mma_f16(d[n], a1, xv.z, xv.w);
+    for (int n = 0; n < NT; ++n) {
+      const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + at + h * 32);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (h * 32 % G == 0) d[r][n][0] = d[r][n][1] = d[r][n][2] = d[r][n][3] = 0.f;
+        mma_f16(d[r][n], a0[r], xv.x, xv.y);
+        mma_f16(d[r][n], a1[r], xv.z, xv.w);
       }
-      if ((b * 64 + h * 32 + 32) % G == 0) {   // end of a group: scales
-        const int q = (b * 64 + h * 32) / G;
+    }
+    if ((h * 32 + 32) % G == 0) {   // end of a group: scales
+      const int q = h * 32 / G;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
         float sc[2], z[2];
-        s[q].get(a.sdtype, sc, z);
+        s[r].two(s[r].sc, q, a.sdtype, sc);
+        if (FMT != kScale16) s[r].two(s[r].zr, q, a.sdtype, z);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float4 v = *reinterpret_cast<const float4*>(xq + q * (8 * NT) + 8 * n);
+          float2 v = make_float2(0.f, 0.f);
+          if (FMT != kScale16) v = *reinterpret_cast<const float2*>(sums + q * (8 * NT) + 8 * n);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (FMT == kScale16) {
-              y[n][2 * r] = fmaf(sc[r], d[n][2 * r] * v.x, y[n][2 * r]);
-              y[n][2 * r + 1] = fmaf(sc[r], d[n][2 * r + 1] * v.z, y[n][2 * r + 1]);
-            } else {
-              y[n][2 * r] = fmaf(sc[r], fmaf(d[n][2 * r], v.x, -z[r] * v.y), y[n][2 * r]);
-              y[n][2 * r + 1] = fmaf(sc[r], fmaf(d[n][2 * r + 1], v.z, -z[r] * v.w), y[n][2 * r + 1]);
-            }
+          for (int k = 0; k < 2; ++k) {
+            const float d0 = FMT == kScale16 ? d[r][n][2 * k] : fmaf(-z[k], v.x, d[r][n][2 * k]);
+            const float d1 = FMT == kScale16 ? d[r][n][2 * k + 1] : fmaf(-z[k], v.y, d[r][n][2 * k + 1]);
+            y[r][n][2 * k] = fmaf(sc[k], d0, y[r][n][2 * k]);
+            y[r][n][2 * k + 1] = fmaf(sc[k], d1, y[r][n][2 * k + 1]);
           }
         }
       }
@@ -183,57 +200,34 @@ __device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4* c,
   }
 }
 
-// N runs of 128 inputs that one warp converts together, four inputs of each per
-// lane, as halves: the nearest in hi, what is left in lo (fp32 rows only), both
-// times a power of two that `down` undoes; f16 rows are taken as they are. With
+__device__ __forceinline__ float largest(const float* v) {   // of a lane's four inputs
+  return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+}
+
+// Four inputs of a lane (of a run of 128) times a power of two as halves: the nearest in hi, what is left in lo. With
 // Sums, the sums of hi and lo over a group of G.
-template <int G, int N, bool Sums>
-__device__ __forceinline__ void convert_runs(const float (*v)[4], int dtype, uint32_t (*hi)[2], uint32_t (*lo)[2],
-                                             float* sh, float* sl, float* down) {
-  float up[N];
-  if (dtype == SFFN_F16) {
+template <int G, bool Sums>
+__device__ __forceinline__ void convert_run(const float* v, float up, uint32_t* hi, uint32_t* lo, float& sh, float& sl) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) up[i] = down[i] = 1.f;
-  } else {
-    float big[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      big[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) big[i] = fmaxf(big[i], __shfl_xor_sync(SFFN_FULL_MASK, big[i], o));
-#pragma unroll
-    for (int i = 0; i < N; ++i) scale_to_half_range(big[i], up[i], down[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int p = 0; p < 2; ++p) split_f16(v[i][2 * p] * up[i], v[i][2 * p + 1] * up[i], hi[i][p], lo[i][p]);
+  for (int p = 0; p < 2; ++p) split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
+  sh = sl = 0.f;
   if (Sums) {
+    const float2 a = __half22float2(u32_h2(hi[0])), b = __half22float2(u32_h2(hi[1]));
+    const float2 c = __half22float2(u32_h2(lo[0])), d = __half22float2(u32_h2(lo[1]));
+    sh = (a.x + a.y) + (b.x + b.y);
+    sl = (c.x + c.y) + (d.x + d.y);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 a = __half22float2(u32_h2(hi[i][0])), b = __half22float2(u32_h2(hi[i][1]));
-      const float2 c = __half22float2(u32_h2(lo[i][0])), d = __half22float2(u32_h2(lo[i][1]));
-      sh[i] = (a.x + a.y) + (b.x + b.y);
-      sl[i] = (c.x + c.y) + (d.x + d.y);
+    for (int o = 1; o < G / 4; o <<= 1) {
+      sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
+      sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
     }
-#pragma unroll
-    for (int o = 1; o < G / 4; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        sh[i] += __shfl_xor_sync(SFFN_FULL_MASK, sh[i], o);
-        sl[i] += __shfl_xor_sync(SFFN_FULL_MASK, sl[i], o);
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) sh[i] = sl[i] = 0.f;
   }
 }
 
-// The sums of a tile ([B][16]) from the fragments of one warp.
+// The sums of a tile ([B][16]) from the fragments of one warp; down undoes the scale of the lane's columns 2t, 2t + 1.
 template <int NT>
-__device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], int B, bool split, bool add, int g, int t) {
+__device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], const float (*down)[2], int B, bool split,
+                                           bool add, int g, int t) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -242,7 +236,7 @@ __device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], int 
         const int b = 4 * n + t;
         if (b < B) {
           float* p = dst + b * 16 + g + 8 * r;
-          const float v = y[n][2 * r] + y[n][2 * r + 1];
+          const float v = (y[n][2 * r] + y[n][2 * r + 1]) * down[n][0];
           *p = add ? *p + v : v;
         }
       } else {
@@ -251,7 +245,8 @@ __device__ __forceinline__ void store_tile(float* dst, const float (*y)[4], int 
           const int b = 8 * n + 2 * t + c;
           if (b < B) {
             float* p = dst + b * 16 + g + 8 * r;
-            *p = add ? *p + y[n][2 * r + c] : y[n][2 * r + c];
+            const float v = y[n][2 * r + c] * down[n][c];
+            *p = add ? *p + v : v;
           }
         }
       }
@@ -292,12 +287,12 @@ __device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* 
   if (cs > 1) cluster_barrier();
 }
 
-// At most eight columns. Shared memory: per warp its columns of x and their
-// (down, down * sum) pairs; [tile][warp][B][16] sums; for clusters [tile][B][16].
+// At most eight columns. Shared memory: per warp its columns of x, their sums
+// over groups and scales; [tile][warp][B][16] sums; for clusters [tile][B][16].
 template <int G, int FMT>
 __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs a, int cs) {
-  constexpr int S = G > 64 ? G : 64, BL = S / 64, GS = S / G;
-  constexpr int kAhead = FMT == kScale32 && G == 32 ? 4 : 8 / BL;
+  constexpr int GS = 128 / G, kAhead = G == 32 && FMT != kScale16 ? (FMT == kScale32 ? 2 : 3) : 4;   // by registers
+  constexpr bool kSums = FMT != kScale16;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
@@ -306,28 +301,26 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   // tiles of the cluster and steps of the warp: equal shares up to one
   const int tper = a.tiles / a.clusters, trest = a.tiles % a.clusters;
   const int tile0 = tper * cluster + min(cluster, trest), nt = tper + (cluster < trest);
-  const int slices = cs * kLinWarps, slice = rank * kLinWarps + warp, all_steps = a.kp / S;
+  const int slices = cs * kLinWarps, slice = rank * kLinWarps + warp, all_steps = a.kp / 128;
   const int sper = all_steps / slices, srest = all_steps % slices;
   const int k_first = sper * slice + min(slice, srest), spt = sper + (slice < srest);
   float* part = reinterpret_cast<float*>(smem + a.off_part);   // [tile][warp][elems]
 
-  const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + ((size_t)tile0 * (a.kp / 64) + (size_t)k_first * BL) * 32 + lane;
-  size_t sp = ((size_t)tile0 * (a.kp / G) + (size_t)k_first * GS) * 8 + g;
-  const size_t cp_skip = (size_t)(a.kp / 64 - spt * BL) * 32, sp_skip = (size_t)(a.kp / G - spt * GS) * 8;
-  const int steps = nt * spt;
-  uint4 cw[kAhead][BL];
-  ScaleWord<FMT> sw[kAhead][GS];
+  const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + ((size_t)tile0 * all_steps + k_first) * 64 + lane;
+  size_t sp = ((size_t)tile0 * all_steps + k_first) * 8 + g;
+  const int skip = all_steps - spt, steps = nt * spt;
+  uint4 cw[kAhead][1][2];
+  StepScales<G, FMT> sw[kAhead][1];
   int left = steps, ld_k = 0;
-  auto load = [&](uint4* c, ScaleWord<FMT>* s) {
+  auto load = [&](uint4 (*c)[2], StepScales<G, FMT>* s) {
     if (left > 0) {
       --left;
-#pragma unroll
-      for (int b = 0; b < BL; ++b) c[b] = ldg_stream(cp + b * 32);
-#pragma unroll
-      for (int q = 0; q < GS; ++q) s[q].load(a, sp + q * 8);
-      cp += BL * 32;
-      sp += GS * 8;
-      if (++ld_k == spt) ld_k = 0, cp += cp_skip, sp += sp_skip;
+      c[0][0] = ldg_stream(cp);
+      c[0][1] = ldg_stream(cp + 32);
+      s[0].load(a, sp);
+      cp += 64;
+      sp += 8;
+      if (++ld_k == spt) ld_k = 0, cp += (size_t)skip * 64, sp += (size_t)skip * 8;
     }
   };
 #pragma unroll
@@ -335,35 +328,53 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the warp's share of x, kBatch runs of 128 inputs at a time
+  // ---- the warp's share of x, token by token, kBatch runs of 128 inputs at a time
   constexpr int kBatch = 4;
   __half* xs = reinterpret_cast<__half*>(smem) + (size_t)warp * cols * a.chunk_stride;
-  float2* xg = reinterpret_cast<float2*>(smem + a.off_xg) + (size_t)warp * (a.chunk / G) * 8;
-  const int k0 = k_first * S, kn = spt * S, runs = (kn + 127) / 128, tasks = runs * a.B;
-  for (int task = 0, b = 0, run = 0; task < tasks; task += kBatch) {
-    float v[kBatch][4], sh[kBatch], sl[kBatch], down[kBatch];
-    uint32_t hi[kBatch][2], lo[kBatch][2];
-    int at[kBatch], bs[kBatch];
+  float* sums = reinterpret_cast<float*>(smem + a.off_sum) + (size_t)warp * (a.chunk / G + 1) * 8;   // last row: down
+  float* downs = sums + (a.chunk / G) * 8;
+  const int k0 = k_first * 128;
+  for (int b = 0; b < a.B; ++b) {
+    float v[kBatch][4];
+    auto fetch = [&](int run0) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int kk = run * 128 + lane * 4;
-      at[i] = task + i < tasks && kk < kn ? kk : -1;
-      bs[i] = b;
-      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-      if (at[i] >= 0 && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
-      if (++run == runs) run = 0, ++b;
+      for (int i = 0; i < kBatch; ++i) {
+        const int kk = (run0 + i) * 128 + lane * 4;
+        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+        if (run0 + i < spt && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
+      }
+    };
+    float up = 1.f, down = 1.f;
+    fetch(0);
+    if (a.dtype != SFFN_F16) {   // f16 rows are taken as they are
+      float big = 0.f;
+      for (int run0 = 0; run0 < spt; run0 += kBatch) {
+        if (run0) fetch(run0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) big = fmaxf(big, largest(v[i]));
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
+      scale_to_half_range(big, up, down);
+      if (spt > kBatch) fetch(0);
     }
-    convert_runs<G, kBatch, FMT != kScale16>(v, a.dtype, hi, lo, sh, sl, down);
+    const int col = split ? 2 * b : b;
+    if (lane == 0) downs[col] = downs[split ? col + 1 : col] = down;
+    for (int run0 = 0; run0 < spt; run0 += kBatch) {
+      if (run0) fetch(run0);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (at[i] < 0) continue;
-      const int col = split ? 2 * bs[i] : bs[i];
-      *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + at[i]) = make_uint2(hi[i][0], hi[i][1]);
-      if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + at[i]) = make_uint2(lo[i][0], lo[i][1]);
-      if (lane % (G / 4) == 0) {
-        float2* p = xg + (at[i] / G) * 8 + col;
-        p[0] = make_float2(down[i], down[i] * sh[i]);
-        if (split) p[1] = make_float2(down[i], down[i] * sl[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        if (run0 + i >= spt) break;
+        uint32_t hi[2], lo[2];
+        float sh, sl;
+        convert_run<G, kSums>(v[i], up, hi, lo, sh, sl);
+        const int kk = (run0 + i) * 128 + lane * 4;
+        *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
+        if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
+        if (kSums && lane % (G / 4) == 0) {
+          sums[kk / G * 8 + col] = sh;
+          if (split) sums[kk / G * 8 + col + 1] = sl;
+        }
       }
     }
   }
@@ -371,19 +382,20 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
 
   // ---- steps
   const __half* xcol[1] = {xs + (size_t)min(g, cols - 1) * a.chunk_stride + 8 * t};   // columns past the end: not used
-  float y[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  const float down[1][2] = {{downs[2 * t], downs[2 * t + 1]}};
+  float y[1][1][4] = {{{0.f, 0.f, 0.f, 0.f}}};
   float* dst = part + (size_t)warp * elems;
   int kk = 0;
   for (int s = 0; s < steps;) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (s < steps) {
-        linear_step<G, 1, FMT>(a, cw[i], sw[i], xcol, kk * S, xg + kk * GS * 8 + 2 * t, y);
+        linear_step<G, 1, 1, FMT>(a, cw[i], sw[i], xcol, kk * 128, sums + kk * GS * 8 + 2 * t, y);
         load(cw[i], sw[i]);
         ++s;
         if (++kk == spt) {
-          store_tile<1>(dst, y, a.B, split, false, g, t);
-          y[0][0] = y[0][1] = y[0][2] = y[0][3] = 0.f;
+          store_tile<1>(dst, y[0], down, a.B, split, false, g, t);
+          y[0][0][0] = y[0][0][1] = y[0][0][2] = y[0][0][3] = 0.f;
           dst += kLinWarps * elems;
           kk = 0;
         }
@@ -391,7 +403,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
     }
   }
   if (spt == 0)   // a warp without inputs
-    for (int i = 0; i < nt; ++i, dst += kLinWarps * elems) store_tile<1>(dst, y, a.B, split, false, g, t);
+    for (int i = threadIdx.x & 31; i < nt * elems; i += 32) part[((size_t)(i / elems) * kLinWarps + warp) * elems + i % elems] = 0.f;
   __syncthreads();
 
   // ---- the block's sums, in warp order
@@ -408,76 +420,116 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   write_outputs(a, acc_s, tile0, nt, cs, rank, kLinThreads);
 }
 
-// x of a call as halves, and its pairs, for k_linear: one warp per token and run of 128 inputs.
-template <int G, int FMT>
-__global__ void __launch_bounds__(256) k_linear_x(const LinearArgs a, int pairs, __half* xh, float2* xg) {
+// x of a call as halves, and its sums over groups, for k_linear: one block per token.
+template <int G, bool Sums>
+__global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int columns, __half* xh, float* downs, float* sums) {
+  constexpr int kKeep = 4;   // runs of 128 inputs that a warp keeps between the two passes
+  __shared__ float s_big[16];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, runs = (a.kp + 127) / 128, task = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (task >= a.B * runs) return;
-  const int b = task / runs, kk = (task - b * runs) * 128 + lane * 4;
-  float v[1][4] = {{0.f, 0.f, 0.f, 0.f}}, sh[1], sl[1], down[1];
-  uint32_t hi[1][2], lo[1][2];
-  if (kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + kk, a.dtype, v[0]);
-  convert_runs<G, 1, FMT != kScale16>(v, a.dtype, hi, lo, sh, sl, down);
-  if (kk >= a.kp) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, runs = a.kp / 128;
+  float v[kKeep][4], big = 0.f;
+  auto fetch = [&](int run, float* o) {
+    const int kk = run * 128 + lane * 4;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+    if (run < runs && kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + kk, a.dtype, o);
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) fetch(warp + 16 * i, v[i]);
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) big = fmaxf(big, largest(v[i]));
+  for (int run = warp + 16 * kKeep; run < runs; run += 16) {
+    float o[4];
+    fetch(run, o);
+    big = fmaxf(big, largest(o));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
+  if (lane == 0) s_big[warp] = big;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) big = fmaxf(big, s_big[w]);
+  float up, down;
+  scale_to_half_range(big, up, down);
   const bool split = a.dtype == SFFN_F32;
   const int col = split ? 2 * b : b;
-  *reinterpret_cast<uint2*>(xh + (size_t)col * a.kp + kk) = make_uint2(hi[0][0], hi[0][1]);
-  if (split) *reinterpret_cast<uint2*>(xh + (size_t)(col + 1) * a.kp + kk) = make_uint2(lo[0][0], lo[0][1]);
-  if (lane % (G / 4) == 0) {
-    float2* p = xg + (size_t)(kk / G) * pairs + col;
-    p[0] = make_float2(down[0], down[0] * sh[0]);
-    if (split) p[1] = make_float2(down[0], down[0] * sl[0]);
+  if (threadIdx.x == 0) downs[col] = downs[split ? col + 1 : col] = down;
+  auto put = [&](int run, const float* o) {
+    uint32_t hi[2], lo[2];
+    float sh, sl;
+    convert_run<G, Sums>(o, up, hi, lo, sh, sl);
+    const int kk = run * 128 + lane * 4;
+    *reinterpret_cast<uint2*>(xh + (size_t)col * a.kp + kk) = make_uint2(hi[0], hi[1]);
+    if (split) *reinterpret_cast<uint2*>(xh + (size_t)(col + 1) * a.kp + kk) = make_uint2(lo[0], lo[1]);
+    if (Sums && lane % (G / 4) == 0) {
+      sums[(size_t)(kk / G) * columns + col] = sh;
+      if (split) sums[(size_t)(kk / G) * columns + col + 1] = sl;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (warp + 16 * i < runs) put(warp + 16 * i, v[i]);
+  for (int run = warp + 16 * kKeep; run < runs; run += 16) {
+    float o[4];
+    fetch(run, o);
+    put(run, o);
   }
 }
 
+// More than eight columns.
 template <int G, int NT, int FMT>
 __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const LinearArgs a, int cs) {
-  constexpr int kWarps = linear_warps(NT), kThreads = kWarps * 32;
-  constexpr int S = G > 64 ? G : 64;        // inputs of a step
-  constexpr int BL = S / 64, GS = S / G;    // 64-input blocks and groups of a step
-  constexpr int kAhead = FMT == kScale32 && G == 32 ? 4 : 8 / BL;   // by registers
+  constexpr int kWarps = linear_warps(NT), kThreads = kWarps * 32, RT = linear_tiles(NT), GS = 128 / G;
+  constexpr int kAhead = RT == 2 ? (FMT == kScale16 || G == 128 ? 3 : 2) : (FMT == kScale32 && G == 32 ? 2 : 4);  // by registers
+  constexpr bool kSums = FMT != kScale16;
   extern __shared__ __align__(16) uint8_t smem[];
   __half* xs = reinterpret_cast<__half*>(smem);                  // [columns][chunk_stride]
-  float2* xg = reinterpret_cast<float2*>(smem + a.off_xg);       // [groups of a chunk][8 NT]: down, down * sum(x)
+  float* sums = reinterpret_cast<float*>(smem + a.off_sum);      // [groups of a chunk][8 NT]
   float* acc_s = reinterpret_cast<float*>(smem + a.off_acc);     // [tiles of the cluster][B][16]
-  float* part = reinterpret_cast<float*>(smem + a.off_part);     // [warp][2][B][16]
-  __shared__ int s_tile[kWarps][2];                              // tile of a part, -1: none
+  float* part = reinterpret_cast<float*>(smem + a.off_part);     // [warp][2][RT][B][16]
+  __shared__ int s_unit[kWarps][2];                              // unit (RT tiles) of a part, -1: none
   __shared__ uint64_t s_bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
-  const int tile0 = (int)((long long)cluster * a.tiles / a.clusters);
-  const int nt = (int)((long long)(cluster + 1) * a.tiles / a.clusters) - tile0;
-  // this block's inputs, in steps
-  const int all_steps = (a.kp + S - 1) / S;
-  const int k_step0 = all_steps * rank / cs, k_step1 = all_steps * (rank + 1) / cs;
+  // units of the cluster and steps of the block: equal shares up to one
+  const int all_units = a.tiles / RT, uper = all_units / a.clusters, urest = all_units % a.clusters;
+  const int unit0 = uper * cluster + min(cluster, urest), nu = uper + (cluster < urest);
+  const int all_steps = a.kp / 128, sper = all_steps / cs, srest = all_steps % cs;
+  const int k_step0 = sper * rank + min(rank, srest), k_step1 = k_step0 + sper + (rank < srest);
   const bool split = a.dtype == SFFN_F32;
-  const int cols = split ? 2 * a.B : a.B, elems = a.B * 16;
-  const int chunk_steps = a.chunk / S;
-  const int groups = a.kp / G, blocks64 = a.kp / 64;
+  const int cols = split ? 2 * a.B : a.B, elems = a.B * 16, uelems = RT * elems;
+  const int chunk_steps = a.chunk / 128;
 
   uint32_t phase = 0;
+  float down[NT][2];
   for (int c0 = k_step0; c0 < k_step1 || c0 == k_step0; c0 += chunk_steps) {
-    const int spt = min(chunk_steps, k_step1 - c0);   // steps of a tile in this chunk
-    const int steps = nt * max(spt, 0);
-    const int s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;
+    const int spt = max(0, min(chunk_steps, k_step1 - c0));   // steps of a unit in this chunk
+    const int steps = nu * spt, s0 = steps * warp / kWarps, s1 = steps * (warp + 1) / kWarps;
 
     // ---- the first loads of codes and scales: these do not depend on an earlier kernel
-    uint4 cw[kAhead][BL];
-    ScaleWord<FMT> sw[kAhead][GS];
-    int ld_tile = spt > 0 ? s0 / spt : 0, ld_k = spt > 0 ? s0 % spt : 0, ld_s = s0;
-    auto load = [&](uint4* c, ScaleWord<FMT>* s) {
-      if (ld_s < s1) {
-        const size_t tile = tile0 + ld_tile;
-        const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + (tile * blocks64 + (size_t)(c0 + ld_k) * BL) * 32 + lane;
+    uint4 cw[kAhead][RT][2];
+    StepScales<G, FMT> sw[kAhead][RT];
+    int unit = spt > 0 ? s0 / spt : 0, kk = spt > 0 ? s0 - unit * spt : 0;
+    const size_t first = (size_t)(unit0 + unit) * RT * all_steps + c0 + kk;
+    const uint4* cp = reinterpret_cast<const uint4*>(a.codes) + first * 64 + lane;
+    size_t sp = first * 8 + g;
+    int left = s1 - s0, ld_k = kk;
+    auto load = [&](uint4 (*c)[2], StepScales<G, FMT>* s) {
+      if (left > 0) {
+        --left;
 #pragma unroll
-        for (int b = 0; b < BL; ++b) c[b] = ldg_stream(cp + b * 32);   // kp is a multiple of S
-        const size_t at = (tile * groups + (size_t)(c0 + ld_k) * GS) * 8 + g;
-#pragma unroll
-        for (int q = 0; q < GS; ++q) s[q].load(a, at + q * 8);
-        if (++ld_k == spt) ld_k = 0, ++ld_tile;
-        ++ld_s;
+        for (int r = 0; r < RT; ++r) {
+          c[r][0] = ldg_stream(cp + (size_t)r * all_steps * 64);
+          c[r][1] = ldg_stream(cp + (size_t)r * all_steps * 64 + 32);
+          s[r].load(a, sp + (size_t)r * all_steps * 8);
+        }
+        cp += 64;
+        sp += 8;
+        if (++ld_k == spt) {
+          ld_k = 0;
+          cp += (size_t)(RT * all_steps - spt) * 64;
+          sp += (size_t)(RT * all_steps - spt) * 8;
+        }
       }
     };
 #pragma unroll
@@ -488,87 +540,94 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
       fence_mbar_init();
       pdl_launch_dependents();
       pdl_wait();
-      for (int i = threadIdx.x; i < nt * elems; i += kThreads) acc_s[i] = 0.f;
-      if (threadIdx.x < 2 * kWarps) (&s_tile[0][0])[threadIdx.x] = -1;
+      for (int i = threadIdx.x; i < nu * uelems; i += kThreads) acc_s[i] = 0.f;
+      if (threadIdx.x < 2 * kWarps) (&s_unit[0][0])[threadIdx.x] = -1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int c = 8 * n + 2 * t;
+        down[n][0] = c < cols ? ld_dep(a.ws_down + c) : 0.f;
+        down[n][1] = c + 1 < cols ? ld_dep(a.ws_down + c + 1) : 0.f;
+      }
     }
     __syncthreads();   // every warp is done with the chunk before
 
-    // ---- x of the chunk: a bulk copy per column, and one for the pairs
+    // ---- x of the chunk: a bulk copy per column, and one for the sums
     if (warp == 0 && spt > 0) {
-      const uint32_t row = (uint32_t)spt * S * 2, pair = (uint32_t)spt * GS * 8 * NT * 8;
-      if (lane == 0) mbar_arrive_expect_tx(&s_bar, row * cols + pair);
+      const uint32_t row = (uint32_t)spt * 256, sum = kSums ? (uint32_t)spt * GS * 8 * NT * 4 : 0u;
+      if (lane == 0) mbar_arrive_expect_tx(&s_bar, row * cols + sum);
       __syncwarp();
       const uint64_t pol = l2_policy_keep();
       for (int c = lane; c < cols; c += 32)
-        bulk_g2s(xs + (size_t)c * a.chunk_stride, a.ws_x + (size_t)c * a.kp + (size_t)c0 * S, row, &s_bar, pol);
-      if (lane == 0) bulk_g2s(xg, a.ws_xg + (size_t)c0 * GS * 8 * NT, pair, &s_bar, pol);
+        bulk_g2s(xs + (size_t)c * a.chunk_stride, a.ws_x + (size_t)c * a.kp + (size_t)c0 * 128, row, &s_bar, pol);
+      if (kSums && lane == 0) bulk_g2s(sums, a.ws_sum + (size_t)c0 * GS * 8 * NT, sum, &s_bar, pol);
     }
-    if (spt > 0 && !mbar_wait_bounded(&s_bar, phase)) {
-      set_device_error(a.err, SFFN_ERR_TIMEOUT);
-      mbar_wait_bounded(&s_bar, phase);   // the copies must land before the block ends
+    if (spt > 0) {
+      if (!mbar_wait_bounded(&s_bar, phase)) {
+        set_device_error(a.err, SFFN_ERR_TIMEOUT);
+        mbar_wait_bounded(&s_bar, phase);   // the copies must land before the block ends
+      }
+      phase ^= 1;
     }
-    phase ^= 1;
 
     // ---- the warp's steps
-    float y[NT][4];
-    int tile = spt > 0 ? s0 / spt : 0, kk = spt > 0 ? s0 % spt : 0;
+    float y[RT][NT][4];
     const int first_k = kk;
-    bool fresh = true, first = true;
+    bool fresh = true, begun = false;
     const __half* xcol[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int c = 8 * n + g;   // columns past the end repeat the last one; their results are not used
-      xcol[n] = xs + (size_t)min(c, cols - 1) * a.chunk_stride + 8 * t;
-    }
-    auto store = [&](float* dst, bool add) { store_tile<NT>(dst, y, a.B, split, add, g, t); };
-    auto step = [&](const uint4* c, const ScaleWord<FMT>* s) {
-      if (fresh) {
-        fresh = false;
+    for (int n = 0; n < NT; ++n)   // columns past the end repeat the last one; their results are not used
+      xcol[n] = xs + (size_t)min(8 * n + g, cols - 1) * a.chunk_stride + 8 * t;
+    auto store = [&](float* dst, bool add) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
-      }
-      linear_step<G, NT, FMT>(a, c, s, xcol, kk * S, xg + (size_t)kk * GS * (8 * NT) + 2 * t, y);
-      if (++kk == spt) {
-        // a tile that began in this warp's run is complete; the tail of an earlier warp's tile is a part
-        if (first && first_k != 0) {
-          store(part + (size_t)(warp * 2) * elems, false);
-          if (lane == 0) s_tile[warp][0] = tile;
-        } else {
-          store(acc_s + (size_t)tile * elems, true);
-        }
-        first = false;
-        fresh = true;
-        kk = 0;
-        ++tile;
-      }
+      for (int r = 0; r < RT; ++r) store_tile<NT>(dst + r * elems, y[r], down, a.B, split, add, g, t);
     };
     for (int s = s0; s < s1;) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (s < s1) {
-          step(cw[i], sw[i]);
+          if (fresh) {
+            fresh = false;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) y[r][n][0] = y[r][n][1] = y[r][n][2] = y[r][n][3] = 0.f;
+          }
+          linear_step<G, NT, RT, FMT>(a, cw[i], sw[i], xcol, kk * 128, sums + kk * GS * (8 * NT) + 2 * t, y);
           load(cw[i], sw[i]);
           ++s;
+          if (++kk == spt) {
+            // units that began in this warp's run are complete; the tail of an earlier warp's is a part
+            if (!begun && first_k != 0) {
+              store(part + (size_t)(warp * 2) * uelems, false);
+              if (lane == 0) s_unit[warp][0] = unit;
+            } else {
+              store(acc_s + (size_t)unit * uelems, true);
+            }
+            begun = fresh = true;
+            kk = 0;
+            ++unit;
+          }
         }
       }
     }
-    if (!fresh) {   // the head of a tile that a later warp completes
-      store(part + (size_t)(warp * 2 + 1) * elems, false);
-      if (lane == 0) s_tile[warp][1] = tile;
+    if (!fresh) {   // the head of a unit that a later warp completes
+      store(part + (size_t)(warp * 2 + 1) * uelems, false);
+      if (lane == 0) s_unit[warp][1] = unit;
     }
     __syncthreads();
     // parts in warp order; a thread keeps to its elements, so no barrier is needed between them
-    for (int e = threadIdx.x; e < elems; e += kThreads)
+    for (int e = threadIdx.x; e < uelems; e += kThreads)
       for (int p = 0; p < 2 * kWarps; ++p) {
-        const int pt = (&s_tile[0][0])[p];
-        if (pt >= 0) acc_s[(size_t)pt * elems + e] += part[(size_t)p * elems + e];
+        const int pu = (&s_unit[0][0])[p];
+        if (pu >= 0) acc_s[(size_t)pu * uelems + e] += part[(size_t)p * uelems + e];
       }
     __syncthreads();
-    if (threadIdx.x < 2 * kWarps) (&s_tile[0][0])[threadIdx.x] = -1;
-    if (spt <= 0) break;
+    if (threadIdx.x < 2 * kWarps) (&s_unit[0][0])[threadIdx.x] = -1;
+    if (spt == 0) break;
   }
 
-  write_outputs(a, acc_s, tile0, nt, cs, rank, kThreads);
+  // ---- the cluster's blocks add their sums; each writes its share of the outputs
+  write_outputs(a, acc_s, unit0 * RT, nu * RT, cs, rank, kThreads);
 }
 
 // Calls f with the kernel of a number of column tiles and a scale format.
@@ -614,9 +673,9 @@ cudaError_t prepare(int nt, int fmt, LinearFit* fit) {
 template <int G>
 cudaError_t run(int nt, int fmt, int cluster, const LinearArgs& a, int blocks, int smem, cudaStream_t st) {
   if (nt > 1) {
-    auto* kx = fmt == kScale16 ? k_linear_x<G, kScale16> : k_linear_x<G, kScale32>;   // sums only where there are zeros
-    const cudaError_t e = launch_ex(kx, dim3((a.B * ((a.kp + 127) / 128) + 7) / 8), dim3(256), 0, st, true, 1, a, 8 * nt,
-                                    const_cast<__half*>(a.ws_x), const_cast<float2*>(a.ws_xg));
+    auto* kx = fmt == kScale16 ? k_linear_x<G, false> : k_linear_x<G, true>;   // sums only where there are zeros
+    const cudaError_t e = launch_ex(kx, dim3(a.B), dim3(512), 0, st, true, 1, a, 8 * nt, const_cast<__half*>(a.ws_x),
+                                    const_cast<float*>(a.ws_down), const_cast<float*>(a.ws_sum));
     if (e != cudaSuccess) return e;
   }
   return with_kernel<G>(nt, fmt, [&](auto* kern) {
