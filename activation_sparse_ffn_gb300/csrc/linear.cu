@@ -184,26 +184,25 @@ cudaError_t launch_linear(const sffn_linear& L, const sffn_rows& x, int B, const
     }
   } else {
     // The split that gives an SM the least to read, among those that keep 40 KB of sums; chunks of x as large as
-    // fit, a barrier between them costs about 8 KB.
+    // fit, since the loads in flight run dry between them, which costs about 64 KB. The warps' parts stand over x.
     const int warps = linear_warps(nt), rt = linear_tiles(nt), units = a.tiles / rt, uelems = rt * elems;
     const int most_units = std::max(1, 40 * 1024 / (uelems * 4));
     for (int c = 0; c < 4; ++c) {
       const int own = (steps + (1 << c) - 1) / (1 << c) * 128, fit = std::max(1, L.fit_large[nti][c]);
       const int clusters = std::max(std::min(units, fit), (units + most_units - 1) / most_units);
       const int most = (units + clusters - 1) / clusters, waves = (clusters + fit - 1) / fit;
-      const int room = kLinLarge - (most + 2 * warps) * uelems * 4 - 64;
+      const int room = kLinLarge - most * uelems * 4 - 64;
       const int per128 = cols * 256 + 128 / G * sum, pad = cols * 64;
       const int runs = std::min(own / 128, (room - pad) / per128);
-      if (runs < 1) continue;
+      if (runs < 1 || warps * uelems * 4 > room) continue;
       const int chunks = (own + runs * 128 - 1) / (runs * 128);
-      const long long cost = ((long long)most * rt * 8 * own + chunks * 8 * 1024) * waves + kClusterCost[c];
+      const long long cost = ((long long)most * rt * 8 * own + chunks * 64 * 1024) * waves + kClusterCost[c];
       if (best >= 0 && cost >= best) continue;
       best = cost, ci = c;
       a.clusters = clusters, a.chunk = runs * 128, a.chunk_stride = a.chunk + 32;
       a.off_sum = up16(cols * a.chunk_stride * 2);
-      a.off_acc = up16(a.off_sum + a.chunk / G * sum);
-      a.off_part = up16(a.off_acc + most * uelems * 4);
-      smem = a.off_part + 2 * warps * uelems * 4;
+      a.off_acc = up16(std::max(a.off_sum + a.chunk / G * sum, warps * uelems * 4));   // parts stand where x stood
+      smem = a.off_acc + most * uelems * 4;
     }
   }
   const int cs = 1 << ci, blocks = a.clusters * cs;

@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
   __half* xs = reinterpret_cast<__half*>(smem);                  // [columns][chunk_stride]
   float* sums = reinterpret_cast<float*>(smem + a.off_sum);      // [groups of a chunk][8 NT]
   float* acc_s = reinterpret_cast<float*>(smem + a.off_acc);     // [tiles of the cluster][B][16]
-  float* part = reinterpret_cast<float*>(smem + a.off_part);     // [warp][2][RT][B][16]
-  __shared__ int s_unit[kWarps][2];                              // unit (RT tiles) of a part, -1: none
+  float* part = reinterpret_cast<float*>(smem);                  // [warp][RT][B][16], over xs once that is read
+  __shared__ int s_unit[kWarps];                                 // unit (RT tiles) of a part, -1: none
   __shared__ uint64_t s_bar;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
@@ -541,7 +541,6 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
       pdl_launch_dependents();
       pdl_wait();
       for (int i = threadIdx.x; i < nu * uelems; i += kThreads) acc_s[i] = 0.f;
-      if (threadIdx.x < 2 * kWarps) (&s_unit[0][0])[threadIdx.x] = -1;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int c = 8 * n + 2 * t;
@@ -549,10 +548,12 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
         down[n][1] = c + 1 < cols ? ld_dep(a.ws_down + c + 1) : 0.f;
       }
     }
+    if (lane == 0) s_unit[warp] = -1;
     __syncthreads();   // every warp is done with the chunk before
 
     // ---- x of the chunk: a bulk copy per column, and one for the sums
     if (warp == 0 && spt > 0) {
+      fence_proxy_async_smem();   // the parts of the chunk before stood where the copies go
       const uint32_t row = (uint32_t)spt * 256, sum = kSums ? (uint32_t)spt * GS * 8 * NT * 4 : 0u;
       if (lane == 0) mbar_arrive_expect_tx(&s_bar, row * cols + sum);
       __syncwarp();
@@ -571,8 +572,7 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
 
     // ---- the warp's steps
     float y[RT][NT][4];
-    const int first_k = kk;
-    bool fresh = true, begun = false;
+    bool fresh = true;
     const __half* xcol[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)   // columns past the end repeat the last one; their results are not used
@@ -596,33 +596,27 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
           load(cw[i], sw[i]);
           ++s;
           if (++kk == spt) {
-            // units that began in this warp's run are complete; the tail of an earlier warp's is a part
-            if (!begun && first_k != 0) {
-              store(part + (size_t)(warp * 2) * uelems, false);
-              if (lane == 0) s_unit[warp][0] = unit;
-            } else {
-              store(acc_s + (size_t)unit * uelems, true);
-            }
-            begun = fresh = true;
+            store(acc_s + (size_t)unit * uelems, true);   // of the warps of a unit, only the one that ends it does this
+            fresh = true;
             kk = 0;
             ++unit;
           }
         }
       }
     }
-    if (!fresh) {   // the head of a unit that a later warp completes
-      store(part + (size_t)(warp * 2 + 1) * uelems, false);
-      if (lane == 0) s_unit[warp][1] = unit;
+    __syncthreads();
+    if (!fresh) {   // the head of a unit that a later warp ended
+      store(part + (size_t)warp * uelems, false);
+      if (lane == 0) s_unit[warp] = unit;
     }
     __syncthreads();
     // parts in warp order; a thread keeps to its elements, so no barrier is needed between them
     for (int e = threadIdx.x; e < uelems; e += kThreads)
-      for (int p = 0; p < 2 * kWarps; ++p) {
-        const int pu = (&s_unit[0][0])[p];
+      for (int p = 0; p < kWarps; ++p) {
+        const int pu = s_unit[p];
         if (pu >= 0) acc_s[(size_t)pu * uelems + e] += part[(size_t)p * uelems + e];
       }
     __syncthreads();
-    if (threadIdx.x < 2 * kWarps) (&s_unit[0][0])[threadIdx.x] = -1;
     if (spt == 0) break;
   }
 
