@@ -166,15 +166,25 @@ __device__ __forceinline__ void linear_step(const LinearArgs& a, const uint4 (*c
       a0[r][0] = weight_low(wa), a0[r][1] = weight_low(wb), a0[r][2] = weight_high(wa), a0[r][3] = weight_high(wb);
       a1[r][0] = weight_low(ra), a1[r][1] = weight_low(rb), a1[r][2] = weight_high(ra), a1[r][3] = weight_high(rb);
     }
+    // two products go into a sum: those of other sums come between them
+    constexpr int NP = NT > 1 ? 2 : 1;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint4 xv = *reinterpret_cast<const uint4*>(xcol[n] + at + h * 32);
+    for (int n0 = 0; n0 < NT; n0 += NP) {
+      uint4 xv[NP];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (h * 32 % G == 0) d[r][n][0] = d[r][n][1] = d[r][n][2] = d[r][n][3] = 0.f;
-        mma_f16(d[r][n], a0[r], xv.x, xv.y);
-        mma_f16(d[r][n], a1[r], xv.z, xv.w);
-      }
+      for (int n = 0; n < NP; ++n) xv[n] = *reinterpret_cast<const uint4*>(xcol[n0 + n] + at + h * 32);
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float* p = d[r][n0 + n];
+          if (h * 32 % G == 0) p[0] = p[1] = p[2] = p[3] = 0.f;
+          mma_f16(p, a0[r], xv[n].x, xv[n].y);
+        }
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mma_f16(d[r][n0 + n], a1[r], xv[n].z, xv[n].w);
     }
     if ((h * 32 + 32) % G == 0) {   // end of a group: scales
       const int q = h * 32 / G;
@@ -280,9 +290,15 @@ __device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* 
       s = *reinterpret_cast<const float4*>(acc_s + 4 * e);
     }
     const float o[4] = {s.x + v.x + r[0], s.y + v.y + r[1], s.z + v.z + r[2], s.w + v.w + r[3]};
+    const size_t at = (size_t)(b * a.y.row_stride) + n;
+    const int es = a.dtype == SFFN_F32 ? 4 : 2;
+    if (n + 3 < a.n && (reinterpret_cast<uintptr_t>(a.y.ptr) + at * es) % (4 * es) == 0) {
+      st_run<4>(a.y.ptr, at, a.dtype, o);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.n) st_elem(a.y.ptr, (size_t)(b * a.y.row_stride) + n + i, o[i], a.dtype);
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.n) st_elem(a.y.ptr, at + i, o[i], a.dtype);
+    }
   }
   if (cs > 1) cluster_barrier();
 }
@@ -610,12 +626,21 @@ __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const Linea
       if (lane == 0) s_unit[warp] = unit;
     }
     __syncthreads();
-    // parts in warp order; a thread keeps to its elements, so no barrier is needed between them
-    for (int e = threadIdx.x; e < uelems; e += kThreads)
-      for (int p = 0; p < kWarps; ++p) {
-        const int pu = s_unit[p];
-        if (pu >= 0) acc_s[(size_t)pu * uelems + e] += part[(size_t)p * uelems + e];
+    // the first warp with a part of a unit adds all of that unit, in warp order
+    const int mine = s_unit[warp];
+    const unsigned same = __ballot_sync(SFFN_FULL_MASK, lane < kWarps && s_unit[min(lane, kWarps - 1)] == mine);
+    if (mine >= 0 && __ffs(same) - 1 == warp) {
+      float4* dst = reinterpret_cast<float4*>(acc_s + (size_t)mine * uelems);
+#pragma unroll 4
+      for (int e = lane; e < uelems / 4; e += 32) {
+        float4 v = dst[e];
+        for (unsigned left = same; left; left &= left - 1) {
+          const float4 x = reinterpret_cast<const float4*>(part + (size_t)(__ffs(left) - 1) * uelems)[e];
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        dst[e] = v;
       }
+    }
     __syncthreads();
     if (spt == 0) break;
   }
