@@ -350,34 +350,40 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   float* sums = reinterpret_cast<float*>(smem + a.off_sum) + (size_t)warp * (a.chunk / G + 1) * 8;   // last row: down
   float* downs = sums + (a.chunk / G) * 8;
   const int k0 = k_first * 128;
-  for (int b = 0; b < a.B; ++b) {
-    float v[kBatch][4];
-    auto fetch = [&](int run0) {
+  float v[kBatch][4], ahead[kBatch][4];   // of this token, and the first runs of the next
+  auto fetch = [&](int b, int run0, float (*o)[4]) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int kk = (run0 + i) * 128 + lane * 4;
-        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-        if (run0 + i < spt && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, v[i]);
-      }
-    };
+    for (int i = 0; i < kBatch; ++i) {
+      const int kk = (run0 + i) * 128 + lane * 4;
+      o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      if (run0 + i < spt && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, o[i]);
+    }
+  };
+  fetch(0, 0, ahead);
+#pragma unroll 1
+  for (int b = 0; b < a.B; ++b) {
     float up = 1.f, down = 1.f;
-    fetch(0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = ahead[i][e];
+    if (b + 1 < a.B) fetch(b + 1, 0, ahead);
     if (a.dtype != SFFN_F16) {   // f16 rows are taken as they are
       float big = 0.f;
       for (int run0 = 0; run0 < spt; run0 += kBatch) {
-        if (run0) fetch(run0);
+        if (run0) fetch(b, run0, v);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) big = fmaxf(big, largest(v[i]));
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
       scale_to_half_range(big, up, down);
-      if (spt > kBatch) fetch(0);
+      if (spt > kBatch) fetch(b, 0, v);
     }
     const int col = split ? 2 * b : b;
     if (lane == 0) downs[col] = downs[split ? col + 1 : col] = down;
     for (int run0 = 0; run0 < spt; run0 += kBatch) {
-      if (run0) fetch(run0);
+      if (run0) fetch(b, run0, v);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (run0 + i >= spt) break;
