@@ -34,8 +34,9 @@
 // units through a private ring in shared memory with bulk copies per page for
 // keys, values and params, so warps never wait for one another in the loop.
 // Rows whose units lie within one warp are finished by it; the others are
-// merged within the block at its end, and those cut by a block border by
-// k_attend_join.
+// merged within the block at its end, and those cut by a block border by the
+// last of their blocks to end, in block order, so that the bits do not depend
+// on which one that is. (A kernel of its own for that cost 3 to 8 us a call.)
 #include "attn.h"
 #include "kv_layout.cuh"
 #include "q4mma.cuh"
@@ -61,7 +62,8 @@ struct Att {
   static constexpr int kWarps = kByRegs < kBySmem ? kByRegs : kBySmem;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = kStage * kWarps * 3 <= kBudget ? 3 : 2;
-  static constexpr int kPart = kRows * D + 2 * kRows;      // floats of a partial result: sums, maxima, totals
+  static constexpr int kPitch = D + 4;                     // floats of a row of sums: rows two apart use other banks
+  static constexpr int kPart = kRows * kPitch + 2 * kRows; // floats of a partial result: sums, maxima, totals
   static constexpr int kSmem = kStage * kStages * kWarps;
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
@@ -80,12 +82,26 @@ __device__ __forceinline__ int warp_start(int u0, int u1, int w) {
   return u0 + n / W * w + n % W * w / W;
 }
 
-// What a block tells k_attend_join about the item its first unit lies in.
-struct Border {
-  int total, item_start, item_end;   // item_end 0: the block has no unit behind its start
-  int q0, n, kh, tile, pad;
-};
-static_assert(sizeof(Border) == 32, "");
+// The block that takes unit u: start(b) <= u holds exactly for b < (u + 1) * blocks / total.
+__device__ __forceinline__ int block_of(int u, int total, int blocks) {
+  return (int)((((long long)u + 1) * blocks - 1) / total);
+}
+
+// The number of blocks that have left their part of an item, in the low half of a word whose high half tells whether
+// the word has been in use as such: the workspace comes with any contents.
+constexpr unsigned long long kTicketMark = 0x9e3779b97f4a7c15ull & 0xffffffff00000000ull;
+__device__ __forceinline__ int take_ticket(unsigned long long* word) {
+  for (;;) {
+    unsigned long long old = atomicAdd(word, 1ull);
+    if ((old & 0xffffffff00000000ull) == kTicketMark) return (int)(uint32_t)old;
+    // contents of before: the first block to replace them takes ticket 0, others count again
+    for (++old; (old & 0xffffffff00000000ull) != kTicketMark;) {
+      const unsigned long long seen = atomicCAS(word, old, kTicketMark | 1ull);
+      if (seen == old) return 0;
+      old = seen;
+    }
+  }
+}
 
 struct AttendArgs {
   const uint8_t* pages;
@@ -97,7 +113,7 @@ struct AttendArgs {
   float* lse;
   int hq, gq, dtype, window;
   float scale;
-  Border* borders;     // [blocks]
+  unsigned long long* tickets;   // [blocks], of the items that begin in a block and end in another
   float* warp_parts;   // [blocks * warps][kPart]
   float* block_parts;  // [blocks][2][kPart]
 };
@@ -199,10 +215,21 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int q0, int n, in
     a.lse[(size_t)i * a.hq + h] = l == 0.f ? __int_as_float(0xff800000) : (m + log2f(l)) * kLn2;
 }
 
+// A lane's channels of a row of sums, from shared or (written by another block or warp) global memory.
+template <int N>
+__device__ __forceinline__ void part_row(const float* p, bool in_smem, float* x) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const float2* q = reinterpret_cast<const float2*>(p + e);
+    const float2 v = in_smem ? *q : __ldcg(q);
+    x[e] = v.x, x[e + 1] = v.y;
+  }
+}
+
 template <int D, int G, bool Exact>
 __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const AttendArgs a) {
   using T = Att<D, G, Exact>;
-  constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads;
+  constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads, kPitch = T::kPitch;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[kAttWarps][T::kStages];
   __shared__ int s_scan[kAttWarps], s_seq[kAttWarps], s_off[kAttWarps];
@@ -211,6 +238,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     int item_start, item_end, q0, n, kh, tile, where;  // where: 0 none, 1 shared memory, 2 the warp's global slot
   };
   __shared__ Entry s_entry[2 * kAttWarps];
+  __shared__ int s_cut[2], s_last[2];   // entries of the items cut by the block's borders
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (threadIdx.x < kAttWarps * T::kStages) mbar_init(&s_bar[0][0] + threadIdx.x, 1);
   if (threadIdx.x < 2 * kAttWarps) s_entry[threadIdx.x].where = 0;
@@ -298,7 +326,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 
   const bool any = u0 < u1;
   Cursor cur{};
-  if (any || (warp == 0 && block_u0 < total)) {
+  if (any) {
     cur.s = first_seq;
     cur.set_seq(a, sq, U);
     const int item = first_off / cur.units;
@@ -306,18 +334,6 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     cur.kh = item / cur.tiles;
     cur.tile = item - cur.kh * cur.tiles;
     cur.set_tile(a, U);
-    if (warp == 0 && lane == 0) {
-      Border bd;
-      bd.total = total;
-      bd.item_start = u0 - cur.u;
-      bd.item_end = bd.item_start + cur.units;
-      bd.q0 = cur.q0, bd.n = cur.n, bd.kh = cur.kh, bd.tile = cur.tile, bd.pad = 0;
-      a.borders[blockIdx.x] = bd;
-    }
-  } else if (warp == 0 && lane == 0) {
-    Border bd{};
-    bd.total = total;
-    a.borders[blockIdx.x] = bd;
   }
 
   // ---- copies: the warp's ring
@@ -370,10 +386,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     ++nu;
     fetch_page();
   };
-  if (any) {
-    fetch_page();
-    for (int i = 0; i < T::kStages - 1; ++i) issue();
-  }
+  if (any) fetch_page();
 
   const int dtype = Exact ? (int)SFFN_F32 : a.dtype;
   const float ninf = __int_as_float(0xff800000);
@@ -433,12 +446,12 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     float* dst = last ? reinterpret_cast<float*>(smem) + warp * T::kPart : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + warp) * T::kPart;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float* row = dst + (2 * t + r) * D + g;
+      float* row = dst + (2 * t + r) * kPitch + g;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) row[16 * x] = o[x][r], row[16 * x + 8] = o[x][2 + r];
       if (g == 0) {
-        dst[kRows * D + 2 * t + r] = mt[r];
-        dst[kRows * D + kRows + 2 * t + r] = lt[r];
+        dst[kRows * kPitch + 2 * t + r] = mt[r];
+        dst[kRows * kPitch + kRows + 2 * t + r] = lt[r];
       }
     }
     if (lane == 0) {
@@ -691,6 +704,10 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       float big = 0.f, fg, up, sum[NG], x[D / 32][8];
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, dtype, x[j]);
+      if (uu == u0) {   // the first copies, while the rows are on their way
+#pragma unroll 1
+        for (int i = 0; i < T::kStages - 1; ++i) issue();
+      }
 #pragma unroll
       for (int j = 0; j < D / 32; ++j)
 #pragma unroll
@@ -766,8 +783,8 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   __syncthreads();
 
   // ---- partial results of the block: warp w merges row w of each item
-  if (warp >= kRows) return;
   const float* sm = reinterpret_cast<const float*>(smem);
+  int cuts = 0;   // the same in every warp
   for (int e0 = 0; e0 < 2 * kAttWarps;) {
     if (s_entry[e0].where == 0) {
       ++e0;
@@ -776,12 +793,21 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     int e1 = e0 + 1;
     while (e1 < 2 * kAttWarps && (s_entry[e1].where == 0 || s_entry[e1].item_start == s_entry[e0].item_start)) ++e1;
     const Entry& it = s_entry[e0];
+    const bool inside = it.item_start >= block_u0 && it.item_end <= block_u1;
+    if (!inside) {
+      if (threadIdx.x == 0) s_cut[cuts] = e0;
+      ++cuts;
+    }
+    if (warp >= kRows) {
+      e0 = e1;
+      continue;
+    }
     float mt = ninf;
     for (int e = e0; e < e1; ++e) {
       if (s_entry[e].where == 0) continue;
       const float* p = s_entry[e].where == 1 ? sm + (e >> 1) * T::kPart
                                              : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
-      mt = fmaxf(mt, s_entry[e].where == 1 ? p[kRows * D + warp] : __ldcg(p + kRows * D + warp));
+      mt = fmaxf(mt, s_entry[e].where == 1 ? p[kRows * kPitch + warp] : __ldcg(p + kRows * kPitch + warp));
     }
     float lt = 0.f, ot[CPL];
 #pragma unroll
@@ -791,89 +817,91 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       const bool in_smem = s_entry[e].where == 1;
       const float* p = in_smem ? sm + (e >> 1) * T::kPart
                                : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
-      const float me = in_smem ? p[kRows * D + warp] : __ldcg(p + kRows * D + warp);
-      const float le = in_smem ? p[kRows * D + kRows + warp] : __ldcg(p + kRows * D + kRows + warp);
+      const float me = in_smem ? p[kRows * kPitch + warp] : __ldcg(p + kRows * kPitch + warp);
+      const float le = in_smem ? p[kRows * kPitch + kRows + warp] : __ldcg(p + kRows * kPitch + kRows + warp);
       const float w = me == mt ? 1.f : ex2(me - mt);
       lt = fmaf(le, w, lt);
+      float x[CPL];
+      part_row<CPL>(p + warp * kPitch + lane * CPL, in_smem, x);
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        const float* x = p + warp * D + lane * CPL + c;
-        ot[c] = fmaf(in_smem ? *x : __ldcg(x), w, ot[c]);
-      }
+      for (int c = 0; c < CPL; ++c) ot[c] = fmaf(x[c], w, ot[c]);
     }
-    if (it.item_start >= block_u0 && it.item_end <= block_u1) {
+    if (inside) {
       write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
     } else {
       float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start <= block_u0 ? 0 : 1)) * T::kPart;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) dst[warp * D + lane * CPL + c] = ot[c];
+      for (int c = 0; c < CPL; c += 2)
+        *reinterpret_cast<float2*>(dst + warp * kPitch + lane * CPL + c) = make_float2(ot[c], ot[c + 1]);
       if (lane == 0) {
-        dst[kRows * D + warp] = mt;
-        dst[kRows * D + kRows + warp] = lt;
+        dst[kRows * kPitch + warp] = mt;
+        dst[kRows * kPitch + kRows + warp] = lt;
       }
     }
     e0 = e1;
   }
-}
-
-// Rows cut by a block border: block c handles the item that the first unit of
-// attention block c + 1 lies in, if that item began before it and no earlier
-// border lies in it; warp w takes row w. Lane k looks at the k-th part.
-template <int D>
-__global__ void __launch_bounds__(kRows * 32) k_attend_join(const AttendArgs a, int blocks) {
-  constexpr int CPL = D / 32, kPart = Att<D, 64, false>::kPart, kAhead = 8;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x + 1, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Border* bp = a.borders + c;
-  const int total = __ldcg(&bp->total), item_start = __ldcg(&bp->item_start), item_end = __ldcg(&bp->item_end);
-  const int q0 = __ldcg(&bp->q0), n = __ldcg(&bp->n), kh = __ldcg(&bp->kh), tile = __ldcg(&bp->tile);
-  const Runs runs(total, blocks);
-  auto start = [&](int k) { return runs.start(k); };
-  if (item_end == 0 || item_start >= start(c) || item_start < start(c - 1)) return;
-  const float ninf = __int_as_float(0xff800000);
-  // parts: the last item of block c - 1 (its first if it begins with it), the first items of c, c + 1, ...
-  int count = 2;
-  while (c + count - 1 < blocks && start(c + count - 1) < item_end) ++count;
-  auto part = [&](int k) {
-    return a.block_parts + ((long long)(c - 1 + k) * 2 + (k == 0 && start(c - 1) < item_start ? 1 : 0)) * kPart;
-  };
-  float mt = ninf, lt = 0.f, ot[CPL];
+  if (cuts == 0) return;
+  __threadfence();   // the block's parts before its tickets
+  __syncthreads();
+  if (threadIdx.x < cuts) {
+    const Entry& it = s_entry[s_cut[threadIdx.x]];
+    const int b0 = block_of(it.item_start, total, gridDim.x), b1 = block_of(it.item_end - 1, total, gridDim.x);
+    // every block has a unit, or every block that has one has one only
+    const int parts_of_item = total >= (int)gridDim.x ? b1 - b0 + 1 : it.item_end - it.item_start;
+    const bool is_last = take_ticket(a.tickets + b0) == parts_of_item - 1;
+    if (is_last) a.tickets[b0] = kTicketMark;   // for the next call
+    s_last[threadIdx.x] = is_last;
+    __threadfence();
+  }
+  __syncthreads();
+  if (warp >= kRows) return;
+  const Runs runs(total, gridDim.x);
+  for (int c = 0; c < cuts; ++c) {
+    if (!s_last[c]) continue;
+    const Entry& it = s_entry[s_cut[c]];
+    const int b0 = block_of(it.item_start, total, gridDim.x), count = block_of(it.item_end - 1, total, gridDim.x) - b0 + 1;
+    // the last item of block b0 (its first if it begins with it), the first items of the blocks after
+    const bool second = runs.start(b0) < it.item_start;
+    auto part = [&](int k) { return a.block_parts + (size_t)((b0 + k) * 2 + (k == 0 && second ? 1 : 0)) * T::kPart; };
+    float mt = ninf, lt = 0.f, ot[CPL];
 #pragma unroll
-  for (int e = 0; e < CPL; ++e) ot[e] = 0.f;
-  for (int k0 = 0; k0 < count; k0 += 32) {
-    const int k = k0 + lane;
-    const bool has = k < count && (k == 0 || start(c + k) > start(c - 1 + k));   // an empty block has no part
-    const float me = has ? __ldcg(part(k) + kRows * D + row) : ninf;
-    const float le = has ? __ldcg(part(k) + kRows * D + kRows + row) : 0.f;
-    float mn = me;
+    for (int e = 0; e < CPL; ++e) ot[e] = 0.f;
+    for (int k0 = 0; k0 < count; k0 += 32) {   // lane k looks at the k-th part
+      const int k = k0 + lane;
+      const bool has = k < count && runs.start(b0 + k + 1) > runs.start(b0 + k);   // an empty block has no part
+      const float me = has ? __ldcg(part(k) + kRows * kPitch + warp) : ninf;
+      const float le = has ? __ldcg(part(k) + kRows * kPitch + kRows + warp) : 0.f;
+      float mn = me;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(SFFN_FULL_MASK, mn, o));
-    mn = fmaxf(mn, mt);
-    const float back = mt == mn ? 1.f : ex2(mt - mn), w = !has ? 0.f : me == mn ? 1.f : ex2(me - mn);
-    mt = mn;
-    lt = lt * back + warp_sum(le * w);
+      for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(SFFN_FULL_MASK, mn, o));
+      mn = fmaxf(mn, mt);
+      const float back = mt == mn ? 1.f : ex2(mt - mn), w = !has ? 0.f : me == mn ? 1.f : ex2(me - mn);
+      mt = mn;
+      lt = lt * back + warp_sum(le * w);
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) ot[e] *= back;
-    const unsigned mask = __ballot_sync(SFFN_FULL_MASK, has);
-    const int here = min(32, count - k0);
-    for (int i0 = 0; i0 < here; i0 += kAhead) {
-      float x[kAhead][CPL];
+      for (int e = 0; e < CPL; ++e) ot[e] *= back;
+      const unsigned mask = __ballot_sync(SFFN_FULL_MASK, has);
+      const int here = min(32, count - k0);
+      constexpr int kAhead = 8;
+      for (int i0 = 0; i0 < here; i0 += kAhead) {
+        float x[kAhead][CPL];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
+        for (int i = 0; i < kAhead; ++i)   // past the last part: that one again, not used
+          part_row<CPL>(part(min(k0 + i0 + i, count - 1)) + warp * kPitch + lane * CPL, false, x[i]);
 #pragma unroll
-        for (int e = 0; e < CPL; ++e)
-          x[i][e] = (mask >> (i0 + i)) & 1 ? __ldcg(part(k0 + i0 + i) + row * D + lane * CPL + e) : 0.f;
+        for (int i = 0; i < kAhead; ++i) {
+          const float wi = __shfl_sync(SFFN_FULL_MASK, w, (i0 + i) & 31);
+          if (i0 + i < 32 && (mask >> (i0 + i) & 1)) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float wi = __shfl_sync(SFFN_FULL_MASK, w, i0 + i);
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) ot[e] = fmaf(x[i][e], wi, ot[e]);
+            for (int e = 0; e < CPL; ++e) ot[e] = fmaf(x[i][e], wi, ot[e]);
+          }
+        }
       }
     }
+    write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
   }
-  write_row<D>(a, q0, n, kh, tile * kRows + row, lane, ot, mt, lt);
 }
+
 
 template <typename F>
 auto by_shape(const sffn_kv& C, F&& f) {
@@ -897,9 +925,9 @@ struct AttWs {
   size_t warp_parts, block_parts, total;
 };
 AttWs att_ws(const sffn_kv& C) {
-  const size_t part = (size_t)(kRows * C.desc.head_dim + 2 * kRows) * 4, blocks = C.num_sms;
+  const size_t part = (size_t)(kRows * (C.desc.head_dim + 4) + 2 * kRows) * 4, blocks = C.num_sms;
   AttWs w;
-  w.warp_parts = up256(blocks * sizeof(Border));
+  w.warp_parts = up256(blocks * sizeof(unsigned long long));
   w.block_parts = up256(w.warp_parts + blocks * kMaxWarps * part);
   w.total = up256(w.block_parts + blocks * 2 * part);
   return w;
@@ -928,15 +956,13 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
   uint8_t* p = static_cast<uint8_t*>(ws);
   const AttendArgs a{C.pages, C.page_bytes, C.head_bytes, C.desc.n_pages, C.desc.page_size,
                      C.desc.page_size == 16 ? 4 : C.desc.page_size == 32 ? 5 : 6, C.desc.n_kv_heads, C.err, b, q, out, lse, n_q_heads, n_q_heads / C.desc.n_kv_heads, dtype, window, scale,
-                     reinterpret_cast<Border*>(p), reinterpret_cast<float*>(p + w.warp_parts),
+                     reinterpret_cast<unsigned long long*>(p), reinterpret_cast<float*>(p + w.warp_parts),
                      reinterpret_cast<float*>(p + w.block_parts)};
   const int blocks = C.num_sms;
   return by_shape(C, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
     auto run = [&](auto* kern, int threads, int smem) {
-      const cudaError_t e = launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, 1, a);
-      if (e != cudaSuccess || blocks < 2) return e;
-      return launch_ex(k_attend_join<D>, dim3(blocks - 1), dim3(kRows * 32), 0, st, true, 1, a, blocks);
+      return launch_ex(kern, dim3(blocks), dim3(threads), smem, st, true, 1, a);
     };
     using E = Att<D, G, true>;
     using N = Att<D, G, false>;

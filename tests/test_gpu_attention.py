@@ -531,3 +531,28 @@ def test_attention_refusals(sffn):
     ):
         with pytest.raises(ValueError):
             call()
+
+
+def test_attention_workspace_comes_with_any_contents(sffn):
+    """Items cut by the borders of blocks, with the workspace full of ones, of noise, and of what a call left there."""
+    lens = [(5000, 1), (70, 2), (1700, 1), (64, 1), (65, 1)]
+    c, q, out, lse = check_attention(sffn, lens, 8, 2, 128, 64, 32, seed=21)
+    ws, scale = c.cache.workspace(c.new, 8), 1 / math.sqrt(128)
+    for fill in (lambda: ws.fill_(255), lambda: ws.random_(0, 256, generator=c.g), lambda: None, lambda: ws.zero_(), lambda: None):
+        fill()
+        o2, l2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+        sffn.sffn_attend(c.cache.handle, c.new, q, o2, l2, scale, 0, ws)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("seqs,hkv", [(1, 1), (2, 1), (1, 8), (3, 5), (40, 8)])
+@pytest.mark.parametrize("n", [64, 150, 9000])
+def test_attention_cuts(sffn, seqs, hkv, n):
+    """From fewer units than blocks to many, whatever the borders cut; equal bits at every call."""
+    n = n if seqs * hkv < 100 else min(n, 700)
+    c, q, out, lse = check_attention(sffn, [(n + 3 * s, 1) for s in range(seqs)], 2 * hkv, hkv, 64, 64, 64, seed=n + seqs)
+    ws = c.cache.workspace(c.new, 2 * hkv)
+    for _ in range(20):
+        o2, l2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+        sffn.sffn_attend(c.cache.handle, c.new, q, o2, l2, 1 / 8, 0, ws)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
