@@ -103,10 +103,12 @@ struct Turn {
   // x: the lane's channels of a row of elements of type dtype
   __device__ __forceinline__ void apply(const sffn_rope& r, float* x, const void* row, int dtype, int lane, bool on) const {
     if (shuffles) {
+      float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __shfl_sync(SFFN_FULL_MASK, x[e], partner);
-        if (on && kind != 0) x[e] = __fadd_rn(__fmul_rn(x[e], cs[e].x), __fmul_rn(y, cs[e].y));
+      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(SFFN_FULL_MASK, x[e], partner);
+      if (on && kind != 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], cs[e].x), __fmul_rn(y[e], cs[e].y));
       }
     } else if (on && kind == 3) {
 #pragma unroll
@@ -138,16 +140,13 @@ struct Turn {
 // Rows r0 .. r1 - 1 of one kind (0 queries, 1 keys, 2 values) of token i.
 template <int D, typename T, int KIND>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
-  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kAhead = 1, dtype = dtype_of<T>();
+  constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, dtype = dtype_of<T>();
   const int sub = lane / LR, lr = lane % LR, c0 = lr * 8;
   const sffn_rows& rows = KIND == 0 ? a.q : KIND == 1 ? a.k : a.v;
   const T* p = static_cast<const T*>(rows.ptr) + i * rows.row_stride + (r0 + sub) * rows.head_stride + c0;
   const int64_t hop = RI * rows.head_stride;
-  Raw<T> next[kAhead] = {};
-  const T* ahead = p;
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k, ahead += hop)
-    if (r0 + sub + k * RI < r1) next[k].load(ahead);
+  Raw<T> next = {};   // the row after the one in hand
+  if (r0 + sub < r1) next.load(p);
   const KvPlace at = kv_place(a.b, i, lane, a.c.P, a.c.err);
   if (at.seq < 0) return;
   Turn<D> turn;
@@ -176,61 +175,55 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
     param = block + kv_param_off(a.c.P, D) + param_off(slot, lr / glanes, a.c.n_groups, KIND == 2);
   }
 
-  for (int rb = r0; rb < r1;) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (rb >= r1) break;
-      const bool in = rb + sub < r1;
-      float x[8];
-      next[k].get(x);
-      if (rb + sub + kAhead * RI < r1) next[k].load(ahead);
-      ahead += hop;
-      if (KIND != 2) turn.apply(a.rope, x, p - c0, dtype, lane, in);
-      p += hop;
-      rb += RI;
-      if (KIND == 0) {
-        if (in) st_run<8>(out, 0, dtype, x);
-        out += RI * a.q_out.head_stride;
-        continue;
-      }
-      // least and largest value of the group, over the lanes that share it
-      float lo = x[0], hi = x[0], nan = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
-        nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
-      }
-      for (int o = 1; o < glanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
-      }
-      const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
-      const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
-      __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
-      const float midf = __half2float(mid);
-      const float far = fmaxf(__fsub_rn(hi, midf), __fsub_rn(midf, lo));
-      __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
-      if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
-      const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
-      // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
-      // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
-      uint32_t codes = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
-        codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
-      }
-      codes -= 0x4b000000u * 0x11111111u;
-      if (stepf == 0.f || bad) codes = 0x88888888u;
-      const uint32_t w = KIND == 2 ? value_word(transpose_codes(codes, lane)) : key_word(codes);
-      if (in) {
-        *reinterpret_cast<uint32_t*>(word) = w;
-        if (lr % glanes == 0) *reinterpret_cast<__half2*>(param) = __halves2half2(step, mid);
-      }
-      word += RI * a.c.head_bytes;
-      param += RI * a.c.head_bytes;
+  for (int left = r1 - r0 - sub; left + sub > 0; left -= RI) {   // rows from the lane's own on
+    const bool in = left > 0;
+    float x[8];
+    next.get(x);
+    if (left > RI) next.load(p + hop);
+    if (KIND != 2) turn.apply(a.rope, x, p - c0, dtype, lane, in);
+    p += hop;
+    if (KIND == 0) {
+      if (in) st_run<8>(out, 0, dtype, x);
+      out += RI * a.q_out.head_stride;
+      continue;
     }
+    // least and largest value of the group, over the lanes that share it
+    float lo = x[0], hi = x[0], nan = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      lo = fminf(lo, x[e]);
+      hi = fmaxf(hi, x[e]);
+      nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
+    }
+    for (int o = 1; o < glanes; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
+    }
+    const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
+    const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
+    __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
+    const float midf = __half2float(mid);
+    const float far = fmaxf(__fsub_rn(hi, midf), __fsub_rn(midf, lo));
+    __half step = __float2half_rn(fminf(__fmul_rn(far, 1.f / 15.f), kHalfMax));
+    if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
+    const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
+    // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
+    // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
+    uint32_t codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
+      codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+    }
+    codes -= 0x4b000000u * 0x11111111u;
+    if (stepf == 0.f || bad) codes = 0x88888888u;
+    const uint32_t w = KIND == 2 ? value_word(transpose_codes(codes, lane)) : key_word(codes);
+    if (in) {
+      *reinterpret_cast<uint32_t*>(word) = w;
+      if (lr % glanes == 0) *reinterpret_cast<__half2*>(param) = __halves2half2(step, mid);
+    }
+    word += RI * a.c.head_bytes;
+    param += RI * a.c.head_bytes;
   }
 }
 
