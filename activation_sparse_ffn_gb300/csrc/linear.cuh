@@ -214,23 +214,30 @@ __device__ __forceinline__ float largest(const float* v) {   // of a lane's four
   return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 }
 
-// Four inputs of a lane (of a run of 128) times a power of two as halves: the nearest in hi, what is left in lo. With
-// Sums, the sums of hi and lo over a group of G.
+// Four inputs of a lane (of a run of 128) times a power of two as halves: the nearest in hi and, if split, what is left
+// in lo. With Sums, the sums of hi and lo over a group of G.
 template <int G, bool Sums>
-__device__ __forceinline__ void convert_run(const float* v, float up, uint32_t* hi, uint32_t* lo, float& sh, float& sl) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p) split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
+__device__ __forceinline__ void convert_run(const float* v, float up, bool split, uint32_t* hi, uint32_t* lo, float& sh,
+                                            float& sl) {
   sh = sl = 0.f;
+  if (split) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) split_f16(v[2 * p] * up, v[2 * p + 1] * up, hi[p], lo[p]);
+    if (Sums) {
+      const float2 c = __half22float2(u32_h2(lo[0])), d = __half22float2(u32_h2(lo[1]));
+      sl = (c.x + c.y) + (d.x + d.y);
+#pragma unroll
+      for (int o = 1; o < G / 4; o <<= 1) sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) hi[p] = h2_u32(__floats2half2_rn(v[2 * p] * up, v[2 * p + 1] * up));
+  }
   if (Sums) {
     const float2 a = __half22float2(u32_h2(hi[0])), b = __half22float2(u32_h2(hi[1]));
-    const float2 c = __half22float2(u32_h2(lo[0])), d = __half22float2(u32_h2(lo[1]));
     sh = (a.x + a.y) + (b.x + b.y);
-    sl = (c.x + c.y) + (d.x + d.y);
 #pragma unroll
-    for (int o = 1; o < G / 4; o <<= 1) {
-      sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
-      sl += __shfl_xor_sync(SFFN_FULL_MASK, sl, o);
-    }
+    for (int o = 1; o < G / 4; o <<= 1) sh += __shfl_xor_sync(SFFN_FULL_MASK, sh, o);
   }
 }
 
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
         if (run0 + i >= spt) break;
         uint32_t hi[2], lo[2];
         float sh, sl;
-        convert_run<G, kSums>(v[i], up, hi, lo, sh, sl);
+        convert_run<G, kSums>(v[i], up, split, hi, lo, sh, sl);
         const int kk = (run0 + i) * 128 + lane * 4;
         *reinterpret_cast<uint2*>(xs + (size_t)col * a.chunk_stride + kk) = make_uint2(hi[0], hi[1]);
         if (split) *reinterpret_cast<uint2*>(xs + (size_t)(col + 1) * a.chunk_stride + kk) = make_uint2(lo[0], lo[1]);
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int column
   auto put = [&](int run, const float* o) {
     uint32_t hi[2], lo[2];
     float sh, sl;
-    convert_run<G, Sums>(o, up, hi, lo, sh, sl);
+    convert_run<G, Sums>(o, up, split, hi, lo, sh, sl);
     const int kk = run * 128 + lane * 4;
     *reinterpret_cast<uint2*>(xh + (size_t)col * a.kp + kk) = make_uint2(hi[0], hi[1]);
     if (split) *reinterpret_cast<uint2*>(xh + (size_t)(col + 1) * a.kp + kk) = make_uint2(lo[0], lo[1]);
