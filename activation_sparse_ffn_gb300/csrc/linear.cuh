@@ -357,6 +357,35 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
   float* sums = reinterpret_cast<float*>(smem + a.off_sum) + (size_t)warp * (a.chunk / G + 1) * 8;   // last row: down
   float* downs = sums + (a.chunk / G) * 8;
   const int k0 = k_first * 128;
+  if (a.dtype == SFFN_F16) {   // taken as they are
+    if (lane < 8) downs[lane] = 1.f;
+    const __half* px = static_cast<const __half*>(a.x.ptr) + k0 + lane * 4;
+    const int tasks = a.B * spt;
+    for (int task = 0, b = 0, run = 0; task < tasks; task += 2 * kBatch) {
+      uint2 w[2 * kBatch];
+      int b1 = b, run1 = run;
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; ++i) {
+        w[i] = make_uint2(0u, 0u);
+        if (task + i < tasks && k0 + run1 * 128 + lane * 4 < a.k)
+          w[i] = __ldcg(reinterpret_cast<const uint2*>(px + b1 * a.x.row_stride + run1 * 128));
+        if (++run1 == spt) run1 = 0, ++b1;
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; ++i) {
+        if (task + i >= tasks) break;
+        *reinterpret_cast<uint2*>(xs + (size_t)b * a.chunk_stride + run * 128 + lane * 4) = w[i];
+        if (kSums) {
+          const float2 p = __half22float2(u32_h2(w[i].x)), q = __half22float2(u32_h2(w[i].y));
+          float sum = (p.x + p.y) + (q.x + q.y);
+#pragma unroll
+          for (int o = 1; o < G / 4; o <<= 1) sum += __shfl_xor_sync(SFFN_FULL_MASK, sum, o);
+          if (lane % (G / 4) == 0) sums[(run * GS + lane / (G / 4)) * 8 + b] = sum;
+        }
+        if (++run == spt) run = 0, ++b;
+      }
+    }
+  }
   float v[kBatch][4], ahead[kBatch][4];   // of this token, and the first runs of the next
   auto fetch = [&](int b, int run0, float (*o)[4]) {
 #pragma unroll
@@ -366,27 +395,25 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
       if (run0 + i < spt && k0 + kk < a.k) ld_run<4>(a.x.ptr, (size_t)(b * a.x.row_stride) + k0 + kk, a.dtype, o[i]);
     }
   };
-  fetch(0, 0, ahead);
+  const int others = a.dtype == SFFN_F16 ? 0 : a.B;
+  if (others) fetch(0, 0, ahead);
 #pragma unroll 1
-  for (int b = 0; b < a.B; ++b) {
-    float up = 1.f, down = 1.f;
+  for (int b = 0; b < others; ++b) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[i][e] = ahead[i][e];
-    if (b + 1 < a.B) fetch(b + 1, 0, ahead);
-    if (a.dtype != SFFN_F16) {   // f16 rows are taken as they are
-      float big = 0.f;
-      for (int run0 = 0; run0 < spt; run0 += kBatch) {
-        if (run0) fetch(b, run0, v);
+    if (b + 1 < others) fetch(b + 1, 0, ahead);
+    float big = 0.f, up, down;
+    for (int run0 = 0; run0 < spt; run0 += kBatch) {
+      if (run0) fetch(b, run0, v);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) big = fmaxf(big, largest(v[i]));
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
-      scale_to_half_range(big, up, down);
-      if (spt > kBatch) fetch(b, 0, v);
+      for (int i = 0; i < kBatch; ++i) big = fmaxf(big, largest(v[i]));
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(SFFN_FULL_MASK, big, o));
+    scale_to_half_range(big, up, down);
+    if (spt > kBatch) fetch(b, 0, v);
     const int col = split ? 2 * b : b;
     if (lane == 0) downs[col] = downs[split ? col + 1 : col] = down;
     for (int run0 = 0; run0 < spt; run0 += kBatch) {
