@@ -54,12 +54,15 @@ template <int D, int G, bool Exact>
 struct Att {
   static constexpr int NG = D / G;
   static constexpr int U = D == 256 ? 32 : 64;             // positions of a unit
+  // Positions whose code is unrolled: with four groups and 64 of them the step and weight registers spill (24 ragged
+  // sequences: 108 us, with 32 of them 96); with one group 32 are slower (131072 positions: 60 us, with 64 of them 54).
+  static constexpr int SU = NG >= 4 ? 32 : U;
   static constexpr int kStage = U * (D + 8 * NG);          // bytes
   // as many warps as the registers of the inner loop and two stages each allow
   static constexpr int kByRegs = D == 64 ? (Exact ? 12 : 16) : D == 128 && !Exact && NG < 4 ? 12 : 8;
   static constexpr int kBudget = 224 * 1024;
   static constexpr int kBySmem = kBudget / (2 * kStage);
-  static constexpr int kWarps = kByRegs < kBySmem ? kByRegs : kBySmem;
+  static constexpr int kWarps = (kByRegs < kBySmem ? kByRegs : kBySmem) / 4 * 4;   // the same on each of an SM's four schedulers
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = kStage * kWarps * 3 <= kBudget ? 3 : 2;
   static constexpr int kPitch = D + 4;                     // floats of a row of sums: rows two apart use other banks
@@ -229,7 +232,7 @@ __device__ __forceinline__ void part_row(const float* p, bool in_smem, float* x)
 template <int D, int G, bool Exact>
 __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const AttendArgs a) {
   using T = Att<D, G, Exact>;
-  constexpr int U = T::U, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads, kPitch = T::kPitch;
+  constexpr int U = T::U, SU = T::SU, NG = T::NG, CPL = D / 32, kAttWarps = T::kWarps, kAttThreads = T::kThreads, kPitch = T::kPitch;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_bar[kAttWarps][T::kStages];
   __shared__ int s_scan[kAttWarps], s_seq[kAttWarps], s_off[kAttWarps];
@@ -463,11 +466,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     return false;
   };
 
-  // one unit of positions, from its copy in shared memory
-  auto unit = [&](auto masked, const uint8_t* sk, int base) {
+  // SU positions of a unit, from its copy in shared memory
+  auto unit = [&](auto masked, const uint8_t* sk, const uint8_t* sv, const uint8_t* sp, int base) {
     constexpr bool Masked = decltype(masked)::value;   // some row does not see some of the positions
-    const uint8_t* sv = sk + U * (D / 2);
-    const uint8_t* sp = sk + U * D;
     const int lo_min = a.window > 0 ? max(0, cur.first - a.window + 1) : 0;   // before it nothing is seen
     // the (step, mid) pairs of slot g of eight positions, all groups
     auto params = [&](int tile, int which, uint32_t* v) {
@@ -487,9 +488,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     };
 
     // ---- scores of U positions: s[i] rows 16i + slot g and 16i + 8 + slot g, each for both query rows
-    float s[U / 16][4];
+    float s[SU / 16][4];
 #pragma unroll
-    for (int i = 0; i < U / 16; ++i) {
+    for (int i = 0; i < SU / 16; ++i) {
       uint32_t w[2][D / 32];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     }
     if (Masked) {
 #pragma unroll
-      for (int i = 0; i < U / 16; ++i)
+      for (int i = 0; i < SU / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = base + 16 * i + 8 * (e >> 1) + kt;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     }
     float mu[2] = {m[0], m[1]};
 #pragma unroll
-    for (int i = 0; i < U / 16; ++i) {
+    for (int i = 0; i < SU / 16; ++i) {
       mu[0] = fmaxf(mu[0], fmaxf(s[i][0], s[i][2]));
       mu[1] = fmaxf(mu[1], fmaxf(s[i][1], s[i][3]));
     }
@@ -569,9 +570,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     }
     const float mf[2] = {m[0] == ninf ? 0.f : m[0] * f[0], m[1] == ninf ? 0.f : m[1] * f[1]};
 
-    uint32_t vw[U / 16][4][D / 64];   // the lane's words of four positions per 16
+    uint32_t vw[SU / 16][4][D / 64];   // the lane's words of four positions per 16
 #pragma unroll
-    for (int k = 0; k < U / 16; ++k)
+    for (int k = 0; k < SU / 16; ++k)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int p8 = (r & 1) ? tb : ta;
@@ -588,9 +589,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       }
     constexpr int GW = G >= 64 ? 1 : 64 / G;   // groups that the 64 channels of a word lie in
 
-    float top = 0.f, step[U / 16][2][NG];
+    float top = 0.f, step[SU / 16][2][NG];
 #pragma unroll
-    for (int i = 0; i < U / 16; ++i) {
+    for (int i = 0; i < SU / 16; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[i][e] = ex2(fmaf(s[i][e], f[e & 1], -mf[e & 1]));
       l[0] += s[i][0] + s[i][2];
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     float up, down;
     scale_to_half_range(row_max(top), up, down);
     const float k0 = Exact ? down : down * 16777216.f, k1 = Exact ? down : down * 1048576.f;  // bare codes: u * 2^-23, 2^-19
-    uint32_t wt[QL][GW][U / 16][2];
+    uint32_t wt[QL][GW][SU / 16][2];
     float ws[GW][4];
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         for (int n = 0; n < GW; ++n) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < U / 16; ++i) {
+          for (int i = 0; i < SU / 16; ++i) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const float st = step[i][k][w * 64 / G + n] * up;
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       for (int hh = 0; hh < 2; ++hh) {
         float acc[2][4];
 #pragma unroll
-        for (int k = 0; k < U / 16; ++k)
+        for (int k = 0; k < SU / 16; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {   // channel tiles 4 hh + 2e and the next
             const int n = (2 * hh + e) * 16 / G % GW;
@@ -761,11 +762,16 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       }
       ++taken;
       const uint8_t* sk = ring + st * T::kStage;
-      const int base = cur.base(U);
-      if (base + U - 1 > cur.first || (a.window > 0 && base < cur.last - a.window + 1))
-        unit(std::true_type(), sk, base);
-      else
-        unit(std::false_type(), sk, base);
+#pragma unroll 1
+      for (int part = 0; part < U; part += SU) {
+        const int base = cur.base(U) + part;
+        if (base > cur.last) break;
+        const uint8_t *pk = sk + part * (D / 2), *pv = pk + U * (D / 2), *pp = sk + U * D + part * 8 * NG;
+        if (base + SU - 1 > cur.first || (a.window > 0 && base < cur.last - a.window + 1))
+          unit(std::true_type(), pk, pv, pp, base);
+        else
+          unit(std::false_type(), pk, pv, pp, base);
+      }
       __syncwarp();
     }
     const bool last = uu + 1 == u1;
