@@ -137,6 +137,18 @@ struct Turn {
   }
 };
 
+// Least and largest of three, NaN if one is NaN.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Rows r0 .. r1 - 1 of one kind (0 queries, 1 keys, 2 values) of token i.
 template <int D, typename T, int KIND>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
@@ -158,7 +170,6 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
       set_device_error(a.c.err, SFFN_ERR_DEVICE);
   }
   const int glanes = LR / a.c.n_groups;
-  const unsigned group_mask = (glanes == 32 ? 0xffffffffu : (1u << glanes) - 1u) << (lane / glanes * glanes);
   uint8_t* word = nullptr;     // of the lane's codes, and of its group's params, in the block of head r0 + sub
   uint8_t* param = nullptr;
   T* out = nullptr;
@@ -188,18 +199,14 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
       continue;
     }
     // least and largest value of the group, over the lanes that share it
-    float lo = x[0], hi = x[0], nan = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      nan = fmaf(x[e], 0.f, nan);   // NaN if a value is not finite
-    }
+    float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min3(x[6], x[7], x[7]));
+    float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
     for (int o = 1; o < glanes; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(SFFN_FULL_MASK, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(SFFN_FULL_MASK, hi, o));
+      const float a = __shfl_xor_sync(SFFN_FULL_MASK, lo, o), c = __shfl_xor_sync(SFFN_FULL_MASK, hi, o);
+      lo = min3(lo, a, a);
+      hi = max3(hi, c, c);
     }
-    const bool bad = (__ballot_sync(SFFN_FULL_MASK, nan != 0.f) & group_mask) != 0u;
+    const bool bad = !(fabsf(lo) < __int_as_float(0x7f800000) && fabsf(hi) < __int_as_float(0x7f800000));
     const float m = __fadd_rn(__fmul_rn(lo, 0.5f), __fmul_rn(hi, 0.5f));
     __half mid = __float2half_rn(fminf(fmaxf(m, -kHalfMax), kHalfMax));
     const float midf = __half2float(mid);
@@ -208,12 +215,22 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
     if (bad) mid = __ushort_as_half(0), step = __ushort_as_half(0x7fff);
     const float stepf = __half2float(step), inv = __frcp_rn(__fmul_rn(2.f, stepf));
     // floor and limits of (x - mid) inv + 8: limits first, then 2^23 + t cut off at the units, whose bit pattern is
-    // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end
+    // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end.
+    // A step that is a normal half and not the largest is within 2^-11 of a fifteenth of the farther end, so that t
+    // stays in (0.49, 15.51): then there is nothing to limit.
     uint32_t codes = 0;
+    if (__all_sync(SFFN_FULL_MASK, stepf >= 6.103515625e-5f && stepf < kHalfMax)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
-      codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+      for (int e = 0; e < 8; ++e) {
+        const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
+        codes += __float_as_uint(__fadd_rz(t, 8388608.f)) << (4 * e);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
+        codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+      }
     }
     codes -= 0x4b000000u * 0x11111111u;
     if (stepf == 0.f || bad) codes = 0x88888888u;
