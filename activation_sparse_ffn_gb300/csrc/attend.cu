@@ -218,6 +218,12 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int q0, int n, in
     a.lse[(size_t)i * a.hq + h] = l == 0.f ? __int_as_float(0xff800000) : (m + log2f(l)) * kLn2;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(SFFN_FULL_MASK, v, o));
+  return v;
+}
+
 // A lane's channels of a row of sums, from shared or (written by another block or warp) global memory.
 template <int N>
 __device__ __forceinline__ void part_row(const float* p, bool in_smem, float* x) {
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     int item_start, item_end, q0, n, kh, tile, where;  // where: 0 none, 1 shared memory, 2 the warp's global slot
   };
   __shared__ Entry s_entry[2 * kAttWarps];
-  __shared__ int s_cut[2], s_last[2];   // entries of the items cut by the block's borders
+  __shared__ int s_last[2];   // whether the block is the last with a part of an item cut by its borders
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (threadIdx.x < kAttWarps * T::kStages) mbar_init(&s_bar[0][0] + threadIdx.x, 1);
   if (threadIdx.x < 2 * kAttWarps) s_entry[threadIdx.x].where = 0;
@@ -788,69 +794,78 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   }
   __syncthreads();
 
-  // ---- partial results of the block: warp w merges row w of each item
+  // ---- partial results of the block, a warp per item and row; lane e looks at entry e
+  static_assert(2 * kAttWarps <= 32, "");
   const float* sm = reinterpret_cast<const float*>(smem);
-  int cuts = 0;   // the same in every warp
-  for (int e0 = 0; e0 < 2 * kAttWarps;) {
-    if (s_entry[e0].where == 0) {
-      ++e0;
-      continue;
-    }
-    int e1 = e0 + 1;
-    while (e1 < 2 * kAttWarps && (s_entry[e1].where == 0 || s_entry[e1].item_start == s_entry[e0].item_start)) ++e1;
+  const bool used = lane < 2 * kAttWarps && s_entry[lane].where != 0;
+  const unsigned used_mask = __ballot_sync(SFFN_FULL_MASK, used), below = used_mask & ((1u << lane) - 1u);
+  const int of_item = used ? s_entry[lane].item_start : 0;
+  const int of_prev = __shfl_sync(SFFN_FULL_MASK, of_item, below ? 31 - __clz(below) : lane);
+  const bool head = used && (below == 0u || of_prev != of_item);   // the first entry of an item
+  const unsigned heads = __ballot_sync(SFFN_FULL_MASK, head);
+  const unsigned cut_heads = __ballot_sync(SFFN_FULL_MASK, head && (of_item < block_u0 || s_entry[lane].item_end > block_u1));
+  const int cuts = __popc(cut_heads);   // at most two
+  auto nth = [](unsigned mask, int n) {
+    for (; n > 0; --n) mask &= mask - 1u;
+    return __ffs(mask) - 1;
+  };
+  auto part_of = [&](int e) {   // a warp's last segment is in shared memory, an earlier one in its slot
+    return e & 1 ? sm + (e >> 1) * T::kPart : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
+  };
+#pragma unroll 1
+  for (int pair = warp; pair < __popc(heads) * kRows; pair += kAttWarps) {
+    const int row = pair % kRows, e0 = nth(heads, pair / kRows);
     const Entry& it = s_entry[e0];
     const bool inside = it.item_start >= block_u0 && it.item_end <= block_u1;
-    if (!inside) {
-      if (threadIdx.x == 0) s_cut[cuts] = e0;
-      ++cuts;
+    const bool member = used && of_item == it.item_start;
+    float me = ninf, le = 0.f;
+    if (member) {
+      const float* p = part_of(lane) + kRows * kPitch + row;
+      me = lane & 1 ? p[0] : __ldcg(p);
+      le = lane & 1 ? p[kRows] : __ldcg(p + kRows);
     }
-    if (warp >= kRows) {
-      e0 = e1;
-      continue;
-    }
-    float mt = ninf;
-    for (int e = e0; e < e1; ++e) {
-      if (s_entry[e].where == 0) continue;
-      const float* p = s_entry[e].where == 1 ? sm + (e >> 1) * T::kPart
-                                             : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
-      mt = fmaxf(mt, s_entry[e].where == 1 ? p[kRows * kPitch + warp] : __ldcg(p + kRows * kPitch + warp));
-    }
-    float lt = 0.f, ot[CPL];
+    const float mt = warp_max(me);
+    const float w = !member ? 0.f : me == mt ? 1.f : ex2(me - mt);
+    const float lt = warp_sum(le * w);
+    float ot[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) ot[c] = 0.f;
-    for (int e = e0; e < e1; ++e) {
-      if (s_entry[e].where == 0) continue;
-      const bool in_smem = s_entry[e].where == 1;
-      const float* p = in_smem ? sm + (e >> 1) * T::kPart
-                               : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
-      const float me = in_smem ? p[kRows * kPitch + warp] : __ldcg(p + kRows * kPitch + warp);
-      const float le = in_smem ? p[kRows * kPitch + kRows + warp] : __ldcg(p + kRows * kPitch + kRows + warp);
-      const float w = me == mt ? 1.f : ex2(me - mt);
-      lt = fmaf(le, w, lt);
-      float x[CPL];
-      part_row<CPL>(p + warp * kPitch + lane * CPL, in_smem, x);
+    for (unsigned todo = __ballot_sync(SFFN_FULL_MASK, member); todo;) {
+      constexpr int kAhead = 4;
+      float x[kAhead][CPL];
+      int e[kAhead];
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) ot[c] = fmaf(x[c], w, ot[c]);
+      for (int i = 0; i < kAhead; ++i) {
+        e[i] = __ffs(todo) - 1;
+        todo &= todo - 1u;
+        if (e[i] >= 0) part_row<CPL>(part_of(e[i]) + row * kPitch + lane * CPL, e[i] & 1, x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (e[i] < 0) break;
+        const float wi = __shfl_sync(SFFN_FULL_MASK, w, e[i]);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) ot[c] = fmaf(x[i][c], wi, ot[c]);
+      }
     }
     if (inside) {
-      write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
+      write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + row, lane, ot, mt, lt);
     } else {
       float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start <= block_u0 ? 0 : 1)) * T::kPart;
 #pragma unroll
       for (int c = 0; c < CPL; c += 2)
-        *reinterpret_cast<float2*>(dst + warp * kPitch + lane * CPL + c) = make_float2(ot[c], ot[c + 1]);
+        *reinterpret_cast<float2*>(dst + row * kPitch + lane * CPL + c) = make_float2(ot[c], ot[c + 1]);
       if (lane == 0) {
-        dst[kRows * kPitch + warp] = mt;
-        dst[kRows * kPitch + kRows + warp] = lt;
+        dst[kRows * kPitch + row] = mt;
+        dst[kRows * kPitch + kRows + row] = lt;
       }
     }
-    e0 = e1;
   }
   if (cuts == 0) return;
   __threadfence();   // the block's parts before its tickets
   __syncthreads();
   if (threadIdx.x < cuts) {
-    const Entry& it = s_entry[s_cut[threadIdx.x]];
+    const Entry& it = s_entry[nth(cut_heads, threadIdx.x)];
     const int b0 = block_of(it.item_start, total, gridDim.x), b1 = block_of(it.item_end - 1, total, gridDim.x);
     // every block has a unit, or every block that has one has one only
     const int parts_of_item = total >= (int)gridDim.x ? b1 - b0 + 1 : it.item_end - it.item_start;
@@ -860,11 +875,12 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     __threadfence();
   }
   __syncthreads();
-  if (warp >= kRows) return;
   const Runs runs(total, gridDim.x);
-  for (int c = 0; c < cuts; ++c) {
+#pragma unroll 1
+  for (int pair = warp; pair < cuts * kRows; pair += kAttWarps) {
+    const int row = pair % kRows, c = pair / kRows;
     if (!s_last[c]) continue;
-    const Entry& it = s_entry[s_cut[c]];
+    const Entry& it = s_entry[nth(cut_heads, c)];
     const int b0 = block_of(it.item_start, total, gridDim.x), count = block_of(it.item_end - 1, total, gridDim.x) - b0 + 1;
     // the last item of block b0 (its first if it begins with it), the first items of the blocks after
     const bool second = runs.start(b0) < it.item_start;
@@ -875,12 +891,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     for (int k0 = 0; k0 < count; k0 += 32) {   // lane k looks at the k-th part
       const int k = k0 + lane;
       const bool has = k < count && runs.start(b0 + k + 1) > runs.start(b0 + k);   // an empty block has no part
-      const float me = has ? __ldcg(part(k) + kRows * kPitch + warp) : ninf;
-      const float le = has ? __ldcg(part(k) + kRows * kPitch + kRows + warp) : 0.f;
-      float mn = me;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(SFFN_FULL_MASK, mn, o));
-      mn = fmaxf(mn, mt);
+      const float me = has ? __ldcg(part(k) + kRows * kPitch + row) : ninf;
+      const float le = has ? __ldcg(part(k) + kRows * kPitch + kRows + row) : 0.f;
+      const float mn = fmaxf(warp_max(me), mt);
       const float back = mt == mn ? 1.f : ex2(mt - mn), w = !has ? 0.f : me == mn ? 1.f : ex2(me - mn);
       mt = mn;
       lt = lt * back + warp_sum(le * w);
@@ -893,7 +906,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         float x[kAhead][CPL];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)   // past the last part: that one again, not used
-          part_row<CPL>(part(min(k0 + i0 + i, count - 1)) + warp * kPitch + lane * CPL, false, x[i]);
+          part_row<CPL>(part(min(k0 + i0 + i, count - 1)) + row * kPitch + lane * CPL, false, x[i]);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const float wi = __shfl_sync(SFFN_FULL_MASK, w, (i0 + i) & 31);
@@ -904,7 +917,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         }
       }
     }
-    write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + warp, lane, ot, mt, lt);
+    write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + row, lane, ot, mt, lt);
   }
 }
 
