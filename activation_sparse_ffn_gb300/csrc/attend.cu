@@ -67,6 +67,10 @@ struct Att {
   static constexpr int kStages = kStage * kWarps * 3 <= kBudget ? 3 : 2;
   static constexpr int kPitch = D + 4;                     // floats of a row of sums: rows two apart use other banks
   static constexpr int kPart = kRows * kPitch + 2 * kRows; // floats of a partial result: sums, maxima, totals
+  // Items of up to so many units are not cut by a block border where the list has at most 32 sequences: another two units
+  // a warp cost less than a join by way of global memory (8 rows over 1024 positions: 12.5 us, joined 14.2; with 8 rows of
+  // each of 32 sequences of 512, D = 64: 16.3 and 19.1; three units a warp are no better).
+  static constexpr int kWhole = 2 * kWarps;
   static constexpr int kSmem = kStage * kStages * kWarps;
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
@@ -274,17 +278,27 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     return v;
   };
   int block_u0, block_u1, u0, u1;
-  auto runs_of = [&]() {
-    const Runs runs(total, gridDim.x);
-    block_u0 = runs.start(blockIdx.x), block_u1 = runs.start(blockIdx.x + 1);
+  auto warp_run = [&]() {
     u0 = warp_start<kAttWarps>(block_u0, block_u1, warp), u1 = warp_start<kAttWarps>(block_u0, block_u1, warp + 1);
   };
   if (a.b.n_seq <= 32) {   // each warp on its own, lane s for sequence s
     look(lane);
     const int upto = warp_scan(mine);
     total = __shfl_sync(SFFN_FULL_MASK, upto, 31);
-    runs_of();
-    const int src = __ffs(__ballot_sync(SFFN_FULL_MASK, u0 < upto)) - 1;
+    const Runs runs(total, gridDim.x);
+    auto owner = [&](int u) { return __ffs(__ballot_sync(SFFN_FULL_MASK, u < upto)) - 1; };
+    // a border within a short item moves to the nearer end of it
+    const int item_units = mine ? units_of(a, sq, U) : 1;
+    auto border = [&](int b) {
+      const int u = runs.start(b), src = max(owner(u), 0);
+      const int off = u - __shfl_sync(SFFN_FULL_MASK, upto - mine, src), n = __shfl_sync(SFFN_FULL_MASK, item_units, src);
+      if (u >= total || n == 1 || n > T::kWhole) return u;
+      const int past = off % n;
+      return 2 * past <= n ? u - past : u - past + n;
+    };
+    block_u0 = border(blockIdx.x), block_u1 = border(blockIdx.x + 1);
+    warp_run();
+    const int src = owner(u0);
     if (src >= 0) {
       first_seq = src;
       first_off = u0 - __shfl_sync(SFFN_FULL_MASK, upto - mine, src);
@@ -312,7 +326,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       lo_u += mine;
     }
     block_scan(lo_u, total);
-    runs_of();
+    const Runs runs(total, gridDim.x);
+    block_u0 = runs.start(blockIdx.x), block_u1 = runs.start(blockIdx.x + 1);
+    warp_run();
     int before = 0;
     for (int s0 = 0; s0 < a.b.n_seq; s0 += kAttThreads) {
       look(s0 + threadIdx.x);
@@ -851,7 +867,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     if (inside) {
       write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + row, lane, ot, mt, lt);
     } else {
-      float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start <= block_u0 ? 0 : 1)) * T::kPart;
+      float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start < block_u0 ? 0 : 1)) * T::kPart;
 #pragma unroll
       for (int c = 0; c < CPL; c += 2)
         *reinterpret_cast<float2*>(dst + row * kPitch + lane * CPL + c) = make_float2(ot[c], ot[c + 1]);
@@ -882,9 +898,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     if (!s_last[c]) continue;
     const Entry& it = s_entry[nth(cut_heads, c)];
     const int b0 = block_of(it.item_start, total, gridDim.x), count = block_of(it.item_end - 1, total, gridDim.x) - b0 + 1;
-    // the last item of block b0 (its first if it begins with it), the first items of the blocks after
-    const bool second = runs.start(b0) < it.item_start;
-    auto part = [&](int k) { return a.block_parts + (size_t)((b0 + k) * 2 + (k == 0 && second ? 1 : 0)) * T::kPart; };
+    auto part = [&](int k) { return a.block_parts + (size_t)((b0 + k) * 2 + (k == 0 ? 1 : 0)) * T::kPart; };
     float mt = ninf, lt = 0.f, ot[CPL];
 #pragma unroll
     for (int e = 0; e < CPL; ++e) ot[e] = 0.f;

@@ -556,3 +556,13 @@ def test_attention_cuts(sffn, seqs, hkv, n):
         o2, l2 = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
         sffn.sffn_attend(c.cache.handle, c.new, q, o2, l2, 1 / 8, 0, ws)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("hkv", [1, 5])
+@pytest.mark.parametrize("first", [(9000, 1), (64 * 15, 1), (64 * 17, 2), (64 * 33, 1)])
+def test_attention_short_and_long_histories_in_one_call(sffn, first, hkv, dtype):
+    """Blocks of work begin and end between short histories, within long ones, and where one follows the other."""
+    lens = [first, (500, 1), (1, 1), (4000, 1), (70, 3), (0, 1), (2000, 1), (0, 0), (64 * 16, 1), (64 * 32, 1), (12000, 1),
+            (64, 64), (1500, 1)]
+    check_attention(sffn, lens, 2 * hkv, hkv, 128, 128, 64, dtype, seed=first[0] + hkv)
