@@ -299,7 +299,7 @@ sffn_status sffn_attend(const sffn_kv* C, const sffn_kv_batch* b, sffn_rows q, i
   const int D = C->desc.head_dim;
   // the kernel's list: blocks of at least 32 positions of every tile of eight rows, counted in 32 bits
   const double tiles = ((double)b->n_tokens * (n_q_heads / C->desc.n_kv_heads) / 8 + b->n_seq) * C->desc.n_kv_heads;
-  if (tiles * ((double)b->table_stride * C->desc.page_size / 32 + 1) > 2147483647.0)
+  if (tiles * ((double)b->table_stride * C->desc.page_size / 32 + 2) > 2147483647.0)
     return invalid("n_tokens * n_q_heads * table_stride * page_size is too large for one call");
   if (!rows_ok(q, b->n_tokens, n_q_heads, D, dtype) || !rows_ok(out, b->n_tokens, n_q_heads, D, dtype))
     return invalid("q, out: need a pointer and strides of at least head_dim, multiples of 16 bytes");

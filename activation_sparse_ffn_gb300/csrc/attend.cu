@@ -71,6 +71,9 @@ struct Att {
   // a warp cost less than a join by way of global memory (8 rows over 1024 positions: 12.5 us, joined 14.2; with 8 rows of
   // each of 32 sequences of 512, D = 64: 16.3 and 19.1; three units a warp are no better).
   static constexpr int kWhole = 2 * kWarps;
+  // What the beginning and the end of an item cost, in units; counted where warps take several units each, so that blocks
+  // with many short items do not end last.
+  static constexpr int kItem = 1;
   static constexpr int kSmem = kStage * kStages * kWarps;
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
 };
@@ -161,9 +164,7 @@ __device__ __forceinline__ int units_of(const AttendArgs& a, const Seq& q, int U
   }
   return max(units, 1);
 }
-__device__ __forceinline__ int total_of(const AttendArgs& a, const Seq& q, int U) {
-  return q.n > 0 ? a.hkv * tiles_of(a, q) * units_of(a, q, U) : 0;
-}
+__device__ __forceinline__ int items_of(const AttendArgs& a, const Seq& q) { return a.hkv * tiles_of(a, q); }
 
 // A place in the list of units.
 struct Cursor {
@@ -171,6 +172,7 @@ struct Cursor {
   int tiles, units;          // of the sequence
   int q0, n, len;
   int base0, first, last;    // position of the tile's unit 0, of its first row, and of its last row
+  int extra;                 // units past the last that an item is given for its beginning and end
 
   __device__ __forceinline__ void set_tile(const AttendArgs& a, int U) {
     const int r0 = tile * kRows, r1 = min(r0 + kRows, n * a.gq) - 1;
@@ -182,7 +184,7 @@ struct Cursor {
   __device__ __forceinline__ void set_seq(const AttendArgs& a, const Seq& q, int U) {
     q0 = q.q0, n = q.n, len = q.len;
     tiles = tiles_of(a, q);
-    units = units_of(a, q, U);
+    units = units_of(a, q, U) + extra;
   }
   __device__ __forceinline__ void advance(const AttendArgs& a, int U) {
     if (++u < units) return;
@@ -261,12 +263,13 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 
   // ---- the block's and the warp's run of units, and the sequence of the warp's first unit
   Seq sq{0, 0, 0};       // that sequence's rows; before that, of the sequence a thread looks at
-  int mine = 0, total, lo_u = 0, first_seq = 0, first_off = 0;
+  int mine = 0, items = 0, total, lo_u = 0, first_seq = 0, first_off = 0, extra = 0;
   auto look = [&](int s) {
-    mine = 0;
+    mine = items = 0;
     if (s < a.b.n_seq) {
       sq = load_seq(a, s);
-      mine = total_of(a, sq, U);
+      items = items_of(a, sq);
+      if (items) mine = items * (units_of(a, sq, U) + extra);
     }
   };
   auto warp_scan = [&](int v) {   // sum over this and earlier lanes
@@ -278,21 +281,24 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     return v;
   };
   int block_u0, block_u1, u0, u1;
+  auto extra_of = [&](int units) { return units > (int)gridDim.x * kAttWarps ? T::kItem : 0; };
   auto warp_run = [&]() {
     u0 = warp_start<kAttWarps>(block_u0, block_u1, warp), u1 = warp_start<kAttWarps>(block_u0, block_u1, warp + 1);
   };
   if (a.b.n_seq <= 32) {   // each warp on its own, lane s for sequence s
     look(lane);
+    extra = extra_of(__reduce_add_sync(SFFN_FULL_MASK, mine));
+    mine += items * extra;
     const int upto = warp_scan(mine);
     total = __shfl_sync(SFFN_FULL_MASK, upto, 31);
     const Runs runs(total, gridDim.x);
     auto owner = [&](int u) { return __ffs(__ballot_sync(SFFN_FULL_MASK, u < upto)) - 1; };
     // a border within a short item moves to the nearer end of it
-    const int item_units = mine ? units_of(a, sq, U) : 1;
+    const int item_units = mine ? mine / items : 1;
     auto border = [&](int b) {
       const int u = runs.start(b), src = max(owner(u), 0);
       const int off = u - __shfl_sync(SFFN_FULL_MASK, upto - mine, src), n = __shfl_sync(SFFN_FULL_MASK, item_units, src);
-      if (u >= total || n == 1 || n > T::kWhole) return u;
+      if (u >= total || n == 1 || n - extra > T::kWhole) return u;
       const int past = off % n;
       return 2 * past <= n ? u - past : u - past + n;
     };
@@ -321,11 +327,18 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       }
       return below + upto - v;
     };
+    int all_items = 0;
     for (int s = threadIdx.x; s < a.b.n_seq; s += kAttThreads) {
       look(s);
       lo_u += mine;
+      all_items += items;
     }
     block_scan(lo_u, total);
+    extra = extra_of(total);
+    if (extra) {
+      block_scan(all_items, all_items);
+      total += all_items * extra;
+    }
     const Runs runs(total, gridDim.x);
     block_u0 = runs.start(blockIdx.x), block_u1 = runs.start(blockIdx.x + 1);
     warp_run();
@@ -353,6 +366,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   Cursor cur{};
   if (any) {
     cur.s = first_seq;
+    cur.extra = extra;
     cur.set_seq(a, sq, U);
     const int item = first_off / cur.units;
     cur.u = first_off - item * cur.units;
