@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   }
   __syncthreads();
 
-  // ---- partial results of the block, a warp per item and row; lane e looks at entry e
+  // ---- partial results of the block: four warps per item, two rows each; lane e looks at entry e
   static_assert(2 * kAttWarps <= 32, "");
   const float* sm = reinterpret_cast<const float*>(smem);
   const bool used = lane < 2 * kAttWarps && s_entry[lane].where != 0;
@@ -842,52 +842,67 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   auto part_of = [&](int e) {   // a warp's last segment is in shared memory, an earlier one in its slot
     return e & 1 ? sm + (e >> 1) * T::kPart : a.warp_parts + (size_t)(blockIdx.x * kAttWarps + (e >> 1)) * T::kPart;
   };
+  const int row0 = warp & 3;
+  float me[2] = {ninf, ninf}, le[2] = {0.f, 0.f};
+  if (used) {
+    const float* p = part_of(lane) + kRows * kPitch + row0;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      me[z] = lane & 1 ? p[4 * z] : __ldcg(p + 4 * z);
+      le[z] = lane & 1 ? p[kRows + 4 * z] : __ldcg(p + kRows + 4 * z);
+    }
+  }
 #pragma unroll 1
-  for (int pair = warp; pair < __popc(heads) * kRows; pair += kAttWarps) {
-    const int row = pair % kRows, e0 = nth(heads, pair / kRows);
-    const Entry& it = s_entry[e0];
+  for (int j = warp >> 2; j < __popc(heads); j += kAttWarps / 4) {
+    const Entry& it = s_entry[nth(heads, j)];
     const bool inside = it.item_start >= block_u0 && it.item_end <= block_u1;
     const bool member = used && of_item == it.item_start;
-    float me = ninf, le = 0.f;
-    if (member) {
-      const float* p = part_of(lane) + kRows * kPitch + row;
-      me = lane & 1 ? p[0] : __ldcg(p);
-      le = lane & 1 ? p[kRows] : __ldcg(p + kRows);
-    }
-    const float mt = warp_max(me);
-    const float w = !member ? 0.f : me == mt ? 1.f : ex2(me - mt);
-    const float lt = warp_sum(le * w);
-    float ot[CPL];
+    float mt[2], lt[2], w[2], ot[2][CPL];
 #pragma unroll
-    for (int c = 0; c < CPL; ++c) ot[c] = 0.f;
+    for (int z = 0; z < 2; ++z) {
+      mt[z] = warp_max(member ? me[z] : ninf);
+      w[z] = !member ? 0.f : me[z] == mt[z] ? 1.f : ex2(me[z] - mt[z]);
+      lt[z] = warp_sum(member ? le[z] * w[z] : 0.f);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) ot[z][c] = 0.f;
+    }
     for (unsigned todo = __ballot_sync(SFFN_FULL_MASK, member); todo;) {
       constexpr int kAhead = 4;
-      float x[kAhead][CPL];
+      float x[kAhead][2][CPL];
       int e[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         e[i] = __ffs(todo) - 1;
         todo &= todo - 1u;
-        if (e[i] >= 0) part_row<CPL>(part_of(e[i]) + row * kPitch + lane * CPL, e[i] & 1, x[i]);
+        if (e[i] < 0) continue;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) part_row<CPL>(part_of(e[i]) + (row0 + 4 * z) * kPitch + lane * CPL, e[i] & 1, x[i][z]);
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (e[i] < 0) break;
-        const float wi = __shfl_sync(SFFN_FULL_MASK, w, e[i]);
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) ot[c] = fmaf(x[i][c], wi, ot[c]);
+        for (int z = 0; z < 2; ++z) {
+          const float wi = __shfl_sync(SFFN_FULL_MASK, w[z], e[i]);
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) ot[z][c] = fmaf(x[i][z][c], wi, ot[z][c]);
+        }
       }
     }
-    if (inside) {
-      write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + row, lane, ot, mt, lt);
-    } else {
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int row = row0 + 4 * z;
+      if (inside) {
+        write_row<D>(a, it.q0, it.n, it.kh, it.tile * kRows + row, lane, ot[z], mt[z], lt[z]);
+        continue;
+      }
       float* dst = a.block_parts + ((long long)blockIdx.x * 2 + (it.item_start < block_u0 ? 0 : 1)) * T::kPart;
 #pragma unroll
       for (int c = 0; c < CPL; c += 2)
-        *reinterpret_cast<float2*>(dst + row * kPitch + lane * CPL + c) = make_float2(ot[c], ot[c + 1]);
+        *reinterpret_cast<float2*>(dst + row * kPitch + lane * CPL + c) = make_float2(ot[z][c], ot[z][c + 1]);
       if (lane == 0) {
-        dst[kRows * kPitch + row] = mt;
-        dst[kRows * kPitch + kRows + row] = lt;
+        dst[kRows * kPitch + row] = mt[z];
+        dst[kRows * kPitch + kRows + row] = lt[z];
       }
     }
   }
