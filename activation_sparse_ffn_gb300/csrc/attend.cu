@@ -18,9 +18,9 @@
 // power of two per row; a weight times its step is rounded to a half once
 // (2^-12 relative, below the result's own rounding; a power of two brings the
 // unit's largest step to 2^13 first, so that small ones keep their bits), the
-// denominator and the mids are summed in fp32. Codes go in as they stand in the word, u times 2^-23 or the
-// like: one mask per pair and no arithmetic; the sums of w are subtracted by
-// starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
+// denominator and the mids are summed in fp32. Codes go in as they stand in the
+// word, u times 2^-23 or the like: one mask per pair and no arithmetic; the sums
+// of w are subtracted by starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
 // p * step are carried by two halves each (22 bits) in two products, and the
 // codes are centred first, because the tensor core truncates its sums: with bare
 // key codes the result is off by 1.3e-6 instead of 0.5e-6 (131072 positions),
@@ -37,6 +37,19 @@
 // merged within the block at its end, and those cut by a block border by the
 // last of their blocks to end, in block order, so that the bits do not depend
 // on which one that is. (A kernel of its own for that cost 3 to 8 us a call.)
+//
+// What bounds it. Memory, for 16-bit rows of long batches: 32 sequences of
+// 32768, 64 heads over 8 of 128 in bf16, 1.14 GB, take 215 us, 5.3 TB/s. Else
+// the warps' own instructions, of which an SM issues 1.5 a cycle at best here
+// (registers allow 8 to 16 warps): fp32 rows need twice the products, one
+// sequence of 131072 takes 53 us (2.7 TB/s; bf16 42); rows of 32 codes a group
+// need four times the params, 24 ragged sequences up to 4099 of 32 heads 86 us
+// (3.1 TB/s); eight proposed tokens of 16 heads a key head read each unit 16
+// times, 34 us. A call's beginning (lengths, page table, first copies) and end
+// (parts of blocks through global memory) are 7 to 16 us of each: 33 positions
+// take 8 us, 1024 12, 16384 19. Tiles of sixteen rows, which decode a unit for
+// twice the rows, hold half as many units in registers and came out even or
+// slower.
 #include "attn.h"
 #include "kv_layout.cuh"
 #include "q4mma.cuh"

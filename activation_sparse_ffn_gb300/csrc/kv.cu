@@ -150,6 +150,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Rows r0 .. r1 - 1 of one kind (0 queries, 1 keys, 2 values) of token i.
+//
+// A group's mid is the middle of its least and largest value and its step a
+// fifteenth of the farther one's distance, each rounded to a half; code u = floor
+// of (x - mid) / (2 step) + 8, limited to 0 .. 15, stands for mid + step (2u - 15).
+// All of it in fp32 with one rounding per operation, in the order of the
+// definition, so that the stored bits can be told beforehand.
+//
+// Bound: queries by memory, keys and values by issue slots (72% busy over the
+// three, arithmetic 57%, DRAM 36%): about 250 instructions per lane and eight
+// channels. 7950 prompt tokens of 32 + 2 x 32 bf16 heads of 128 (297 MB) take 93
+// us, 3.2 TB/s; one token 3 us. Four channels a lane took 2.5 times as long, a
+// loop that serves the three kinds 1.5 times; rows loaded 1 to 4 ahead make no
+// difference, and neither do packed fp32 operations.
 template <int D, typename T, int KIND>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, dtype = dtype_of<T>();
@@ -273,6 +286,10 @@ struct GatherArgs {
   int per, tasks;   // rows of a task, tasks of a token's key rows and of its value rows
 };
 
+// Rows r0 .. r1 - 1 of the keys or values of token i, read back: mid + step (2u - 15),
+// rounded once in fp32 and once to the rows' type. Bound by issue slots (63%
+// busy, DRAM 33%): 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take 43 us,
+// 3.9 TB/s.
 template <int D, typename T, bool VALUE>
 __device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kBatch = 4;

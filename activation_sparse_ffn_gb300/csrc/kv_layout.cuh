@@ -22,9 +22,9 @@
 //
 // Params: for eight positions, the (step, mid) pairs of the keys, then those of
 // the values, each position by position in the order T(0) .. T(7) with its D/G
-// groups beside each other; T(i) = i for i < 4 and i ^ 1 above is the order in which the eight
-// rows (keys) or columns (values) of a matrix operand are assigned to
-// positions. A group with a non-finite value has step = NaN and mid = 0: a
+// groups beside each other; T(i) = i for i < 4 and i ^ 1 above is the order in
+// which the eight rows (keys) or columns (values) of a matrix operand are
+// assigned to positions. A group with a non-finite value has step = NaN and mid = 0: a
 // weight can be cleared before it meets a step, but not before it meets a mid.
 #pragma once
 
@@ -34,11 +34,6 @@ namespace sffn {
 
 // Row or column of a matrix operand <-> position within eight (its own inverse).
 __host__ __device__ constexpr int kv_pos_of_col(int c) { return c ^ (c >> 2); }
-
-template <int D>
-__host__ __device__ constexpr int kv_row_bytes() {
-  return D / 2;
-}
 
 __host__ __device__ constexpr size_t kv_head_bytes(int P, int D, int G) {
   return (size_t)P * D + (size_t)P * (D / G) * 8;
@@ -126,7 +121,6 @@ __device__ __forceinline__ uint32_t transpose_codes(uint32_t w, int lane) {
 struct KvPlace {
   int seq;   // -1: the row belongs to no sequence
   int pos;   // may be negative: no place in the cache
-  int len;   // cached positions of the sequence
 };
 
 __device__ __forceinline__ int kv_len_of(const sffn_kv_batch& b, int s, int P, uint32_t* err) {
@@ -140,11 +134,10 @@ __device__ __forceinline__ int kv_len_of(const sffn_kv_batch& b, int s, int P, u
 }
 
 __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int lane, int P, uint32_t* err) {
-  KvPlace r{-1, -1, 0};
+  KvPlace r{-1, -1};
   if (!b.q_start) {
     r.seq = i;
-    r.len = kv_len_of(b, i, P, err);
-    r.pos = r.len - 1;
+    r.pos = kv_len_of(b, i, P, err) - 1;
     return r;
   }
   for (int s0 = 0; s0 < b.n_seq; s0 += 32) {
@@ -156,14 +149,14 @@ __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int l
     if (past) {
       const int src = __ffs(past) - 1;
       r.seq = s0 + src;
-      r.len = __shfl_sync(SFFN_FULL_MASK, n, src);
+      int len = __shfl_sync(SFFN_FULL_MASK, n, src);
       const int e = __shfl_sync(SFFN_FULL_MASK, end, src);
       const long long most = (long long)b.table_stride * P;
-      if (r.len < 0 || r.len > most) {
+      if (len < 0 || len > most) {
         set_device_error(err, SFFN_ERR_DEVICE);
-        r.len = r.len < 0 ? 0 : (int)most;
+        len = len < 0 ? 0 : (int)most;
       }
-      const long long pos = (long long)r.len - ((long long)e - i);
+      const long long pos = (long long)len - ((long long)e - i);
       r.pos = pos < 0 ? -1 : (int)pos;
       return r;
     }

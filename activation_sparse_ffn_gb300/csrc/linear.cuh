@@ -312,6 +312,15 @@ __device__ __forceinline__ void write_outputs(const LinearArgs& a, const float* 
 
 // At most eight columns. Shared memory: per warp its columns of x, their sums
 // over groups and scales; [tile][warp][B][16] sums; for clusters [tile][B][16].
+//
+// Bound: on paper by the codes (10240 x 8192: 43 MB, 6.4 us at the copy rate);
+// in fact by how long one wave of blocks takes to begin (x converted, first
+// codes from memory) and end (sums through distributed shared memory), about 5
+// of its 13.7 us. Alone and cold it takes 17.9 us with DRAM 31% and issue slots
+// 34% busy; 4096 x 4096 for one token 5.6, 4099 x 11008 with zeros for five
+// 14.0 (replayed from a graph). A barrier between converting x and the products
+// cost 4.6 us (20.5), one chunk of x after another instead of a share per warp
+// is slower at every size.
 template <int G, int FMT>
 __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs a, int cs) {
   constexpr int GS = 128 / G, kAhead = G == 32 && FMT != kScale16 ? (FMT == kScale32 ? 2 : 3) : 4;   // by registers
@@ -477,6 +486,9 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear_few(const LinearArgs 
 }
 
 // x of a call as halves, and its sums over groups, for k_linear: one block per token.
+// Two passes over a token's row, the first for its largest element; the second
+// takes what a warp kept of the first from registers. Bound by latency: 6.7 us
+// for 32 tokens of 8192 alone, of which the next kernel's loads hide a part.
 template <int G, bool Sums>
 __global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int columns, __half* xh, float* downs, float* sums) {
   constexpr int kKeep = 4;   // runs of 128 inputs that a warp keeps between the two passes
@@ -533,6 +545,14 @@ __global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int column
 }
 
 // More than eight columns.
+//
+// Bound: by the warp-level product. At 32 columns each code enters four of them;
+// 2.7e9 products of a 10240 x 8192 layer with 32 tokens are 21K cycles an SM at
+// the rate measured here (850 multiply-adds a cycle and SM), of 31K in the loop
+// and 55K in all: 30 us with k_linear_x before it, 178 TFLOP/s. Two tiles a warp halve the reads of x from shared memory (one:
+// 39 us); three chunks of x instead of one cost 10 us, so the warps' parts take
+// the place of x once it is read (45 us before). Cold: 32.3 us, tensor pipe 34%,
+// DRAM 17%, most waits for codes between steps.
 template <int G, int NT, int FMT>
 __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const LinearArgs a, int cs) {
   constexpr int kWarps = linear_warps(NT), kThreads = kWarps * 32, RT = linear_tiles(NT), GS = 128 / G;
