@@ -159,10 +159,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 //
 // Bound: queries by memory, keys and values by issue slots (72% busy over the
 // three, arithmetic 57%, DRAM 36%): about 250 instructions per lane and eight
-// channels. 7950 prompt tokens of 32 + 2 x 32 bf16 heads of 128 (297 MB) take 93
-// us, 3.2 TB/s; one token 3 us. Four channels a lane took 2.5 times as long, a
-// loop that serves the three kinds 1.5 times; rows loaded 1 to 4 ahead make no
-// difference, and neither do packed fp32 operations.
+// channels. 7950 prompt tokens of 32 + 2 x 32 bf16 heads of 128 (297 MB) take 88
+// us, 3.4 TB/s, of which keys and values alone 73; one token 3 us. Four channels
+// a lane took 2.5 times as long, a loop that serves the three kinds 1.5 times;
+// rows loaded 1 to 4 ahead make no difference, and neither do packed fp32
+// operations.
 template <int D, typename T, int KIND>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, dtype = dtype_of<T>();
@@ -231,18 +232,20 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
     // 0x4b000000 + floor(t); the eight of them are added up with their shifts and the constant taken off at the end.
     // A step that is a normal half and not the largest is within 2^-11 of a fifteenth of the farther end, so that t
     // stays in (0.49, 15.51): then there is nothing to limit.
+    // of keys in the order of their word, before its rotation; of values by channel, for the exchange
+    auto place = [](int e) { return KIND == 1 ? key_field(e) : 4 * e; };
     uint32_t codes = 0;
     if (__all_sync(SFFN_FULL_MASK, stepf >= 6.103515625e-5f && stepf < kHalfMax)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
-        codes += __float_as_uint(__fadd_rz(t, 8388608.f)) << (4 * e);
+        codes += __float_as_uint(__fadd_rz(t, 8388608.f)) << place(e);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[e], midf), inv), 8.f);
-        codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << (4 * e);
+        codes += __float_as_uint(__fadd_rz(fminf(fmaxf(t, 0.f), 15.f), 8388608.f)) << place(e);
       }
     }
     codes -= 0x4b000000u * 0x11111111u;
@@ -262,10 +265,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, tasks = a.q_tasks + 2 * a.kv_tasks;
-  const int task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (task >= a.b.n_tokens * tasks) return;
-  // neighbouring warps take neighbouring tokens, so that those of an SM mostly run the same of the three loops
-  const int part = task / a.b.n_tokens, i = task - part * a.b.n_tokens;
+  // A block's warps take neighbouring tokens and run the same of the three loops (mixed within a block: 1.25 times as
+  // long); blocks take turns, so that the queries' loads and stores are under way beside the others' arithmetic (7950
+  // prompt tokens: 88 us; all queries, then keys, then values 92).
+  const int part = blockIdx.x % tasks, i = blockIdx.x / tasks * kWarps + (threadIdx.x >> 5);
+  if (i >= a.b.n_tokens) return;
   if (part < a.q_tasks) {
     append_rows<D, T, 0>(a, i, part * a.per, min((part + 1) * a.per, a.hq), lane);
   } else {
@@ -288,8 +292,8 @@ struct GatherArgs {
 
 // Rows r0 .. r1 - 1 of the keys or values of token i, read back: mid + step (2u - 15),
 // rounded once in fp32 and once to the rows' type. Bound by issue slots (63%
-// busy, DRAM 33%): 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take 43 us,
-// 3.9 TB/s.
+// busy, DRAM 33%): 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take 41 us,
+// 4.1 TB/s.
 template <int D, typename T, bool VALUE>
 __device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kBatch = 4;
@@ -320,14 +324,15 @@ __device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, 
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const uint32_t codes = VALUE ? transpose_codes(value_codes(w[k]), lane) : key_codes(w[k]);
+      const uint32_t codes = VALUE ? transpose_codes(value_codes(w[k]), lane) : key_fields(w[k]);
       const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pm[k]));
       float x[8];
       // 2u - 15 from the bit pattern of 2^23 + 2u; its product with step is exact in fp32 (a 4-bit by an 11-bit
       // number), so there is one rounding
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t u2 = e == 0 ? codes << 1 : codes >> (4 * e - 1);
+        const int at = VALUE ? 4 * e : key_field(e);
+        const uint32_t u2 = at == 0 ? codes << 1 : codes >> (at - 1);
         x[e] = __fmaf_rn(__uint_as_float((u2 & 30u) | 0x4b000000u) - 8388623.f, sm.x, sm.y);
       }
       if (rb + sub + k * RI < r1) st_run<8>(out, 0, dtype_of<T>(), x);   // no place: step and mid are 0
@@ -340,9 +345,9 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (task >= a.b.n_tokens * 2 * a.tasks) return;
-  const int part = task / a.b.n_tokens, i = task - part * a.b.n_tokens, value = part >= a.tasks;
+  const int lane = threadIdx.x & 31, part = blockIdx.x % (2 * a.tasks), value = part >= a.tasks;
+  const int i = blockIdx.x / (2 * a.tasks) * kWarps + (threadIdx.x >> 5);
+  if (i >= a.b.n_tokens) return;
   const int r0 = (part - value * a.tasks) * a.per, r1 = min(r0 + a.per, a.c.hkv);
   if (value)
     gather_rows<D, T, true>(a, i, r0, r1, lane);
@@ -378,8 +383,7 @@ cudaError_t launch_kv_append(const sffn_kv& C, const sffn_kv_batch& b, const sff
   a.per = rows_per_task((long long)b.n_tokens * (a.hq + 2 * a.c.hkv), std::max(a.hq, a.c.hkv), at_once, C.num_sms);
   a.q_tasks = (a.hq + a.per - 1) / a.per;
   a.kv_tasks = (a.c.hkv + a.per - 1) / a.per;
-  const long long tasks = (long long)b.n_tokens * (a.q_tasks + 2 * a.kv_tasks);
-  const dim3 grid((unsigned)((tasks + kWarps - 1) / kWarps));
+  const dim3 grid((unsigned)((b.n_tokens + kWarps - 1) / kWarps * (a.q_tasks + 2 * a.kv_tasks)));
   return by_dim(C.desc.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     auto run = [&](auto* kern) { return launch_ex(kern, grid, dim3(kWarps * 32), 0, st, true, 1, a); };
@@ -394,8 +398,7 @@ cudaError_t launch_kv_gather(const sffn_kv& C, const sffn_kv_batch& b, const sff
   const int at_once = 32 / (C.desc.head_dim / 8);
   a.per = rows_per_task((long long)b.n_tokens * 2 * a.c.hkv, a.c.hkv, at_once, C.num_sms);
   a.tasks = (a.c.hkv + a.per - 1) / a.per;
-  const long long tasks = (long long)b.n_tokens * 2 * a.tasks;
-  const dim3 grid((unsigned)((tasks + kWarps - 1) / kWarps));
+  const dim3 grid((unsigned)((b.n_tokens + kWarps - 1) / kWarps * 2 * a.tasks));
   return by_dim(C.desc.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     auto run = [&](auto* kern) { return launch_ex(kern, grid, dim3(kWarps * 32), 0, st, true, 1, a); };

@@ -71,22 +71,10 @@ __host__ __device__ constexpr int param_off(int pos, int grp, int n_groups, int 
 // rotated left by one bit. A code lies at bits 1-4 or 5-8 of a half (after a
 // rotation by 8 for e = 2, 3): as a half-precision number the masked bits are
 // u * 2^-23 (or u * 2^-19), exactly.
-// From the codes in channel order, four bits each:
-__host__ __device__ __forceinline__ uint32_t key_word(uint32_t nat) {
-  uint32_t e = nat & 0x0f0f0f0fu, o = (nat >> 4) & 0x0f0f0f0fu;
-  e = (e | e >> 4) & 0x00ff00ffu, o = (o | o >> 4) & 0x00ff00ffu;
-  e = (e | e >> 8) & 0xffffu, o = (o | o >> 8) & 0xffffu;
-  const uint32_t w = e | o << 16;
-  return w << 1 | w >> 31;
-}
-// and back.
-__host__ __device__ __forceinline__ uint32_t key_codes(uint32_t w) {
-  w = w >> 1 | w << 31;
-  uint32_t e = w & 0xffffu, o = w >> 16;
-  e = (e | e << 8) & 0x00ff00ffu, o = (o | o << 8) & 0x00ff00ffu;
-  e = (e | e << 4) & 0x0f0f0f0fu, o = (o | o << 4) & 0x0f0f0f0fu;
-  return e | o << 4;
-}
+// From the codes, that of channel e at bits key_field(e), and back:
+__host__ __device__ constexpr int key_field(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
+__host__ __device__ __forceinline__ uint32_t key_word(uint32_t fields) { return fields << 1 | fields >> 31; }
+__host__ __device__ __forceinline__ uint32_t key_fields(uint32_t w) { return w >> 1 | w << 31; }
 
 // Value word: codes i = 0..3 (channels 64 w + 8 i + g) at bits 4 i of the low
 // half, i = 4..7 likewise of the high half, each half then rotated left by one
