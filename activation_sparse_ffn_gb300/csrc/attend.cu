@@ -30,7 +30,9 @@
 //
 // Work split. The visible blocks of U positions (`units`) of every (sequence,
 // key head, tile of eight rows) are numbered through, and each warp of the grid
-// takes an equal run of that list, whatever the lengths are. A warp streams its
+// takes an equal run of that list, whatever the lengths are; where runs are long
+// an item counts a unit more, for its beginning and end, and short items are kept
+// within a block (kItem and kWhole below). A warp streams its
 // units through a private ring in shared memory with bulk copies per page for
 // keys, values and params, so warps never wait for one another in the loop.
 // Rows whose units lie within one warp are finished by it; the others are
@@ -143,7 +145,7 @@ struct AttendArgs {
   float* block_parts;  // [blocks][2][kPart]
 };
 
-// A sequence's rows and length, made safe for indexing.
+// A sequence's rows and length, made safe for indexing; n is -1 if the rows end before they begin.
 struct Seq {
   int q0, n, len;
 };
@@ -158,8 +160,9 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int s) {
   }
   q.len = len;
   if (a.b.q_start) {
-    q.q0 = min(max(ld_dep(a.b.q_start + s), 0), a.b.n_tokens);
-    q.n = min(max(ld_dep(a.b.q_start + s + 1), q.q0), a.b.n_tokens) - q.q0;
+    const int from = ld_dep(a.b.q_start + s), to = ld_dep(a.b.q_start + s + 1);
+    q.q0 = min(max(from, 0), a.b.n_tokens);
+    q.n = to < from ? -1 : min(max(to, q.q0), a.b.n_tokens) - q.q0;
   } else {
     q.q0 = s;
     q.n = 1;
@@ -179,7 +182,9 @@ __device__ __forceinline__ int units_of(const AttendArgs& a, const Seq& q, int U
   }
   return max(units, 1);
 }
-__device__ __forceinline__ int items_of(const AttendArgs& a, const Seq& q) { return a.hkv * tiles_of(a, q); }
+__device__ __forceinline__ int items_of(const AttendArgs& a, const Seq& q) {
+  return q.n > 0 ? a.hkv * tiles_of(a, q) : 0;
+}
 
 // A place in the list of units.
 struct Cursor {
@@ -213,7 +218,7 @@ struct Cursor {
           ++s;
           if (s >= a.b.n_seq) return;  // past the end of the list: never used
           q = load_seq(a, s);
-        } while (q.n == 0);
+        } while (q.n <= 0);
         set_seq(a, q, U);
       }
     }
@@ -279,10 +284,12 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   // ---- the block's and the warp's run of units, and the sequence of the warp's first unit
   Seq sq{0, 0, 0};       // that sequence's rows; before that, of the sequence a thread looks at
   int mine = 0, items = 0, total, lo_u = 0, first_seq = 0, first_off = 0, extra = 0;
+  bool bad = false;      // starts that descend: rows could lie in many sequences and the list outgrow 32 bits
   auto look = [&](int s) {
     mine = items = 0;
     if (s < a.b.n_seq) {
       sq = load_seq(a, s);
+      bad |= sq.n < 0;
       items = items_of(a, sq);
       if (items) mine = items * (units_of(a, sq, U) + extra);
     }
@@ -302,6 +309,10 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   };
   if (a.b.n_seq <= 32) {   // each warp on its own, lane s for sequence s
     look(lane);
+    if (__any_sync(SFFN_FULL_MASK, bad)) {
+      if (bad) set_device_error(a.err, SFFN_ERR_DEVICE);
+      return;
+    }
     extra = extra_of(__reduce_add_sync(SFFN_FULL_MASK, mine));
     mine += items * extra;
     const int upto = warp_scan(mine);
@@ -347,6 +358,10 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       look(s);
       lo_u += mine;
       all_items += items;
+    }
+    if (__syncthreads_or(bad)) {
+      if (bad) set_device_error(a.err, SFFN_ERR_DEVICE);
+      return;
     }
     block_scan(lo_u, total);
     extra = extra_of(total);
@@ -1032,7 +1047,8 @@ cudaError_t launch_attend(const sffn_kv& C, const sffn_kv_batch& b, const sffn_r
   const AttWs w = att_ws(C);
   uint8_t* p = static_cast<uint8_t*>(ws);
   const AttendArgs a{C.pages, C.page_bytes, C.head_bytes, C.desc.n_pages, C.desc.page_size,
-                     C.desc.page_size == 16 ? 4 : C.desc.page_size == 32 ? 5 : 6, C.desc.n_kv_heads, C.err, b, q, out, lse, n_q_heads, n_q_heads / C.desc.n_kv_heads, dtype, window, scale,
+                     C.desc.page_size == 16 ? 4 : C.desc.page_size == 32 ? 5 : 6, C.desc.n_kv_heads, C.err,
+                     b, q, out, lse, n_q_heads, n_q_heads / C.desc.n_kv_heads, dtype, window, scale,
                      reinterpret_cast<unsigned long long*>(p), reinterpret_cast<float*>(p + w.warp_parts),
                      reinterpret_cast<float*>(p + w.block_parts)};
   const int blocks = C.num_sms;

@@ -549,10 +549,11 @@ __global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int column
 // Bound: by the warp-level product. At 32 columns each code enters four of them;
 // 2.7e9 products of a 10240 x 8192 layer with 32 tokens are 21K cycles an SM at
 // the rate measured here (850 multiply-adds a cycle and SM), of 31K in the loop
-// and 55K in all: 30 us with k_linear_x before it, 178 TFLOP/s. Two tiles a warp halve the reads of x from shared memory (one:
-// 39 us); three chunks of x instead of one cost 10 us, so the warps' parts take
-// the place of x once it is read (45 us before). Cold: 32.3 us, tensor pipe 34%,
-// DRAM 17%, most waits for codes between steps.
+// and 55K in all: 30 us with k_linear_x before it, 178 TFLOP/s. Two tiles a warp
+// halve the reads of x from shared memory (one: 39 us); three chunks of x
+// instead of one cost 10 us, so the warps' parts take the place of x once it is
+// read (45 us before). Cold: 32.3 us, tensor pipe 34%, DRAM 17%, most waits for
+// codes between steps.
 template <int G, int NT, int FMT>
 __global__ void __launch_bounds__(linear_warps(NT) * 32, 1) k_linear(const LinearArgs a, int cs) {
   constexpr int kWarps = linear_warps(NT), kThreads = kWarps * 32, RT = linear_tiles(NT), GS = 128 / G;

@@ -575,7 +575,8 @@ size_t sffn_kv_bytes(const sffn_kv_desc* desc);
 sffn_status sffn_kv_create(const sffn_kv_desc* desc, sffn_kv** out);
 sffn_status sffn_kv_get_desc(const sffn_kv* kv, sffn_kv_desc* out /* host */);
 /* Synchronize the stream, then read and clear the cache's device error word
- * (DEVICE: a page id, length or rotation position out of range was seen). */
+ * (DEVICE: a page id, length, row start or rotation position out of range was
+ * seen). */
 sffn_status sffn_kv_check_error(const sffn_kv* kv, sffn_stream stream);
 void sffn_kv_destroy(sffn_kv* kv);
 
@@ -592,6 +593,7 @@ void sffn_kv_destroy(sffn_kv* kv);
  * A length above table_stride * page_size is taken as that, and a page id
  * outside [0, n_pages) as page 0 in reads and nowhere in writes; both set
  * the cache's device error word. Rows outside every sequence are ignored.
+ * Starts that descend set it too, and sffn_attend then writes nothing.
  * table_stride * page_size: at most 2^30. */
 typedef struct {
   const int32_t* table;

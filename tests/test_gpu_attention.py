@@ -566,3 +566,21 @@ def test_attention_short_and_long_histories_in_one_call(sffn, first, hkv, dtype)
     lens = [first, (500, 1), (1, 1), (4000, 1), (70, 3), (0, 1), (2000, 1), (0, 0), (64 * 16, 1), (64 * 32, 1), (12000, 1),
             (64, 64), (1500, 1)]
     check_attention(sffn, lens, 2 * hkv, hkv, 128, 128, 64, dtype, seed=first[0] + hkv)
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+def test_attention_refuses_rows_that_lie_in_several_sequences(sffn, seqs):
+    """Row starts that descend set the error word; nothing is written, and the cache works on."""
+    c = Case(sffn, [(64, 2)] * seqs, 2, 64, 64, 16)
+    c.fill_cache(sffn, 1.0)
+    q = c.randn(c.fresh, 4, 64)
+    out = torch.full_like(q, 7.0)
+    ws = c.cache.workspace(c.new, 4)
+    starts = c.new.q_start.clone()
+    c.new.q_start[seqs - 1] = 0
+    sffn.sffn_attend(c.cache.handle, c.new, q, out, None, 1.0, 0, ws)
+    with pytest.raises(sffn.SffnError):
+        c.cache.check_error()
+    assert (out == 7.0).all()
+    c.new.q_start.copy_(starts)
+    check_attention(sffn, [(64, 2)] * seqs, 4, 2, 64, 64, 16, case=c)
