@@ -9,7 +9,8 @@
 // cost nothing: the tensor core cuts its addends off at 2^-24 of the largest,
 // and activations have large elements. Tokens are the 8-column operand,
 // as halves: 16-bit activations exactly, up to a power of two per token (and
-// share of the inputs) that brings the largest to 2^13; fp32 activations as two
+// share of the inputs) that brings the largest to 2^13 (bf16 elements below 2^-27
+// of it lose bits); fp32 activations as two
 // columns, the nearest half and the nearest half of what is left (22 bits).
 //
 // Work split. The codes are read once, straight to registers, with kAhead steps'
