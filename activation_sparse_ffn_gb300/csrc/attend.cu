@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   if (threadIdx.x < kAttWarps * T::kStages) mbar_init(&s_bar[0][0] + threadIdx.x, 1);
   if (threadIdx.x < 2 * kAttWarps) s_entry[threadIdx.x].where = 0;
   fence_mbar_init();
+  __syncthreads();   // the first warps initialise the barriers and entries of all
   pdl_launch_dependents();
   pdl_wait();
 
