@@ -14,19 +14,21 @@
 // again the eight rows. The weights change from the first product's result
 // layout to the second's operand layout by an 8 x 8 transpose in registers.
 //
-// Two arithmetics. 16-bit rows (Exact = false): q is exact as halves up to a
-// power of two per row; a weight times its step is rounded to a half once
-// (2^-12 relative, below the result's own rounding; a power of two brings the
-// unit's largest step to 2^13 first, so that small ones keep their bits), the
-// denominator and the mids are summed in fp32. Codes go in as they stand in the
-// word, u times 2^-23 or the like: one mask per pair and no arithmetic; the sums
-// of w are subtracted by starting the sums of w u from -7.5 sum(w). fp32 rows (Exact = true): q and
-// p * step are carried by two halves each (22 bits) in two products, and the
-// codes are centred first, because the tensor core truncates its sums: with bare
-// key codes the result is off by 1.3e-6 instead of 0.5e-6 (131072 positions),
-// and with bare value codes, all weights being positive, by far more over a long
-// history. Either way the sums of one unit's positions leave the tensor core
-// and are added up in fp32.
+// Arithmetic. A weight times its step is carried by two halves (22 bits) in two
+// products, after a power of two that brings the unit's largest step to 2^13, so
+// that small ones keep their bits. With one half the results of fp16 rows were a
+// quarter further from the exact ones than fp32 arithmetic leaves them (2.7e-4
+// and 2.1e-4 of their norm). Value codes are centred first, because the tensor
+// core truncates its sums: with bare codes, all weights being positive, that adds
+// up over a long history (131072 positions of fp16 rows: 2.3e-4). Key codes of
+// fp32 rows (Exact = true) are centred too and q is carried by two halves: with
+// bare key codes the result is off by 1.3e-6 instead of 0.5e-6 (131072
+// positions). Key codes of 16-bit rows (Exact = false) go in as they stand in the
+// word, u times 2^-23 or the like, one mask per pair and no arithmetic, and q is
+// one half after a power of two per row: exact for elements down to 2^-23 of the
+// row's largest, smaller ones to 2^-34 of it. Either way the sums of one unit's
+// positions leave the tensor core and are added up in fp32, like the denominator
+// and the mids.
 //
 // Work split. The visible blocks of U positions (`units`) of every (sequence,
 // key head, tile of eight rows) are numbered through, and each warp of the grid
@@ -686,17 +688,14 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     }
     float up, down;
     scale_to_half_range(row_max(top), up, down);
-    const float k0 = Exact ? down : down * 16777216.f, k1 = Exact ? down : down * 1048576.f;  // bare codes: u * 2^-23, 2^-19
-    uint32_t wt[QL][GW][SU / 16][2];
-    float ws[GW][4];
+    uint32_t wt[2][GW][SU / 16][2];
 #pragma unroll
     for (int w = 0; w < D / 64; ++w) {
       if (w * 64 % G == 0) {
 #pragma unroll
-        for (int n = 0; n < GW; ++n) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < GW; ++n)
 #pragma unroll
-          for (int i = 0; i < SU / 16; ++i) {
+          for (int i = 0; i < SU / 16; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const float st = step[i][k][w * 64 / G + n] * up;
@@ -705,24 +704,11 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
                 if (s[i][2 * k] == 0.f) x0 = 0.f;
                 if (s[i][2 * k + 1] == 0.f) x1 = 0.f;
               }
-              if (Exact) {
-                uint32_t hi, lw;
-                split_f16(x0, x1, hi, lw);
-                wt[0][n][i][k] = transpose_8x8(hi);
-                wt[QL - 1][n][i][k] = transpose_8x8(lw);
-              } else {
-                wt[0][n][i][k] = transpose_8x8(h2_u32(__floats2half2_rn(x0, x1)));
-              }
+              uint32_t hi, lw;
+              split_f16(x0, x1, hi, lw);
+              wt[0][n][i][k] = transpose_8x8(hi);
+              wt[1][n][i][k] = transpose_8x8(lw);
             }
-            if (!Exact) {
-              const uint32_t one[4] = {0x3c003c00u, 0u, 0x3c003c00u, 0u};
-              mma_f16(c, one, wt[0][n][i][0], wt[0][n][i][1]);
-            }
-          }
-          // -15 sum(w) in units of the products of bare codes
-          ws[n][0] = c[0] * -8.940697e-7f, ws[n][1] = c[1] * -8.940697e-7f;
-          ws[n][2] = ws[n][0] * 16.f, ws[n][3] = ws[n][1] * 16.f;
-        }
       }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -736,23 +722,18 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
             const int pick = hh ? (e ? 0x6723 : 0x7632) : (e ? 0x4501 : 0x5410);
             const uint32_t x0 = __byte_perm(vw[k][0][w], vw[k][1][w], pick);
             const uint32_t x1 = __byte_perm(vw[k][2][w], vw[k][3][w], pick);
-            if (Exact) {
-              const uint32_t av[4] = {value_low(x0), value_high(x0), value_low(x1), value_high(x1)};
-              if (k == 0) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
-              mma_f16(acc[e], av, wt[0][n][k][0], wt[0][n][k][1]);
-              mma_f16(acc[e], av, wt[QL - 1][n][k][0], wt[QL - 1][n][k][1]);
-            } else {
-              const uint32_t av[4] = {x0 & 0x001e001eu, x0 & 0x01e001e0u, x1 & 0x001e001eu, x1 & 0x01e001e0u};
-              mma_f16_from(acc[e], av, wt[0][n][k][0], wt[0][n][k][1], k == 0 ? ws[n] : acc[e]);
-            }
+            const uint32_t av[4] = {value_low(x0), value_high(x0), value_low(x1), value_high(x1)};
+            if (k == 0) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+            mma_f16(acc[e], av, wt[0][n][k][0], wt[0][n][k][1]);
+            mma_f16(acc[e], av, wt[1][n][k][0], wt[1][n][k][1]);
           }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float* ox = o[4 * w + 2 * hh + e];
-          ox[0] = fmaf(acc[e][0], k0, ox[0]);
-          ox[1] = fmaf(acc[e][1], k0, ox[1]);
-          ox[2] = fmaf(acc[e][2], k1, ox[2]);
-          ox[3] = fmaf(acc[e][3], k1, ox[3]);
+          ox[0] = fmaf(acc[e][0], down, ox[0]);
+          ox[1] = fmaf(acc[e][1], down, ox[1]);
+          ox[2] = fmaf(acc[e][2], down, ox[2]);
+          ox[3] = fmaf(acc[e][3], down, ox[3]);
         }
       }
     }
