@@ -414,6 +414,11 @@ def sffn_stack_destroy(stack) -> None:
 # These calls are launched once per layer and token and take a few microseconds on the device, so the marshalling
 # below asks each tensor for each property once.
 
+# The C calls see pointers and strides, not how many elements stand behind them, so the sizes of every handle made here
+# are kept, and the tensors of a call are compared with them.
+_linear_sizes = {}   # handle: (in_features, out_features)
+_kv_sizes = {}       # handle: (n_kv_heads, head_dim)
+
 _NO_ROWS = RowsC()
 _IO_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -438,6 +443,33 @@ def _io_dtype(dtype) -> int:
     return d
 
 
+def _flat_rows(t, width, name) -> None:
+    """Rows of `width` elements beside each other: (rows, width), or (rows, heads, dim) with contiguous heads."""
+    shape = t.shape
+    if len(shape) == 3 and (shape[1] == 1 or t.stride(1) == shape[2]):
+        shape = (shape[0], shape[1] * shape[2])
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} given, rows of {width} contiguous elements wanted")
+
+
+def _linear_size(linear):
+    """Of a handle that was made elsewhere."""
+    d = sffn_linear_get_desc(linear)
+    return d.in_features, d.out_features
+
+
+def _kv_size(kv):
+    """Of a handle that was made elsewhere."""
+    d = sffn_kv_get_desc(kv)
+    return d.n_kv_heads, d.head_dim
+
+
+def _kv_rows(t, shape, name) -> None:
+    """Rows of every key head: (n, heads, dim), or (n, dim) with one head."""
+    if t.shape != shape and (shape[1] != 1 or t.shape != (shape[0], shape[2])):
+        _want(t, shape, name)
+
+
 def _want(t, shape, name) -> None:
     if t is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} given, {tuple(shape)} wanted")
@@ -460,10 +492,21 @@ def sffn_linear_validate(desc: LinearDesc) -> int:
 def sffn_linear_create(desc: LinearDesc) -> int:
     h = _vp()
     _check(_lib.sffn_linear_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_linear_create")
+    _linear_sizes[h.value] = (desc.in_features, desc.out_features)
     return h.value
 
 
 def sffn_linear_pack(linear, codes, scales, zeros=None, bias=None, stream=None) -> None:
+    d = sffn_linear_get_desc(linear)
+    scale_type = {v: k for k, v in _IO_DTYPE.items()}[d.scale_dtype]
+    groups = (d.out_features, d.in_features // d.group)
+    for t, shape, dtype, name in ((codes, (d.out_features, d.in_features), torch.int8, "codes"),
+                                  (scales, groups, scale_type, "scales"), (zeros, groups, scale_type, "zeros"),
+                                  (bias, (d.out_features,), torch.float32, "bias")):
+        if isinstance(t, torch.Tensor):
+            _want(t, shape, name)
+            if t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous {dtype} tensor is wanted")
     _check(_lib.sffn_linear_pack(linear, _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _stream(stream)),
            "sffn_linear_pack")
 
@@ -481,10 +524,18 @@ def sffn_linear_workspace_bytes(linear, B: int) -> int:
 def sffn_linear_forward(linear, x, y, residual=None, ws=None, stream=None) -> None:
     """y (B, out) = x (B, in) through the layer, plus residual (B, out) if given (it may be y itself)."""
     B, dtype, shape = x.shape[0], x.dtype, y.shape
+    n_in, n_out = _linear_sizes.get(linear) or _linear_size(linear)
+    if x.shape != (B, n_in):
+        _flat_rows(x, n_in, "x")
+    if shape != (B, n_out):
+        _flat_rows(y, n_out, "y")
     if shape[0] != B:
         raise ValueError("x and y differ in their number of rows")
-    if residual is not None and residual.shape != shape:
-        _want(residual, shape, "residual")
+    if residual is not None:
+        if residual.shape != shape:
+            _want(residual, shape, "residual")
+        if len(shape) != 2:
+            _flat_rows(residual, n_out, "residual")
     ws_ptr, ws_bytes = _ws_args(ws)
     rc = _lib.sffn_linear_forward(linear, _rows(x, None, "x"), B, _rows(residual, dtype, "residual"),
                                   _rows(y, dtype, "y"), _io_dtype(dtype), ws_ptr, ws_bytes, _stream(stream))
@@ -497,6 +548,7 @@ def sffn_linear_check_error(linear, stream=None) -> None:
 
 
 def sffn_linear_destroy(linear) -> None:
+    _linear_sizes.pop(linear, None)
     _lib.sffn_linear_destroy(linear)
 
 
@@ -516,6 +568,7 @@ def sffn_kv_bytes(desc: KvDesc) -> int:
 def sffn_kv_create(desc: KvDesc) -> int:
     h = _vp()
     _check(_lib.sffn_kv_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_kv_create")
+    _kv_sizes[h.value] = (desc.n_kv_heads, desc.head_dim)
     return h.value
 
 
@@ -530,30 +583,33 @@ def sffn_kv_check_error(kv, stream=None) -> None:
 
 
 def sffn_kv_destroy(kv) -> None:
+    _kv_sizes.pop(kv, None)
     _lib.sffn_kv_destroy(kv)
 
 
-def _token_rows(t, n, name) -> None:
-    if t.shape[0] != n:
-        raise ValueError(f"{name}: {t.shape[0]} rows given, {n} wanted")
+def _head_rows(shape, n, dim, name) -> int:
+    """Heads of a (n, heads, dim) shape."""
+    if len(shape) != 3 or shape[0] != n or shape[2] != dim:
+        raise ValueError(f"{name}: shape {tuple(shape)} given, ({n}, heads, {dim}) wanted")
+    return shape[1]
 
 
 def sffn_kv_append(kv, batch: "KvBatch", q, k, v, q_out=None, rope: "Rope | None" = None, stream=None) -> None:
     """Append k, v (tokens, kv heads, dim); rotate q (tokens, heads, dim) into q_out if q is not None."""
-    n, dtype, shape, n_q_heads = batch.n_tokens, k.dtype, k.shape, 0
-    if shape[0] != n:
-        _token_rows(k, n, "k")
+    n, dtype, n_q_heads = batch.n_tokens, k.dtype, 0
+    heads, dim = _kv_sizes.get(kv) or _kv_size(kv)
+    shape = (n, heads, dim)
+    if k.shape != shape:
+        _kv_rows(k, shape, "k")
     if v.shape != shape:
-        _want(v, shape, "v")
+        _kv_rows(v, shape, "v")
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is required with q")
         q_shape = q.shape
-        if q_shape[0] != n:
-            _token_rows(q, n, "q")
+        n_q_heads = _head_rows(q_shape, n, dim, "q")
         if q_out.shape != q_shape:
             _want(q_out, q_shape, "q_out")
-        n_q_heads = q_shape[1]
     if rope is not None and rope.positions is not None:
         _want(rope.positions, (n,), "positions")
     rc = _lib.sffn_kv_append(kv, batch.ref, _rows(q, dtype, "q"), n_q_heads, _rows(k, None, "k"),
@@ -566,10 +622,12 @@ def sffn_kv_append(kv, batch: "KvBatch", q, k, v, q_out=None, rope: "Rope | None
 def sffn_kv_gather(kv, batch: "KvBatch", k_out, v_out, stream=None) -> None:
     """Values the cache holds for the batch's tokens; either output may be None."""
     dtype = (k_out if k_out is not None else v_out).dtype
-    if k_out is not None:
-        _token_rows(k_out, batch.n_tokens, "k_out")
-    if v_out is not None:
-        _token_rows(v_out, batch.n_tokens, "v_out")
+    heads, dim = _kv_sizes.get(kv) or _kv_size(kv)
+    shape = (batch.n_tokens, heads, dim)
+    if k_out is not None and k_out.shape != shape:
+        _kv_rows(k_out, shape, "k_out")
+    if v_out is not None and v_out.shape != shape:
+        _kv_rows(v_out, shape, "v_out")
     rc = _lib.sffn_kv_gather(kv, batch.ref, _rows(k_out, dtype, "k_out"), _rows(v_out, dtype, "v_out"),
                              _io_dtype(dtype), _stream(stream))
     if rc:
@@ -583,8 +641,7 @@ def sffn_attend_workspace_bytes(kv, n_q_heads: int, n_seq: int, n_tokens: int) -
 def sffn_attend(kv, batch: "KvBatch", q, out, lse, scale, window=0, ws=None, stream=None) -> None:
     """out (tokens, heads, dim) = attention of q over the cache; lse (tokens, heads) float32 or None."""
     shape, dtype = q.shape, q.dtype
-    if shape[0] != batch.n_tokens:
-        _token_rows(q, batch.n_tokens, "q")
+    _head_rows(shape, batch.n_tokens, (_kv_sizes.get(kv) or _kv_size(kv))[1], "q")
     if out.shape != shape:
         _want(out, shape, "out")
     lse_ptr = None
