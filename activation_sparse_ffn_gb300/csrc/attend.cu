@@ -147,24 +147,19 @@ struct AttendArgs {
   float* block_parts;  // [blocks][2][kPart]
 };
 
-// A sequence's rows and length, made safe for indexing; n is -1 if the rows end before they begin.
+// A sequence's rows and length, made safe for indexing; n is -1 if the rows are out of order or not the call's.
 struct Seq {
   int q0, n, len;
 };
 
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int s) {
   Seq q;
-  const long long most = (long long)a.b.table_stride * a.P;
-  int len = ld_dep(a.b.kv_len + s);
-  if (len < 0 || len > most) {
-    set_device_error(a.err, SFFN_ERR_DEVICE);
-    len = len < 0 ? 0 : (int)most;
-  }
-  q.len = len;
+  q.len = kv_len_of(a.b, s, a.P, a.err);
   if (a.b.q_start) {
-    const int from = ld_dep(a.b.q_start + s), to = ld_dep(a.b.q_start + s + 1);
-    q.q0 = min(max(from, 0), a.b.n_tokens);
-    q.n = to < from ? -1 : min(max(to, q.q0), a.b.n_tokens) - q.q0;
+    KvSpan rows;
+    const bool ok = kv_span(a.b, s, rows);
+    q.q0 = rows.from;
+    q.n = ok ? rows.to - rows.from : -1;
   } else {
     q.q0 = s;
     q.n = 1;
@@ -287,7 +282,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   // ---- the block's and the warp's run of units, and the sequence of the warp's first unit
   Seq sq{0, 0, 0};       // that sequence's rows; before that, of the sequence a thread looks at
   int mine = 0, items = 0, total, lo_u = 0, first_seq = 0, first_off = 0, extra = 0;
-  bool bad = false;      // starts that descend: rows could lie in many sequences and the list outgrow 32 bits
+  bool bad = false;      // starts out of order: rows could lie in many sequences and the list outgrow 32 bits
   auto look = [&](int s) {
     mine = items = 0;
     if (s < a.b.n_seq) {

@@ -111,8 +111,7 @@ struct KvPlace {
   int pos;   // may be negative: no place in the cache
 };
 
-__device__ __forceinline__ int kv_len_of(const sffn_kv_batch& b, int s, int P, uint32_t* err) {
-  const int n = ld_dep(b.kv_len + s);
+__device__ __forceinline__ int kv_len_in_table(const sffn_kv_batch& b, int n, int P, uint32_t* err) {
   const long long most = (long long)b.table_stride * P;
   if (n < 0 || n > most) {
     set_device_error(err, SFFN_ERR_DEVICE);
@@ -120,7 +119,20 @@ __device__ __forceinline__ int kv_len_of(const sffn_kv_batch& b, int s, int P, u
   }
   return n;
 }
+__device__ __forceinline__ int kv_len_of(const sffn_kv_batch& b, int s, int P, uint32_t* err) {
+  return kv_len_in_table(b, ld_dep(b.kv_len + s), P, err);
+}
 
+// The rows of sequence s: q_start[s] .. q_start[s + 1] - 1. False if they do not ascend within the call's rows.
+struct KvSpan {
+  int from, to;
+};
+__device__ __forceinline__ bool kv_span(const sffn_kv_batch& b, int s, KvSpan& r) {
+  r.from = ld_dep(b.q_start + s), r.to = ld_dep(b.q_start + s + 1);
+  return r.from >= 0 && r.to >= r.from && r.to <= b.n_tokens;
+}
+
+// Every sequence is looked at, not only those up to the row's: where starts are out of order no row has a place.
 __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int lane, int P, uint32_t* err) {
   KvPlace r{-1, -1};
   if (!b.q_start) {
@@ -128,27 +140,29 @@ __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int l
     r.pos = kv_len_of(b, i, P, err) - 1;
     return r;
   }
+  bool bad = false;
+  int len = 0;
   for (int s0 = 0; s0 < b.n_seq; s0 += 32) {
     const int s = s0 + lane;
-    const bool in = s < b.n_seq;
-    const int end = in ? ld_dep(b.q_start + s + 1) : 0x7fffffff;
-    const int n = in ? ld_dep(b.kv_len + s) : 0;
-    const unsigned past = __ballot_sync(SFFN_FULL_MASK, in && end > i);
-    if (past) {
-      const int src = __ffs(past) - 1;
+    KvSpan rows{0, 0};
+    int n = 0;
+    if (s < b.n_seq) {
+      n = ld_dep(b.kv_len + s);
+      bad |= !kv_span(b, s, rows);
+    }
+    const unsigned here = __ballot_sync(SFFN_FULL_MASK, rows.from <= i && i < rows.to);
+    if (here) {
+      const int src = __ffs(here) - 1;
       r.seq = s0 + src;
-      int len = __shfl_sync(SFFN_FULL_MASK, n, src);
-      const int e = __shfl_sync(SFFN_FULL_MASK, end, src);
-      const long long most = (long long)b.table_stride * P;
-      if (len < 0 || len > most) {
-        set_device_error(err, SFFN_ERR_DEVICE);
-        len = len < 0 ? 0 : (int)most;
-      }
-      const long long pos = (long long)len - ((long long)e - i);
-      r.pos = pos < 0 ? -1 : (int)pos;
-      return r;
+      r.pos = __shfl_sync(SFFN_FULL_MASK, rows.to, src) - i;   // rows from this one to the sequence's last
+      len = __shfl_sync(SFFN_FULL_MASK, n, src);
     }
   }
+  if (__any_sync(SFFN_FULL_MASK, bad)) {
+    set_device_error(err, SFFN_ERR_DEVICE);
+    r.seq = -1;
+  }
+  if (r.seq >= 0) r.pos = max(kv_len_in_table(b, len, P, err) - r.pos, -1);
   return r;
 }
 

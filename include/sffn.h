@@ -588,12 +588,14 @@ void sffn_kv_destroy(sffn_kv* kv);
  * place in the cache (a sequence that is padded at its front).
  *   table   [n_seq][table_stride] page ids, device
  *   kv_len  [n_seq] device
- *   q_start [n_seq + 1] device, ascending from 0, at most n_tokens; or NULL:
- *           one token per sequence (n_tokens == n_seq)
+ *   q_start [n_seq + 1] device, ascending from at least 0 to at most
+ *           n_tokens; or NULL: one token per sequence (n_tokens == n_seq)
  * A length above table_stride * page_size is taken as that, and a page id
  * outside [0, n_pages) as page 0 in reads and nowhere in writes; both set
- * the cache's device error word. Rows outside every sequence are ignored.
- * Starts that descend set it too, and sffn_attend then writes nothing.
+ * the cache's device error word. Rows outside every sequence (before
+ * q_start[0] or from q_start[n_seq] on) are ignored: nothing is read from or
+ * written to their places. Starts that descend or lie outside 0 .. n_tokens
+ * set the error word too, and the call then writes nothing.
  * table_stride * page_size: at most 2^30. */
 typedef struct {
   const int32_t* table;

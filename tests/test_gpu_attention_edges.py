@@ -40,3 +40,84 @@ def test_attention_of_16_bit_rows_keeps_fp32_sums(sffn, D, G, dtype):
         R.assert_close(oh[row:row + m], want, tol, dtype, f"attention len {n} new {m}")
         at, row = at + n, row + m
     c.cache.check_error()
+
+
+# ------------------------------------------------------------------ rows outside a call's sequences
+
+def call_all(sffn, c, batch, heads=4):
+    """(queries, keys, values, attention) that append, read-back and attention leave in arrays of sevens."""
+    n = batch.n_tokens
+    q, k, v = c.randn(n, heads, c.D), c.randn(n, c.hkv, c.D), c.randn(n, c.hkv, c.D)
+    qo, ko, vo, out = (torch.full_like(t, 7.0) for t in (q, k, v, q))
+    sffn.sffn_kv_append(c.cache.handle, batch, q, k, v, qo)
+    errors = [flagged(sffn, c)]
+    sffn.sffn_kv_gather(c.cache.handle, batch, ko, vo)
+    errors.append(flagged(sffn, c))
+    sffn.sffn_attend(c.cache.handle, batch, q, out, None, 0.1, 0, c.cache.workspace(batch, heads))
+    return (q, k, v), (qo, ko, vo, out), errors + [flagged(sffn, c)]
+
+
+def flagged(sffn, c):
+    try:
+        c.cache.check_error()
+    except sffn.SffnError as e:
+        assert e.status == sffn.SFFN_ERR_DEVICE
+        return True
+    return False
+
+
+def held(sffn, c):
+    k, v = (torch.empty(c.total, c.hkv, c.D, device="cuda") for _ in range(2))
+    sffn.sffn_kv_gather(c.cache.handle, c.all, k, v)
+    c.cache.check_error()
+    return k, v
+
+
+@pytest.mark.parametrize("seqs", [1, 3, 40])
+def test_rows_before_the_first_start_and_after_the_last_are_ignored(sffn, seqs):
+    lens = [(20 + s % 7, 2) for s in range(seqs)]
+    c = Case(sffn, lens, 2, 64, 64, 16, seed=seqs)
+    c.fill_cache(sffn)
+    before = held(sffn, c)
+    b = sffn.KvBatch(c.table, c.kv_len, c.new.q_start + 5, c.fresh + 9)        # rows 0 .. 4 and the last four
+    (q, k, v), (qo, ko, vo, out), errors = call_all(sffn, c, b)
+    assert errors == [False] * 3
+    for t in (qo, ko, vo, out):
+        assert (t[:5] == 7).all() and (t[5 + c.fresh:] == 7).all()
+    rows = slice(5, 5 + c.fresh)
+    assert torch.equal(qo[rows], q[rows])
+    assert np.array_equal(ko[rows].cpu().numpy(), R.stored(k[rows].cpu().numpy(), 64))
+    assert np.array_equal(vo[rows].cpu().numpy(), R.stored(v[rows].cpu().numpy(), 64))
+    at = 0
+    after = held(sffn, c)
+    for n, m in lens:                                                          # nothing before the new positions changed
+        for x, y in zip(before, after):
+            assert torch.equal(x[at:at + n - m], y[at:at + n - m])
+        at += n
+    want, _ = attend(sffn, c, c.new, q[rows].contiguous(), 0.1)
+    assert torch.equal(out[rows], want)
+
+
+@pytest.mark.parametrize("seqs", [1, 3, 40])
+@pytest.mark.parametrize("what", ["descends early", "descends late", "negative", "past the end"])
+def test_starts_out_of_order_write_nothing(sffn, seqs, what):
+    lens = [(20 + s % 7, 2) for s in range(seqs)]
+    c = Case(sffn, lens, 2, 64, 64, 16, seed=seqs)
+    c.fill_cache(sffn)
+    before = held(sffn, c)
+    good = c.new.q_start.clone()
+    if what == "descends early":
+        c.new.q_start[0] = good[1] + 1
+    elif what == "descends late":
+        c.new.q_start[seqs] = good[seqs - 1] - 1          # one sequence: negative too
+    elif what == "negative":
+        c.new.q_start[0] = -1
+    else:
+        c.new.q_start[seqs] = c.fresh + 1
+    _, outs, errors = call_all(sffn, c, c.new)
+    assert errors == [True] * 3
+    assert all((t == 7).all() for t in outs)
+    assert all(torch.equal(x, y) for x, y in zip(before, held(sffn, c)))
+    c.new.q_start.copy_(good)
+    _, _, errors = call_all(sffn, c, c.new)
+    assert errors == [False] * 3
