@@ -432,9 +432,11 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
     const int st = slot_of(issued), base = nxt.base(U);
     uint8_t* dst = ring + st * T::kStage;
     const int n_runs = min(parts, ((nxt.last - base) >> rp_log2) + 1);
-    if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][st], (uint32_t)((n_runs << rp_log2) * (D + 8 * NG)));
+    // runs that lie before the window hold nothing any row sees, and their pages may be gone
+    const int run0 = a.window > 0 ? max(0, nxt.first - a.window + 1 - base) >> rp_log2 : 0;
+    if (lane == 0) mbar_arrive_expect_tx(&s_bar[warp][st], (uint32_t)(((n_runs - run0) << rp_log2) * (D + 8 * NG)));
     __syncwarp();
-    if (lane < n_runs) {
+    if (lane >= run0 && lane < n_runs) {
       if (page < 0 || page >= a.n_pages) {
         set_device_error(a.err, SFFN_ERR_DEVICE);
         page = 0;

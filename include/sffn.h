@@ -641,7 +641,8 @@ sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host
  *   lse[i][h] = log sum_j exp(scale * q[i][h] . K[j])  (fp32, or NULL),
  * softmax statistics and sums in fp32. A token that sees nothing gives out =
  * 0 and lse = -infinity. Positions a token does not see never reach its
- * result, whatever is stored there. q, out in `dtype`; q and out must not
+ * result, whatever is stored there, and the ids of pages that no token of the
+ * call sees are not looked at: those before a window may have been retired. q, out in `dtype`; q and out must not
  * overlap. The same arguments give the same bits at every call.
  * n_q_heads: a multiple of n_kv_heads, n_q_heads * n_tokens at most 2^30, and
  * (n_q_heads * n_tokens / 8 + n_kv_heads * n_seq) * (table_stride * page_size

@@ -121,3 +121,31 @@ def test_starts_out_of_order_write_nothing(sffn, seqs, what):
     c.new.q_start.copy_(good)
     _, _, errors = call_all(sffn, c, c.new)
     assert errors == [False] * 3
+
+
+# ------------------------------------------------------------------ pages outside a window
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (128, 64), (256, 16)])
+@pytest.mark.parametrize("window", [1, 17, 40, 100])
+def test_pages_before_the_window_may_be_gone(sffn, D, P, window):
+    """Page ids no row of the call sees are replaced by invalid ones: the same bits and no error. A page that is seen in
+    part is still looked at."""
+    lens = [(300, 1), (250, 9), (64, 64), (33, 2), (129, 3)]
+    c = Case(sffn, lens, 2, D, 64, P, seed=window + P)
+    c.fill_cache(sffn)
+    q = c.randn(c.fresh, 16, D)
+    want, wlse = attend(sffn, c, c.new, q, 0.1, window)
+    c.cache.check_error()
+    first = [max(0, n - m - window + 1) // P for n, m in lens]                # first page that is seen
+    gone = c.table.clone()
+    for s, f in enumerate(first):
+        gone[s, :f] = -1 if s % 2 else c.n_pages + 5
+        gone[s, -(-lens[s][0] // P):] = -7
+    assert sum(first) > 0
+    b = sffn.KvBatch(gone, c.kv_len, c.new.q_start, c.fresh)
+    out, lse = attend(sffn, c, b, q, 0.1, window)
+    c.cache.check_error()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    gone[0, first[0]] = -1
+    attend(sffn, c, b, q, 0.1, window)
+    assert flagged(sffn, c)
