@@ -605,13 +605,14 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         }
       }
     }
+    uint32_t unseen = 0u;   // bit 4i + e: the row does not see the position of s[i][e]
     if (Masked) {
 #pragma unroll
       for (int i = 0; i < SU / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = base + 16 * i + 8 * (e >> 1) + kt;
-          if (j > pos[e & 1] || j < lo[e & 1]) s[i][e] = ninf;
+          if (j > pos[e & 1] || j < lo[e & 1]) s[i][e] = ninf, unseen |= 1u << (4 * i + e);
         }
     }
     float mu[2] = {m[0], m[1]};
@@ -697,9 +698,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
             for (int k = 0; k < 2; ++k) {
               const float st = step[i][k][w * 64 / G + n] * up;
               float x0 = s[i][2 * k] * st, x1 = s[i][2 * k + 1] * st;
-              if (Masked) {   // a step may be NaN for the rows that see it
-                if (s[i][2 * k] == 0.f) x0 = 0.f;
-                if (s[i][2 * k + 1] == 0.f) x1 = 0.f;
+              if (Masked) {   // a step may be NaN for the rows that see it, also where their weight has become 0
+                if (unseen >> (4 * i + 2 * k) & 1u) x0 = 0.f;
+                if (unseen >> (4 * i + 2 * k + 1) & 1u) x1 = 0.f;
               }
               uint32_t hi, lw;
               split_f16(x0, x1, hi, lw);

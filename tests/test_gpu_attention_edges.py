@@ -149,3 +149,25 @@ def test_pages_before_the_window_may_be_gone(sffn, D, P, window):
     gone[0, first[0]] = -1
     attend(sffn, c, b, q, 0.1, window)
     assert flagged(sffn, c)
+
+
+# ------------------------------------------------------------------ what stands at positions
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("j", [35, 63, 100, 126, 129])
+def test_a_visible_nan_value_is_seen_whatever_its_weight(sffn, dtype, window, j):
+    """Scores so far apart that most weights are 0: the NaN channels of a position are NaN in every row that sees it, in
+    units that all rows see whole and in the others, and in no other row or channel."""
+    lens = [(131, 3)]
+    c = Case(sffn, lens, 1, 128, 64, 16, dtype, seed=j)
+    k, v = c.fill_cache(sffn)
+    v = v.clone()
+    v[j, 0, 70] = float("nan")                           # channels 64 .. 127
+    sffn.sffn_kv_append(c.cache.handle, c.all, None, k, v)
+    q = c.randn(3, 16, 128)
+    out, lse = attend(sffn, c, c.new, q, 60.0, window)
+    sees = torch.tensor([j <= p and (not window or j > p - window) for p in (128, 129, 130)], device="cuda")
+    assert torch.equal(out[..., 64:].isnan(), sees[:, None, None].expand(3, 16, 64))
+    assert out[..., :64].isfinite().all() and lse.isfinite().all()
+    c.cache.check_error()
