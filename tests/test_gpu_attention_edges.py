@@ -171,3 +171,44 @@ def test_a_visible_nan_value_is_seen_whatever_its_weight(sffn, dtype, window, j)
     assert torch.equal(out[..., 64:].isnan(), sees[:, None, None].expand(3, 16, 64))
     assert out[..., :64].isfinite().all() and lse.isfinite().all()
     c.cache.check_error()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 32), (256, 128)])
+def test_huge_values_a_row_does_not_see_leave_its_bits_alone(sffn, D, G, dtype):
+    """The last of three tokens and the positions before the first one's window get values of 60000 (the second's window
+    begins within the change): every row that does not see them has the bits it had."""
+    lens, window = [(150, 3)], 70
+    c = Case(sffn, lens, 1, D, G, 16, dtype, seed=D)
+    k, v = c.fill_cache(sffn)
+    q = c.randn(3, 4, D)
+    want, wlse = attend(sffn, c, c.new, q, 1 / math.sqrt(D), window)
+    for low, high, same in ((149, 150, [0, 1]), (0, 79, [1, 2]), (0, 78, [0, 1, 2])):
+        w = v.clone()
+        w[low:high] = 60000.0 * torch.sign(w[low:high])
+        sffn.sffn_kv_append(c.cache.handle, c.all, None, k, w)
+        out, lse = attend(sffn, c, c.new, q, 1 / math.sqrt(D), window)
+        assert torch.equal(out[same], want[same]) and torch.equal(lse, wlse)
+        assert torch.equal(out, want) == (len(same) == 3)
+    c.cache.check_error()
+
+
+@pytest.mark.parametrize("D,G", [(64, 32), (128, 64), (128, 128), (256, 64)])
+@pytest.mark.parametrize("n", [40, 97, 300])
+def test_values_of_very_different_sizes_keep_the_fp32_bound(sffn, D, G, n):
+    """Groups from 1e5 down to 1e-3, and one position of 1e5 in all channels whose score is 40 below the others."""
+    c = Case(sffn, [(n, 1)], 1, D, G, 32, seed=n)
+    k, v = c.randn(n, 1, D), c.randn(n, 1, D)
+    v *= torch.logspace(5, -3, D // G, device="cuda").repeat_interleave(G)
+    q = c.randn(1, 1, D)
+    scale = 1 / math.sqrt(D)
+    k[n // 3] = q[0] * (-40 / (scale * q.square().sum()))
+    v[n // 3] = 1e5 * torch.sign(v[n // 3])
+    sffn.sffn_kv_append(c.cache.handle, c.all, None, k, v)
+    out, _ = attend(sffn, c, c.new, q, scale)
+    kh, vh = (R.stored(t.cpu().numpy(), G) for t in (k, v))
+    step, mid, _ = R.group_params(k.cpu().numpy(), G)
+    ksize = np.repeat(abs(mid.astype(np.float64)) + 15 * step.astype(np.float64), G, axis=-1)
+    want, _, tol = R.attention(host(q), kh, vh, 1, scale, 0, ksize)
+    R.assert_close(host(out), want, tol, "f32", f"attention len {n}")
+    c.cache.check_error()
