@@ -646,7 +646,7 @@ sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host
  * overlap. The same arguments give the same bits at every call.
  * n_q_heads: a multiple of n_kv_heads, n_q_heads * n_tokens at most 2^30, and
  * (n_q_heads * n_tokens / 8 + n_kv_heads * n_seq) * (table_stride * page_size
- * / 32 + 1) below 2^31. scale: finite.
+ * / 32 + 2) below 2^31. scale: finite.
  * ws: at least sffn_attend_workspace_bytes, 256-byte aligned. */
 size_t sffn_attend_workspace_bytes(const sffn_kv* kv, int32_t n_q_heads, int32_t n_seq, int32_t n_tokens);
 sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */, sffn_rows q, int32_t n_q_heads,

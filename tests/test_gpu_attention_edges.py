@@ -212,3 +212,37 @@ def test_values_of_very_different_sizes_keep_the_fp32_bound(sffn, D, G, n):
     want, _, tol = R.attention(host(q), kh, vh, 1, scale, 0, ksize)
     R.assert_close(host(out), want, tol, "f32", f"attention len {n}")
     c.cache.check_error()
+
+
+# ------------------------------------------------------------------ limits
+
+@pytest.mark.parametrize("pages", [1, 4, 30, 1000])
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_the_limit_of_one_call_is_the_documented_one(sffn, pages, hkv):
+    """On both sides of the header's bound on rows and table, judged on the host: without a workspace nothing is launched,
+    and the message tells which check a call met."""
+    import ctypes
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "sffn.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    past = int(re.search(r"\(table_stride page_size / 32 \+ (\d+)\) below 2\^31", text)[1])
+    c = Case(sffn, [(5, 1)], hkv, 64, 64, 16)
+    rows = sffn.RowsC(c.kv_len.data_ptr() // 256 * 256, 4096, 64)              # never read
+    heads = 8 * hkv
+
+    def message(n_tokens):
+        b = sffn.KvBatchC(c.table.data_ptr(), c.kv_len.data_ptr(), c.new.q_start.data_ptr(), 1, n_tokens, pages)
+        rc = sffn._lib.sffn_attend(c.cache.handle, ctypes.byref(b), rows, heads, rows, None, 1.0, 0, 0, None, 0, None)
+        assert rc == sffn.SFFN_ERR_INVALID_ARG
+        return sffn.last_error()
+
+    each = pages * 16 / 32 + past                                             # units of a tile of eight rows, at most
+    most = int((2 ** 31 - 1) / each / hkv) - 1                                 # tokens: heads * n / 8 tiles and one a head
+    assert "2^30" in message((2 ** 30) // heads + 1)
+    if most * heads <= 2 ** 30:
+        assert "too large" in message(most + 1)
+        assert "ws is NULL" in message(most - 1)
+    else:
+        assert "ws is NULL" in message(2 ** 30 // heads)
