@@ -8,10 +8,11 @@
 // to the sums of a group in fp32. Codes go in centred although bare ones would
 // cost nothing: the tensor core cuts its addends off at 2^-24 of the largest,
 // and activations have large elements. Tokens are the 8-column operand,
-// as halves: 16-bit activations exactly, up to a power of two per token (and
-// share of the inputs) that brings the largest to 2^13 (bf16 elements below 2^-27
-// of it lose bits); fp32 activations as two
-// columns, the nearest half and the nearest half of what is left (22 bits).
+// as halves: fp16 activations as they are; others after a power of two per token
+// (and share of the inputs) that brings the largest to 2^13: bf16 activations
+// exactly down to 2^-30 of it, fp32 activations as two columns, the nearest half
+// and the nearest half of what is left (22 bits); of elements too small for that
+// what is above 2^-38 of the largest counts.
 //
 // Work split. The codes are read once, straight to registers, with kAhead steps'
 // loads in flight per warp, begun before the wait for the kernel that produces
@@ -518,8 +519,8 @@ __global__ void __launch_bounds__(512) k_linear_x(const LinearArgs a, int column
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 16; ++w) big = fmaxf(big, s_big[w]);
-  float up, down;
-  scale_to_half_range(big, up, down);
+  float up = 1.f, down = 1.f;
+  if (a.dtype != SFFN_F16) scale_to_half_range(big, up, down);   // fp16 rows are taken as they are
   const bool split = a.dtype == SFFN_F32;
   const int col = split ? 2 * b : b;
   if (threadIdx.x == 0) downs[col] = downs[split ? col + 1 : col] = down;

@@ -537,9 +537,12 @@ sffn_status sffn_linear_get_desc(const sffn_linear* linear, sffn_linear_desc* ou
  * initialisation; 0 if the arguments are invalid or none is needed). */
 size_t sffn_linear_workspace_bytes(const sffn_linear* linear, int32_t B);
 /* x [B][in], y [B][out] and residual [B][out] (ptr NULL = none) in `dtype`;
- * sums in fp32, y rounded once. residual may be y itself; x must not overlap
- * y. A token with a non-finite x gives non-finite values in its own outputs only. y and
- * residual need only be aligned to their elements, with any stride >= out.
+ * sums in fp32, y rounded once. fp16 x is taken as it is; of bf16 and fp32 x,
+ * what lies below 2^-38 of a token's largest element does not count (a bf16
+ * element loses nothing down to 2^-30 of it; fp32 elements keep 22 bits).
+ * residual may be y itself; x must not overlap y. A token with a non-finite x
+ * gives non-finite values in its own outputs only. y and residual need only be
+ * aligned to their elements, with any stride >= out.
  * Errors: INVALID_ARG (also: not packed), CUDA. */
 sffn_status sffn_linear_forward(const sffn_linear* linear, sffn_rows x, int32_t B, sffn_rows residual, sffn_rows y,
                                 int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);

@@ -246,3 +246,23 @@ def test_the_limit_of_one_call_is_the_documented_one(sffn, pages, hkv):
         assert "ws is NULL" in message(most - 1)
     else:
         assert "ws is NULL" in message(2 ** 30 // heads)
+
+
+# ------------------------------------------------------------------ projections
+
+@pytest.mark.parametrize("B", [5, 12, 32])
+def test_fp16_rows_of_a_projection_are_taken_as_they_are(sffn, B):
+    """Elements from the least subnormal on beside the largest half, which meets codes of 0: nothing of them is lost."""
+    n, k, group = 40, 512, 64
+    g = gen(B)
+    codes = torch.randint(-8, 8, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    codes[:, 7] = 0
+    scales = 1e4 * (0.5 + torch.rand(n, k // group, generator=g, device="cuda"))
+    lin = sffn.Linear.from_weights(codes, scales, max_batch=B)
+    x = (torch.randint(-40, 41, (B, k), generator=g, device="cuda") * 2.0 ** -24).half()
+    x[:, 7] = 65504.0
+    y = torch.empty(B, n, device="cuda", dtype=torch.float16)
+    sffn.sffn_linear_forward(lin.handle, x, y, None, lin.workspace(B))
+    want, tol = R.linear(host(x), codes.cpu().numpy(), host(scales), None, None, None, group)
+    R.assert_close(host(y), want, tol, "f16", f"B {B}")
+    lin.check_error()
