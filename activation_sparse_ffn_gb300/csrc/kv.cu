@@ -157,9 +157,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // All of it in fp32 with one rounding per operation, in the order of the
 // definition, so that the stored bits can be told beforehand.
 //
-// Bound: queries by memory, keys and values by issue slots (72% busy over the
-// three, arithmetic 57%, DRAM 36%): about 250 instructions per lane and eight
-// channels. 7950 prompt tokens of 32 + 2 x 32 bf16 heads of 128 (297 MB) take 88
+// Bound: queries by memory; keys and values by about 250 instructions per lane
+// and eight channels, which keep 77% of the issue slots of an active SM busy
+// (DRAM 38% of its peak): no unit is at its limit, and the rest is waits for
+// fixed latencies and loads. 7950 prompt tokens of 32 + 2 x 32 bf16 heads of 128 (297 MB) take 88
 // us, 3.4 TB/s, of which keys and values alone 73; one token 3 us. Four channels
 // a lane took 2.5 times as long, a loop that serves the three kinds 1.5 times;
 // rows loaded 1 to 4 ahead make no difference, and neither do packed fp32
@@ -291,9 +292,9 @@ struct GatherArgs {
 };
 
 // Rows r0 .. r1 - 1 of the keys or values of token i, read back: mid + step (2u - 15),
-// rounded once in fp32 and once to the rows' type. Bound by issue slots (63%
-// busy, DRAM 33%): 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take 41 us,
-// 4.1 TB/s.
+// rounded once in fp32 and once to the rows' type. Issue slots are 72% busy,
+// DRAM 31%, the rest waits: 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take
+// 42 us, 4.0 TB/s.
 template <int D, typename T, bool VALUE>
 __device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kBatch = 4;

@@ -63,9 +63,11 @@ int column_tiles(int B, int dtype) {   // of eight columns, rounded up to a powe
   return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8;
 }
 
-// What a cluster of 1, 2, 4 or 8 blocks costs, in bytes of codes an SM reads in that time: fitted to 10240 x 8192 at
-// one token (17.1, 15.5, 15.5 and 19.8 us), and the order found at 32 tokens (42.2, 37.4, 34.4, 57.5) and at 4099 x
-// 11008 with five (36.3, 25.8, 19.8, 20.6) is the same.
+// What a cluster of 1, 2, 4 or 8 blocks costs, in bytes of codes an SM reads in that time: fitted on an earlier form of
+// the kernels to 10240 x 8192 at one token, now 13.7, 12.7, 12.9 and 15.9 us (codes in L2), at 32 tokens 41.6, 34.8, 27.4
+// and 52.4, at 4099 x 11008 with zeros and five 18.4, 15.3, 13.5 and 14.8. Of 17 sizes from 1024 x 1024 to 28672 x 8192,
+// one to 32 tokens, the choice was the fastest or within 7% of it at eleven, 8 to 11% slower at five (8192 x 8192, one
+// token: 11.7, two blocks 10.6) and 19% at one (2048 x 2048: 4.3, one block 3.6).
 constexpr long long kClusterCost[4] = {0, 16 * 1024, 56 * 1024, 224 * 1024};
 
 int scale_format(const sffn_linear& L) {

@@ -645,8 +645,10 @@ sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host
  * softmax statistics and sums in fp32. A token that sees nothing gives out =
  * 0 and lse = -infinity. Positions a token does not see never reach its
  * result, whatever is stored there, and the ids of pages that no token of the
- * call sees are not looked at: those before a window may have been retired. q, out in `dtype`; q and out must not
- * overlap. The same arguments give the same bits at every call.
+ * call sees are not looked at: those before a window may have been retired.
+ * q, out in `dtype`; q and out must not overlap. Of a query row, what lies below
+ * 2^-34 of its largest element does not count (fp32: 2^-38, and elements keep
+ * 22 bits). The same arguments give the same bits at every call.
  * n_q_heads: a multiple of n_kv_heads, n_q_heads * n_tokens at most 2^30, and
  * (n_q_heads * n_tokens / 8 + n_kv_heads * n_seq) * (table_stride * page_size
  * / 32 + 2) below 2^31. scale: finite.
