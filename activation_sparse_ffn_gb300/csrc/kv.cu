@@ -166,7 +166,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // rows loaded 1 to 4 ahead make no difference, and neither do packed fp32
 // operations.
 template <int D, typename T, int KIND>
-__device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, int r1, int lane) {
+__device__ __forceinline__ void append_rows(const AppendArgs& a, int i, const KvPlace* place, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, dtype = dtype_of<T>();
   const int sub = lane / LR, lr = lane % LR, c0 = lr * 8;
   const sffn_rows& rows = KIND == 0 ? a.q : KIND == 1 ? a.k : a.v;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int i, int r0, 
   const int64_t hop = RI * rows.head_stride;
   Raw<T> next = {};   // the row after the one in hand
   if (r0 + sub < r1) next.load(p);
-  const KvPlace at = kv_place(a.b, i, lane, a.c.P, a.c.err);
+  const KvPlace at = kv_many(a.b) ? *place : kv_place(a.b, i, lane, a.c.P, a.c.err);
   if (at.seq < 0) return;
   Turn<D> turn;
   if (KIND != 2 && a.rope.table) {
@@ -269,17 +269,19 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_append(const AppendArgs a) {
   // A block's warps take neighbouring tokens and run the same of the three loops (mixed within a block: 1.25 times as
   // long); blocks take turns, so that the queries' loads and stores are under way beside the others' arithmetic (7950
   // prompt tokens: 88 us; all queries, then keys, then values 92).
-  const int part = blockIdx.x % tasks, i = blockIdx.x / tasks * kWarps + (threadIdx.x >> 5);
+  const int part = blockIdx.x % tasks, i0 = blockIdx.x / tasks * kWarps, warp = threadIdx.x >> 5, i = i0 + warp;
+  __shared__ KvPlace s_places[kWarps];
+  if (kv_many(a.b)) kv_places<kWarps>(a.b, i0, kWarps * 32, a.c.P, a.c.err, s_places);
   if (i >= a.b.n_tokens) return;
   if (part < a.q_tasks) {
-    append_rows<D, T, 0>(a, i, part * a.per, min((part + 1) * a.per, a.hq), lane);
+    append_rows<D, T, 0>(a, i, s_places + warp, part * a.per, min((part + 1) * a.per, a.hq), lane);
   } else {
     const int n = part - a.q_tasks, value = n >= a.kv_tasks, r0 = (n - value * a.kv_tasks) * a.per;
     const int r1 = min(r0 + a.per, a.c.hkv);
     if (value)
-      append_rows<D, T, 2>(a, i, r0, r1, lane);
+      append_rows<D, T, 2>(a, i, s_places + warp, r0, r1, lane);
     else
-      append_rows<D, T, 1>(a, i, r0, r1, lane);
+      append_rows<D, T, 1>(a, i, s_places + warp, r0, r1, lane);
   }
 }
 
@@ -296,12 +298,12 @@ struct GatherArgs {
 // DRAM 31%, the rest waits: 7950 tokens of 2 x 32 bf16 heads of 128 (167 MB) take
 // 42 us, 4.0 TB/s.
 template <int D, typename T, bool VALUE>
-__device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, int r0, int r1, int lane) {
+__device__ __forceinline__ void gather_rows(const GatherArgs& a, int i, const KvPlace* place, int r0, int r1, int lane) {
   constexpr int LR = RowLanes<D>::kLanes, RI = RowLanes<D>::kRows, kBatch = 4;
   const sffn_rows& rows = VALUE ? a.v : a.k;
   if (!rows.ptr) return;
   const int sub = lane / LR, lr = lane % LR;
-  const KvPlace at = kv_place(a.b, i, lane, a.c.P, a.c.err);
+  const KvPlace at = kv_many(a.b) ? *place : kv_place(a.b, i, lane, a.c.P, a.c.err);
   if (at.seq < 0) return;
   const bool placed = at.pos >= 0;
   const int page = placed ? max(0, kv_page(a.b, at.seq, at.pos / a.c.P, a.c.n_pages, a.c.err)) : 0;
@@ -347,13 +349,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv_gather(const GatherArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, part = blockIdx.x % (2 * a.tasks), value = part >= a.tasks;
-  const int i = blockIdx.x / (2 * a.tasks) * kWarps + (threadIdx.x >> 5);
+  const int i0 = blockIdx.x / (2 * a.tasks) * kWarps, warp = threadIdx.x >> 5, i = i0 + warp;
+  __shared__ KvPlace s_places[kWarps];
+  if (kv_many(a.b)) kv_places<kWarps>(a.b, i0, kWarps * 32, a.c.P, a.c.err, s_places);
   if (i >= a.b.n_tokens) return;
   const int r0 = (part - value * a.tasks) * a.per, r1 = min(r0 + a.per, a.c.hkv);
   if (value)
-    gather_rows<D, T, true>(a, i, r0, r1, lane);
+    gather_rows<D, T, true>(a, i, s_places + warp, r0, r1, lane);
   else
-    gather_rows<D, T, false>(a, i, r0, r1, lane);
+    gather_rows<D, T, false>(a, i, s_places + warp, r0, r1, lane);
 }
 
 // Rows that a task takes: all of a token's where there are tokens enough to fill

@@ -132,7 +132,13 @@ __device__ __forceinline__ bool kv_span(const sffn_kv_batch& b, int s, KvSpan& r
   return r.from >= 0 && r.to >= r.from && r.to <= b.n_tokens;
 }
 
-// Every sequence is looked at, not only those up to the row's: where starts are out of order no row has a place.
+// Every sequence is looked at, not only those up to the row's: where starts are out of order no row has a place. Up to
+// kPlaceLanes sequences a warp does that on its own, lane s for sequence s; more, the block does for its rows together
+// (kv_places), which reads them once a block (1024 sequences of one token, 8 + 2 x 8 heads of 128, append and read-back:
+// 118 us with each warp on its own).
+constexpr int kPlaceLanes = 32;
+__device__ __forceinline__ bool kv_many(const sffn_kv_batch& b) { return b.q_start && b.n_seq > kPlaceLanes; }
+
 __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int lane, int P, uint32_t* err) {
   KvPlace r{-1, -1};
   if (!b.q_start) {
@@ -140,30 +146,48 @@ __device__ __forceinline__ KvPlace kv_place(const sffn_kv_batch& b, int i, int l
     r.pos = kv_len_of(b, i, P, err) - 1;
     return r;
   }
+  KvSpan rows{0, 0};
+  int n = 0;
   bool bad = false;
-  int len = 0;
-  for (int s0 = 0; s0 < b.n_seq; s0 += 32) {
-    const int s = s0 + lane;
-    KvSpan rows{0, 0};
-    int n = 0;
-    if (s < b.n_seq) {
-      n = ld_dep(b.kv_len + s);
-      bad |= !kv_span(b, s, rows);
-    }
-    const unsigned here = __ballot_sync(SFFN_FULL_MASK, rows.from <= i && i < rows.to);
-    if (here) {
-      const int src = __ffs(here) - 1;
-      r.seq = s0 + src;
-      r.pos = __shfl_sync(SFFN_FULL_MASK, rows.to, src) - i;   // rows from this one to the sequence's last
-      len = __shfl_sync(SFFN_FULL_MASK, n, src);
-    }
+  if (lane < b.n_seq) {
+    n = ld_dep(b.kv_len + lane);
+    bad = !kv_span(b, lane, rows);
   }
+  const unsigned here = __ballot_sync(SFFN_FULL_MASK, rows.from <= i && i < rows.to);
   if (__any_sync(SFFN_FULL_MASK, bad)) {
     set_device_error(err, SFFN_ERR_DEVICE);
-    r.seq = -1;
+  } else if (here) {
+    r.seq = __ffs(here) - 1;
+    const int left = __shfl_sync(SFFN_FULL_MASK, rows.to, r.seq) - i;   // rows from this one to the sequence's last
+    r.pos = max(kv_len_in_table(b, __shfl_sync(SFFN_FULL_MASK, n, r.seq), P, err) - left, -1);
   }
-  if (r.seq >= 0) r.pos = max(kv_len_in_table(b, len, P, err) - r.pos, -1);
   return r;
+}
+
+// The places of rows i0 .. i0 + N - 1, left at places by the threads of the block together.
+template <int N>
+__device__ __forceinline__ void kv_places(const sffn_kv_batch& b, int i0, int threads, int P, uint32_t* err, KvPlace* places) {
+  if (threadIdx.x < N) places[threadIdx.x] = KvPlace{-1, -1};
+  __syncthreads();
+  bool bad = false;
+#pragma unroll 4
+  for (int s = threadIdx.x; s < b.n_seq; s += threads) {
+    KvSpan rows;
+    bad |= !kv_span(b, s, rows);
+    for (int i = max(rows.from, i0); i < min(rows.to, i0 + N); ++i) places[i - i0] = KvPlace{s, rows.to - i};
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x < N) {   // what was found, or nothing
+    KvPlace r = places[threadIdx.x];
+    if (bad) {
+      set_device_error(err, SFFN_ERR_DEVICE);
+      r.seq = -1;
+    } else if (r.seq >= 0) {
+      r.pos = max(kv_len_of(b, r.seq, P, err) - r.pos, -1);
+    }
+    places[threadIdx.x] = r;
+  }
+  __syncthreads();
 }
 
 // Page of a position, or -1 (and the device error word) if its id is out of range.

@@ -123,6 +123,23 @@ def test_starts_out_of_order_write_nothing(sffn, seqs, what):
     assert errors == [False] * 3
 
 
+@pytest.mark.parametrize("seqs", [31, 32, 33, 129, 700])
+def test_places_of_few_and_many_sequences(sffn, seqs):
+    """Up to 32 sequences are looked at by each warp, more by the block together: none to five rows each, some without a place."""
+    lens = [((7 * s) % 23, (5 * s) % 6) for s in range(seqs)]
+    c = Case(sffn, lens, 1, 64, 32, 16, seed=seqs)
+    k, v = c.randn(c.fresh, 1, 64), c.randn(c.fresh, 1, 64)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    sffn.sffn_kv_append(c.cache.handle, c.new, None, k, v)
+    sffn.sffn_kv_gather(c.cache.handle, c.new, ko, vo)
+    placed = np.concatenate([np.arange(n - m, n) >= 0 for n, m in lens])
+    for got, rows in ((ko, k), (vo, v)):
+        want = R.stored(rows.cpu().numpy(), 32)
+        want[~placed] = 0
+        assert np.array_equal(got.cpu().numpy(), want)
+    c.cache.check_error()
+
+
 # ------------------------------------------------------------------ pages outside a window
 
 @pytest.mark.parametrize("D,P", [(64, 16), (128, 32), (128, 64), (256, 16)])
