@@ -4,7 +4,7 @@
 // head) and position j, in units of log2: S = f q_r . K_j with f = scale *
 // log2(e). A cached key is mid + step * (2u - 15) per group of channels, so
 // S / f = sum over groups (step * (q_g . (2u - 15)) + mid * sum(q_g)): the
-// tensor cores multiply q with the bare codes, exact as halves, and step and
+// tensor cores multiply q with 2u - 15, exact as halves, and step and
 // mid are applied once per group in fp32. In the same way sum_j p_j V_j = sum_j
 // (p_j step_j) (2u_j - 15) + sum_j p_j mid_j, with the running maximum and sum
 // of the softmax in fp32.
@@ -19,17 +19,17 @@
 // unit to 2^13: what a row does not see, or sees with no weight, or the size of
 // other groups leaves its bits alone. (One power of two from the unit's largest
 // step, whoever sees it, cost 2 to 7% less: 24 ragged sequences with groups of 32
-// 94 us, now 101; 131072 positions 52.6 and 54.1.) With one half the results of fp16 rows were a
-// quarter further from the exact ones than fp32 arithmetic leaves them (2.7e-4
-// and 2.1e-4 of their norm). Value codes are centred first, because the tensor
-// core truncates its sums: with bare codes, all weights being positive, that adds
-// up over a long history (131072 positions of fp16 rows: 2.3e-4). Key codes of
-// fp32 rows (Exact = true) are centred too and q is carried by two halves: with
-// bare key codes the result is off by 1.3e-6 instead of 0.5e-6 (131072
-// positions). Key codes of 16-bit rows (Exact = false) go in as they stand in the
-// word, u times 2^-23 or the like, one mask per pair and no arithmetic, and q is
-// one half after a power of two per row: exact for elements down to 2^-23 of the
-// row's largest, smaller ones to 2^-34 of it. Either way the sums of one unit's
+// 94 us, so 101; 131072 positions 52.6 and 54.1.) With one half the results of
+// fp16 rows were a quarter further from the exact ones than fp32 arithmetic leaves
+// them (2.7e-4 and 2.1e-4 of their norm). q of 16-bit rows (Exact = false) is one
+// half: fp16 as it is, bf16 after a power of two per row and group, exactly down to
+// 2^-30 of the group's largest; q of fp32 rows (Exact = true) is two halves after
+// one. Codes are centred, because the tensor core truncates its sums: bare value codes, all
+// weights being positive, add up over a long history (131072 positions of fp16
+// rows: 2.3e-4 instead of 2.1e-4), bare key codes left the result of fp32 rows off
+// by 1.3e-6 instead of 0.5e-6 and lse of 16-bit rows by 8e-8 instead of 3e-8, and
+// cost q of 16-bit rows four bits. (Bare, they would be one mask per pair and no
+// arithmetic: 32 x 32768 of bf16 265 us, centred 276.) The sums of one unit's
 // positions leave the tensor core and are added up in fp32, like the denominator
 // and the mids.
 //
@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
   constexpr int QL = Exact ? 2 : 1;          // halves that carry a query element
   uint32_t q[QL][D / 16][2];                 // column g of the operand
   float qs[NG][2];                           // sums of q over a group, rows 2t and 2t + 1 as everything below
+  float gs[NG][2];                           // what the products of a group are multiplied with to match the row's others
   float o[D / 16][4];                        // channels 16x + g and 16x + 8 + g, each for both rows
   float l[2] = {0.f, 0.f};                   // the lane's share of sum p
   float mid_sum[NG][2];                      // and of sum p mid
@@ -588,13 +589,8 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 #pragma unroll
         for (int j = n * G / 32; j < (n + 1) * G / 32; ++j) {
           uint32_t p0[4], p1[4];
-          if (Exact) {
-            key_halves(w[0][j], p0);
-            key_halves(w[1][j], p1);
-          } else {
-            key_bits(w[0][j], p0);
-            key_bits(w[1][j], p1);
-          }
+          key_halves(w[0][j], p0);
+          key_halves(w[1][j], p1);
           const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]}, a1[4] = {p0[2], p1[2], p0[3], p1[3]};
 #pragma unroll
           for (int h = 0; h < QL; ++h) {
@@ -605,9 +601,9 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 sm = __half22float2(u32_h2(kp[k][n]));
-          const float off = Exact ? sm.y : fmaf(-15.f, sm.x, sm.y);
-          s[i][2 * k] = fmaf(sm.x, c[2 * k], fmaf(off, qs[n][0], s[i][2 * k]));
-          s[i][2 * k + 1] = fmaf(sm.x, c[2 * k + 1], fmaf(off, qs[n][1], s[i][2 * k + 1]));
+          const float st[2] = {NG == 1 ? sm.x : sm.x * gs[n][0], NG == 1 ? sm.x : sm.x * gs[n][1]};
+          s[i][2 * k] = fmaf(st[0], c[2 * k], fmaf(sm.y, qs[n][0], s[i][2 * k]));
+          s[i][2 * k + 1] = fmaf(st[1], c[2 * k + 1], fmaf(sm.y, qs[n][1], s[i][2 * k + 1]));
         }
       }
     }
@@ -765,7 +761,7 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
       const size_t at = (size_t)((cur.q0 + rg / a.gq) * a.q.row_stride + (cur.kh * a.gq + rg % a.gq) * a.q.head_stride);
       // the sign of the scale goes with q, its size with f; rows past the end are zero
       const float sign = row >= rows || a.scale == 0.f ? 0.f : a.scale < 0.f ? -1.f : 1.f;
-      float big = 0.f, fg, up, sum[NG], x[D / 32][8];
+      float big[NG], fg[NG], up[NG], sum[NG], x[D / 32][8];
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) ld_run<8>(a.q.ptr, at + 32 * j + 8 * t, dtype, x[j]);
       if (uu == u0) {   // the first copies, while the rows are on their way
@@ -773,39 +769,49 @@ __global__ void __launch_bounds__(Att<D, G, Exact>::kThreads, 1) k_attend(const 
         for (int i = 0; i < T::kStages - 1; ++i) issue();
       }
 #pragma unroll
+      for (int n = 0; n < NG; ++n) big[n] = sum[n] = 0.f;
+#pragma unroll
       for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[j][e]));
-      scale_to_half_range(quad_max(big), up, fg);
-      fg = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e * fg, 1.1754944e-38f);
+        for (int e = 0; e < 8; ++e) big[j * 32 / G] = fmaxf(big[j * 32 / G], fabsf(x[j][e]));
+      float row_fg = 0.f;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) sum[n] = 0.f;
+      for (int n = 0; n < NG; ++n) {
+        scale_to_half_range(quad_max(big[n]), up[n], fg[n]);
+        if (!Exact && dtype == SFFN_F16) up[n] = fg[n] = 1.f;   // fp16 rows are taken as they are
+        row_fg = fmaxf(row_fg, fg[n]);
+      }
+      const float f_g = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e * row_fg, 1.1754944e-38f);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[j][e] = sign == 0.f ? 0.f : x[j][e] * (up * sign);
+          x[j][e] = sign == 0.f ? 0.f : x[j][e] * (up[j * 32 / G] * sign);
           sum[j * 32 / G] += x[j][e];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float c = !Exact && (e & 1) ? 0.0625f : 1.f;   // odd pairs meet bare codes sixteen times as large
           uint32_t* hi = &q[0][2 * j + (e >> 1)][e & 1];
           if (Exact)
-            split_f16(x[j][2 * e] * c, x[j][2 * e + 1] * c, *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
+            split_f16(x[j][2 * e], x[j][2 * e + 1], *hi, q[QL - 1][2 * j + (e >> 1)][e & 1]);
           else
-            *hi = h2_u32(__floats2half2_rn(x[j][2 * e] * c, x[j][2 * e + 1] * c));
+            *hi = h2_u32(__floats2half2_rn(x[j][2 * e], x[j][2 * e + 1]));
         }
       }
-      if (!Exact) fg *= 16777216.f;   // codes are u * 2^-23: the products are 2^-24 of those with 2u
 #pragma unroll
-      for (int n = 0; n < NG; ++n) sum[n] = quad_sum(sum[n]) * (Exact ? 1.f : 5.9604645e-8f);
+      for (int n = 0; n < NG; ++n) {
+        fg[n] /= row_fg;   // powers of two
+        sum[n] = quad_sum(sum[n]) * fg[n];
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int src = 4 * (2 * t + r);
 #pragma unroll
-        for (int n = 0; n < NG; ++n) qs[n][r] = __shfl_sync(SFFN_FULL_MASK, sum[n], src);
-        f[r] = __shfl_sync(SFFN_FULL_MASK, fg, src);
+        for (int n = 0; n < NG; ++n) {
+          qs[n][r] = __shfl_sync(SFFN_FULL_MASK, sum[n], src);
+          gs[n][r] = NG == 1 ? 1.f : __shfl_sync(SFFN_FULL_MASK, fg[n], src);
+        }
+        f[r] = __shfl_sync(SFFN_FULL_MASK, f_g, src);
         pos[r] = __shfl_sync(SFFN_FULL_MASK, pos_g, src);
         lo[r] = __shfl_sync(SFFN_FULL_MASK, lo_g, src);
         m[r] = ninf;

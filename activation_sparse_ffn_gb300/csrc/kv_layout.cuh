@@ -69,8 +69,8 @@ __host__ __device__ constexpr int param_off(int pos, int grp, int n_groups, int 
 // Key word: the codes of channel pairs e = 0..3 (channels 2e and 2e + 1 of the
 // eight) stand at bits 4 e of the two 16-bit halves; the whole word is then
 // rotated left by one bit. A code lies at bits 1-4 or 5-8 of a half (after a
-// rotation by 8 for e = 2, 3): as a half-precision number the masked bits are
-// u * 2^-23 (or u * 2^-19), exactly.
+// rotation by 8 for e = 2, 3), where the exponent of 1024 above it makes it a
+// half-precision number, as for value words below.
 // From the codes, that of channel e at bits key_field(e), and back:
 __host__ __device__ constexpr int key_field(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
 __host__ __device__ __forceinline__ uint32_t key_word(uint32_t fields) { return fields << 1 | fields >> 31; }

@@ -56,17 +56,7 @@ __device__ __forceinline__ __half2 code_bits(uint32_t w, uint32_t mask) {
   return u32_h2(r);
 }
 
-// The four pairs of a key word (kv_layout.cuh) as they stand: u * 2^-23 for p[0] and p[2],
-// u * 2^-19 for p[1] and p[3] (subnormal halves, which the tensor cores take exactly).
-__device__ __forceinline__ void key_bits(uint32_t w, uint32_t* p) {
-  const uint32_t r = __funnelshift_r(w, w, 8);
-  p[0] = w & 0x001e001eu;
-  p[1] = w & 0x01e001e0u;
-  p[2] = r & 0x001e001eu;
-  p[3] = r & 0x01e001e0u;
-}
-
-// The same as 2u - 15: 1024 + 2u - 1039 and (1024 + 32u) / 16 - 79, both exact.
+// The four pairs of a key word (kv_layout.cuh) as 2u - 15: 1024 + 2u - 1039 and (1024 + 32u) / 16 - 79, both exact.
 __device__ __forceinline__ void key_halves(uint32_t w, uint32_t* p) {
   const uint32_t r = __funnelshift_r(w, w, 8);
   const __half2 k1 = u32_h2(0xe40fe40fu), k16 = u32_h2(0x2c002c00u), k79 = u32_h2(0xd4f0d4f0u);  // -1039, 1/16, -79

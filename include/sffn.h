@@ -646,9 +646,11 @@ sffn_status sffn_kv_gather(const sffn_kv* kv, const sffn_kv_batch* batch /* host
  * 0 and lse = -infinity. Positions a token does not see never reach its
  * result, whatever is stored there, and the ids of pages that no token of the
  * call sees are not looked at: those before a window may have been retired.
- * q, out in `dtype`; q and out must not overlap. Of a query row, what lies below
- * 2^-34 of its largest element does not count (fp32: 2^-38, and elements keep
- * 22 bits). The same arguments give the same bits at every call.
+ * q, out in `dtype`; q and out must not overlap. fp16 q is taken as it is; of
+ * bf16 and fp32 q, what lies below 2^-38 of the largest element of a row and
+ * group of channels does not count (a bf16 element loses nothing down to 2^-30
+ * of it; fp32 elements keep 22 bits). The same arguments give the same bits at
+ * every call.
  * n_q_heads: a multiple of n_kv_heads, n_q_heads * n_tokens at most 2^30, and
  * (n_q_heads * n_tokens / 8 + n_kv_heads * n_seq) * (table_stride * page_size
  * / 32 + 2) below 2^31. scale: finite.

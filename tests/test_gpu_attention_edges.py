@@ -42,6 +42,28 @@ def test_attention_of_16_bit_rows_keeps_fp32_sums(sffn, D, G, dtype):
     c.cache.check_error()
 
 
+@pytest.mark.parametrize("D,G", [(64, 32), (128, 32), (128, 64), (256, 128)])
+@pytest.mark.parametrize("dtype,big", [("f16", 60000.0), ("bf16", 2.0 ** 18), ("f32", 2.0 ** 18)])
+def test_small_elements_of_a_query_count_beside_large_ones(sffn, D, G, dtype, big):
+    """One element 10^8 times the others that meets keys of 0: out and lse stay within the fp32 bound of the rest."""
+    n, scale = 200, 4.0
+    c = Case(sffn, [(n, 1)], 1, D, G, 16, dtype, seed=D + G)
+    k, v = c.randn(n, 1, D) * 100, c.randn(n, 1, D)
+    k[..., :G] = 0
+    q = c.randn(1, 4, D) * 1e-3
+    q[..., 3] = big
+    sffn.sffn_kv_append(c.cache.handle, c.all, None, k, v)
+    out, lse = attend(sffn, c, c.new, q, scale)
+    kh, vh = (R.stored(t.float().cpu().numpy(), G) for t in (k, v))
+    step, mid, _ = R.group_params(k.float().cpu().numpy(), G)
+    ksize = np.repeat(abs(mid.astype(np.float64)) + 15 * step.astype(np.float64), G, axis=-1)
+    want, wlse, tol = R.attention(host(q), kh, vh, 1, scale, 0, ksize)
+    R.assert_close(host(out), want, tol, dtype, f"attention {dtype}")
+    es = 2.0 ** -20 * scale * np.einsum("hd,ld->hl", abs(host(q)[0]), ksize[:, 0]).max(1)
+    assert (abs(host(lse)[0] - wlse[0]) <= es + 2.0 ** -20 * np.maximum(1, abs(wlse[0]))).all()
+    c.cache.check_error()
+
+
 # ------------------------------------------------------------------ rows outside a call's sequences
 
 def call_all(sffn, c, batch, heads=4):
