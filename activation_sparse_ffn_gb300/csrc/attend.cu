@@ -48,12 +48,12 @@
 // What bounds it. The warps' own instructions, of which an SM issues 1.5 to 2 a
 // cycle here (registers allow 8 to 16 warps; fixed latencies and instruction
 // fetches stand between them): 32 sequences of 32768, 64 heads over 8 of 128 in
-// bf16, 1.14 GB, take 264 us, 4.3 TB/s; one sequence of 131072 50 us (2.9 TB/s)
+// bf16, 1.14 GB, take 275 us, 4.1 TB/s; one sequence of 131072 51 us (2.8 TB/s)
 // and in fp32 rows, which need two products for the scores too, 54; rows of 32
 // codes a group need four times the params and scales, 24 ragged sequences up to
-// 4099 of 32 heads 101 us (2.6 TB/s); eight proposed tokens of 16 heads a key
-// head read each unit 16 times, 37 us; heads of 256, 8 sequences of 8192 of 32
-// over 8, 60 us in bf16 and 66 in fp32 (a part of their registers spills). A
+// 4099 of 32 heads 109 us (2.4 TB/s); eight proposed tokens of 16 heads a key
+// head read each unit 16 times, 38 us; heads of 256, 8 sequences of 8192 of 32
+// over 8, 64 us in bf16 and 70 in fp32 (a part of their registers spills). A
 // call's beginning (lengths, page table, first copies) and end (parts of blocks
 // through global memory) are 7 to 16 us of each: 33 positions take 8 us, 1024 12,
 // 16384 19. Tiles of sixteen rows, which decode a unit for twice the rows, hold
@@ -76,12 +76,13 @@ struct Att {
   static constexpr int NG = D / G;
   static constexpr int U = D == 256 ? 32 : 64;             // positions of a unit
   // Positions whose code is unrolled: with four groups and 64 of them the step and weight registers spill (24 ragged
-  // sequences: 115 us, with 32 of them 101); with fewer groups 32 are slower (131072 positions of fp32 rows: 58 us, with 64
-  // of them 54; 32 x 32768 of bf16: 279 and 265; 4 x 8 x 16 rows of 64 channels: 40 and 37).
+  // sequences: 129 us, with 32 of them 109); with fewer groups 32 are slower (131072 positions of fp32 rows: 58 us, with 64
+  // of them 54; 32 x 32768 of bf16: 287 and 276; 4 x 8 x 16 rows of 64 channels: 41 and 38; the exception is two groups of
+  // 16-bit rows, 8 x 4 x 8 rows over 8192: 97 and 103).
   static constexpr int SU = NG >= 4 ? 32 : U;
   static constexpr int kStage = U * (D + 8 * NG);          // bytes
   // as many warps as the registers of the inner loop and two stages each allow; where a few values spill all the same,
-  // fewer warps were slower (32 x 32768 of bf16: 258 us with 12, 274 with 8 and no spills)
+  // fewer warps were slower (32 x 32768 of bf16: 276 us with 12, 302 with 8 and no spills)
   static constexpr int kByRegs = D == 64 ? (Exact ? 12 : 16) : D == 128 && !Exact && NG < 4 ? 12 : 8;
   static constexpr int kBudget = 224 * 1024;
   static constexpr int kBySmem = kBudget / (2 * kStage);
@@ -91,13 +92,13 @@ struct Att {
   static constexpr int kPitch = D + 4;                     // floats of a row of sums: rows two apart use other banks
   static constexpr int kPart = kRows * kPitch + 2 * kRows; // floats of a partial result: sums, maxima, totals
   // Items of up to so many units are not cut by a block border where the list has at most 32 sequences: another two units
-  // a warp cost less than a join by way of global memory (8 rows over 1024 positions: 12.4 us, joined 14.1; with 16 rows of
-  // each of 32 sequences of 512, D = 64: 15.1 and 18.5; three units a warp are no better). More sequences are placed by the
-  // block, whose borders stay where they fall (33 of 512: 21.4).
+  // a warp cost less than a join by way of global memory (8 rows over 1024 positions: 12.5 us, joined 14.1; with 16 rows of
+  // each of 32 sequences of 512, D = 64: 15.5 and 19.0; three units a warp are no better). More sequences are placed by the
+  // block, whose borders stay where they fall (33 of 512: 21.7).
   static constexpr int kWhole = 2 * kWarps;
   // What the beginning and the end of an item cost, in units; counted where warps take several units each, so that blocks
-  // with many short items do not end last (24 ragged sequences: 107 us without, 101 with; two units instead of one are as
-  // good there and cost 17.4 instead of 15.1 us with 16 rows of each of 32 sequences of 512).
+  // with many short items do not end last (24 ragged sequences: 117 us without, 109 with; two units instead of one are as
+  // good there and cost 17.9 instead of 15.5 us with 16 rows of each of 32 sequences of 512).
   static constexpr int kItem = 1;
   static constexpr int kSmem = kStage * kStages * kWarps;
   static_assert(kWarps >= kRows && kWarps <= kMaxWarps && kSmem >= kPart * 4 * kWarps, "");
