@@ -1,0 +1,259 @@
+// Linear layer with 8-bit codes for rows of 8-bit codes: packing, the choice of
+// the kernel, and the kernel for few tokens (k_lin8_few).
+//
+// k_lin8_few: a cluster of blocks takes a run of rows (any number of them: equal
+// shares to a row) and its blocks split the inputs, as do the 16 warps of a
+// block, so that every code is read once, straight into the registers of the
+// lane that needs it, and a token's codes are held once. Sums leave the tensor
+// cores as whole numbers and meet in shared memory, where the order of
+// additions does not matter.
+#include <algorithm>
+
+#include "linear8.cuh"
+#include "q4mma.cuh"
+#include "rows_io.cuh"
+#include "step.h"
+
+namespace sffn {
+
+namespace {
+
+// One thread per 16-byte chunk of the packed codes.
+__global__ void k_pack_codes8(const int8_t* codes, uint4* out, int n, int k, int kb, size_t chunks) {
+  const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= chunks) return;
+  const int in = (int)(i % (kL8Block / 16)), r = in / 4, t = (in & 3) ^ ((r >> 1) & 3);
+  const size_t block = i / (kL8Block / 16);
+  const int row = (int)(block / kb) * kL8Rows + r, col = (int)(block % kb) * kL8Inputs + t * 16;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row < n && col < k) v = *reinterpret_cast<const uint4*>(codes + (size_t)row * k + col);   // k is a multiple of 16
+  out[i] = make_uint4(v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u);
+}
+
+__global__ void k_pack_rows8(const float* in, float* out, int n, int np) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < np) out[i] = in && i < n ? in[i] : 0.f;
+}
+
+constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
+constexpr int kFewTokens = 32;
+constexpr int kFewSmem = 200 * 1024;
+constexpr int kFewRows = 512;      // most rows of a cluster
+constexpr int kFewAhead = 4;       // units of codes that a lane has on their way
+
+struct Lin8Args {
+  const uint8_t* codes;
+  const float* scales;
+  const float* bias;
+  sffn_rows x, residual, y;
+  const float* x_scales;
+  int n, k, kb, B, dtype, clusters;
+  int x_stride, off_sum;   // bytes of a token's codes held by a block, and where the sums begin
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster_int(uint32_t smem_addr, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
+// NT column tiles of eight tokens.
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, int cs) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
+  const int row0 = (int)((long long)a.n * cluster / a.clusters), row1 = (int)((long long)a.n * (cluster + 1) / a.clusters);
+  const int kb0 = (int)((long long)a.kb * rank / cs), kb1 = (int)((long long)a.kb * (rank + 1) / cs);
+  const int wk0 = kb0 + (kb1 - kb0) * warp / kFewWarps, wk1 = kb0 + (kb1 - kb0) * (warp + 1) / kFewWarps;
+  const int tiles = (row1 - row0 + 15) / 16, nk = wk1 - wk0, units = tiles * nk;
+  int* sums = reinterpret_cast<int*>(smem + a.off_sum);   // [row][8 NT]
+
+  pdl_launch_dependents();
+  // unit u: 16 rows of tile u / nk, 64 inputs wk0 + u % nk; the first are on their way before the wait (codes are packed
+  // by a call that synchronizes)
+  uint4 next[kFewAhead][2];
+  int ft = 0, fk = 0;   // the unit to be fetched next
+  auto fetch = [&](uint4* f) {
+    f[0] = f[1] = make_uint4(0, 0, 0, 0);
+    if (ft < tiles) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row0 + ft * 16 + h * 8 + g;
+        if (row < row1)
+          f[h] = ldg_stream(a.codes + ((size_t)(row / kL8Rows) * a.kb + wk0 + fk) * kL8Block + l8_chunk(row % kL8Rows, t));
+      }
+      if (++fk == nk) fk = 0, ++ft;
+    }
+  };
+  if (nk) {
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) fetch(next[i]);
+  }
+  for (int i = tid; i < (row1 - row0) * 8 * NT; i += kFewThreads) sums[i] = 0;
+  pdl_wait();
+  const int own = (kb1 - kb0) * 4;   // 16-byte chunks of a token
+  for (int i = tid; i < own * 8 * NT; i += kFewThreads) {
+    const int b = i / own, c = i - b * own, col = kb0 * kL8Inputs + c * 16;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (b < a.B && col < a.k)
+      v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.x.ptr) + b * a.x.row_stride + col));
+    *reinterpret_cast<uint4*>(smem + b * a.x_stride + c * 16) =
+        make_uint4(v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u);
+  }
+  __syncthreads();
+
+  float acc[NT][4];
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+  auto leave = [&](int tile) {
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = tile * 16 + g + 8 * (e >> 1);
+        if (row < row1 - row0) atomicAdd(&sums[row * 8 * NT + c * 8 + 2 * t + (e & 1)], __float2int_rn(acc[c][e]));
+        acc[c][e] = 0.f;
+      }
+  };
+  int tile = 0, kk = 0;
+  for (int u = 0; u < units; u += kFewAhead) {
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) {
+      if (u + i < units) {
+        uint4 w[2] = {next[i][0], next[i][1]};
+        fetch(next[i]);
+        uint32_t ah[2][4][2];   // half h of the rows, step s: inputs 16 t + 4 s + (0, 1), (2, 3)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l8_halves(w[h].x, ah[h][0][0], ah[h][0][1]);
+          l8_halves(w[h].y, ah[h][1][0], ah[h][1][1]);
+          l8_halves(w[h].z, ah[h][2][0], ah[h][2][1]);
+          l8_halves(w[h].w, ah[h][3][0], ah[h][3][1]);
+        }
+        const uint8_t* xs = smem + (wk0 - kb0 + kk) * kL8Inputs + t * 16;
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(xs + (c * 8 + g) * a.x_stride);
+          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t b0, b1;
+            l8_halves(xw[s], b0, b1);
+            const uint32_t af[4] = {ah[0][s][0], ah[1][s][0], ah[0][s][1], ah[1][s][1]};
+            mma_f16(acc[c], af, b0, b1);
+          }
+        }
+        ++kk;
+        if (kk == nk || kk % (kL8Exact / kL8Inputs) == 0) {
+          leave(tile);
+          if (kk == nk) kk = 0, ++tile;
+        }
+      }
+    }
+  }
+  if (cs > 1) cluster_barrier(); else __syncthreads();
+  // outputs, a share of the rows for each block of the cluster
+  const int rows = row1 - row0, from = rows * rank / cs, to = rows * (rank + 1) / cs, mine = to - from;
+  const uint32_t base = smem_u32(sums);
+  for (int i = tid; i < mine * a.B; i += kFewThreads) {
+    const int b = i / mine, r = from + i - b * mine, row = row0 + r;
+    int s = 0;
+    if (cs > 1) {
+      for (int k = 0; k < cs; ++k) s += ld_cluster_int(base + (r * 8 * NT + b) * 4, k);
+    } else {
+      s = sums[r * 8 * NT + b];
+    }
+    float v = l8_value(s, a.scales[row], __ldcg(a.x_scales + b), a.bias[row]);
+    if (a.residual.ptr) v = __fadd_rn(v, ld_elem(a.residual.ptr, b * a.residual.row_stride + row, a.dtype));
+    st_elem(a.y.ptr, b * a.y.row_stride + row, v, a.dtype);
+  }
+  if (cs > 1) cluster_barrier();   // sums are read by the others until here
+}
+
+template <int NT>
+cudaError_t run_few(const Lin8Args& a, int cs, int smem, cudaStream_t st) {
+  return launch_ex(k_lin8_few<NT>, dim3(a.clusters * cs), dim3(kFewThreads), smem, st, true, cs, a, cs);
+}
+
+// Up to 32 tokens.
+cudaError_t launch_few(const sffn_linear8& L, Lin8Args a, cudaStream_t st) {
+  const int nt = a.B <= 8 ? 1 : a.B <= 16 ? 2 : 4;
+  // The smallest cluster whose blocks hold their share of the tokens' codes, and larger ones while rows are too few to
+  // give every SM a tile.
+  int cs = 1, smem = 0;
+  for (;; cs *= 2) {
+    const int own = (L.kp / kL8Inputs + cs - 1) / cs * kL8Inputs;
+    a.x_stride = own + (own % 128 ? 0 : 64);
+    a.clusters = std::max(std::min(L.num_sms / cs, (a.n + 15) / 16), (a.n + kFewRows - 1) / kFewRows);
+    const int rows = (a.n + a.clusters - 1) / a.clusters;
+    a.off_sum = 8 * nt * a.x_stride;
+    smem = a.off_sum + rows * 8 * nt * 4;
+    const bool spare = a.n < L.num_sms / cs * 16 && own > 1024;
+    if (cs == 8 || (smem <= kFewSmem && !spare)) break;
+  }
+  if (smem > kFewSmem) return cudaErrorInvalidConfiguration;
+  return nt == 1 ? run_few<1>(a, cs, smem, st) : nt == 2 ? run_few<2>(a, cs, smem, st) : run_few<4>(a, cs, smem, st);
+}
+
+}  // namespace
+
+sffn_status pack_linear8(sffn_linear8& L, const int8_t* codes, const float* scales, const float* bias, cudaStream_t st) {
+  const int kb = L.kp / kL8Inputs, np = L.tiles * kL8Rows;
+  const size_t chunks = (size_t)L.tiles * kb * (kL8Block / 16);
+  L.packed = false;
+  k_pack_codes8<<<(unsigned)((chunks + 255) / 256), 256, 0, st>>>(codes, reinterpret_cast<uint4*>(L.codes),
+                                                                  L.desc.out_features, L.desc.in_features, kb, chunks);
+  k_pack_rows8<<<(np + 255) / 256, 256, 0, st>>>(scales, L.scales, L.desc.out_features, np);
+  k_pack_rows8<<<(np + 255) / 256, 256, 0, st>>>(bias, L.bias, L.desc.out_features, np);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(e, "sffn_linear8_pack");
+  L.packed = true;
+  return SFFN_OK;
+}
+
+cudaError_t configure_linear8_kernels(sffn_linear8& L) {
+  int optin = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, L.device);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<1>, optin);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<2>, optin);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<4>, optin);
+  return e;
+}
+
+size_t linear8_ws_bytes(const sffn_linear8&, int) { return 0; }
+
+cudaError_t launch_linear8(const sffn_linear8& L, const sffn_rows& x, const float* x_scales, int B,
+                           const sffn_rows& residual, const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
+  Lin8Args a = {};
+  a.codes = L.codes, a.scales = L.scales, a.bias = L.bias, a.n = L.desc.out_features, a.k = L.desc.in_features;
+  a.kb = L.kp / kL8Inputs, a.dtype = dtype;
+  const int elem = dtype == SFFN_F32 ? 4 : 2;
+  // tokens that a cluster of eight can hold the codes of
+  const int most = std::max(1, std::min(kFewTokens, kFewSmem * 5 / 8 * 8 / (L.kp + 64) / 8 * 8));
+  for (int b = 0; b < B; b += most) {
+    a.B = std::min(most, B - b);
+    a.x = x, a.y = y, a.residual = residual, a.x_scales = x_scales + b;
+    a.x.ptr = static_cast<int8_t*>(x.ptr) + b * x.row_stride;
+    a.y.ptr = static_cast<uint8_t*>(y.ptr) + b * y.row_stride * elem;
+    if (residual.ptr) a.residual.ptr = static_cast<uint8_t*>(residual.ptr) + b * residual.row_stride * elem;
+    const cudaError_t e = launch_few(L, a, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace sffn

@@ -1,0 +1,293 @@
+// Root-mean-square norm with the residual's addition, and rows of 8-bit codes.
+//
+// One block per row, which stays in registers from the one read to the one
+// write. The codes have to be defined, so every step but the mean is one fp32
+// rounding, and the mean, whose order of summation differs from block to
+// block, is carried far enough that its rounding to f does not depend on it:
+// squares and sums as two floats each (the second has what the first's
+// rounding left, by fma(t, t, -t^2) and by Knuth's two-sum), 2^-44 or better
+// after all additions, and the root in 64 bits.
+#include <algorithm>
+
+#include "rows_io.cuh"
+#include "step.h"
+
+namespace sffn {
+
+namespace {
+
+constexpr int kMaxThreads = 1024;
+
+template <typename T>
+constexpr int kRun = 16 / sizeof(T);   // elements of one 16-byte access
+
+// s + p into s, what the rounding left into c.
+__device__ __forceinline__ void two_sum(float& s, float& c, float p) {
+  const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
+  c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
+  s = t;
+}
+
+// Sum of two-float numbers and largest of bit patterns over the block; every thread gets the result.
+__device__ __forceinline__ void block_reduce(float& s, float& c, uint32_t& top, float* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float ps = __shfl_xor_sync(SFFN_FULL_MASK, s, o), pc = __shfl_xor_sync(SFFN_FULL_MASK, c, o);
+    two_sum(s, c, ps);
+    c = __fadd_rn(c, pc);
+  }
+  // lanes may differ in the last bits of c: the block goes by the first's
+  s = __shfl_sync(SFFN_FULL_MASK, s, 0), c = __shfl_sync(SFFN_FULL_MASK, c, 0);
+  top = __reduce_max_sync(SFFN_FULL_MASK, top);
+  if (warps == 1) return;
+  __syncthreads();   // red may still be read from an earlier call
+  if (lane == 0) red[warp] = s, red[32 + warp] = c, red[64 + warp] = __uint_as_float(top);
+  __syncthreads();
+  s = lane < warps ? red[lane] : 0.f;
+  c = lane < warps ? red[32 + lane] : 0.f;
+  top = lane < warps ? __float_as_uint(red[64 + lane]) : 0u;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float ps = __shfl_xor_sync(SFFN_FULL_MASK, s, o), pc = __shfl_xor_sync(SFFN_FULL_MASK, c, o);
+    two_sum(s, c, ps);
+    c = __fadd_rn(c, pc);
+  }
+  s = __shfl_sync(SFFN_FULL_MASK, s, 0), c = __shfl_sync(SFFN_FULL_MASK, c, 0);
+  top = __reduce_max_sync(SFFN_FULL_MASK, top);
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t top, float* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  top = __reduce_max_sync(SFFN_FULL_MASK, top);
+  if (warps == 1) return top;
+  __syncthreads();
+  if (lane == 0) red[warp] = __uint_as_float(top);
+  __syncthreads();
+  return __reduce_max_sync(SFFN_FULL_MASK, lane < warps ? __float_as_uint(red[lane]) : 0u);
+}
+
+// |v| as bits: ordered like the values, infinity and then NaN above them.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  return top >= kInfBits ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
+}
+
+// y / scale rounded to the nearest whole number, ties to even, as the quotient rounded to fp32 gives it. The product
+// with 1 / scale is off by less than 2^-15 where the quotient is at most 128, so only near a tie is the quotient itself
+// looked at, which takes the division.
+__device__ __forceinline__ int code_of(float y, float scale, float inv) {
+  float q = __fmul_rn(y, inv);
+  float r = rintf(q);
+  if (!(fabsf(fabsf(q - r) - 0.5f) > 0x1p-14f)) r = rintf(__fdiv_rn(y, scale));
+  return (int)fminf(fmaxf(r, -127.f), 127.f);
+}
+
+// Where rows may be read and written 16 bytes (codes: one run) at a time.
+struct NormVec {
+  bool x, residual, sum, y, codes, weight;
+};
+
+template <int N>
+__device__ __forceinline__ void load_some(const void* p, size_t i, int left, int dtype, bool vec, float* o) {
+  if (vec && left >= N) {
+    ld_run<N>(p, i, dtype, o);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = j < left ? ld_elem(p, i + j, dtype) : 0.f;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_some(void* p, size_t i, int left, int dtype, bool vec, const float* v) {
+  if (vec && left >= N) {
+    st_run<N>(p, i, dtype, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < left) st_elem(p, i + j, v[j], dtype);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(int8_t* p, int left, bool vec, const float* y, float scale, float inv) {
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = scale > 0.f ? code_of(y[j + e], scale, inv) : 0;
+      u |= (uint32_t)(c & 255) << (8 * e);
+    }
+    w[j / 4] = u;
+  }
+  if (vec && left >= N) {
+    if (N == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[N / 4 - 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < left) p[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+
+template <typename T>
+constexpr int dtype_of() {
+  return sizeof(T) == 4 ? SFFN_F32 : std::is_same<T, __half>::value ? SFFN_F16 : SFFN_BF16;
+}
+
+// EPT elements a thread, in runs of 16 bytes: run r of thread t begins at (r * threads + t) * kRun.
+template <typename T, int EPT>
+__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const NormVec vec) {
+  constexpr int N = kRun<T>, RUNS = EPT / N, D = dtype_of<T>();
+  __shared__ float red[96];
+  pdl_launch_dependents();
+  pdl_wait();
+  const size_t row = blockIdx.x;
+  const int step = blockDim.x * N, at0 = threadIdx.x * N;
+  float t[EPT];
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r)
+    load_some<N>(a.x.ptr, row * a.x.row_stride + at0 + r * step, a.width - at0 - r * step, D, vec.x, t + r * N);
+  if (a.residual.ptr) {
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      float o[N];
+      load_some<N>(a.residual.ptr, row * a.residual.row_stride + at0 + r * step, a.width - at0 - r * step, D,
+                   vec.residual, o);
+#pragma unroll
+      for (int j = 0; j < N; ++j) t[r * N + j] = __fadd_rn(t[r * N + j], o[j]);
+    }
+  }
+  if (a.sum.ptr) {
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r)
+      store_some<N>(a.sum.ptr, row * a.sum.row_stride + at0 + r * step, a.width - at0 - r * step, D, vec.sum, t + r * N);
+  }
+  if (a.norm) {
+    float s = 0.f, c = 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const float p = __fmul_rn(t[j], t[j]);
+      two_sum(s, c, p);
+      c = __fadd_rn(c, __fmaf_rn(t[j], t[j], -p));
+      top = max(top, abs_bits(t[j]));
+    }
+    block_reduce(s, c, top, red);
+    double sum = (double)s + (double)c;
+    if (top >= kInfBits) {
+      sum = top > kInfBits ? nan("") : (double)INFINITY;
+    } else if (top && (top > __float_as_uint(0x1p56f) || top < __float_as_uint(0x1p-39f))) {
+      // squares or what they leave would pass fp32's range: the row times a power of two
+      const int e = 127 - (int)(top >> 23);   // of a subnormal row: 127
+      const float up = scalbnf(1.f, e / 2), up2 = scalbnf(1.f, e - e / 2);
+      s = c = 0.f;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        const float v = __fmul_rn(__fmul_rn(t[j], up), up2), p = __fmul_rn(v, v);
+        two_sum(s, c, p);
+        c = __fadd_rn(c, __fmaf_rn(v, v, -p));
+      }
+      block_reduce(s, c, top, red);
+      sum = scalbn((double)s + (double)c, -2 * e);
+    }
+    const float f = (float)(1.0 / sqrt(sum / a.width + a.eps));
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      const int at = at0 + r * step, left = a.width - at;
+      float w[N];
+      if (a.weight) load_some<N>(a.weight, at, left, SFFN_F32, vec.weight, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        float v = __fmul_rn(t[r * N + j], f);
+        if (a.weight) v = __fmul_rn(v, w[j]);
+        t[r * N + j] = j < left ? v : 0.f;
+      }
+    }
+    if (a.y.ptr) {
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r)
+        store_some<N>(a.y.ptr, row * a.y.row_stride + at0 + r * step, a.width - at0 - r * step, a.y_dtype, vec.y,
+                      t + r * N);
+    }
+  }
+  if (a.codes.ptr) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) top = max(top, abs_bits(t[j]));
+    top = block_max(top, red);
+    const float scale = scale_of(top);
+    const float inv = __fdiv_rn(1.f, scale);   // infinite for a subnormal scale: code_of divides then
+    if (threadIdx.x == 0) a.scales[row] = scale;
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      const int at = at0 + r * step;
+      if (at < a.width)
+        store_codes<N>(static_cast<int8_t*>(a.codes.ptr) + row * a.codes.row_stride + at, a.width - at, vec.codes,
+                       t + r * N, scale, inv);
+    }
+  }
+}
+
+// Rows too wide for a block's registers, as they are: read twice.
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreads) k_quantize_wide(const NormArgs a, const NormVec vec) {
+  constexpr int N = kRun<T>, D = dtype_of<T>();
+  __shared__ float red[96];
+  pdl_launch_dependents();
+  pdl_wait();
+  const size_t row = blockIdx.x;
+  uint32_t top = 0;
+  float t[N];
+  for (int at = threadIdx.x * N; at < a.width; at += blockDim.x * N) {
+    load_some<N>(a.x.ptr, row * a.x.row_stride + at, a.width - at, D, vec.x, t);
+#pragma unroll
+    for (int j = 0; j < N; ++j) top = max(top, abs_bits(t[j]));
+  }
+  top = block_max(top, red);
+  const float scale = scale_of(top), inv = __fdiv_rn(1.f, scale);
+  if (threadIdx.x == 0) a.scales[row] = scale;
+  for (int at = threadIdx.x * N; at < a.width; at += blockDim.x * N) {
+    load_some<N>(a.x.ptr, row * a.x.row_stride + at, a.width - at, D, vec.x, t);
+    store_codes<N>(static_cast<int8_t*>(a.codes.ptr) + row * a.codes.row_stride + at, a.width - at, vec.codes, t, scale,
+                   inv);
+  }
+}
+
+bool on(const sffn_rows& r, int64_t rows, int elem, int run_bytes) {
+  return reinterpret_cast<uintptr_t>(r.ptr) % run_bytes == 0 && (rows <= 1 || r.row_stride * elem % run_bytes == 0);
+}
+
+template <typename T>
+cudaError_t launch_typed(const NormArgs& a, cudaStream_t st) {
+  constexpr int N = kRun<T>;
+  const int ye = a.y_dtype == SFFN_F32 ? 4 : 2;
+  NormVec vec;
+  vec.x = on(a.x, a.rows, sizeof(T), 16), vec.residual = on(a.residual, a.rows, sizeof(T), 16);
+  vec.sum = on(a.sum, a.rows, sizeof(T), 16), vec.y = on(a.y, a.rows, ye, 16);
+  vec.codes = on(a.codes, a.rows, 1, N), vec.weight = reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+  if (a.width > kMaxThreads * 32)
+    return launch_ex(k_quantize_wide<T>, dim3(a.rows), dim3(kMaxThreads), 0, st, true, 1, a, vec);
+  // Few rows: as many threads as there are, for the shortest way through one row. Many: blocks of 256, so that an SM
+  // holds several and one loads while another waits at its barriers.
+  int ept = 8;
+  while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > 304 && a.width > 256 * ept))) ept *= 2;
+  const int threads = std::min(kMaxThreads, ((a.width + ept - 1) / ept + 31) / 32 * 32);
+  auto kern = ept == 8 ? k_norm<T, 8> : ept == 16 ? k_norm<T, 16> : k_norm<T, 32>;
+  return launch_ex(kern, dim3(a.rows), dim3(threads), 0, st, true, 1, a, vec);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
+  if (a.dtype == SFFN_F32) return launch_typed<float>(a, st);
+  return a.dtype == SFFN_F16 ? launch_typed<__half>(a, st) : launch_typed<__nv_bfloat16>(a, st);
+}
+
+}  // namespace sffn

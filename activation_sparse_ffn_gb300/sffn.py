@@ -85,6 +85,14 @@ class RopeC(ctypes.Structure):
     _fields_ = [("table", _vp), ("positions", _vp), ("length", _i32), ("dim", _i32), ("style", _i32)]
 
 
+class Linear8Desc(ctypes.Structure):
+    _fields_ = [("in_features", _i32), ("out_features", _i32), ("max_batch", _i32)]
+
+
+class BeamDesc(ctypes.Structure):
+    _fields_ = [("vocab", _i32), ("beams", _i32), ("n_out", _i32), ("max_batch", _i32)]
+
+
 class TamOutputsC(ctypes.Structure):
     _fields_ = [("cand", _vp), ("resident", _vp), ("load", _vp), ("evict", _vp), ("changed", _vp), ("topk", _vp),
                 ("n_cand", _vp), ("n_res", _vp)]
@@ -160,6 +168,24 @@ _sig("sffn_kv_append", _c, _vp, _P(KvBatchC), RowsC, _i32, RowsC, RowsC, RowsC, 
 _sig("sffn_kv_gather", _c, _vp, _P(KvBatchC), RowsC, RowsC, _i32, _vp)
 _sig("sffn_attend_workspace_bytes", _size, _vp, _i32, _i32, _i32)
 _sig("sffn_attend", _c, _vp, _P(KvBatchC), RowsC, _i32, RowsC, _vp, _f32, _i32, _i32, _vp, _size, _vp)
+_sig("sffn_norm", _c, RowsC, RowsC, _vp, ctypes.c_double, _i32, _i32, RowsC, RowsC, RowsC, _vp, _i32, _i32, _vp)
+_sig("sffn_quantize", _c, RowsC, _i32, _i32, RowsC, _vp, _i32, _vp)
+_sig("sffn_linear8_validate", _c, _P(Linear8Desc))
+_sig("sffn_linear8_create", _c, _P(Linear8Desc), _P(_vp))
+_sig("sffn_linear8_pack", _c, _vp, _vp, _vp, _vp, _vp)
+_sig("sffn_linear8_get_desc", _c, _vp, _P(Linear8Desc))
+_sig("sffn_linear8_workspace_bytes", _size, _vp, _i32)
+_sig("sffn_linear8_forward", _c, _vp, RowsC, _vp, _i32, RowsC, RowsC, _i32, _vp, _size, _vp)
+_sig("sffn_linear8_check_error", _c, _vp, _vp)
+_sig("sffn_linear8_destroy", None, _vp)
+_sig("sffn_beam_validate", _c, _P(BeamDesc))
+_sig("sffn_beam_create", _c, _P(BeamDesc), _P(_vp))
+_sig("sffn_beam_get_desc", _c, _vp, _P(BeamDesc))
+_sig("sffn_beam_workspace_bytes", _size, _vp, _i32)
+_sig("sffn_beam_select", _c, _vp, RowsC, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _size, _vp)
+_sig("sffn_beam_check_error", _c, _vp, _vp)
+_sig("sffn_beam_destroy", None, _vp)
+_sig("sffn_kv_reorder", _c, _P(_vp), _i32, _P(KvBatchC), _vp, _i32, _vp, _i32, _vp)
 
 EXPORTS = [
     "sffn_status_string", "sffn_last_error", "sffn_version", "sffn_layer_validate", "sffn_layer_create",
@@ -176,6 +202,11 @@ EXPORTS = [
     "sffn_linear_workspace_bytes", "sffn_linear_forward", "sffn_linear_check_error", "sffn_linear_destroy",
     "sffn_kv_validate", "sffn_kv_bytes", "sffn_kv_create", "sffn_kv_get_desc", "sffn_kv_check_error",
     "sffn_kv_destroy", "sffn_kv_append", "sffn_kv_gather", "sffn_attend_workspace_bytes", "sffn_attend",
+    "sffn_norm", "sffn_quantize",
+    "sffn_linear8_validate", "sffn_linear8_create", "sffn_linear8_pack", "sffn_linear8_get_desc",
+    "sffn_linear8_workspace_bytes", "sffn_linear8_forward", "sffn_linear8_check_error", "sffn_linear8_destroy",
+    "sffn_beam_validate", "sffn_beam_create", "sffn_beam_get_desc", "sffn_beam_workspace_bytes", "sffn_beam_select",
+    "sffn_beam_check_error", "sffn_beam_destroy", "sffn_kv_reorder",
 ]
 
 
@@ -658,6 +689,220 @@ def sffn_attend(kv, batch: "KvBatch", q, out, lse, scale, window=0, ws=None, str
         raise SffnError(rc, "sffn_attend")
 
 
+# ----------------------------------------------------------------- around the halves: norm, 8-bit rows, beams
+
+_linear8_sizes = {}   # handle: (in_features, out_features)
+_beam_sizes = {}      # handle: (vocab, beams, n_out)
+
+
+def _width_rows(t, n, width, dtype, name) -> RowsC:
+    """RowsC of (n, width) rows, or (n, heads, dim) with contiguous heads, of one type."""
+    if t.shape != (n, width):
+        _flat_rows(t, width, name)
+        if t.shape[0] != n:
+            raise ValueError(f"{name}: {t.shape[0]} rows given, {n} wanted")
+    return _rows(t, dtype, name)
+
+
+def _flat(t, n, dtype, name) -> int:
+    """Address of n contiguous elements."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous elements of {dtype} are wanted")
+    return t.data_ptr()
+
+
+def _row_shape(x):
+    """(rows, elements of a row) of a (rows, width) or (rows, heads, dim) tensor."""
+    shape = x.shape
+    if len(shape) == 3:
+        return shape[0], shape[1] * shape[2]
+    if len(shape) != 2:
+        raise ValueError("rows: two or three dimensions are wanted")
+    return shape
+
+
+def sffn_norm(x, weight=None, eps=1e-5, residual=None, sum=None, y=None, codes=None, scales=None, stream=None) -> None:
+    """Root-mean-square norm of x (rows, width) + residual: the sum to `sum`, the norm times weight (width,) to y
+    and, rounded to 8 bits, to codes (rows, width) int8 with scales (rows,) float32. Each output may be None, but y or
+    codes is required. y may have another type than x."""
+    n, width = _row_shape(x)
+    dtype = x.dtype
+    w = None if weight is None else _flat(weight, width, torch.float32, "weight")
+    s = None
+    if codes is not None:
+        if scales is None:
+            raise ValueError("codes need scales")
+        s = _flat(scales, n, torch.float32, "scales")
+    rc = _lib.sffn_norm(_width_rows(x, n, width, None, "x"),
+                        _NO_ROWS if residual is None else _width_rows(residual, n, width, dtype, "residual"), w, eps, n,
+                        width, _NO_ROWS if sum is None else _width_rows(sum, n, width, dtype, "sum"),
+                        _NO_ROWS if y is None else _width_rows(y, n, width, None, "y"),
+                        _NO_ROWS if codes is None else _width_rows(codes, n, width, torch.int8, "codes"), s,
+                        _io_dtype(dtype), _io_dtype(dtype if y is None else y.dtype), _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_norm")
+
+
+def sffn_quantize(x, codes, scales, stream=None) -> None:
+    """x (rows, width) rounded to codes (rows, width) int8 with scales (rows,) float32."""
+    n, width = _row_shape(x)
+    rc = _lib.sffn_quantize(_width_rows(x, n, width, None, "x"), n, width,
+                            _width_rows(codes, n, width, torch.int8, "codes"),
+                            _flat(scales, n, torch.float32, "scales"), _io_dtype(x.dtype), _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_quantize")
+
+
+def make_linear8_desc(in_features, out_features, max_batch=1) -> Linear8Desc:
+    return Linear8Desc(in_features, out_features, max_batch)
+
+
+def sffn_linear8_validate(desc: Linear8Desc) -> int:
+    """Host-only check; returns the status code (no exception)."""
+    return _lib.sffn_linear8_validate(ctypes.byref(desc))
+
+
+def sffn_linear8_create(desc: Linear8Desc) -> int:
+    h = _vp()
+    _check(_lib.sffn_linear8_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_linear8_create")
+    _linear8_sizes[h.value] = (desc.in_features, desc.out_features)
+    return h.value
+
+
+def sffn_linear8_pack(linear, codes, scales, bias=None, stream=None) -> None:
+    d = sffn_linear8_get_desc(linear)
+    for t, shape, dtype, name in ((codes, (d.out_features, d.in_features), torch.int8, "codes"),
+                                  (scales, (d.out_features,), torch.float32, "scales"),
+                                  (bias, (d.out_features,), torch.float32, "bias")):
+        if isinstance(t, torch.Tensor):
+            _want(t, shape, name)
+            if t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous {dtype} tensor is wanted")
+    _check(_lib.sffn_linear8_pack(linear, _ptr(codes), _ptr(scales), _ptr(bias), _stream(stream)), "sffn_linear8_pack")
+
+
+def sffn_linear8_get_desc(linear) -> Linear8Desc:
+    out = Linear8Desc()
+    _check(_lib.sffn_linear8_get_desc(linear, ctypes.byref(out)), "sffn_linear8_get_desc")
+    return out
+
+
+def sffn_linear8_workspace_bytes(linear, B: int) -> int:
+    return int(_lib.sffn_linear8_workspace_bytes(linear, B))
+
+
+def _linear8_size(linear):
+    """Of a handle that was made elsewhere."""
+    d = sffn_linear8_get_desc(linear)
+    return d.in_features, d.out_features
+
+
+def sffn_linear8_forward(linear, x, x_scales, y, residual=None, ws=None, stream=None) -> None:
+    """y (B, out) = x (B, in) int8 with x_scales (B,) through the layer, plus residual (B, out) if given (it may be y)."""
+    B, dtype = x.shape[0], y.dtype
+    n_in, n_out = _linear8_sizes.get(linear) or _linear8_size(linear)
+    ws_ptr, ws_bytes = _ws_args(ws)
+    rc = _lib.sffn_linear8_forward(linear, _width_rows(x, B, n_in, torch.int8, "x"),
+                                   _flat(x_scales, B, torch.float32, "x_scales"), B,
+                                   _NO_ROWS if residual is None else _width_rows(residual, B, n_out, dtype, "residual"),
+                                   _width_rows(y, B, n_out, None, "y"), _io_dtype(dtype), ws_ptr, ws_bytes,
+                                   _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_linear8_forward")
+
+
+def sffn_linear8_check_error(linear, stream=None) -> None:
+    _check(_lib.sffn_linear8_check_error(linear, _stream(stream)), "sffn_linear8_check_error")
+
+
+def sffn_linear8_destroy(linear) -> None:
+    _linear8_sizes.pop(linear, None)
+    _lib.sffn_linear8_destroy(linear)
+
+
+def make_beam_desc(vocab, beams, n_out, max_batch=1) -> BeamDesc:
+    return BeamDesc(vocab, beams, n_out, max_batch)
+
+
+def sffn_beam_validate(desc: BeamDesc) -> int:
+    """Host-only check; returns the status code (no exception)."""
+    return _lib.sffn_beam_validate(ctypes.byref(desc))
+
+
+def sffn_beam_create(desc: BeamDesc) -> int:
+    h = _vp()
+    _check(_lib.sffn_beam_create(ctypes.byref(desc), ctypes.byref(h)), "sffn_beam_create")
+    _beam_sizes[h.value] = (desc.vocab, desc.beams, desc.n_out)
+    return h.value
+
+
+def sffn_beam_get_desc(beam) -> BeamDesc:
+    out = BeamDesc()
+    _check(_lib.sffn_beam_get_desc(beam, ctypes.byref(out)), "sffn_beam_get_desc")
+    return out
+
+
+def sffn_beam_workspace_bytes(beam, batch: int) -> int:
+    return int(_lib.sffn_beam_workspace_bytes(beam, batch))
+
+
+def _beam_size(beam):
+    """Of a handle that was made elsewhere."""
+    d = sffn_beam_get_desc(beam)
+    return d.vocab, d.beams, d.n_out
+
+
+def sffn_beam_select(beam, logits, scores, out_scores, out_parents, out_tokens, done=None, end_token=0, ws=None,
+                     stream=None) -> None:
+    """The n_out best continuations of logits (batch * beams, vocab) after scores (batch, beams) float32: out_scores
+    float32, out_parents and out_tokens int32, (batch, n_out) each. done (batch, beams) bool or uint8 or None."""
+    vocab, beams, n_out = _beam_sizes.get(beam) or _beam_size(beam)
+    rows = logits.shape[0]
+    batch = rows // beams
+    if batch * beams != rows:
+        raise ValueError(f"logits: {rows} rows given, a multiple of {beams} wanted")
+    ended = None
+    if done is not None:
+        if done.dtype not in (torch.bool, torch.uint8) or done.numel() != rows or not done.is_contiguous():
+            raise ValueError(f"done: {rows} contiguous elements of bool or uint8 are wanted")
+        ended = done.data_ptr()
+    ws_ptr, ws_bytes = _ws_args(ws)
+    rc = _lib.sffn_beam_select(beam, _width_rows(logits, rows, vocab, None, "logits"),
+                               _flat(scores, rows, torch.float32, "scores"), ended, end_token, batch,
+                               _flat(out_scores, batch * n_out, torch.float32, "out_scores"),
+                               _flat(out_parents, batch * n_out, torch.int32, "out_parents"),
+                               _flat(out_tokens, batch * n_out, torch.int32, "out_tokens"), _io_dtype(logits.dtype),
+                               ws_ptr, ws_bytes, _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_beam_select")
+
+
+def sffn_beam_check_error(beam, stream=None) -> None:
+    _check(_lib.sffn_beam_check_error(beam, _stream(stream)), "sffn_beam_check_error")
+
+
+def sffn_beam_destroy(beam) -> None:
+    _beam_sizes.pop(beam, None)
+    _lib.sffn_beam_destroy(beam)
+
+
+def sffn_kv_reorder(caches: "KvCaches", batch: "KvBatch", parents, beams, table_out=None, stream=None) -> None:
+    """Reorder the caches (KvCaches) by parents (n_seq,) int32: page ids of batch.table go to table_out (the table itself if None),
+    the filled part of every sequence's last page to the page it keeps."""
+    n_seq, out, stride = batch.c.n_seq, batch.table, batch.c.table_stride
+    if table_out is not None and table_out is not out:
+        out = table_out
+        if out.dtype is not torch.int32 or out.shape != batch.table.shape or out.shape[1] > 1 and out.stride(1) != 1:
+            raise ValueError(f"table_out: int32 rows like the table's, {tuple(batch.table.shape)}, are wanted")
+        stride = out.stride(0) if n_seq > 1 else out.shape[1]
+        if stride < out.shape[1]:
+            raise ValueError("table_out: rows must not overlap")
+    rc = _lib.sffn_kv_reorder(caches.handles, caches.n, batch.ref, _flat(parents, n_seq, torch.int32, "parents"),
+                              beams, out.data_ptr(), stride, _stream(stream))
+    if rc:
+        raise SffnError(rc, "sffn_kv_reorder")
+
+
 # ----------------------------------------------------------------- TAM calls
 
 def tam_create(n_layers: int, n_groups: int, lambda0: float) -> int:
@@ -960,6 +1205,76 @@ class KvCache:
             self.close()
         except Exception:
             pass
+
+
+class Linear8:
+    """Owns one sffn_linear8 handle: 8-bit codes with a scale for each output channel."""
+
+    def __init__(self, in_features, out_features, max_batch=1):
+        self.desc = make_linear8_desc(in_features, out_features, max_batch)
+        self.handle = sffn_linear8_create(self.desc)
+        self.in_features, self.out_features, self.max_batch = in_features, out_features, max_batch
+
+    @classmethod
+    def from_weights(cls, codes, scales, bias=None, max_batch=1, stream=None) -> "Linear8":
+        """codes (out, in) int8; scales and bias (out,) float32."""
+        out_features, in_features = codes.shape
+        linear = cls(in_features, out_features, max_batch)
+        sffn_linear8_pack(linear.handle, codes.contiguous(), scales.contiguous(),
+                          None if bias is None else bias.contiguous(), stream)
+        return linear
+
+    def workspace(self, B=1, device="cuda") -> torch.Tensor:
+        return torch.empty(max(256, sffn_linear8_workspace_bytes(self.handle, B)), dtype=torch.uint8, device=device)
+
+    def check_error(self, stream=None) -> None:
+        sffn_linear8_check_error(self.handle, stream)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            sffn_linear8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Beams:
+    """Owns one sffn_beam handle: the n_out best continuations of searches with `beams` sequences each."""
+
+    def __init__(self, vocab, beams, n_out, max_batch=1):
+        self.desc = make_beam_desc(vocab, beams, n_out, max_batch)
+        self.handle = sffn_beam_create(self.desc)
+        self.vocab, self.beams, self.n_out, self.max_batch = vocab, beams, n_out, max_batch
+
+    def workspace(self, batch=1, device="cuda") -> torch.Tensor:
+        return torch.empty(max(256, sffn_beam_workspace_bytes(self.handle, batch)), dtype=torch.uint8, device=device)
+
+    def check_error(self, stream=None) -> None:
+        sffn_beam_check_error(self.handle, stream)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            sffn_beam_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvCaches:
+    """The caches of a model's layers, for calls that take them together (kept alive)."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        self.n = len(self.caches)
+        self.handles = (_vp * self.n)(*(c.handle for c in self.caches))
 
 
 class KvBatch:

@@ -660,6 +660,157 @@ sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */
                         sffn_rows out, float* lse /* [n_tokens][n_q_heads] */, float scale, int32_t window,
                         int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);
 
+/* ------------------------------------- around the halves: norm and 8-bit rows */
+
+/* What a decode step needs before, between and after its two halves: the
+ * norm with the residual's addition, rows rounded to 8 bits and the
+ * projections that take them, the choice of the best continuations, and the
+ * reordering of the cache by the sequences that go on. Hot calls: sffn_norm,
+ * sffn_quantize, sffn_linear8_forward, sffn_beam_select, sffn_kv_reorder
+ * (same rules as above: they allocate nothing, never synchronize, and may be
+ * captured in a CUDA graph). */
+
+/* Root-mean-square norm of n_rows rows of `width` elements, with the
+ * residual's addition before it and, if asked for, rows of 8-bit codes after
+ * it:
+ *   t = x + residual                         (t = x without one)
+ *   f = f32(1 / sqrt(mean(t^2) + eps))       (mean and root in 64 bits)
+ *   y = (t * f) * weight                     (y = t * f without one)
+ *   scale = max |y| / 127,  code = y / scale rounded to the nearest whole
+ *                                            number, ties to even
+ * in fp32, one rounding per operation, so that codes and scales are defined.
+ *   x, residual, sum_out (t, rounded once) in `dtype`; y in `y_dtype`;
+ *   weight [width] fp32; codes int8, scales [n_rows] fp32.
+ * residual, weight, sum_out, y and (codes, scales) are optional (NULL), but
+ * one of y and codes is required. x, residual and sum_out may be the same
+ * rows; y may be x, residual or sum_out if it has their type and not both y
+ * and sum_out are wanted there; rows must not overlap otherwise. A row whose
+ * y are all 0 has scale 0 and codes 0; a row with a y that is not finite has
+ * scale NaN and codes 0. Pointers and strides need only be aligned to their
+ * elements (rows on 16 bytes are faster).
+ * n_rows: 0 .. 2^30.  width: 1 .. 32768.  eps: finite, not negative.
+ * Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_norm(sffn_rows x, sffn_rows residual, const float* weight, double eps, int32_t n_rows, int32_t width,
+                      sffn_rows sum_out, sffn_rows y, sffn_rows codes, float* scales, int32_t dtype, int32_t y_dtype,
+                      sffn_stream stream);
+
+/* Codes and scales of rows as they are: scale = max |x| / 127 and so on, as
+ * above with y = x. width: 1 .. 65536. Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_quantize(sffn_rows x, int32_t n_rows, int32_t width, sffn_rows codes, float* scales, int32_t dtype,
+                          sffn_stream stream);
+
+/* A linear layer with 8-bit codes, a scale for each output channel, and rows
+ * of 8-bit codes with a scale each:
+ *   y[b][n] = (sum_k code[n][k] * x[b][k]) * (scale[n] * x_scale[b])
+ *             + bias[n] + residual[b][n].
+ * The sum is exact (32-bit whole numbers), what follows is fp32 with one
+ * rounding per operation, so that a token's y does not depend on the batch
+ * it comes in.
+ *   in_features: multiple of 16, 16 .. 65536.  out_features: 1 .. 1048576.
+ *   max_batch: largest B the layer will be called with, 1 .. 65536. */
+typedef struct {
+  int32_t in_features, out_features, max_batch;
+} sffn_linear8_desc;
+
+typedef struct sffn_linear8 sffn_linear8;
+
+/* Host-only check of a description (no CUDA call). */
+sffn_status sffn_linear8_validate(const sffn_linear8_desc* desc);
+/* Allocates the packed arrays on the current device. Errors: INVALID_ARG, OOM, CUDA. */
+sffn_status sffn_linear8_create(const sffn_linear8_desc* desc, sffn_linear8** out);
+/* Pack codes [out][in] int8, scales [out] fp32 and bias [out] fp32 or NULL.
+ * Setup call: synchronizes the stream. Device pointers, 16-byte aligned.
+ * Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_linear8_pack(sffn_linear8* linear, const int8_t* codes, const float* scales, const float* bias,
+                              sffn_stream stream);
+sffn_status sffn_linear8_get_desc(const sffn_linear8* linear, sffn_linear8_desc* out /* host */);
+/* Bytes of caller workspace for batch B (256-byte aligned, contents need no
+ * initialisation; 0 if the arguments are invalid or none is needed). */
+size_t sffn_linear8_workspace_bytes(const sffn_linear8* linear, int32_t B);
+/* x [B][in] int8 (pointer and stride multiples of 16 bytes) with x_scales [B]
+ * fp32, y and residual [B][out] in `dtype` (residual.ptr NULL = none; it may
+ * be y itself), element-aligned, with any stride >= out. y must not overlap
+ * x. A token whose scale is NaN gives NaN in its own outputs only.
+ * Errors: INVALID_ARG (also: not packed), CUDA. */
+sffn_status sffn_linear8_forward(const sffn_linear8* linear, sffn_rows x, const float* x_scales, int32_t B,
+                                 sffn_rows residual, sffn_rows y, int32_t dtype, void* ws, size_t ws_bytes,
+                                 sffn_stream stream);
+/* Synchronize the stream, then read and clear the layer's device error word
+ * (TIMEOUT: a bounded wait ran out). */
+sffn_status sffn_linear8_check_error(const sffn_linear8* linear, sffn_stream stream);
+void sffn_linear8_destroy(sffn_linear8* linear);
+
+/* -------------------------------------------- search over several continuations */
+
+/* The n_out best continuations of each of `batch` searches with `beams`
+ * sequences each, over a vocabulary: with z = logits[b * beams + j],
+ *   total[j][v] = scores[b][j] + z[v] - log sum_u exp(z[u]),
+ * the n_out largest by (total, then lowest j * vocab + v), largest first.
+ *   vocab: 1 .. 2^24.  beams: 1 .. 64.  n_out: 1 .. 64.
+ *   max_batch: largest batch the handle will be called with, at least 1, max_batch * beams at most 65535. */
+typedef struct {
+  int32_t vocab, beams, n_out, max_batch;
+} sffn_beam_desc;
+
+typedef struct sffn_beam sffn_beam;
+
+sffn_status sffn_beam_validate(const sffn_beam_desc* desc);
+/* A handle of the current device (a device error word only). Errors: INVALID_ARG, OOM, CUDA. */
+sffn_status sffn_beam_create(const sffn_beam_desc* desc, sffn_beam** out);
+sffn_status sffn_beam_get_desc(const sffn_beam* beam, sffn_beam_desc* out /* host */);
+/* Bytes of caller workspace for `batch` searches (256-byte aligned, contents
+ * need no initialisation; 0 if the arguments are invalid). */
+size_t sffn_beam_workspace_bytes(const sffn_beam* beam, int32_t batch);
+/* logits [batch * beams][vocab] in `dtype`, element-aligned, any stride >=
+ * vocab (rows on 16 bytes are faster); scores [batch][beams] fp32.
+ * done [batch][beams] bytes or NULL: a sequence whose byte is not 0 has ended,
+ * its logits are not read, and its only continuation is end_token with the
+ * score it has. A sequence whose score is -infinity has none, nor has one
+ * whose logits are all -infinity (masked tokens are -infinity and are never
+ * chosen). Logits with a NaN or +infinity, or a score that is NaN or
+ * +infinity, have none either and set the handle's device error word.
+ * out_scores fp32, out_parents (j) and out_tokens (v) [batch][n_out]; places
+ * that nothing is left for have score -infinity, parent 0 and token 0.
+ * Sums of exponentials are carried to about 2^-26 of their value and compared
+ * in 64 bits; the same arguments give the same bits at every call.
+ * out_scores may be `scores` if n_out is `beams`. Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_beam_select(const sffn_beam* beam, sffn_rows logits, const float* scores, const uint8_t* done,
+                             int32_t end_token, int32_t batch, float* out_scores, int32_t* out_parents,
+                             int32_t* out_tokens, int32_t dtype, void* ws, size_t ws_bytes, sffn_stream stream);
+/* Synchronize the stream, then read and clear the handle's device error word
+ * (DEVICE: logits or a score that have no distribution were seen). */
+sffn_status sffn_beam_check_error(const sffn_beam* beam, sffn_stream stream);
+void sffn_beam_destroy(sffn_beam* beam);
+
+/* Reorder the cache by the sequences that go on. The batch's sequences come
+ * in groups of `beams`, all sequences of a group with the same kv_len n;
+ * sequence s of group g goes on as a copy of sequence m = g * beams +
+ * parents[s]:
+ *   - pages that are full (the first n / page_size) are shared: their ids in
+ *     row s of table_out are those of row m of batch->table. Nothing is
+ *     written to them from then on (append writes from position n on).
+ *   - the n % page_size positions of the page that is not full are copied, in
+ *     every one of the n_kv caches, from the page that row m of batch->table
+ *     names to the one that row s of table_out named before the call.
+ * Ids of table_out from that page on are left as they are. table_out may be
+ * batch->table itself with the same stride (the usual case): every sequence
+ * then keeps its own last page, whatever it is a copy of. Otherwise it must
+ * not overlap it, and the last pages that it names must differ from those of
+ * batch->table. The last pages of a call's sequences must differ from each
+ * other in either table.
+ *   kvs [n_kv] host array of caches that differ in n_pages at most (the
+ *       layers of a model, which share their tables), 1 .. 128.
+ *   batch: table, kv_len, n_seq and table_stride are used; n_seq is a
+ *       multiple of beams.  parents [n_seq] device, each in 0 .. beams - 1.
+ *   beams: 1 .. 64.  out_stride: at least table_stride.
+ * A group whose lengths differ or do not fit the table, or with a parent out
+ * of range, is left as it was; a last page's id out of range is not copied
+ * from or to. All of these set the error word of the first cache.
+ * Errors: INVALID_ARG, CUDA. */
+sffn_status sffn_kv_reorder(const sffn_kv* const* kvs /* host */, int32_t n_kv, const sffn_kv_batch* batch /* host */,
+                            const int32_t* parents, int32_t beams, int32_t* table_out, int32_t out_stride,
+                            sffn_stream stream);
+
 /* ---------------------------------------------------------------- self-test */
 
 /* Exercise the bounded-wait path without any fault: one thread block waits
