@@ -231,13 +231,15 @@ cudaError_t configure_linear8_kernels(sffn_linear8& L) {
   if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<1>, optin);
   if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<2>, optin);
   if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<4>, optin);
+  if (e == cudaSuccess) e = configure_linear8_tc(L);
   return e;
 }
 
-size_t linear8_ws_bytes(const sffn_linear8&, int) { return 0; }
+size_t linear8_ws_bytes(const sffn_linear8& L, int B) { return B > kFewTokens ? linear8_tc_ws_bytes(L, B) : 0; }
 
 cudaError_t launch_linear8(const sffn_linear8& L, const sffn_rows& x, const float* x_scales, int B,
                            const sffn_rows& residual, const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
+  if (B > kFewTokens) return launch_linear8_tc(L, x, x_scales, B, residual, y, dtype, ws, st);
   Lin8Args a = {};
   a.codes = L.codes, a.scales = L.scales, a.bias = L.bias, a.n = L.desc.out_features, a.k = L.desc.in_features;
   a.kb = L.kp / kL8Inputs, a.dtype = dtype;

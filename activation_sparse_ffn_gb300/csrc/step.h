@@ -39,6 +39,10 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 
 sffn_status pack_linear8(sffn_linear8& L, const int8_t* codes, const float* scales, const float* bias, cudaStream_t st);
 cudaError_t configure_linear8_kernels(sffn_linear8& L);
+cudaError_t configure_linear8_tc(const sffn_linear8& L);
+size_t linear8_tc_ws_bytes(const sffn_linear8& L, int B);
+cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const float* x_scales, int B,
+                              const sffn_rows& residual, const sffn_rows& y, int dtype, void* ws, cudaStream_t st);
 size_t linear8_ws_bytes(const sffn_linear8& L, int B);
 cudaError_t launch_linear8(const sffn_linear8& L, const sffn_rows& x, const float* x_scales, int B,
                            const sffn_rows& residual, const sffn_rows& y, int dtype, void* ws, cudaStream_t st);
