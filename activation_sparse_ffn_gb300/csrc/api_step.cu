@@ -116,7 +116,7 @@ sffn_status sffn_linear8_create(const sffn_linear8_desc* d, sffn_linear8** out) 
   sffn_linear8* L = new (std::nothrow) sffn_linear8();
   if (!L) return invalid("host allocation failed");
   L->desc = *d;
-  L->kp = (d->in_features + 63) / 64 * 64;
+  L->kp = (d->in_features + 127) / 128 * 128;   // steps of 128
   L->tiles = (d->out_features + 255) / 256 * 2;   // blocks work on them in pairs
   const size_t np = (size_t)L->tiles * 128;
   cudaError_t e = cudaGetDevice(&L->device);

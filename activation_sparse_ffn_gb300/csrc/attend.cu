@@ -123,22 +123,6 @@ __device__ __forceinline__ int block_of(int u, int total, int blocks) {
   return (int)((((long long)u + 1) * blocks - 1) / total);
 }
 
-// The number of blocks that have left their part of an item, in the low half of a word whose high half tells whether
-// the word has been in use as such: the workspace comes with any contents.
-constexpr unsigned long long kTicketMark = 0x9e3779b97f4a7c15ull & 0xffffffff00000000ull;
-__device__ __forceinline__ int take_ticket(unsigned long long* word) {
-  for (;;) {
-    unsigned long long old = atomicAdd(word, 1ull);
-    if ((old & 0xffffffff00000000ull) == kTicketMark) return (int)(uint32_t)old;
-    // contents of before: the first block to replace them takes ticket 0, others count again
-    for (++old; (old & 0xffffffff00000000ull) != kTicketMark;) {
-      const unsigned long long seen = atomicCAS(word, old, kTicketMark | 1ull);
-      if (seen == old) return 0;
-      old = seen;
-    }
-  }
-}
-
 struct AttendArgs {
   const uint8_t* pages;
   size_t page_bytes, head_bytes;

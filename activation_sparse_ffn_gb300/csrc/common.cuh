@@ -22,6 +22,24 @@ __device__ __forceinline__ void set_device_error(uint32_t* err, uint32_t code) {
   if (err) atomicCAS(err, 0u, code);
 }
 
+// ----------------------------------------------------------------- tickets
+
+// The number of blocks that have left their part of something, in the low half of a word whose high half tells whether
+// the word has been in use as such: the workspace comes with any contents.
+constexpr unsigned long long kTicketMark = 0x9e3779b97f4a7c15ull & 0xffffffff00000000ull;
+__device__ __forceinline__ int take_ticket(unsigned long long* word) {
+  for (;;) {
+    unsigned long long old = atomicAdd(word, 1ull);
+    if ((old & 0xffffffff00000000ull) == kTicketMark) return (int)(uint32_t)old;
+    // contents of before: the first block to replace them takes ticket 0, others count again
+    for (++old; (old & 0xffffffff00000000ull) != kTicketMark;) {
+      const unsigned long long seen = atomicCAS(word, old, kTicketMark | 1ull);
+      if (seen == old) return 0;
+      old = seen;
+    }
+  }
+}
+
 // ----------------------------------------------------------------- PTX
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -1,20 +1,27 @@
 // The 8-bit linear layer for many tokens, on the fifth-generation tensor cores.
 //
 // GB300 has no 8-bit whole-number kind of the product, so codes become halves
-// on the way (linear8.cuh). The rows of the layer are the product's operand A:
-// 128 of them a block, whose codes arrive in shared memory by bulk copies, are
-// widened in registers by the thread of their row and written to tensor memory,
-// from where the product takes A, so that the widened codes cross shared memory
-// neither way. The tokens are operand B, widened once by k_lin8_widen before
-// and laid out in the order in which a tile's rows stand in shared memory
-// (128-byte swizzle), so that a tile is one run of bytes. CG = 2: two blocks of
-// a cluster work on 256 rows together and hold half of the tokens each.
+// (linear8.cuh). Two blocks of a cluster compute 256 rows x up to 192 tokens
+// together (cta_group::2). The rows of the layer are the product's operand A:
+// each block brings 128 rows of 64 codes to shared memory by bulk copies, the
+// thread of a row widens them and writes them to tensor memory, from where the
+// product takes A, so that the widened codes cross shared memory neither way.
+// The tokens are operand B, each block holding half of them. They are widened
+// once, by k_lin8_widen before, into the order in which a tile stands in shared
+// memory (128-byte swizzle), so that a block's half is one run of bytes;
+// widened on the way like the rows they took more instructions than the
+// product left time for.
 //
 // Sums leave their fp32 accumulators as whole numbers every 1024 inputs, into
 // registers, while the product goes on in a second accumulator.
 //
-// Tiles that fill whole waves are computed one at a time; the steps (of 64
-// inputs) of those left over are shared out evenly. A block that has part of
+// A step is 128 inputs: eight products a turn, since what surrounds them (a
+// wait, two commits) takes 500 cycles of the thread that issues them, as long as
+// five products, however many there are (64 inputs a step: 10240 x 8192 for 4096
+// tokens 775 us).
+//
+// Tiles that fill whole waves are computed one at a time; the steps of those
+// left over are shared out evenly. A block that has part of
 // a tile leaves its sums in the workspace, and whichever comes last adds them:
 // whole numbers, so that the order does not matter.
 #include <algorithm>
@@ -28,28 +35,31 @@ namespace sffn {
 
 namespace {
 
-constexpr int kConvWarps = 4, kEpiWarps = 8, kTcThreads = 512;
-constexpr int kWarpW = 12, kWarpX = 13, kWarpMma = 14;   // one thread each; warps 0-3 widen, 4-11 take the sums
+// Warps 0-3 widen even steps and 4-7 odd ones, 8-15 take the sums, and one thread each of 16 to 19 copies codes, copies
+// tokens, reports their arrival and issues products. Registers go where the sums are: 2 x 96 + 2 x 128 + 32 of the 5 x 96 a thread has at launch.
+constexpr int kConvWarps = 4, kEpiWarps = 8, kEpiWarp0 = 8, kTcThreads = 640;
+constexpr int kWarpW = 16, kWarpX = 17, kWarpTold = 18, kWarpMma = 19;
 constexpr int kMaxTokens = 192;                          // of a tile
-constexpr int kSlots = 4, kSlotCols = 32;                // of A in tensor memory
+constexpr int kStep = 2 * kL8Inputs, kStepW = 2 * kL8Block;
+constexpr int kSlots = 2, kSlotCols = 64;                // of A in tensor memory, one for each set of warps that widen
 constexpr int kAccCols = 192, kTmemCols = 512;           // accumulators at 0 and 192, A at 384
-constexpr int kStagesW = 8, kMaxStagesX = 8;
-constexpr int kStepsExact = kL8Exact / kL8Inputs;
-constexpr bool kPair = false;
-constexpr int kLeastSteps = 8;                           // of a tile that a block takes a part of
+constexpr int kStagesW = 6, kStagesX = 4;                // the first even: a set of warps keeps its own
+constexpr int kStepsExact = kL8Exact / kStep;
+constexpr int kLeastSteps = 4;                           // of a tile that a block takes a part of
+constexpr int CG = 2;                                    // blocks of a cluster
 
 struct TcArgs {
-  const uint8_t* codes;   // [tiles of 128 rows][steps][8 KB]
-  const uint8_t* xh;      // [steps][tokens][128 bytes]
+  const uint8_t* codes;   // [tiles of 128 rows][steps][16 KB]
+  const uint8_t* xh;      // [2 steps][tokens][128 bytes]
   const float* scales;
   const float* bias;
   const float* x_scales;
   sffn_rows residual, y;
   int32_t* parts;         // [block][2][tokens of a tile][128]
-  uint32_t* tickets;      // [tiles left over][CG]
+  unsigned long long* tickets;   // [tiles left over][CG]
   uint32_t* err;
   int n, B, dtype, steps, nt, token_tiles, tokens;   // nt: tokens of a tile; tokens: token_tiles * nt
-  int stages_x, groups;                              // groups: clusters
+  int groups;                                        // clusters
   int whole, left, parted;                           // whole waves of tiles, tiles after them, clusters that share those
 };
 
@@ -82,101 +92,94 @@ struct Segments {
   }
 };
 
-__device__ __forceinline__ uint32_t block_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
+// True in one lane of the warp, always the same. The warps that issue copies and products run their loops with every lane
+// and pick one for the instruction alone: the instructions take their operands from uniform registers, and in a branch
+// that one lane enters everything has to be brought there first (2 x 150 cycles for the two commits of a step).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Arrives on the barrier of the pair's first block (CG = 2) or on its own.
-template <int CG>
+// Arrives on the barrier of the pair's first block.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  if (CG == 1) {
-    mbar_arrive(bar);
-  } else {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+
+// Waits for the phase of the given parity, a second at most. The clock is looked at rarely: a wait that reads it first is
+// longer than most.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i % 256 == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > kWaitLimitNs) return false;
+    }
   }
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// A place in a ring of N and the parity of its turn, STEP places at a time.
+template <int N, int STEP>
+struct Ring {
+  int at;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int from) : at(from) {}
+  __device__ __forceinline__ void next() {
+    at += STEP;
+    if (at >= N) at -= N, phase ^= 1;
+  }
+};
 
-template <int CG>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-  if (CG == 1) return mbar_wait_bounded(bar, parity);
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_cluster(bar, parity))
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  return true;
-}
-
-// Instruction descriptor of kind::f16 with fp32 sums and halves on both sides, both K-major.
-template <int CG>
+// Instruction descriptor of kind::f16 with fp32 sums and halves on both sides, both K-major, 256 rows, n columns.
 __device__ __forceinline__ uint32_t half_desc(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 * CG >> 4) << 24);
 }
 
-// d (tensor memory) += a (tensor memory) b (shared memory).
-template <int CG>
+// d (tensor memory) += a (tensor memory) b (shared memory), of both blocks.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool add) {
-  if (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
 }
 
-// One arrival on the barrier (of both blocks) once the thread's products so far have completed.
-template <int CG>
-__device__ __forceinline__ void commit_to(uint64_t* bar) {
-  if (CG == 1)
-    tc::commit(bar);
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
+// One arrival on the barrier of both blocks once the thread's products so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
-template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst) {
-  if (CG == 1) {
-    tc::alloc(dst, kTmemCols);
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t t) {
-  if (CG == 1)
-    tc::dealloc(t, kTmemCols);
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmemCols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmemCols) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // 32 columns of 32-bit words of the warp's 32 lanes.
@@ -209,32 +212,32 @@ __device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
 // The barrier of the eight warps that take the sums.
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int CG>
-__global__ void __launch_bounds__(kTcThreads, 1) k_lin8_tc(const TcArgs a) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_lin8_tc(const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* smem = dyn_smem + (1024 - (smem_u32(dyn_smem) & 1023)) % 1024;   // the swizzle counts from there
-  __shared__ uint64_t wfull[kStagesW], wempty[kStagesW], xfull[kMaxStagesX], xempty[kMaxStagesX];
-  __shared__ uint64_t ready[kSlots], aempty[kSlots], accfull[2], accempty[2], drain;
+  __shared__ uint64_t wfull[kStagesW], wempty[kStagesW], xfull[kStagesX], xempty[kStagesX];
+  __shared__ uint64_t ready[kSlots], freed[kSlots], accfull[2], accempty[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_last;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = CG == 2 ? (int)block_rank() : 0, cluster = blockIdx.x / CG;
-  const int x_bytes = a.nt / CG * 128;                    // of a step's tokens in this block
-  uint8_t* ring_w = smem;
-  uint8_t* ring_x = smem + kStagesW * kL8Block;
+  const int tid = threadIdx.x, warp = __shfl_sync(SFFN_FULL_MASK, tid >> 5, 0), lane = tid & 31;
+  const int rank = blockIdx.x % CG, cluster = blockIdx.x / CG;   // clusters are consecutive blocks
+  const int x_bytes = a.nt / CG * 128;          // of the block's tokens, 64 inputs
+  uint8_t* ring_w = smem;                       // codes of 128 rows
+  uint8_t* ring_x = smem + kStagesW * kStepW;   // widened tokens, two times 64 inputs a stage
   if (tid == 0) {
     for (int s = 0; s < kStagesW; ++s) mbar_init(&wfull[s], 1), mbar_init(&wempty[s], kConvWarps);
-    for (int s = 0; s < kMaxStagesX; ++s) mbar_init(&xfull[s], 1), mbar_init(&xempty[s], 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], kConvWarps * CG), mbar_init(&aempty[s], 1);
+    for (int s = 0; s < kStagesX; ++s) mbar_init(&xfull[s], 1), mbar_init(&xempty[s], 1);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], (kConvWarps + 1) * CG), mbar_init(&freed[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&accfull[s], 1), mbar_init(&accempty[s], kEpiWarps * CG);
     mbar_init(&drain, 1);
     fence_mbar_init();
     s_abort = 0;
   }
-  if (warp == kWarpMma) tmem_alloc<CG>(&s_tmem);
+  if (warp == kWarpMma) tmem_alloc(&s_tmem);
   tc::fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();   // the other block's barriers are initialised too
+  cluster_sync_all();   // the other block's barriers are initialised too
   tc::fence_after();
   const uint32_t tmem = s_tmem;
   pdl_launch_dependents();
@@ -247,142 +250,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_lin8_tc(const TcArgs a) {
   Segments work(a, cluster);
   Segment seg;
 
-  if (warp == kWarpW) {
-    // ------------------------------------------------------------ codes; they are no earlier kernel's
-    if (lane == 0) {
-      const uint64_t policy = a.token_tiles > 1 ? tc::l2_policy_evict_last() : l2_policy_evict_first();
-      int it = 0;
-      bool ok = true;
-      while (ok && work.next(a, seg)) {
-        const int row_tile = seg.tile / a.token_tiles * CG + rank;
-        const uint8_t* src = a.codes + ((size_t)row_tile * a.steps + seg.s0) * kL8Block;
-        for (int k = seg.s0; k < seg.s1; ++k, ++it, src += kL8Block) {
-          const int s = it % kStagesW;
-          ok = it < kStagesW || mbar_wait_bounded(&wempty[s], (uint32_t)((it / kStagesW - 1) & 1));
-          if (!ok || aborted()) break;
-          mbar_arrive_expect_tx(&wfull[s], kL8Block);
-          bulk_g2s(ring_w + s * kL8Block, src, kL8Block, &wfull[s], policy);
-        }
-        if (!ok) fail();
-        if (aborted()) break;
-      }
-      if (aborted())   // copies in flight land before the block ends
-        for (int q = max(0, it - kStagesW); q < it; ++q) mbar_wait_bounded(&wfull[q % kStagesW], (uint32_t)((q / kStagesW) & 1));
-    }
-    pdl_wait();
-  } else if (warp == kWarpX) {
-    // ------------------------------------------------------------ tokens
-    pdl_wait();
-    if (lane == 0) {
-      const uint64_t policy = tc::l2_policy_evict_last();
-      int it = 0;
-      bool ok = true;
-      while (ok && work.next(a, seg)) {
-        const int token0 = seg.tile % a.token_tiles * a.nt + rank * (a.nt / CG);
-        const uint8_t* src = a.xh + ((size_t)seg.s0 * a.tokens + token0) * 128;
-        for (int k = seg.s0; k < seg.s1; ++k, ++it, src += (size_t)a.tokens * 128) {
-          const int s = it % a.stages_x;
-          ok = it < a.stages_x || wait_for<CG>(&xempty[s], (uint32_t)((it / a.stages_x - 1) & 1));
-          if (!ok || aborted()) break;
-          mbar_arrive_expect_tx(&xfull[s], x_bytes);
-          bulk_g2s(ring_x + s * x_bytes, src, x_bytes, &xfull[s], policy);
-        }
-        if (!ok) fail();
-        if (aborted()) break;
-      }
-      if (aborted())
-        for (int q = max(0, it - a.stages_x); q < it; ++q)
-          mbar_wait_bounded(&xfull[q % a.stages_x], (uint32_t)((q / a.stages_x) & 1));
-    }
-  } else if (warp < kConvWarps) {
-    // ------------------------------------------------------------ codes to halves in tensor memory, a row a thread
-    pdl_wait();
-    const int row = tid;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16) + 2 * kAccCols;
+  if (warp < 2 * kConvWarps) {
+    // ------------------------------------------------------------ codes to halves
+    pdl_wait();   // keeps the registers it has
+    const int row = tid & 127, set = warp / kConvWarps;
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * kAccCols;
+    Ring<kStagesW, 2> w(set);
+    Ring<kSlots, 2> out(set);
     int it = 0;
     bool ok = true;
     while (ok && work.next(a, seg)) {
-      for (int k = seg.s0; k < seg.s1; ++k, ++it) {
-        const int s = it % kStagesW, sa = it % kSlots, sx = it % a.stages_x;
-        ok = mbar_wait_bounded(&wfull[s], (uint32_t)((it / kStagesW) & 1));
-        ok = __all_sync(SFFN_FULL_MASK, ok);
-        if (!ok || __any_sync(SFFN_FULL_MASK, aborted())) break;
-        uint32_t h[32];
+      const int len = seg.s1 - seg.s0;
+      for (int k = (it ^ set) & 1; k < len; k += 2) {
+        ok = wait_for(&wfull[w.at], w.phase);
+        const uint8_t* src = ring_w + w.at * kStepW;
+        uint32_t h[64];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint4 v = *reinterpret_cast<const uint4*>(ring_w + s * kL8Block + l8_chunk(row, t));
+        for (int t = 0; t < 8; ++t) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (t >> 2) * kL8Block + l8_chunk(row, t & 3));
           l8_halves(v.x, h[8 * t], h[8 * t + 1]), l8_halves(v.y, h[8 * t + 2], h[8 * t + 3]);
           l8_halves(v.z, h[8 * t + 4], h[8 * t + 5]), l8_halves(v.w, h[8 * t + 6], h[8 * t + 7]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[s]);
-        ok = it < kSlots || wait_for<CG>(&aempty[sa], (uint32_t)((it / kSlots - 1) & 1));
-        ok = __all_sync(SFFN_FULL_MASK, ok);
-        if (!ok) break;
+        if (lane == 0) mbar_arrive(&wempty[w.at]);
+        ok = wait_for(&freed[out.at], out.phase ^ 1) && ok;   // passes at once the first time round
+        if (!__all_sync(SFFN_FULL_MASK, ok)) break;
         tc::fence_after();
-        tmem_store32(lane_base + sa * kSlotCols, h);
+        tmem_store32(mine + out.at * kSlotCols, h);
+        tmem_store32(mine + out.at * kSlotCols + 32, h + 32);
         tmem_store_wait();
         tc::fence_before();
-        // the step's tokens too are there before the product is told
-        ok = mbar_wait_bounded(&xfull[sx], (uint32_t)((it / a.stages_x) & 1));
-        ok = __all_sync(SFFN_FULL_MASK, ok);
-        if (!ok) break;
-        if (lane == 0) arrive_first<CG>(&ready[sa]);
+        __syncwarp();
+        if (lane == 0) arrive_first(&ready[out.at]);
+        w.next(), out.next();
       }
+      it += len;
+      ok = __all_sync(SFFN_FULL_MASK, ok);
       if (!ok && lane == 0) fail();
-      if (__any_sync(SFFN_FULL_MASK, aborted())) break;
     }
-  } else if (warp == kWarpMma) {
-    // ------------------------------------------------------------ products, one thread of the pair
-    pdl_wait();
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = half_desc<CG>(a.nt);
-      int it = 0, chunk = 0;
-      bool ok = true, issued = false;
-      while (ok && work.next(a, seg)) {
-        for (int k = seg.s0; ok && k < seg.s1;) {
-          const int end = min(k + kStepsExact, seg.s1), buf = chunk & 1;
-          ok = chunk < 2 || wait_for<CG>(&accempty[buf], (uint32_t)((chunk / 2 - 1) & 1));
-          tc::fence_after();
-          for (bool add = false; ok && k < end; ++k, ++it) {
-            const int sa = it % kSlots, sx = it % a.stages_x;
-            ok = wait_for<CG>(&ready[sa], (uint32_t)((it / kSlots) & 1));
-            if (!ok || aborted()) break;
-            tc::fence_after();
-            const uint32_t xs = smem_u32(ring_x + sx * x_bytes), as = tmem + 2 * kAccCols + sa * kSlotCols;
-#pragma unroll
-            for (int step = 0; step < 4; ++step) {
-              mma_ts<CG>(tmem + buf * kAccCols, as + step * 8, tc::smem_desc(xs + step * 32, 16, 1024), idesc, add);
-              add = true;
-            }
-            commit_to<CG>(&aempty[sa]);
-            commit_to<CG>(&xempty[sx]);
-            issued = true;
-          }
-          if (!ok || aborted()) break;
-          commit_to<CG>(&accfull[buf]);
-          ++chunk;
-        }
-        if (!ok) fail();
-        if (aborted()) break;
-      }
-      if (issued) {   // every product has ended before tensor memory is given back
-        tc::fence_before();
-        if (CG == 1)
-          tc::commit(&drain);
-        else
-          asm volatile(
-              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&drain))
-              : "memory");
-        mbar_wait_bounded(&drain, 0u);
-      }
-    }
-  } else if (warp >= kConvWarps && warp < kConvWarps + kEpiWarps) {
+  } else if (warp < kEpiWarp0 + kEpiWarps) {
     // ------------------------------------------------------------ sums to whole numbers to outputs
+    more_registers<128>();
     pdl_wait();
-    const int q = warp & 3, half = (warp - kConvWarps) >> 2, blocks = a.nt / 16;
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2, blocks = a.nt / 16;
     const int b0 = half ? (blocks + 1) / 2 : 0, nb = half ? blocks - b0 : (blocks + 1) / 2;   // of 16 tokens, at most 6
-    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + b0 * 16;
+    const uint32_t mine = tmem + ((uint32_t)(q * 32) << 16) + b0 * 16;
     const int r = q * 32 + lane;
     int chunk = 0;
     bool ok = true;
@@ -392,54 +304,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_lin8_tc(const TcArgs a) {
       for (int i = 0; i < 96; ++i) sum[i] = 0;
       for (int k = seg.s0; k < seg.s1; k += kStepsExact, ++chunk) {
         const int buf = chunk & 1;
-        ok = wait_for<CG>(&accfull[buf], (uint32_t)((chunk / 2) & 1));
-        ok = __all_sync(SFFN_FULL_MASK, ok);
-        if (!ok || __any_sync(SFFN_FULL_MASK, aborted())) break;
+        ok = __all_sync(SFFN_FULL_MASK, wait_for(&accfull[buf], (uint32_t)((chunk / 2) & 1)));
+        if (!ok) break;
         tc::fence_after();
 #pragma unroll
         for (int b = 0; b < 6; ++b)
           if (b < nb) {
             float v[16];
-            tmem_load16(lane_base + buf * kAccCols + b * 16, v);
+            tmem_load16(mine + buf * kAccCols + b * 16, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[b * 16 + i] += __float2int_rn(v[i]);
           }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first<CG>(&accempty[buf]);
+        if (lane == 0) arrive_first(&accempty[buf]);
       }
-      if (!ok && lane == 0) fail();
-      if (__any_sync(SFFN_FULL_MASK, aborted())) break;
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
+      }
       const int row_tile = seg.tile / a.token_tiles * CG + rank, token0 = seg.tile % a.token_tiles * a.nt + b0 * 16;
       if (seg.part) {
         // this block's sums to its place; the last to arrive adds the others'
         const int left = seg.tile - a.whole * a.groups;
-        const size_t tile_ints = (size_t)a.nt * kL8Rows;
-        const size_t own = (size_t)b0 * 16 * kL8Rows + r;
-        int32_t* mine = a.parts + ((size_t)blockIdx.x * 2 + seg.slot) * tile_ints + own;
+        const size_t tile_ints = (size_t)a.nt * kL8Rows, at = (size_t)b0 * 16 * kL8Rows + r;
+        int32_t* place = a.parts + ((size_t)blockIdx.x * 2 + seg.slot) * tile_ints + at;
 #pragma unroll
         for (int i = 0; i < 96; ++i)
-          if (i / 16 < nb) __stcg(mine + (size_t)i * kL8Rows, sum[i]);
+          if (i / 16 < nb) __stcg(place + (size_t)i * kL8Rows, sum[i]);
         __threadfence();
         epilogue_barrier();
         // clusters that share the tile: those whose steps reach into it
         const long long units = (long long)a.left * a.steps, begin = (long long)left * a.steps, end = begin + a.steps;
-        int first = (int)(begin * a.parted / units), last = (int)((end - 1) * a.parted / units);
-        while (units * first / a.parted > begin) --first;
-        while (units * (first + 1) / a.parted <= begin) ++first;
-        while (units * last / a.parted >= end) --last;
-        while (units * (last + 1) / a.parted < end) ++last;
-        if (warp == kConvWarps && lane == 0)
-          s_last = atomicAdd(&a.tickets[left * CG + rank], 1u) == (uint32_t)(last - first);
+        int from = (int)(begin * a.parted / units), to = (int)((end - 1) * a.parted / units);
+        while (units * from / a.parted > begin) --from;
+        while (units * (from + 1) / a.parted <= begin) ++from;
+        while (units * to / a.parted >= end) --to;
+        while (units * (to + 1) / a.parted < end) ++to;
+        if (warp == kEpiWarp0 && lane == 0) {
+          unsigned long long* word = a.tickets + left * CG + rank;
+          s_last = take_ticket(word) == to - from;
+          if (s_last) *word = kTicketMark;   // for the next call
+        }
         epilogue_barrier();
         const bool join = s_last;
         epilogue_barrier();   // read by all before it is written again
         if (!join) continue;
         __threadfence();
-        for (int c = first; c <= last; ++c) {
+        for (int c = from; c <= to; ++c) {
           if (c == cluster) continue;
           const int slot = units * c / a.parted >= begin ? 0 : 1;   // its first steps are this tile's, or its last
-          const int32_t* other = a.parts + ((size_t)(c * CG + rank) * 2 + slot) * tile_ints + own;
+          const int32_t* other = a.parts + ((size_t)(c * CG + rank) * 2 + slot) * tile_ints + at;
 #pragma unroll
           for (int i = 0; i < 96; ++i)
             if (i / 16 < nb) sum[i] += __ldcg(other + (size_t)i * kL8Rows);
@@ -447,11 +362,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_lin8_tc(const TcArgs a) {
       }
       const int n = row_tile * kL8Rows + r;
       const float scale = a.scales[n], bias = a.bias[n];   // padded to whole tiles
+      float xs[3];   // the tokens' scales, one a lane
+#pragma unroll
+      for (int i = 0; i < 3; ++i) xs[i] = token0 + 32 * i + lane < a.B ? __ldcg(a.x_scales + token0 + 32 * i + lane) : 0.f;
+      const int tokens = min(nb * 16, a.B - token0);
 #pragma unroll
       for (int i = 0; i < 96; ++i) {
-        const int token = token0 + i;
-        if (i / 16 < nb && token < a.B && n < a.n) {
-          float v = l8_value(sum[i], scale, __ldcg(a.x_scales + token), bias);
+        const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[i / 32], i % 32);
+        if (i < tokens && n < a.n) {
+          const int token = token0 + i;
+          float v = l8_value(sum[i], scale, x_scale, bias);
           if (a.residual.ptr) v = __fadd_rn(v, ld_elem(a.residual.ptr, token * a.residual.row_stride + n, a.dtype));
           st_elem(a.y.ptr, token * a.y.row_stride + n, v, a.dtype);
         }
@@ -459,25 +379,120 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_lin8_tc(const TcArgs a) {
       __syncwarp();
     }
   } else {
-    pdl_wait();
+    fewer_registers<32>();
+    if (warp == kWarpW) {
+      // ---------------------------------------------------------- codes of rows, which are no earlier kernel's
+      const uint64_t policy = a.token_tiles > 1 ? tc::l2_policy_evict_last() : l2_policy_evict_first();
+      Ring<kStagesW, 1> w(0);
+      int it = 0;
+      bool ok = true;
+      while (ok && work.next(a, seg)) {
+        const int row_tile = seg.tile / a.token_tiles * CG + rank;
+        const uint8_t* src = a.codes + ((size_t)row_tile * a.steps + seg.s0) * kStepW;
+        for (int k = seg.s0; k < seg.s1; ++k, ++it, src += kStepW, w.next()) {
+          ok = __all_sync(SFFN_FULL_MASK, wait_for(&wempty[w.at], w.phase ^ 1));
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&wfull[w.at], kStepW);
+            bulk_g2s(ring_w + w.at * kStepW, src, kStepW, &wfull[w.at], policy);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail();
+      if (aborted())   // copies in flight land before the block ends
+        for (int q = max(0, it - kStagesW); q < it; ++q) wait_for(&wfull[q % kStagesW], (uint32_t)((q / kStagesW) & 1));
+      pdl_wait();
+    } else if (warp == kWarpX) {
+      // ---------------------------------------------------------- tokens
+      pdl_wait();
+      const uint64_t policy = tc::l2_policy_evict_last();
+      Ring<kStagesX, 1> x(0);
+      int it = 0;
+      bool ok = true;
+      while (ok && work.next(a, seg)) {
+        const int token0 = seg.tile % a.token_tiles * a.nt + rank * (a.nt / CG);
+        const uint8_t* src = a.xh + ((size_t)seg.s0 * 2 * a.tokens + token0) * 128;
+        for (int k = seg.s0; k < seg.s1; ++k, ++it, src += (size_t)a.tokens * 256, x.next()) {
+          ok = __all_sync(SFFN_FULL_MASK, wait_for(&xempty[x.at], x.phase ^ 1));
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&xfull[x.at], 2 * x_bytes);
+            bulk_g2s(ring_x + 2 * x.at * x_bytes, src, x_bytes, &xfull[x.at], policy);
+            bulk_g2s(ring_x + (2 * x.at + 1) * x_bytes, src + (size_t)a.tokens * 128, x_bytes, &xfull[x.at], policy);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail();
+      if (aborted())
+        for (int q = max(0, it - kStagesX); q < it; ++q) wait_for(&xfull[q % kStagesX], (uint32_t)((q / kStagesX) & 1));
+    } else if (warp == kWarpTold) {
+      // ---------------------------------------------------------- tokens that have arrived are reported to the pair's first block
+      pdl_wait();
+      Ring<kStagesX, 1> x(0);
+      Ring<kSlots, 1> slot(0);
+      bool ok = true;
+      while (ok && work.next(a, seg))
+        for (int k = seg.s0; ok && k < seg.s1; ++k, x.next(), slot.next()) {
+          // a slot's report counts for the product that comes next in it
+          ok = wait_for(&xfull[x.at], x.phase) && wait_for(&freed[slot.at], slot.phase ^ 1);
+          ok = __all_sync(SFFN_FULL_MASK, ok);
+          if (ok && elect_one()) arrive_first(&ready[slot.at]);
+        }
+      if (!ok && lane == 0) fail();
+    } else if (warp == kWarpMma) {
+      // ---------------------------------------------------------- products, one thread of the pair
+      pdl_wait();
+      if (rank == 0) {
+        const uint32_t idesc = half_desc(a.nt), first_x = smem_u32(ring_x);
+        Ring<kStagesX, 1> x(0);
+        Ring<kSlots, 1> slot(0);
+        int chunk = 0;
+        bool ok = true;
+        while (ok && work.next(a, seg)) {
+          for (int k = seg.s0; ok && k < seg.s1; ++chunk) {
+            const int end = min(k + kStepsExact, seg.s1), buf = chunk & 1;
+            ok = chunk < 2 || __all_sync(SFFN_FULL_MASK, wait_for(&accempty[buf], (uint32_t)((chunk / 2 - 1) & 1)));
+            const uint32_t acc = tmem + buf * kAccCols;
+            bool add = false;
+            for (; ok && k < end; ++k, x.next(), slot.next(), add = true) {
+              ok = __all_sync(SFFN_FULL_MASK, wait_for(&ready[slot.at], slot.phase));
+              if (!ok) break;
+              tc::fence_after();
+              const uint32_t xs = first_x + 2 * x.at * x_bytes, as = tmem + 2 * kAccCols + slot.at * kSlotCols;
+              if (elect_one()) {
+#pragma unroll
+                for (int step = 0; step < 8; ++step)
+                  mma_ts(acc, as + step * 8, tc::smem_desc(xs + (step >> 2) * x_bytes + (step & 3) * 32, 16, 1024), idesc,
+                         add || step);
+                commit_pair(&freed[slot.at]);
+                commit_pair(&xempty[x.at]);
+              }
+            }
+            if (ok && elect_one()) commit_pair(&accfull[buf]);
+          }
+        }
+        if (!ok && lane == 0) fail();
+        // every product has ended before tensor memory is given back
+        if (elect_one()) commit_own(&drain);
+        wait_for(&drain, 0u);
+      }
+    }
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   tc::fence_after();
-  if (warp == kWarpMma) tmem_free<CG>(tmem);
+  if (warp == kWarpMma) tmem_free(tmem);
 }
 
-// Tokens' codes as halves: step k, token b: 128 bytes at (k * tokens + b) * 128, their 16-byte chunk j (inputs 8 j ..) at
-// chunk position j ^ (b & 7). A thread widens 16 codes. Clears the tickets.
-__global__ void k_lin8_widen(sffn_rows x, int B, int k, int steps, int tokens, uint4* xh, uint32_t* tickets,
-                             unsigned n_tickets) {
+// Tokens' codes as halves: inputs 64 k .., token b: 128 bytes at (k * tokens + b) * 128, their 16-byte chunk j (inputs 8 j ..) at
+// chunk position j ^ (b & 7). A thread widens 16 codes.
+__global__ void k_lin8_widen(sffn_rows x, int B, int k, int runs, int tokens, uint4* xh) {
   pdl_launch_dependents();
   pdl_wait();
-  const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;   // at most 65536 tokens of 4096 runs
-  if (i < n_tickets) tickets[i] = 0;
-  const int per = steps * 4, b = i / per, c = i % per, col = c * 16;
+  const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;   // at most 65536 tokens of 4096 runs, and a tile's padding
+  const int b = i / runs, c = i % runs, col = c * 16;
   if (b >= tokens) return;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (b < B && col < k) v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(x.ptr) + b * x.row_stride + col));
@@ -503,28 +518,15 @@ TcShape tc_shape(int B) {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct TcWs {
-  size_t parts, tickets, total;
+  size_t xh, parts, total;   // the tickets come first
 };
 TcWs tc_ws(const sffn_linear8& L, const TcShape& s) {
   TcWs w;
-  w.parts = up256((size_t)s.tokens * L.kp * 2);
+  w.xh = up256((size_t)L.num_sms * sizeof(unsigned long long));
+  w.parts = w.xh + up256((size_t)s.tokens * L.kp * 2);
   const int nt = s.token_tiles > 1 ? kMaxTokens : s.nt;   // the workspace of a batch serves every smaller one
-  w.tickets = w.parts + up256((size_t)L.num_sms * 2 * nt * kL8Rows * 4);
-  w.total = w.tickets + up256((size_t)L.num_sms * 2 * 4);
+  w.total = w.parts + (size_t)L.num_sms * 2 * nt * kL8Rows * 4;
   return w;
-}
-
-template <int CG>
-cudaError_t run_tc(const sffn_linear8& L, TcArgs a, cudaStream_t st) {
-  a.groups = L.num_sms / CG;
-  const int tiles = L.tiles / CG * a.token_tiles;
-  a.whole = tiles / a.groups, a.left = tiles % a.groups;
-  a.parted = a.left ? (int)std::min<long long>(a.groups, std::max<long long>(a.left, (long long)a.left * a.steps / kLeastSteps)) : 0;
-  const int x_bytes = a.nt / CG * 128;
-  a.stages_x = std::min(kMaxStagesX, 128 * 1024 / x_bytes);
-  const int smem = 1024 + kStagesW * kL8Block + a.stages_x * x_bytes;
-  const int clusters = a.whole ? a.groups : a.parted;
-  return launch_ex(k_lin8_tc<CG>, dim3(clusters * CG), dim3(kTcThreads), smem, st, true, CG, a);
 }
 
 }  // namespace
@@ -532,9 +534,7 @@ cudaError_t run_tc(const sffn_linear8& L, TcArgs a, cudaStream_t st) {
 cudaError_t configure_linear8_tc(const sffn_linear8& L) {
   int optin = 0;
   cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, L.device);
-  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_tc<1>, optin);
-  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_tc<2>, optin);
-  return e;
+  return e == cudaSuccess ? set_dynamic_smem_max(k_lin8_tc, optin) : e;
 }
 
 size_t linear8_tc_ws_bytes(const sffn_linear8& L, int B) { return tc_ws(L, tc_shape(B)).total; }
@@ -545,17 +545,22 @@ cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const f
   const TcWs w = tc_ws(L, s);
   uint8_t* base = static_cast<uint8_t*>(ws);
   TcArgs a = {};
-  a.codes = L.codes, a.xh = base, a.scales = L.scales, a.bias = L.bias, a.x_scales = x_scales;
-  a.residual = residual, a.y = y, a.parts = reinterpret_cast<int32_t*>(base + w.parts);
-  a.tickets = reinterpret_cast<uint32_t*>(base + w.tickets), a.err = L.err;
-  a.n = L.desc.out_features, a.B = B, a.dtype = dtype, a.steps = L.kp / kL8Inputs;
+  a.codes = L.codes, a.xh = base + w.xh, a.scales = L.scales, a.bias = L.bias, a.x_scales = x_scales;
+  a.residual = residual, a.y = y, a.tickets = static_cast<unsigned long long*>(ws);
+  a.parts = reinterpret_cast<int32_t*>(base + w.parts);
+  a.err = L.err, a.n = L.desc.out_features, a.B = B, a.dtype = dtype, a.steps = L.kp / kStep;
   a.nt = s.nt, a.token_tiles = s.token_tiles, a.tokens = s.tokens;
-  const long long threads = std::max<long long>((long long)s.tokens * a.steps * 4, L.num_sms * 2);
-  cudaError_t e = launch_ex(k_lin8_widen, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, true, 1, x, B,
-                            L.desc.in_features, a.steps, s.tokens, reinterpret_cast<uint4*>(base), a.tickets,
-                            L.num_sms * 2);
+  a.groups = L.num_sms / CG;
+  const int tiles = L.tiles / CG * a.token_tiles;
+  a.whole = tiles / a.groups, a.left = tiles % a.groups;
+  a.parted = a.left ? (int)std::min<long long>(a.groups, std::max<long long>(a.left, (long long)a.left * a.steps / kLeastSteps)) : 0;
+  const int runs = L.kp / 16;
+  const unsigned threads = (unsigned)s.tokens * runs;
+  cudaError_t e = launch_ex(k_lin8_widen, dim3((threads + 255) / 256), dim3(256), 0, st, true, 1, x, B, L.desc.in_features,
+                            runs, s.tokens, reinterpret_cast<uint4*>(base + w.xh));
   if (e != cudaSuccess) return e;
-  return kPair ? run_tc<2>(L, a, st) : run_tc<1>(L, a, st);
+  const int smem = 1024 + kStagesW * kStepW + kStagesX * (a.nt / CG * 256);
+  return launch_ex(k_lin8_tc, dim3((a.whole ? a.groups : a.parted) * CG), dim3(kTcThreads), smem, st, true, CG, a);
 }
 
 }  // namespace sffn

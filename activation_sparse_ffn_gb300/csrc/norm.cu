@@ -67,6 +67,25 @@ __device__ __forceinline__ uint32_t block_max(uint32_t top, float* red) {
   return __reduce_max_sync(SFFN_FULL_MASK, lane < warps ? __float_as_uint(red[lane]) : 0u);
 }
 
+// f32(1 / sqrt(sum / width + eps)), by one warp for the block: 64-bit arithmetic issues at a sixteenth of a warp a cycle, and
+// all warps of a row of 8192 together took 9 us for it. Newton's iteration from the fp32 estimate doubles its 22
+// bits twice.
+__device__ __forceinline__ float factor(double sum, double inv_width, double eps, float* red) {
+  if (threadIdx.x < 32) {
+    const double v = fma(sum, inv_width, eps);
+    double r = rsqrtf((float)v);
+    if (v > 1e-30 && v < 1e30) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-v * r, r, 1.0), r);
+    } else {
+      r = 1.0 / sqrt(v);   // past what the estimate holds, 0, infinity or no number
+    }
+    if (threadIdx.x == 0) red[96] = (float)r;
+  }
+  __syncthreads();
+  return red[96];
+}
+
 // |v| as bits: ordered like the values, infinity and then NaN above them.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
@@ -143,9 +162,9 @@ constexpr int dtype_of() {
 
 // EPT elements a thread, in runs of 16 bytes: run r of thread t begins at (r * threads + t) * kRun.
 template <typename T, int EPT>
-__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const NormVec vec) {
+__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const NormVec vec, double inv_width) {
   constexpr int N = kRun<T>, RUNS = EPT / N, D = dtype_of<T>();
-  __shared__ float red[96];
+  __shared__ float red[97];
   pdl_launch_dependents();
   pdl_wait();
   const size_t row = blockIdx.x;
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const No
       block_reduce(s, c, top, red);
       sum = scalbn((double)s + (double)c, -2 * e);
     }
-    const float f = (float)(1.0 / sqrt(sum / a.width + a.eps));
+    const float f = factor(sum, inv_width, a.eps, red);
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       const int at = at0 + r * step, left = a.width - at;
@@ -239,7 +258,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const No
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) k_quantize_wide(const NormArgs a, const NormVec vec) {
   constexpr int N = kRun<T>, D = dtype_of<T>();
-  __shared__ float red[96];
+  __shared__ float red[97];
   pdl_launch_dependents();
   pdl_wait();
   const size_t row = blockIdx.x;
@@ -280,7 +299,7 @@ cudaError_t launch_typed(const NormArgs& a, cudaStream_t st) {
   while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > 304 && a.width > 256 * ept))) ept *= 2;
   const int threads = std::min(kMaxThreads, ((a.width + ept - 1) / ept + 31) / 32 * 32);
   auto kern = ept == 8 ? k_norm<T, 8> : ept == 16 ? k_norm<T, 16> : k_norm<T, 32>;
-  return launch_ex(kern, dim3(a.rows), dim3(threads), 0, st, true, 1, a, vec);
+  return launch_ex(kern, dim3(a.rows), dim3(threads), 0, st, true, 1, a, vec, 1.0 / a.width);
 }
 
 }  // namespace

@@ -10,7 +10,7 @@ struct sffn_linear8 {
   int device = 0;
   int num_sms = 0;
   bool packed = false;
-  int kp = 0;             // in_features rounded up to 64
+  int kp = 0;             // in_features rounded up to 128
   int tiles = 0;          // 128-row tiles of out_features
   uint8_t* codes = nullptr;   // [tiles][kp / 64][128][64 bytes], see linear8.cu
   float* scales = nullptr;    // [tiles * 128], zeros beyond out_features

@@ -161,7 +161,7 @@ def linear_inputs(n, k, rows, seed=0, extreme=False):
 
 SIZES = [(1, 16, 1), (5, 48, 3), (130, 64, 33), (100, 4096, 7), (129, 1040, 32), (300, 8192, 64), (40, 65536, 9),
          (1000, 2048, 200), (4099, 512, 193), (2433, 11008, 17), (64, 16384, 1), (10240, 1024, 1), (257, 192, 1000),
-         (700, 65536, 70), (20000, 64, 40), (128, 1088, 385)]
+         (700, 65536, 70), (20000, 64, 40), (128, 1088, 385), (64, 16, 40)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
