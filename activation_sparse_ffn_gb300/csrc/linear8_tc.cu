@@ -212,6 +212,54 @@ __device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
 // The barrier of the eight warps that take the sums.
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+template <typename T>
+__device__ __forceinline__ float as_float(T v) {
+  if (sizeof(T) == 4) return *reinterpret_cast<const float*>(&v);
+  const unsigned short u = *reinterpret_cast<const unsigned short*>(&v);
+  return std::is_same<T, __half>::value ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Outputs of row n and `tokens` tokens from token0 on (xs: their scales, one a lane). The type is settled outside: 96
+// times a choice of three types, code that no cache of instructions holds, took longer than a tile's products.
+template <typename T>
+__device__ __forceinline__ void put_outputs(const TcArgs& a, const int (&sum)[96], const float (&xs)[3], float scale,
+                                            float bias, int n, int token0, int tokens) {
+  const bool in = n < a.n;
+  T* y = static_cast<T*>(a.y.ptr) + token0 * a.y.row_stride + n;
+  if (a.residual.ptr) {
+    const T* res = static_cast<const T*>(a.residual.ptr) + token0 * a.residual.row_stride + n;
+#pragma unroll
+    for (int b = 0; b < 96; b += 8) {
+      T r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (in && b + i < tokens) r[i] = __ldcg(res + i * a.residual.row_stride);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[(b + i) / 32], (b + i) % 32);
+        if (in && b + i < tokens) *y = from_float<T>(__fadd_rn(l8_value(sum[b + i], scale, x_scale, bias), as_float(r[i])));
+        y += a.y.row_stride;
+      }
+      res += 8 * a.residual.row_stride;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 96; ++i) {
+      const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[i / 32], i % 32);
+      if (in && i < tokens) *y = from_float<T>(l8_value(sum[i], scale, x_scale, bias));
+      y += a.y.row_stride;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_lin8_tc(const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t dyn_smem[];
@@ -336,10 +384,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         epilogue_barrier();
         // clusters that share the tile: those whose steps reach into it
         const long long units = (long long)a.left * a.steps, begin = (long long)left * a.steps, end = begin + a.steps;
-        int from = (int)(begin * a.parted / units), to = (int)((end - 1) * a.parted / units);
+        int from = cluster, to = cluster;   // a few each way
         while (units * from / a.parted > begin) --from;
-        while (units * (from + 1) / a.parted <= begin) ++from;
-        while (units * to / a.parted >= end) --to;
         while (units * (to + 1) / a.parted < end) ++to;
         if (warp == kEpiWarp0 && lane == 0) {
           unsigned long long* word = a.tickets + left * CG + rank;
@@ -366,16 +412,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < 3; ++i) xs[i] = token0 + 32 * i + lane < a.B ? __ldcg(a.x_scales + token0 + 32 * i + lane) : 0.f;
       const int tokens = min(nb * 16, a.B - token0);
-#pragma unroll
-      for (int i = 0; i < 96; ++i) {
-        const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[i / 32], i % 32);
-        if (i < tokens && n < a.n) {
-          const int token = token0 + i;
-          float v = l8_value(sum[i], scale, x_scale, bias);
-          if (a.residual.ptr) v = __fadd_rn(v, ld_elem(a.residual.ptr, token * a.residual.row_stride + n, a.dtype));
-          st_elem(a.y.ptr, token * a.y.row_stride + n, v, a.dtype);
-        }
-      }
+      if (a.dtype == SFFN_F32)
+        put_outputs<float>(a, sum, xs, scale, bias, n, token0, tokens);
+      else if (a.dtype == SFFN_F16)
+        put_outputs<__half>(a, sum, xs, scale, bias, n, token0, tokens);
+      else
+        put_outputs<__nv_bfloat16>(a, sum, xs, scale, bias, n, token0, tokens);
       __syncwarp();
     }
   } else {
