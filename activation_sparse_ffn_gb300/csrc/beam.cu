@@ -1,24 +1,30 @@
 // The best continuations over beams and vocabulary.
 //
-// k_beam_rows reads every logit once: a block takes a chunk of one row into
-// registers, sums its exponentials and keeps its n_out best. k_beam_merge, a
-// block for each search, joins the sums of a row, turns the kept logits into
-// totals and picks the n_out best of those.
+// k_beam_rows reads every logit once: a block takes a part of one row, a chunk
+// at a time with the next on its way, sums the exponentials and keeps the n_out
+// best so far. k_beam_merge, a block for each search, joins the sums of a row,
+// turns the kept logits into totals and picks the n_out best of those.
 //
-// Sums of exponentials. exp(z) = 2^(z log2 e); the reference that a chunk takes
-// off is a whole number R near the largest z log2 e, so that sums of different
-// chunks are brought together by a power of two, exactly. log2 e is carried by
-// two floats: one alone is off by 2^-26 of itself, which a logit of 20 makes
-// 2^-21. Above |z| = 2^22 a whole number no longer lies near enough; the
-// chunk's largest z is the reference there.
+// Sums of exponentials. exp(z) = 2^(z log2 e); the reference that a thread takes
+// off is a whole number R near its largest z log2 e, so that sums are brought
+// together by powers of two, exactly. log2 e rounded to a float is off by 2^-26
+// of itself, which a logit of 20 makes 2^-21; what the rounding left is put right
+// for the part's largest z at the end, by one product. Above |z| = 2^22 a
+// whole number no longer lies near enough: such a part is summed again, its
+// largest z the reference.
 //
-// The n_out best of a chunk. The n_out-th largest of the threads' own maxima
-// bounds the n_out-th largest element from below; a binary search over the upper
-// bits of their ordered patterns finds it nearly, and the few elements that
-// reach it go to a list, where each counts those ahead of it. Where too many are
-// equal for the list, a search over all bits and then over indices takes exactly
-// the first of them.
+// The n_out best. A bound that at least n_out elements of the first chunk reach,
+// and few others: the ceil(n_out / 8)-th largest of the lanes' own maxima, in
+// each of eight warps, and the least of those over the warps. What reaches it
+// goes to a list, of every chunk, with no barrier between them. At the end the
+// same is done with the list, and each of the few that are left counts those
+// ahead of it. (Keeping the n_out best in order after every chunk took 40 us of
+// 32 x 8 rows of 131072 bf16 logits, most of it at barriers.) Where too many
+// reach the bound for the list, a search over all bits and then over indices,
+// which reads the logits again, takes exactly the first of them.
 #include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include "rows_io.cuh"
 #include "step.h"
@@ -31,7 +37,10 @@ constexpr int kThreads = 256;
 constexpr int kMergeThreads = 512;
 constexpr int kMaxOut = 64;
 constexpr int kMaxBeams = 64;
-constexpr int kList = 2048;   // (kMaxOut - 1) * 32 elements of fewer than kMaxOut threads always fit
+constexpr int kList = 2048;
+constexpr int kRuns = 2;      // times 16 bytes of a chunk that a thread holds, and as many on their way
+constexpr int kRowBlocks = 6; // of an SM
+constexpr int kRanked = 256;  // entries that are put in order by counting
 
 struct BeamArgs {
   sffn_rows logits;
@@ -42,9 +51,9 @@ struct BeamArgs {
   int32_t* out_tokens;
   uint32_t* err;
   // workspace: sums of each row's chunks, and their candidates
-  float4* sums;    // [rows][chunks]: reference, sum, mode, -
-  int2* found;     // [rows][chunks][n_out]: logit, token; token -1: none
-  int vocab, beams, n_out, batch, end_token, dtype, chunks;
+  float4* sums;    // [rows][parts]: reference, sum, mode, largest logit
+  int2* found;     // [rows][parts][n_out]: logit, token; token -1: none
+  int vocab, beams, n_out, batch, end_token, dtype, parts, chunks;   // parts of a row, chunks of one
   bool vec;
 };
 
@@ -58,17 +67,30 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 
+// The number of a pattern.
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
+template <typename T>
+__device__ __forceinline__ float lowest() {   // finite
+  return sizeof(T) == 4 ? -3.402823466e38f : std::is_same<T, __half>::value ? -65504.f : -3.3895313892515355e38f;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-constexpr float kLog2eHi = 1.44269502f;        // log2(e) rounded
-constexpr float kLog2eLo = 1.92596303e-8f;     // and what that left
+// 2^d of a whole number d up to 0; 0 far below it.
+__device__ __forceinline__ float power_of_two(float d) {
+  return d < -126.f ? 0.f : __int_as_float((127 + (int)fminf(d, 0.f)) << 23);
+}
+
+constexpr float kLog2eHi = 1.44269502f;           // log2(e) rounded
+constexpr double kLeftOver = 1.33497581575e-8;     // (log2(e) - kLog2eHi) * ln 2
+constexpr double kLn2 = 0.6931471805599453;
 constexpr float kWholeLimit = 0x1p22f;
 
-enum ChunkMode { kNothing = 0, kWhole = 1, kOwnMax = 2, kBad = 3 };
+enum PartMode { kNothing = 0, kWhole = 1, kOwnMax = 2, kBad = 3 };
 
 template <typename V>
 __device__ __forceinline__ V block_sum(V v, V* red) {
@@ -95,17 +117,132 @@ __device__ __forceinline__ uint32_t reached(uint32_t best, int want) {
   return t;
 }
 
-template <typename T, int EPT>
-__global__ void __launch_bounds__(kThreads) k_beam_rows(const BeamArgs a) {
-  constexpr int N = 16 / sizeof(T), RUNS = EPT / N;
-  __shared__ float red[32];
-  __shared__ int s_count, s_int[32];
-  __shared__ float s_value[kList];
-  __shared__ int s_token[kList];
+// The want-th largest pattern among the lanes of a warp (want of 1 to 32; 0 counts as none).
+__device__ __forceinline__ uint32_t nth_largest(uint32_t best, int want) {
+  uint32_t t = 0;
+  for (int i = 0; i < want; ++i) {
+    t = __reduce_max_sync(SFFN_FULL_MASK, best);
+    const unsigned who = __ballot_sync(SFFN_FULL_MASK, best == t);
+    if ((threadIdx.x & 31) == __ffs(who) - 1) best = 0;
+  }
+  return t;
+}
+
+// Elements of a row by their index, for the rare paths.
+struct Range {
+  const void* p;
+  size_t row;
+  int from, to, dtype;
+  __device__ __forceinline__ float at(int token) const { return ld_elem(p, row + token, dtype); }
+};
+
+// The first n_out of a range by (value, index), to the list; all threads of the block.
+__device__ __noinline__ void exact_best(const Range c, int n_out, float* value, int* token, int* count, int* red) {
+  const int tid = threadIdx.x;
+  auto reach = [&](uint32_t t, int last) {   // elements above t, or at t up to index `last`
+    int n = 0;
+    for (int i = c.from + tid; i < c.to; i += kThreads) {
+      const float z = c.at(i);
+      const uint32_t o = ordered(z);
+      n += z > -INFINITY && (o > t || (o == t && i <= last));
+    }
+    return block_sum(n, red);
+  };
+  uint32_t t = 0;
+  for (int b = 31; b >= 0; --b)
+    if (reach(t | 1u << b, INT_MAX) >= n_out) t |= 1u << b;
+  int last = 0;   // the smallest index with which there are enough
+  for (int b = 30; b >= 0; --b)
+    if (reach(t, last + (1 << b) - 1) < n_out) last += 1 << b;
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  for (int i = c.from + tid; i < c.to; i += kThreads) {
+    const float z = c.at(i);
+    const uint32_t o = ordered(z);
+    if (z > -INFINITY && (o > t || (o == t && i <= last))) {
+      const int k = atomicAdd(count, 1);
+      if (k < kList) value[k] = z, token[k] = i;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+constexpr int type_of() {
+  return sizeof(T) == 4 ? SFFN_F32 : std::is_same<T, __half>::value ? SFFN_F16 : SFFN_BF16;
+}
+
+// Element j of 16 bytes.
+template <typename T>
+__device__ __forceinline__ float element(const uint4& v, int j) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (sizeof(T) == 4) return __uint_as_float(w[j & 3]);
+  const uint32_t u = w[(j >> 1) & 3];
+  if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)(j & 1 ? u >> 16 : u)));
+  return __uint_as_float(j & 1 ? u & 0xffff0000u : u << 16);
+}
+
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Largest logit of a range and, relative to it, the sum of exponentials: for logits that are far from 0, or none.
+__device__ __noinline__ float2 far_sum(const Range c, float* red) {
+  float m = -INFINITY, sum = 0.f;
+  for (int i = c.from + threadIdx.x; i < c.to; i += kThreads) m = fmaxf(m, c.at(i));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(SFFN_FULL_MASK, m, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
+  for (int i = c.from + threadIdx.x; i < c.to; i += kThreads) sum += exp2_fast((c.at(i) - m) * kLog2eHi);
+  __syncthreads();
+  return make_float2(m, block_sum(sum, red));
+}
+
+// Largest element of 16 bytes; NaN aside.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    using P = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+    const P m = __hmax2(__hmax2(*reinterpret_cast<const P*>(&v.x), *reinterpret_cast<const P*>(&v.y)),
+                        __hmax2(*reinterpret_cast<const P*>(&v.z), *reinterpret_cast<const P*>(&v.w)));
+    return fmaxf(to_float(m.x), to_float(m.y));
+  }
+}
+
+// Which elements of 16 bytes reach `bound`, a value of their type: bit p for element 2 p and bit 16 + p for 2 p + 1, or bit
+// j for element j of fp32, shifted up by `at`.
+template <typename T>
+__device__ __forceinline__ uint32_t which_reach(const uint4& v, float bound, int at) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    if constexpr (sizeof(T) == 4) {
+      if (__uint_as_float(w[p]) >= bound) m |= 1u << (at + p);
+    } else {
+      using P = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+      P b;
+      if constexpr (std::is_same<T, __half>::value) b = __float2half2_rn(bound); else b = __float2bfloat162_rn(bound);
+      m |= __hge2_mask(*reinterpret_cast<const P*>(&w[p]), b) & (0x10001u << (at + p));
+    }
+  }
+  return m;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamArgs a) {
+  constexpr int N = 16 / sizeof(T), kWarps = kThreads / 32, kChunk = kThreads * kRuns * N;
+  __shared__ float s_red[32], s_value[kList], s_best[kRanked];
+  __shared__ int s_token[kList], s_at[kRanked], s_int[32], s_count, s_left;
+  __shared__ uint32_t s_bound[kWarps];
   pdl_launch_dependents();
   pdl_wait();
-  const int row = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x;
-  const size_t slot = (size_t)row * a.chunks + chunk;
+  const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const size_t slot = (size_t)row * a.parts + part;
   int2* found = a.found + slot * a.n_out;
   const float score = __ldcg(a.scores + row);
   if (!(fabsf(score) < INFINITY) || (a.done && __ldcg(a.done + row))) {   // its logits are not looked at
@@ -113,209 +250,275 @@ __global__ void __launch_bounds__(kThreads) k_beam_rows(const BeamArgs a) {
     for (int i = tid; i < a.n_out; i += kThreads) found[i] = make_int2(0, -1);
     return;
   }
-  const int at0 = chunk * (kThreads * EPT) + tid * N;
-  float z[EPT];
+  const int c0 = (int)((long long)a.chunks * part / a.parts), c1 = (int)((long long)a.chunks * (part + 1) / a.parts);
+  const size_t base = row * a.logits.row_stride;
+  auto load = [&](int c, uint4* v) {
 #pragma unroll
-  for (int r = 0; r < RUNS; ++r) {
-    const int at = at0 + r * kThreads * N, left = a.vocab - at;
-    const size_t i = row * a.logits.row_stride + at;
-    if (a.vec && left >= N) {
-      ld_run<N>(a.logits.ptr, i, sizeof(T) == 4 ? SFFN_F32 : std::is_same<T, __half>::value ? SFFN_F16 : SFFN_BF16,
-                z + r * N);
-    } else {
+    for (int r = 0; r < kRuns; ++r) {
+      const int at = c * kChunk + (r * kThreads + tid) * N, left = a.vocab - at;
+      if (a.vec && left >= N) {
+        v[r] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits.ptr) + base + at));
+      } else {
+        uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < N; ++j) z[r * N + j] = j < left ? ld_elem(a.logits.ptr, i + j, a.dtype) : -INFINITY;
+        for (int k = 0; k < 4; ++k) {
+          if (sizeof(T) == 4) {
+            w[k] = k < left ? __ldcg(static_cast<const uint32_t*>(a.logits.ptr) + base + at + k) : 0xff800000u;
+          } else {
+            const unsigned short* p = static_cast<const unsigned short*>(a.logits.ptr) + base + at + 2 * k;
+            const uint32_t none = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+            w[k] = (2 * k < left ? __ldcg(p) : none) | (2 * k + 1 < left ? __ldcg(p + 1) : none) << 16;
+          }
+        }
+        v[r] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-  }
-  // -- largest, and whether anything is no number
-  float top = -INFINITY;
-  bool bad = false;
+  };
+  if (tid == 0) s_count = s_left = 0;
+  uint4 v[kRuns];
+  load(c0, v);
+  // of this thread; until something is above -2^22 the reference is there, and nothing adds to the sum
+  float ref = -kWholeLimit, most = -INFINITY;
+  float2 sum2 = make_float2(0.f, 0.f);
+  uint32_t bound = 0;   // what an element has to reach
+  for (int c = c0; c < c1; ++c) {
+    uint4 nv[kRuns];
+    if (c + 1 < c1) load(c + 1, nv);
+    float top = largest<T>(v[0]);
 #pragma unroll
-  for (int j = 0; j < EPT; ++j) top = fmaxf(top, z[j]), bad |= !(z[j] < INFINITY);
-  const uint32_t best = ordered(top);
-  const uint32_t wtop = __reduce_max_sync(SFFN_FULL_MASK, best);
-  if (tid == 0) s_count = 0;
-  if ((tid & 31) == 0) s_int[tid >> 5] = (int)wtop;
-  bad = __syncthreads_or(bad);
-  const int lane = tid & 31;
-  const uint32_t btop = __reduce_max_sync(SFFN_FULL_MASK, lane < kThreads / 32 ? (uint32_t)s_int[lane] : 0u);
-  const float m = __uint_as_float(btop & 0x80000000u ? btop ^ 0x80000000u : ~btop);
-  if (bad || m == -INFINITY) {
-    if (tid == 0) a.sums[slot] = make_float4(0.f, 0.f, (float)(bad ? kBad : kNothing), 0.f);
-    for (int i = tid; i < a.n_out; i += kThreads) found[i] = make_int2(0, -1);
-    return;
-  }
-  // -- sum of exponentials
-  const bool whole = fabsf(m) <= kWholeLimit;
-  const float ref = whole ? rintf(m * kLog2eHi) : m;
-  float sum = 0.f;
-  if (whole) {
-#pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-      // a masked logit: -infinity in the first product, nothing in the sum
-      const float x = fmaf(z[j], kLog2eHi, -ref);
-      sum += exp2_fast(z[j] == -INFINITY ? -INFINITY : fmaf(z[j], kLog2eLo, x));
+    for (int r = 1; r < kRuns; ++r) top = fmaxf(top, largest<T>(v[r]));
+    // -- sum of exponentials; a masked logit's is 0, that of no number is none
+    if (top > most) {
+      const float near = rintf(top * kLog2eHi);
+      if (top >= -kWholeLimit && (most < -kWholeLimit || near > ref + 64.f)) {
+        const float down = power_of_two(ref - near);
+        sum2.x *= down, sum2.y *= down, ref = near;
+      }
+      most = top;
     }
-  } else {
-    for (int j = 0; j < EPT; ++j) sum += exp2_fast((z[j] - m) * kLog2eHi);
-  }
-  sum = block_sum(sum, red);
-  if (tid == 0) a.sums[slot] = make_float4(ref, sum, (float)(whole ? kWhole : kOwnMax), 0.f);
-  // -- the n_out best
-  uint32_t bound = reached<16>(best, a.n_out);
+    const float2 hi = make_float2(kLog2eHi, kLog2eHi), off = make_float2(-ref, -ref);
 #pragma unroll
-  for (int j = 0; j < EPT; ++j)
-    if (ordered(z[j]) >= bound && z[j] > -INFINITY) {
-      const int n = atomicAdd(&s_count, 1);
-      if (n < kList) s_value[n] = z[j], s_token[n] = at0 + (j / N) * kThreads * N + j % N;
+    for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 x = __ffma2_rn(make_float2(element<T>(v[r], j), element<T>(v[r], j + 1)), hi, off);
+        sum2 = __fadd2_rn(sum2, make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+      }
+    // -- what may be among the best
+    const uint32_t best = top > -INFINITY ? ordered(top) : 0u;
+    if (bound == 0) {   // at the first chunk, and until one has enough elements; before that, everything goes
+      const uint32_t wbound = nth_largest(best, (a.n_out + kWarps - 1) / kWarps);
+      __syncthreads();
+      if (lane == 0) s_bound[warp] = wbound;
+      __syncthreads();
+      bound = ~0u;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) bound = min(bound, s_bound[w]);
     }
+    if (best >= bound && best) {
+      // their places only: values are fetched again at the end. With no bound yet, what is not masked.
+      const float from = bound ? value_of(bound) : lowest<T>();
+      uint32_t hits = 0;
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) hits |= which_reach<T>(v[r], from, 4 * r);
+      while (hits) {
+        const int bit = __ffs(hits) - 1, p = bit & 15;
+        hits &= hits - 1;
+        const int j = sizeof(T) == 4 ? p & 3 : 2 * (p & 3) + (bit >> 4);
+        const int n = atomicAdd(&s_count, 1);
+        if (n < kList) s_token[n] = c * kChunk + ((p >> 2) * kThreads + tid) * N + j;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) v[r] = nv[r];
+  }
   __syncthreads();
   int n = s_count;
   if (n > kList) {
-    // too many equal ones: the first of them by index
-    auto count = [&](uint32_t t, int last) {   // elements above t, or at t up to index `last`
-      int c = 0;
-      for (int j = 0; j < EPT; ++j) {
-        const uint32_t o = ordered(z[j]);
-        c += z[j] > -INFINITY && (o > t || (o == t && at0 + (j / N) * kThreads * N + j % N <= last));
-      }
-      return block_sum(c, s_int);
-    };
-    uint32_t t = 0;
-    for (int b = 31; b >= 0; --b)
-      if (count(t | 1u << b, INT_MAX) >= a.n_out) t |= 1u << b;
-    int last = 0;   // the smallest index with which there are enough
-    for (int b = 30; b >= 0; --b)
-      if (count(t, last + (1 << b) - 1) < a.n_out) last += 1 << b;
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    for (int j = 0; j < EPT; ++j) {
-      const uint32_t o = ordered(z[j]);
-      const int token = at0 + (j / N) * kThreads * N + j % N;
-      if (z[j] > -INFINITY && (o > t || (o == t && token <= last))) {
-        const int k = atomicAdd(&s_count, 1);
-        if (k < kList) s_value[k] = z[j], s_token[k] = token;
-      }
-    }
-    __syncthreads();
+    const Range all = {a.logits.ptr, base, c0 * kChunk, min(c1 * kChunk, a.vocab), a.dtype};
+    exact_best(all, a.n_out, s_value, s_token, &s_count, s_int);
     n = min(s_count, kList);
+  } else {
+    for (int i = tid; i < n; i += kThreads) s_value[i] = ld_elem(a.logits.ptr, base + s_token[i], a.dtype);
+    __syncthreads();
   }
+  // -- a bound for the list: of the warps whose lanes all have an entry of it
+  const int warps = min(kWarps, n / 32), want = warps ? (a.n_out + warps - 1) / warps : 33;
+  uint32_t best = 0, least = 0;
+  for (int i = tid; i < n; i += kThreads) best = max(best, ordered(s_value[i]));
+  if (want <= 32 && n > 48) {
+    const uint32_t wbound = nth_largest(best, want);
+    if (lane == 0) s_bound[warp] = wbound;
+    __syncthreads();
+    least = ~0u;
+    for (int w = 0; w < warps; ++w) least = min(least, s_bound[w]);
+  }
+  for (int i = tid; i < n; i += kThreads)
+    if (ordered(s_value[i]) >= least) {
+      const int k = atomicAdd(&s_left, 1);
+      if (k < kRanked) s_best[k] = s_value[i], s_at[k] = s_token[i];
+    }
+  __syncthreads();
+  const bool few = s_left <= kRanked;   // else the list itself is put in order
+  const float* value = few ? s_best : s_value;
+  const int* token = few ? s_at : s_token;
+  n = few ? s_left : n;
   for (int i = tid; i < n; i += kThreads) {
-    const float v = s_value[i];
-    const int token = s_token[i];
+    const float z = value[i];
+    const int t = token[i];
     int ahead = 0;
-    for (int k = 0; k < n; ++k) ahead += s_value[k] > v || (s_value[k] == v && s_token[k] < token);
-    if (ahead < a.n_out) found[ahead] = make_int2(__float_as_int(v), token);
+    for (int k = 0; k < n; ++k) ahead += value[k] > z || (value[k] == z && token[k] < t);
+    if (ahead < a.n_out) found[ahead] = make_int2(__float_as_int(z), t);
   }
   for (int i = n + tid; i < a.n_out; i += kThreads) found[i] = make_int2(0, -1);
+  // -- the block's sum, relative to the largest reference
+  float bref = most >= -kWholeLimit ? ref : -INFINITY, bmost = most;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    bref = fmaxf(bref, __shfl_xor_sync(SFFN_FULL_MASK, bref, o));
+    bmost = fmaxf(bmost, __shfl_xor_sync(SFFN_FULL_MASK, bmost, o));
+  }
+  if (lane == 0) s_red[warp] = bref, s_red[kWarps + warp] = bmost;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) bref = fmaxf(bref, s_red[w]), bmost = fmaxf(bmost, s_red[kWarps + w]);
+  __syncthreads();
+  float sum = block_sum((sum2.x + sum2.y) * power_of_two(ref - bref), s_red);
+  int mode = bmost == -INFINITY ? kNothing : kWhole;
+  if (fabsf(bmost) > kWholeLimit && mode == kWhole) {
+    const Range all = {a.logits.ptr, base, c0 * kChunk, min(c1 * kChunk, a.vocab), a.dtype};
+    const float2 f = far_sum(all, s_red);
+    bref = bmost = f.x, sum = f.y, mode = kOwnMax;
+  }
+  if (sum != sum || bmost == INFINITY) mode = kBad;
+  if (tid == 0) a.sums[slot] = make_float4(bref, sum, (float)mode, bmost);
 }
 
 __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) {
-  __shared__ double s_lse[kMaxBeams];   // log of the row's sum
-  __shared__ double s_score[kMaxBeams];    // -infinity: no candidates
-  __shared__ bool s_done[kMaxBeams];
+  constexpr int kWarps = kMergeThreads / 32;
+  __shared__ double s_lse[kMaxBeams];      // log of the row's sum
+  __shared__ double s_sum[kMaxBeams], s_ref[kMaxBeams];
+  __shared__ float s_score[kMaxBeams];     // -infinity: no candidates
+  __shared__ int s_done[kMaxBeams];
   __shared__ int s_int[32], s_count;
   __shared__ double s_total[kList];
   __shared__ int s_place[kList][2];
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // -- a warp for each row
-  for (int j = warp; j < a.beams; j += kMergeThreads / 32) {
+  // -- a warp for each row: its sum, as a power of two or a logarithm times a number
+  for (int j = warp; j < a.beams; j += kWarps) {
     const int row = b * a.beams + j;
     const float score = __ldcg(a.scores + row);
     const bool ended = a.done && __ldcg(a.done + row);
-    double lse = -INFINITY;
     bool bad = !(score < INFINITY);
+    double sum = 0.0, ref = 0.0;
     if (!ended && fabsf(score) < INFINITY) {
-      const float4* sums = a.sums + (size_t)row * a.chunks;
-      float ref = -INFINITY;
+      const float4* sums = a.sums + (size_t)row * a.parts;
+      float top = -INFINITY, peak = -INFINITY;
       bool own = false;
-      for (int c = lane; c < a.chunks; c += 32) {
+      for (int c = lane; c < a.parts; c += 32) {
         const float4 s = __ldcg(sums + c);
         bad |= s.z == (float)kBad, own |= s.z == (float)kOwnMax;
+        if (s.z == (float)kWhole) top = fmaxf(top, s.x), peak = fmaxf(peak, s.w);
       }
       own = __any_sync(SFFN_FULL_MASK, own), bad = __any_sync(SFFN_FULL_MASK, bad);
-      // references in the same measure: whole powers of two, or logits where some chunk has its own largest
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float4 s = __ldcg(sums + c);
-        if (s.z != (float)kNothing) ref = fmaxf(ref, own && s.z == (float)kWhole ? s.x * 0.693147181f : s.x);
-      }
+      if (!own) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(SFFN_FULL_MASK, ref, o));
-      double sum = 0.0;
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float4 s = __ldcg(sums + c);
-        if (s.z == (float)kNothing || bad) continue;
-        if (!own)
-          sum += scalbn((double)s.y, max((int)(s.x - ref), -1000));
-        else
-          sum += s.y * exp((s.z == (float)kWhole ? s.x * 0.6931471805599453 : (double)s.x) - ref);
+        for (int o = 16; o; o >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(SFFN_FULL_MASK, top, o));
+          peak = fmaxf(peak, __shfl_xor_sync(SFFN_FULL_MASK, peak, o));
+        }
+        for (int c = lane; c < a.parts; c += 32) {
+          const float4 s = __ldcg(sums + c);
+          if (s.z == (float)kWhole)
+            sum += (double)(s.y * power_of_two(s.x - top)) * (1.0 + (s.w - peak) * kLeftOver);
+        }
+        ref = top * kLn2 + peak * kLeftOver;
+      } else {
+        // some part's own largest is its reference: in the measure of logits
+        double most = -INFINITY;
+        for (int c = lane; c < a.parts; c += 32) {
+          const float4 s = __ldcg(sums + c);
+          if (s.z != (float)kNothing) most = fmax(most, s.z == (float)kWhole ? s.x * kLn2 : (double)s.x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(SFFN_FULL_MASK, most, o));
+        for (int c = lane; c < a.parts; c += 32) {
+          const float4 s = __ldcg(sums + c);
+          if (s.z != (float)kNothing) sum += s.y * exp((s.z == (float)kWhole ? s.x * kLn2 : (double)s.x) - most);
+        }
+        ref = most;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(SFFN_FULL_MASK, sum, o);
-      if (!bad && sum > 0.0) lse = (own ? (double)ref : ref * 0.6931471805599453) + log(sum);
     }
     if (lane == 0) {
-      s_lse[j] = lse, s_score[j] = bad || (!ended && lse == -INFINITY) ? -INFINITY : score, s_done[j] = ended;
+      s_sum[j] = sum, s_ref[j] = ref, s_done[j] = ended;
+      s_score[j] = bad || (!ended && !(sum > 0.0)) ? -INFINITY : score;
       if (bad) set_device_error(a.err, SFFN_ERR_DEVICE);
     }
   }
   if (tid == 0) s_count = 0;
   __syncthreads();
-  // -- candidates: those found in chunks, and the last places of sequences that have ended
-  const int per_row = a.chunks * a.n_out, entries = a.beams * per_row;
-  const int2* found = a.found + (size_t)b * entries;
-  auto total = [&](int e, int& j, int& token) {   // NaN: none
-    j = e / per_row;
-    if (s_done[j]) {
-      token = a.end_token;
-      return e == j * per_row && s_score[j] > -INFINITY ? s_score[j] : nan("");
+  // logarithms in 64 bits, a lane each: every warp that does one takes a microsecond of the SM
+  for (int j = tid; j < a.beams; j += kMergeThreads) s_lse[j] = s_ref[j] + log(s_sum[j]);
+  __syncthreads();
+  // -- candidates: those found in chunks, and the last places of sequences that have ended. Warps share a row's.
+  const int per_row = a.parts * a.n_out, parts = max(1, kWarps / a.beams);
+  const int2* found = a.found + (size_t)b * a.beams * per_row;
+  auto each = [&](auto&& take) {   // take(j, token, logit)
+    for (int i = warp; i < a.beams * parts; i += kWarps) {
+      const int j = i / parts, part = i - j * parts;
+      if (s_score[j] == -INFINITY) continue;
+      if (s_done[j]) {
+        if (part == 0 && lane == 0) take(j, a.end_token, 0.f);
+        continue;
+      }
+      for (int e = part * 32 + lane; e < per_row; e += parts * 32) {
+        const int2 f = __ldcg(found + (size_t)j * per_row + e);
+        if (f.y >= 0) take(j, f.y, __int_as_float(f.x));
+      }
     }
-    const int2 f = __ldcg(found + e);
-    token = f.y;
-    return token < 0 || s_score[j] == -INFINITY ? nan("") : (__int_as_float(f.x) - s_lse[j]) + s_score[j];
   };
-  int j, token;
+  auto total = [&](int j, float z) { return s_done[j] ? (double)s_score[j] : (z - s_lse[j]) + s_score[j]; };
   uint32_t best = 0;
-  for (int e = tid; e < entries; e += kMergeThreads) {
-    const double v = total(e, j, token);
-    if (v == v) best = max(best, ordered((float)v));
-  }
-  const uint32_t bound = reached<24>(best, a.n_out);
-  for (int e = tid; e < entries; e += kMergeThreads) {
-    const double v = total(e, j, token);
-    if (v == v && ordered((float)v) >= bound) {
+  each([&](int j, int, float z) { best = max(best, ordered((float)total(j, z))); });
+  const uint32_t bound = reached<20>(best, a.n_out);
+  each([&](int j, int token, float z) {
+    const double v = total(j, z);
+    if (ordered((float)v) >= bound) {
       const int n = atomicAdd(&s_count, 1);
       if (n < kList) s_total[n] = v, s_place[n][0] = j, s_place[n][1] = token;
     }
-  }
+  });
   __syncthreads();
   int n = s_count;
   if (n > kList) {
-    auto count = [&](unsigned long long t, long long last) {
+    auto reach = [&](unsigned long long t, long long last) {
       int c = 0;
-      for (int e = tid; e < entries; e += kMergeThreads) {
-        const double v = total(e, j, token);
-        if (v == v) c += ordered(v) > t || (ordered(v) == t && (long long)j * a.vocab + token <= last);
-      }
+      each([&](int j, int token, float z) {
+        const unsigned long long o = ordered(total(j, z));
+        c += o > t || (o == t && (long long)j * a.vocab + token <= last);
+      });
       return block_sum(c, s_int);
     };
     unsigned long long t = 0;
     for (int i = 63; i >= 0; --i)
-      if (count(t | 1ull << i, LLONG_MAX) >= a.n_out) t |= 1ull << i;
+      if (reach(t | 1ull << i, LLONG_MAX) >= a.n_out) t |= 1ull << i;
     long long last = 0;
     for (int i = 32; i >= 0; --i)
-      if (count(t, last + (1ll << i) - 1) < a.n_out) last += 1ll << i;
+      if (reach(t, last + (1ll << i) - 1) < a.n_out) last += 1ll << i;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    for (int e = tid; e < entries; e += kMergeThreads) {
-      const double v = total(e, j, token);
-      if (v == v && (ordered(v) > t || (ordered(v) == t && (long long)j * a.vocab + token <= last))) {
+    each([&](int j, int token, float z) {
+      const double v = total(j, z);
+      const unsigned long long o = ordered(v);
+      if (o > t || (o == t && (long long)j * a.vocab + token <= last)) {
         const int k = atomicAdd(&s_count, 1);
         if (k < kList) s_total[k] = v, s_place[k][0] = j, s_place[k][1] = token;
       }
-    }
+    });
     __syncthreads();
     n = min(s_count, kList);
   }
@@ -334,32 +537,30 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
     a.out_scores[out + i] = -INFINITY, a.out_parents[out + i] = 0, a.out_tokens[out + i] = 0;
 }
 
-// Elements of a thread: few, so that a small call has blocks for every SM; more where there are rows enough.
-int elements(const sffn_beam& H, int batch) {
-  const long long cells = (long long)batch * H.desc.beams * H.desc.vocab;
-  int ept = 8;
-  while (ept < 32 && cells > (long long)H.num_sms * 8 * kThreads * ept) ept *= 2;
-  return ept;
+// Parts of a row: as many as give every SM its blocks in one wave, a chunk at least each.
+struct Split {
+  int chunks, parts;
+};
+Split split_of(const sffn_beam& H, int batch, int elem) {
+  Split s;
+  s.chunks = (H.desc.vocab + kThreads * kRuns * 16 / elem - 1) / (kThreads * kRuns * 16 / elem);
+  s.parts = std::min(s.chunks, std::max(1, H.num_sms * kRowBlocks / (batch * H.desc.beams)));
+  return s;
 }
-int chunks_of(const sffn_beam& H, int ept) { return (H.desc.vocab + kThreads * ept - 1) / (kThreads * ept); }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename T>
-cudaError_t launch_rows(const BeamArgs& a, int ept, cudaStream_t st) {
-  auto kern = ept == 8 ? k_beam_rows<T, 8> : ept == 16 ? k_beam_rows<T, 16> : k_beam_rows<T, 32>;
-  return launch_ex(kern, dim3(a.chunks, a.batch * a.beams), dim3(kThreads), 0, st, true, 1, a);
+cudaError_t launch_rows(const BeamArgs& a, cudaStream_t st) {
+  return launch_ex(k_beam_rows<T>, dim3(a.parts, a.batch * a.beams), dim3(kThreads), 0, st, true, 1, a);
 }
 
 }  // namespace
 
-// Enough for every smaller batch too, whose rows may be cut into more chunks.
+// Enough for every smaller batch too, whose rows are cut into more parts: rows times parts is at most what fills the SMs
+// once, or the rows.
 size_t beam_ws_bytes(const sffn_beam& H, int batch) {
-  size_t most = 0;
-  for (int ept = 8; ept <= 32; ept *= 2) {
-    const long long cells = (long long)H.desc.beams * H.desc.vocab, limit = (long long)H.num_sms * 8 * kThreads * ept;
-    const long long b = ept == 32 ? batch : std::min((long long)batch, std::max(1ll, limit / cells));
-    most = std::max(most, (size_t)b * H.desc.beams * chunks_of(H, ept));
-  }
+  const size_t rows = (size_t)batch * H.desc.beams;
+  size_t most = std::max(rows, std::min((size_t)H.num_sms * kRowBlocks, rows * split_of(H, 1, 4).chunks));
   return up256(most * sizeof(float4)) + up256(most * H.desc.n_out * sizeof(int2));
 }
 
@@ -367,20 +568,20 @@ cudaError_t launch_beam(const sffn_beam& H, const sffn_rows& logits, const float
                         int end_token, int batch, float* out_scores, int32_t* out_parents, int32_t* out_tokens,
                         int dtype, void* ws, cudaStream_t st) {
   BeamArgs a = {};
-  const int ept = elements(H, batch);
+  const int elem = dtype == SFFN_F32 ? 4 : 2;
+  const Split s = split_of(H, batch, elem);
   a.logits = logits, a.scores = scores, a.done = done, a.out_scores = out_scores, a.out_parents = out_parents;
   a.out_tokens = out_tokens, a.err = H.err;
   a.vocab = H.desc.vocab, a.beams = H.desc.beams, a.n_out = H.desc.n_out, a.batch = batch, a.end_token = end_token;
-  a.dtype = dtype, a.chunks = chunks_of(H, ept);
-  const size_t slots = (size_t)batch * a.beams * a.chunks;
+  a.dtype = dtype, a.chunks = s.chunks, a.parts = s.parts;
+  const size_t slots = (size_t)batch * a.beams * a.parts;
   a.sums = static_cast<float4*>(ws);
   a.found = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + up256(slots * sizeof(float4)));
-  const int elem = dtype == SFFN_F32 ? 4 : 2;
   a.vec = reinterpret_cast<uintptr_t>(logits.ptr) % 16 == 0 &&
           ((long long)batch * a.beams <= 1 || logits.row_stride * elem % 16 == 0);
-  cudaError_t e = dtype == SFFN_F32   ? launch_rows<float>(a, ept, st)
-                  : dtype == SFFN_F16 ? launch_rows<__half>(a, ept, st)
-                                      : launch_rows<__nv_bfloat16>(a, ept, st);
+  cudaError_t e = dtype == SFFN_F32   ? launch_rows<float>(a, st)
+                  : dtype == SFFN_F16 ? launch_rows<__half>(a, st)
+                                      : launch_rows<__nv_bfloat16>(a, st);
   if (e != cudaSuccess) return e;
   return launch_ex(k_beam_merge, dim3(batch), dim3(kMergeThreads), 0, st, true, 1, a);
 }

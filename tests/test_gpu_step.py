@@ -343,6 +343,20 @@ def test_select_reports_what_has_no_distribution(sffn):
     check_select(sffn, z, bad, 8, fault=True)
 
 
+def test_select_of_logits_that_rise_and_fall(sffn):
+    """Parts whose largest logits come late, or lie far below those before, and references between -2^22 and 2^22."""
+    z = logits_of(6, 60000, "f32", 11)
+    at = torch.arange(60000, device="cuda")
+    z[0] += at * 0.01
+    z[1] -= at * 0.01
+    z[2] += (at // 8192) * 90.0
+    z[3] -= 4.1e6
+    z[4] += 4.1e6
+    z[5, :59000] = -1e9
+    check_select(sffn, z, scores_of(1, 6, 11), 12, off=2.0 ** -24 * 4.1e6)
+    check_select(sffn, z[:1].half(), scores_of(1, 1, 11), 50)
+
+
 def test_select_of_large_logits(sffn):
     """Logits beyond the range of a whole-number reference, in all chunks or some."""
     z = logits_of(4, 9000, "f32", 7)
