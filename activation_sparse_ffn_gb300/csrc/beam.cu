@@ -40,6 +40,8 @@ constexpr int kMaxBeams = 64;
 constexpr int kList = 2048;
 constexpr int kRuns = 2;      // times 16 bytes of a chunk that a thread holds, and as many on their way
 constexpr int kRowBlocks = 6; // of an SM
+constexpr int kSteps = 256;   // of 1/16 below the largest total
+constexpr int kKept = 4;      // candidates that a thread of k_beam_merge holds
 constexpr int kRanked = 256;  // entries that are put in order by counting
 
 struct BeamArgs {
@@ -61,6 +63,10 @@ struct BeamArgs {
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);   // -0 is 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+// The number of a pattern.
+__device__ __forceinline__ double number(unsigned long long o) {
+  return __longlong_as_double(o >> 63 ? o ^ 1ull << 63 : ~o);
 }
 __device__ __forceinline__ unsigned long long ordered(double v) {
   const unsigned long long u = __double_as_longlong(v + 0.0);
@@ -103,17 +109,6 @@ __device__ __forceinline__ V block_sum(V v, V* red) {
   V t = lane < warps ? red[lane] : V(0);
 #pragma unroll
   for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(SFFN_FULL_MASK, t, o);
-  return t;
-}
-
-// Largest pattern t (of its upper bits) that at least `want` threads' `best` reach; 0 if fewer have anything.
-template <int BITS>
-__device__ __forceinline__ uint32_t reached(uint32_t best, int want) {
-  uint32_t t = 0;
-  for (int b = 31; b > 31 - BITS; --b) {
-    const uint32_t up = t | 1u << b;
-    if (__syncthreads_count(best >= up) >= want) t = up;
-  }
   return t;
 }
 
@@ -401,11 +396,20 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   __shared__ float s_score[kMaxBeams];     // -infinity: no candidates
   __shared__ int s_done[kMaxBeams];
   __shared__ int s_int[32], s_count;
-  __shared__ double s_total[kList];
+  __shared__ float s_top[kWarps];
+  __shared__ int s_steps[kSteps], s_step;
+  __shared__ unsigned long long s_key[kList];
   __shared__ int s_place[kList][2];
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the first candidates of a thread are on their way while the rows' sums are joined
+  int2 kept[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int e = tid + i * kMergeThreads, all = a.beams * a.parts * a.n_out;
+    kept[i] = e < all ? __ldcg(a.found + (size_t)b * all + e) : make_int2(0, -1);
+  }
   // -- a warp for each row: its sum, as a power of two or a logarithm times a number
   for (int j = warp; j < a.beams; j += kWarps) {
     const int row = b * a.beams + j;
@@ -415,10 +419,11 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
     double sum = 0.0, ref = 0.0;
     if (!ended && fabsf(score) < INFINITY) {
       const float4* sums = a.sums + (size_t)row * a.parts;
+      const float4 first = lane < a.parts ? __ldcg(sums + lane) : make_float4(0.f, 0.f, (float)kNothing, 0.f);
       float top = -INFINITY, peak = -INFINITY;
       bool own = false;
       for (int c = lane; c < a.parts; c += 32) {
-        const float4 s = __ldcg(sums + c);
+        const float4 s = c < 32 ? first : __ldcg(sums + c);
         bad |= s.z == (float)kBad, own |= s.z == (float)kOwnMax;
         if (s.z == (float)kWhole) top = fmaxf(top, s.x), peak = fmaxf(peak, s.w);
       }
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
           peak = fmaxf(peak, __shfl_xor_sync(SFFN_FULL_MASK, peak, o));
         }
         for (int c = lane; c < a.parts; c += 32) {
-          const float4 s = __ldcg(sums + c);
+          const float4 s = c < 32 ? first : __ldcg(sums + c);
           if (s.z == (float)kWhole)
             sum += (double)(s.y * power_of_two(s.x - top)) * (1.0 + (s.w - peak) * kLeftOver);
         }
@@ -439,13 +444,13 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
         // some part's own largest is its reference: in the measure of logits
         double most = -INFINITY;
         for (int c = lane; c < a.parts; c += 32) {
-          const float4 s = __ldcg(sums + c);
+          const float4 s = c < 32 ? first : __ldcg(sums + c);
           if (s.z != (float)kNothing) most = fmax(most, s.z == (float)kWhole ? s.x * kLn2 : (double)s.x);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(SFFN_FULL_MASK, most, o));
         for (int c = lane; c < a.parts; c += 32) {
-          const float4 s = __ldcg(sums + c);
+          const float4 s = c < 32 ? first : __ldcg(sums + c);
           if (s.z != (float)kNothing) sum += s.y * exp((s.z == (float)kWhole ? s.x * kLn2 : (double)s.x) - most);
         }
         ref = most;
@@ -460,36 +465,80 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
     }
   }
   if (tid == 0) s_count = 0;
+  if (tid < kSteps) s_steps[tid] = 0;
   __syncthreads();
   // logarithms in 64 bits, a lane each: every warp that does one takes a microsecond of the SM
   for (int j = tid; j < a.beams; j += kMergeThreads) s_lse[j] = s_ref[j] + log(s_sum[j]);
   __syncthreads();
-  // -- candidates: those found in chunks, and the last places of sequences that have ended. Warps share a row's.
-  const int per_row = a.parts * a.n_out, parts = max(1, kWarps / a.beams);
-  const int2* found = a.found + (size_t)b * a.beams * per_row;
-  auto each = [&](auto&& take) {   // take(j, token, logit)
-    for (int i = warp; i < a.beams * parts; i += kWarps) {
-      const int j = i / parts, part = i - j * parts;
-      if (s_score[j] == -INFINITY) continue;
-      if (s_done[j]) {
-        if (part == 0 && lane == 0) take(j, a.end_token, 0.f);
-        continue;
+  // -- candidates: those found in parts, and the last places of sequences that have ended
+  const int per_row = a.parts * a.n_out, entries = a.beams * per_row;
+  const int2* found = a.found + (size_t)b * entries;
+  auto fetch = [&](int e) { return e < entries ? __ldcg(found + e) : make_int2(0, -1); };
+  // the candidate at place e: its pattern (0: none), beam and token
+  auto candidate = [&](int e, const int2& f, int& j, int& token) -> unsigned long long {
+    if (e >= entries) return 0;
+    j = e / per_row, token = s_done[j] ? a.end_token : f.y;
+    if (s_score[j] == -INFINITY || (s_done[j] ? e != j * per_row : token < 0)) return 0;
+    return ordered(s_done[j] ? (double)s_score[j] : (__int_as_float(f.x) - s_lse[j]) + s_score[j]);
+  };
+  // those that a thread holds are worked out once: 64-bit arithmetic is slow
+  unsigned long long keys[kKept];
+  float values[kKept];
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    int j, token;
+    keys[i] = candidate(tid + i * kMergeThreads, kept[i], j, token);
+    values[i] = keys[i] ? (float)number(keys[i]) : -INFINITY;
+  }
+  auto each = [&](auto&& take) {   // take(pattern, value, j, token)
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+      if (keys[i]) {
+        const int j = (tid + i * kMergeThreads) / per_row;
+        take(keys[i], values[i], j, s_done[j] ? a.end_token : kept[i].y);
       }
-      for (int e = part * 32 + lane; e < per_row; e += parts * 32) {
-        const int2 f = __ldcg(found + (size_t)j * per_row + e);
-        if (f.y >= 0) take(j, f.y, __int_as_float(f.x));
-      }
+    for (int e = tid + kKept * kMergeThreads; e < entries; e += kMergeThreads) {
+      int j, token;
+      const unsigned long long o = candidate(e, fetch(e), j, token);
+      if (o) take(o, (float)number(o), j, token);
     }
   };
-  auto total = [&](int j, float z) { return s_done[j] ? (double)s_score[j] : (z - s_lse[j]) + s_score[j]; };
-  uint32_t best = 0;
-  each([&](int j, int, float z) { best = max(best, ordered((float)total(j, z))); });
-  const uint32_t bound = reached<20>(best, a.n_out);
-  each([&](int j, int token, float z) {
-    const double v = total(j, z);
-    if (ordered((float)v) >= bound) {
+  // a bound that n_out totals reach and few others: how many lie how far below the largest, in steps of 1/16
+  float best = -INFINITY;
+  each([&](unsigned long long, float v, int, int) { best = fmaxf(best, v); });
+#pragma unroll
+  for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(SFFN_FULL_MASK, best, o));
+  if (lane == 0) s_top[warp] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) best = fmaxf(best, s_top[w]);
+  auto step_of = [&](float v) { return (int)fminf((best - v) * 16.f, kSteps - 1.f); };
+  each([&](unsigned long long, float v, int, int) { atomicAdd(&s_steps[step_of(v)], 1); });
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0, at = kSteps - 1;
+#pragma unroll
+    for (int i = 0; i < kSteps / 32; ++i) n += s_steps[lane * (kSteps / 32) + i];
+    int upto = n;   // in the steps of this lane and those before
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int p = __shfl_up_sync(SFFN_FULL_MASK, upto, o);
+      if (lane >= o) upto += p;
+    }
+#pragma unroll
+    for (int i = kSteps / 32 - 1; i >= 0; --i) {
+      if (upto >= a.n_out) at = lane * (kSteps / 32) + i;
+      upto -= s_steps[lane * (kSteps / 32) + i];
+    }
+    at = __reduce_min_sync(SFFN_FULL_MASK, at);
+    if (lane == 0) s_step = at;
+  }
+  __syncthreads();
+  const int last_step = s_step;   // the last of all has no end
+  each([&](unsigned long long o, float v, int j, int token) {
+    if (step_of(v) <= last_step) {
       const int n = atomicAdd(&s_count, 1);
-      if (n < kList) s_total[n] = v, s_place[n][0] = j, s_place[n][1] = token;
+      if (n < kList) s_key[n] = o, s_place[n][0] = j, s_place[n][1] = token;
     }
   });
   __syncthreads();
@@ -497,8 +546,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   if (n > kList) {
     auto reach = [&](unsigned long long t, long long last) {
       int c = 0;
-      each([&](int j, int token, float z) {
-        const unsigned long long o = ordered(total(j, z));
+      each([&](unsigned long long o, float, int j, int token) {
         c += o > t || (o == t && (long long)j * a.vocab + token <= last);
       });
       return block_sum(c, s_int);
@@ -511,12 +559,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
       if (reach(t, last + (1ll << i) - 1) < a.n_out) last += 1ll << i;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    each([&](int j, int token, float z) {
-      const double v = total(j, z);
-      const unsigned long long o = ordered(v);
+    each([&](unsigned long long o, float, int j, int token) {
       if (o > t || (o == t && (long long)j * a.vocab + token <= last)) {
         const int k = atomicAdd(&s_count, 1);
-        if (k < kList) s_total[k] = v, s_place[k][0] = j, s_place[k][1] = token;
+        if (k < kList) s_key[k] = o, s_place[k][0] = j, s_place[k][1] = token;
       }
     });
     __syncthreads();
@@ -524,14 +570,15 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   }
   const size_t out = (size_t)b * a.n_out;
   for (int i = tid; i < n; i += kMergeThreads) {
-    const double v = s_total[i];
+    const unsigned long long v = s_key[i];
     const int pj = s_place[i][0], pt = s_place[i][1];
     int ahead = 0;
     for (int k = 0; k < n; ++k) {
-      const double o = s_total[k];
+      const unsigned long long o = s_key[k];
       ahead += o > v || (o == v && (s_place[k][0] < pj || (s_place[k][0] == pj && s_place[k][1] < pt)));
     }
-    if (ahead < a.n_out) a.out_scores[out + ahead] = (float)v, a.out_parents[out + ahead] = pj, a.out_tokens[out + ahead] = pt;
+    if (ahead < a.n_out)
+      a.out_scores[out + ahead] = (float)number(v), a.out_parents[out + ahead] = pj, a.out_tokens[out + ahead] = pt;
   }
   for (int i = n + tid; i < a.n_out; i += kMergeThreads)
     a.out_scores[out + i] = -INFINITY, a.out_parents[out + i] = 0, a.out_tokens[out + i] = 0;

@@ -39,7 +39,6 @@ constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
 constexpr int kFewTokens = 32;
 constexpr int kFewSmem = 200 * 1024;
 constexpr int kFewRows = 512;      // most rows of a cluster
-constexpr int kFewAhead = 4;       // units of codes that a lane has on their way
 
 struct Lin8Args {
   const uint8_t* codes;
@@ -70,6 +69,7 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t smem_addr, uint32_t rank)
 // NT column tiles of eight tokens.
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, int cs) {
+  constexpr int kFewAhead = NT == 4 ? 6 : 8;   // units of codes that a lane has on their way
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
@@ -102,14 +102,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, i
   }
   for (int i = tid; i < (row1 - row0) * 8 * NT; i += kFewThreads) sums[i] = 0;
   pdl_wait();
-  const int own = (kb1 - kb0) * 4;   // 16-byte chunks of a token
-  for (int i = tid; i < own * 8 * NT; i += kFewThreads) {
-    const int b = i / own, c = i - b * own, col = kb0 * kL8Inputs + c * 16;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (b < a.B && col < a.k)
-      v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.x.ptr) + b * a.x.row_stride + col));
-    *reinterpret_cast<uint4*>(smem + b * a.x_stride + c * 16) =
-        make_uint4(v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u);
+  // a chunk of 16 bytes of every token a thread, eight on their way together
+  const int own = (kb1 - kb0) * 4;   // chunks of a token
+  for (int c = tid; c < own; c += kFewThreads) {
+    const int col = kb0 * kL8Inputs + c * 16;
+    const int8_t* src = static_cast<const int8_t*>(a.x.ptr) + col;
+#pragma unroll
+    for (int b0 = 0; b0 < 8 * NT; b0 += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (b0 + i < a.B && col < a.k) v[i] = __ldcg(reinterpret_cast<const uint4*>(src + (b0 + i) * a.x.row_stride));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(smem + (b0 + i) * a.x_stride + c * 16) =
+            make_uint4(v[i].x ^ 0x80808080u, v[i].y ^ 0x80808080u, v[i].z ^ 0x80808080u, v[i].w ^ 0x80808080u);
+    }
   }
   __syncthreads();
 

@@ -695,12 +695,15 @@ _linear8_sizes = {}   # handle: (in_features, out_features)
 _beam_sizes = {}      # handle: (vocab, beams, n_out)
 
 
-def _width_rows(t, n, width, dtype, name) -> RowsC:
-    """RowsC of (n, width) rows, or (n, heads, dim) with contiguous heads, of one type."""
-    if t.shape != (n, width):
-        _flat_rows(t, width, name)
-        if t.shape[0] != n:
-            raise ValueError(f"{name}: {t.shape[0]} rows given, {n} wanted")
+def _width_rows(t, shape, dtype, name) -> RowsC:
+    """RowsC of rows of `shape` = (n, width), or (n, heads, dim) with contiguous heads, of one type."""
+    if t.shape == shape:
+        if t.dtype is dtype and t.is_contiguous():
+            return RowsC(t.data_ptr(), shape[1])
+    else:
+        _flat_rows(t, shape[1], name)
+        if t.shape[0] != shape[0]:
+            raise ValueError(f"{name}: {t.shape[0]} rows given, {shape[0]} wanted")
     return _rows(t, dtype, name)
 
 
@@ -725,30 +728,33 @@ def sffn_norm(x, weight=None, eps=1e-5, residual=None, sum=None, y=None, codes=N
     """Root-mean-square norm of x (rows, width) + residual: the sum to `sum`, the norm times weight (width,) to y
     and, rounded to 8 bits, to codes (rows, width) int8 with scales (rows,) float32. Each output may be None, but y or
     codes is required. y may have another type than x."""
-    n, width = _row_shape(x)
-    dtype = x.dtype
-    w = None if weight is None else _flat(weight, width, torch.float32, "weight")
-    s = None
+    shape, dtype, s = _row_shape(x), x.dtype, None
+    n, width = shape
+    kind = y_kind = _io_dtype(dtype)
+    no = _NO_ROWS
+    if y is not None and y.dtype is not dtype:
+        y_kind = _io_dtype(y.dtype)
     if codes is not None:
         if scales is None:
             raise ValueError("codes need scales")
         s = _flat(scales, n, torch.float32, "scales")
-    rc = _lib.sffn_norm(_width_rows(x, n, width, None, "x"),
-                        _NO_ROWS if residual is None else _width_rows(residual, n, width, dtype, "residual"), w, eps, n,
-                        width, _NO_ROWS if sum is None else _width_rows(sum, n, width, dtype, "sum"),
-                        _NO_ROWS if y is None else _width_rows(y, n, width, None, "y"),
-                        _NO_ROWS if codes is None else _width_rows(codes, n, width, torch.int8, "codes"), s,
-                        _io_dtype(dtype), _io_dtype(dtype if y is None else y.dtype), _stream(stream))
+    rc = _lib.sffn_norm(_width_rows(x, shape, dtype, "x"),
+                        no if residual is None else _width_rows(residual, shape, dtype, "residual"),
+                        None if weight is None else _flat(weight, width, torch.float32, "weight"), eps, n, width,
+                        no if sum is None else _width_rows(sum, shape, dtype, "sum"),
+                        no if y is None else _width_rows(y, shape, y.dtype, "y"),
+                        no if codes is None else _width_rows(codes, shape, torch.int8, "codes"), s, kind, y_kind,
+                        _stream(stream))
     if rc:
         raise SffnError(rc, "sffn_norm")
 
 
 def sffn_quantize(x, codes, scales, stream=None) -> None:
     """x (rows, width) rounded to codes (rows, width) int8 with scales (rows,) float32."""
-    n, width = _row_shape(x)
-    rc = _lib.sffn_quantize(_width_rows(x, n, width, None, "x"), n, width,
-                            _width_rows(codes, n, width, torch.int8, "codes"),
-                            _flat(scales, n, torch.float32, "scales"), _io_dtype(x.dtype), _stream(stream))
+    shape, dtype = _row_shape(x), x.dtype
+    rc = _lib.sffn_quantize(_width_rows(x, shape, dtype, "x"), shape[0], shape[1],
+                            _width_rows(codes, shape, torch.int8, "codes"),
+                            _flat(scales, shape[0], torch.float32, "scales"), _io_dtype(dtype), _stream(stream))
     if rc:
         raise SffnError(rc, "sffn_quantize")
 
@@ -801,11 +807,11 @@ def sffn_linear8_forward(linear, x, x_scales, y, residual=None, ws=None, stream=
     """y (B, out) = x (B, in) int8 with x_scales (B,) through the layer, plus residual (B, out) if given (it may be y)."""
     B, dtype = x.shape[0], y.dtype
     n_in, n_out = _linear8_sizes.get(linear) or _linear8_size(linear)
-    ws_ptr, ws_bytes = _ws_args(ws)
-    rc = _lib.sffn_linear8_forward(linear, _width_rows(x, B, n_in, torch.int8, "x"),
+    shape, (ws_ptr, ws_bytes) = (B, n_out), _ws_args(ws)
+    rc = _lib.sffn_linear8_forward(linear, _width_rows(x, (B, n_in), torch.int8, "x"),
                                    _flat(x_scales, B, torch.float32, "x_scales"), B,
-                                   _NO_ROWS if residual is None else _width_rows(residual, B, n_out, dtype, "residual"),
-                                   _width_rows(y, B, n_out, None, "y"), _io_dtype(dtype), ws_ptr, ws_bytes,
+                                   _NO_ROWS if residual is None else _width_rows(residual, shape, dtype, "residual"),
+                                   _width_rows(y, shape, dtype, "y"), _io_dtype(dtype), ws_ptr, ws_bytes,
                                    _stream(stream))
     if rc:
         raise SffnError(rc, "sffn_linear8_forward")
@@ -867,7 +873,7 @@ def sffn_beam_select(beam, logits, scores, out_scores, out_parents, out_tokens, 
             raise ValueError(f"done: {rows} contiguous elements of bool or uint8 are wanted")
         ended = done.data_ptr()
     ws_ptr, ws_bytes = _ws_args(ws)
-    rc = _lib.sffn_beam_select(beam, _width_rows(logits, rows, vocab, None, "logits"),
+    rc = _lib.sffn_beam_select(beam, _width_rows(logits, (rows, vocab), logits.dtype, "logits"),
                                _flat(scores, rows, torch.float32, "scores"), ended, end_token, batch,
                                _flat(out_scores, batch * n_out, torch.float32, "out_scores"),
                                _flat(out_parents, batch * n_out, torch.int32, "out_parents"),
