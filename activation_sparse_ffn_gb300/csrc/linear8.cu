@@ -66,46 +66,72 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t smem_addr, uint32_t rank)
   return v;
 }
 
-// NT column tiles of eight tokens.
-template <int NT>
+// Four stored codes u = c + 128 as four halves u 2^-24: a byte alone in a half is a subnormal number.
+__device__ __forceinline__ void small_halves(uint32_t u, uint32_t& lo, uint32_t& hi) {
+  lo = __byte_perm(u, 0, 0x4140), hi = __byte_perm(u, 0, 0x4342);
+}
+
+// NT column tiles of eight tokens, RT row tiles of 16 at a time, whose inputs are widened once for all of them. Codes of
+// rows are widened to u 2^-24, which takes half of what c takes, and 128 times the sum of a token's codes is taken off at
+// the end: a product is below 2^15, so that 512 inputs are summed exactly.
+template <int NT, int RT>
 __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, int cs) {
-  constexpr int kFewAhead = NT == 4 ? 6 : 8;   // units of codes that a lane has on their way
+  constexpr int kAhead = NT == 1 ? 5 : 2, kExactBlocks = 512 / kL8Inputs;   // steps of codes that a lane has on their way
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int x_sum[8 * NT];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int rank = cs > 1 ? (int)cluster_rank() : 0, cluster = blockIdx.x / cs;
   const int row0 = (int)((long long)a.n * cluster / a.clusters), row1 = (int)((long long)a.n * (cluster + 1) / a.clusters);
   const int kb0 = (int)((long long)a.kb * rank / cs), kb1 = (int)((long long)a.kb * (rank + 1) / cs);
   const int wk0 = kb0 + (kb1 - kb0) * warp / kFewWarps, wk1 = kb0 + (kb1 - kb0) * (warp + 1) / kFewWarps;
-  const int tiles = (row1 - row0 + 15) / 16, nk = wk1 - wk0, units = tiles * nk;
+  const int tiles = (row1 - row0 + 15) / 16, nk = wk1 - wk0, groups = (tiles + RT - 1) / RT;
   int* sums = reinterpret_cast<int*>(smem + a.off_sum);   // [row][8 NT]
 
   pdl_launch_dependents();
-  // unit u: 16 rows of tile u / nk, 64 inputs wk0 + u % nk; the first are on their way before the wait (codes are packed
-  // by a call that synchronizes)
-  uint4 next[kFewAhead][2];
-  int ft = 0, fk = 0;   // the unit to be fetched next
-  auto fetch = [&](uint4* f) {
-    f[0] = f[1] = make_uint4(0, 0, 0, 0);
-    if (ft < tiles) {
+  // a step: the rows of a group of tiles, 64 inputs; the first are on their way before the wait (codes are packed by a call
+  // that synchronizes)
+  uint4 next[kAhead][RT][2];
+  const int tile_first = row0 / kL8Rows;
+  const uint8_t* codes = a.codes + ((size_t)tile_first * a.kb + wk0) * kL8Block;
+  const int per = tiles / max(groups, 1), rest = tiles - per * groups;   // tiles of a group; the first `rest` have one more
+  int place[RT][2];      // of the lane's rows of the group that is fetched, from `codes` on; -1: none
+  int fleft = 0, fgroup = -1, frow = row0, fstep = 0;   // steps left of it; its number; rows after it; bytes of the steps before
+  auto fetch = [&](uint4 (*f)[2]) {
+    if (fleft == 0) {
+      const int count = ++fgroup < groups ? per + (fgroup < rest) : 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = row0 + ft * 16 + h * 8 + g;
-        if (row < row1)
-          f[h] = ldg_stream(a.codes + ((size_t)(row / kL8Rows) * a.kb + wk0 + fk) * kL8Block + l8_chunk(row % kL8Rows, t));
-      }
-      if (++fk == nk) fk = 0, ++ft;
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = frow + r * 16 + h * 8 + g;
+          place[r][h] = r < count && row < row1
+                            ? (row / kL8Rows - tile_first) * a.kb * kL8Block + l8_chunk(row % kL8Rows, t) : -1;
+        }
+      frow += count * 16, fleft = nk, fstep = 0;
     }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (place[r][h] >= 0) f[r][h] = ldg_stream(codes + (uint32_t)(place[r][h] + fstep));
+    --fleft, fstep += kL8Block;
   };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) next[i][r][0] = next[i][r][1] = make_uint4(0, 0, 0, 0);
   if (nk) {
 #pragma unroll
-    for (int i = 0; i < kFewAhead; ++i) fetch(next[i]);
+    for (int i = 0; i < kAhead; ++i) fetch(next[i]);
   }
   for (int i = tid; i < (row1 - row0) * 8 * NT; i += kFewThreads) sums[i] = 0;
+  if (tid < 8 * NT) x_sum[tid] = 0;
+  __syncthreads();
   pdl_wait();
   // a chunk of 16 bytes of every token a thread, eight on their way together
   const int own = (kb1 - kb0) * 4;   // chunks of a token
-  for (int c = tid; c < own; c += kFewThreads) {
-    const int col = kb0 * kL8Inputs + c * 16;
+  for (int c0 = 0; c0 < own; c0 += kFewThreads) {
+    const int c = c0 + tid, col = kb0 * kL8Inputs + c * 16;
     const int8_t* src = static_cast<const int8_t*>(a.x.ptr) + col;
 #pragma unroll
     for (int b0 = 0; b0 < 8 * NT; b0 += 8) {
@@ -113,63 +139,76 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, i
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
-        if (b0 + i < a.B && col < a.k) v[i] = __ldcg(reinterpret_cast<const uint4*>(src + (b0 + i) * a.x.row_stride));
+        if (b0 + i < a.B && c < own && col < a.k)
+          v[i] = __ldcg(reinterpret_cast<const uint4*>(src + (b0 + i) * a.x.row_stride));
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(smem + (b0 + i) * a.x_stride + c * 16) =
-            make_uint4(v[i].x ^ 0x80808080u, v[i].y ^ 0x80808080u, v[i].z ^ 0x80808080u, v[i].w ^ 0x80808080u);
+      for (int i = 0; i < 8; ++i) {
+        if (c < own)
+          *reinterpret_cast<uint4*>(smem + (b0 + i) * a.x_stride + c * 16) =
+              make_uint4(v[i].x ^ 0x80808080u, v[i].y ^ 0x80808080u, v[i].z ^ 0x80808080u, v[i].w ^ 0x80808080u);
+        const int ones = 0x01010101;
+        int p = __dp4a((int)v[i].x, ones, __dp4a((int)v[i].y, ones, __dp4a((int)v[i].z, ones, __dp4a((int)v[i].w, ones, 0))));
+        p = __reduce_add_sync(SFFN_FULL_MASK, p);
+        if (lane == 0 && b0 + i < a.B) atomicAdd(&x_sum[b0 + i], p);
+      }
     }
   }
   __syncthreads();
 
-  float acc[NT][4];
+  float acc[RT][NT][4];
 #pragma unroll
-  for (int c = 0; c < NT; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-  auto leave = [&](int tile) {
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = tile * 16 + g + 8 * (e >> 1);
-        if (row < row1 - row0) atomicAdd(&sums[row * 8 * NT + c * 8 + 2 * t + (e & 1)], __float2int_rn(acc[c][e]));
-        acc[c][e] = 0.f;
-      }
-  };
-  int tile = 0, kk = 0;
-  for (int u = 0; u < units; u += kFewAhead) {
+      for (int e = 0; e < 4; ++e) acc[r][c][e] = 0.f;
+  int group = 0, kk = 0, first = 0, count = per + (0 < rest);
+  const uint8_t* xs = smem + (wk0 - kb0) * kL8Inputs + t * 16 + g * a.x_stride;
+  auto leave = [&]() {   // sums of a group of tiles, to those of the other warps
 #pragma unroll
-    for (int i = 0; i < kFewAhead; ++i) {
-      if (u + i < units) {
-        uint4 w[2] = {next[i][0], next[i][1]};
-        fetch(next[i]);
-        uint32_t ah[2][4][2];   // half h of the rows, step s: inputs 16 t + 4 s + (0, 1), (2, 3)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l8_halves(w[h].x, ah[h][0][0], ah[h][0][1]);
-          l8_halves(w[h].y, ah[h][1][0], ah[h][1][1]);
-          l8_halves(w[h].z, ah[h][2][0], ah[h][2][1]);
-          l8_halves(w[h].w, ah[h][3][0], ah[h][3][1]);
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = (first + r) * 16 + g + 8 * (e >> 1);
+          if (r < count && row < row1 - row0)
+            atomicAdd(&sums[row * 8 * NT + c * 8 + 2 * t + (e & 1)], __float2int_rn(acc[r][c][e] * 0x1p24f));
+          acc[r][c][e] = 0.f;
         }
-        const uint8_t* xs = smem + (wk0 - kb0 + kk) * kL8Inputs + t * 16;
+  };
+  const int steps = groups * nk;
+  for (int u = 0; u < steps; u += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (u + i < steps) {
+        uint32_t xf[NT][4][2];
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xs + (c * 8 + g) * a.x_stride);
-          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+          const uint4 xv = *reinterpret_cast<const uint4*>(xs + kk * kL8Inputs + c * 8 * a.x_stride);
+          l8_halves(xv.x, xf[c][0][0], xf[c][0][1]), l8_halves(xv.y, xf[c][1][0], xf[c][1][1]);
+          l8_halves(xv.z, xf[c][2][0], xf[c][2][1]), l8_halves(xv.w, xf[c][3][0], xf[c][3][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (r >= count) break;
+          const uint4 w0 = next[i][r][0], w1 = next[i][r][1];
+          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            uint32_t b0, b1;
-            l8_halves(xw[s], b0, b1);
-            const uint32_t af[4] = {ah[0][s][0], ah[1][s][0], ah[0][s][1], ah[1][s][1]};
-            mma_f16(acc[c], af, b0, b1);
+            uint32_t af[4];   // rows g, g + 8; inputs 16 t + 4 s + (0, 1), then (2, 3)
+            small_halves(wa[s], af[0], af[2]);
+            small_halves(wb[s], af[1], af[3]);
+#pragma unroll
+            for (int c = 0; c < NT; ++c) mma_f16(acc[r][c], af, xf[c][s][0], xf[c][s][1]);
           }
         }
+        fetch(next[i]);
         ++kk;
-        if (kk == nk || kk % (kL8Exact / kL8Inputs) == 0) {
-          leave(tile);
-          if (kk == nk) kk = 0, ++tile;
+        if (kk == nk || kk % kExactBlocks == 0) {
+          leave();
+          if (kk == nk) kk = 0, first += count, ++group, count = per + (group < rest);
         }
       }
     }
@@ -182,9 +221,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, i
     const int b = i / mine, r = from + i - b * mine, row = row0 + r;
     int s = 0;
     if (cs > 1) {
-      for (int k = 0; k < cs; ++k) s += ld_cluster_int(base + (r * 8 * NT + b) * 4, k);
+      for (int k = 0; k < cs; ++k)
+        s += ld_cluster_int(base + (r * 8 * NT + b) * 4, k) - 128 * ld_cluster_int(smem_u32(x_sum + b), k);
     } else {
-      s = sums[r * 8 * NT + b];
+      s = sums[r * 8 * NT + b] - 128 * x_sum[b];
     }
     float v = l8_value(s, a.scales[row], __ldcg(a.x_scales + b), a.bias[row]);
     if (a.residual.ptr) v = __fadd_rn(v, ld_elem(a.residual.ptr, b * a.residual.row_stride + row, a.dtype));
@@ -193,9 +233,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_lin8_few(const Lin8Args a, i
   if (cs > 1) cluster_barrier();   // sums are read by the others until here
 }
 
-template <int NT>
+template <int NT, int RT>
 cudaError_t run_few(const Lin8Args& a, int cs, int smem, cudaStream_t st) {
-  return launch_ex(k_lin8_few<NT>, dim3(a.clusters * cs), dim3(kFewThreads), smem, st, true, cs, a, cs);
+  return launch_ex(k_lin8_few<NT, RT>, dim3(a.clusters * cs), dim3(kFewThreads), smem, st, true, cs, a, cs);
 }
 
 // Up to 32 tokens.
@@ -215,7 +255,7 @@ cudaError_t launch_few(const sffn_linear8& L, Lin8Args a, cudaStream_t st) {
     if (cs == 8 || (smem <= kFewSmem && !spare)) break;
   }
   if (smem > kFewSmem) return cudaErrorInvalidConfiguration;
-  return nt == 1 ? run_few<1>(a, cs, smem, st) : nt == 2 ? run_few<2>(a, cs, smem, st) : run_few<4>(a, cs, smem, st);
+  return nt == 1 ? run_few<1, 2>(a, cs, smem, st) : nt == 2 ? run_few<2, 3>(a, cs, smem, st) : run_few<4, 2>(a, cs, smem, st);
 }
 
 }  // namespace
@@ -238,9 +278,9 @@ sffn_status pack_linear8(sffn_linear8& L, const int8_t* codes, const float* scal
 cudaError_t configure_linear8_kernels(sffn_linear8& L) {
   int optin = 0;
   cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, L.device);
-  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<1>, optin);
-  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<2>, optin);
-  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<4>, optin);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<1, 2>, optin);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<2, 3>, optin);
+  if (e == cudaSuccess) e = set_dynamic_smem_max(k_lin8_few<4, 2>, optin);
   if (e == cudaSuccess) e = configure_linear8_tc(L);
   return e;
 }
