@@ -4,8 +4,8 @@ cache and the activation-sparse FFN:
     h  = x + Wo . attend(cache + append(Wq x', Wk x', Wv x')),   x' = x / rms(x)
     y  = h + FFN(h / rms(h))
 
-for one new token of each of a batch of sequences. The normalisation is a plain
-torch stand-in; everything else runs in libsffn's kernels on one stream, and a
+for one new token of each of a batch of sequences. Everything but the last
+addition runs in libsffn's kernels on one stream, and a
 step is captured once in a CUDA graph and replayed, the cache lengths and page
 tables being read on the device at every replay.
 
@@ -61,14 +61,14 @@ class DecoderLayer:
         self.rows = torch.empty(batch, heads + 2 * kv_heads, self.dim, **kw)
         self.q, self.k, self.v = self.rows.split((heads, kv_heads, kv_heads), 1)
         self.att = torch.empty(batch, heads, self.dim, **kw)
-        self.h, self.y, self.out = (torch.empty(batch, spec.d, **kw) for _ in range(3))
+        self.h, self.y, self.out, self.xn = (torch.empty(batch, spec.d, **kw) for _ in range(4))
         self.masks = self.ffn.masks(batch)
         self.ws_qkv, self.ws_proj = self.qkv.workspace(batch), self.proj.workspace(batch)
         self.ws_att, self.ws_ffn = self.cache.workspace(self.tokens, heads), self.ffn.workspace(batch)
 
-    @staticmethod
-    def norm(x: torch.Tensor) -> torch.Tensor:
-        return torch.nn.functional.rms_norm(x, x.shape[-1:])
+    def norm(self, x: torch.Tensor) -> torch.Tensor:
+        sffn.sffn_norm(x, None, torch.finfo(x.dtype).eps, y=self.xn)
+        return self.xn
 
     def fill(self, n: int, seed: int = 1) -> None:
         """Append n positions of random keys and values to every sequence, as a prompt would have."""
@@ -98,7 +98,8 @@ class DecoderLayer:
         """h of the step that was just run, in plain fp32 torch, on the cache's own values."""
         def weights(codes, scales):
             return codes.float() * scales.float().repeat_interleave(codes.shape[1] // scales.shape[1], 1)
-        rows = (self.norm(self.x) @ weights(self.w_qkv, self.s_qkv).T).view(self.batch, -1, self.dim)
+        x = torch.nn.functional.rms_norm(self.x, self.x.shape[-1:])
+        rows = (x @ weights(self.w_qkv, self.s_qkv).T).view(self.batch, -1, self.dim)
         n, half = int(self.kv_len[0]), self.dim // 2
         turn = self.rope.table[n - 1]
         a, b = rows[:, :self.heads, :half], rows[:, :self.heads, half:]

@@ -787,8 +787,9 @@ void sffn_beam_destroy(sffn_beam* beam);
  * sequence s of group g goes on as a copy of sequence m = g * beams +
  * parents[s]:
  *   - pages that are full (the first n / page_size) are shared: their ids in
- *     row s of table_out are those of row m of batch->table. Nothing is
- *     written to them from then on (append writes from position n on).
+ *     row s of table_out are those of row m of batch->table. Nothing may be
+ *     written to them from then on (append writes from position n on; a
+ *     search that starts anew starts from a table without shared pages).
  *   - the n % page_size positions of the page that is not full are copied, in
  *     every one of the n_kv caches, from the page that row m of batch->table
  *     names to the one that row s of table_out named before the call.
