@@ -38,8 +38,8 @@ constexpr int kMergeThreads = 512;
 constexpr int kMaxOut = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kList = 2048;
-constexpr int kRuns = 2;      // times 16 bytes of a chunk that a thread holds, and as many on their way
-constexpr int kRowBlocks = 6; // of an SM
+constexpr int kRuns = 4;      // times 16 bytes of a chunk that a thread holds, and as many on their way
+constexpr int kRowBlocks = 4; // of an SM
 constexpr int kSteps = 256;   // of 1/16 below the largest total
 constexpr int kKept = 4;      // candidates that a thread of k_beam_merge holds
 constexpr int kRanked = 256;  // entries that are put in order by counting

@@ -3,8 +3,8 @@
 // Full pages change hands by their ids alone. Of the page that is not full, the
 // filled positions are copied: per head three runs of bytes (keys, values,
 // params of every eight positions). Sequences of a group may swap pages, so all
-// that a block writes it has read before: a block takes the same bytes of the
-// last pages of every sequence of a group through shared memory.
+// that is written has been read before: a thread takes the same 16 bytes of the
+// last page of every sequence of a group, through shared memory of its own.
 #include <algorithm>
 
 #include "kv_layout.cuh"
@@ -28,7 +28,7 @@ struct ReorderArgs {
   uint32_t* err;
   size_t page_bytes;
   int head_bytes, page_size, row_bytes, param_bytes;   // of a head: page, keys of a position, params of eight positions
-  int beams, out_stride;
+  int heads, beams, out_stride;
   int chunk, copies;   // bytes of each page that a block copies, blocks of a group for that
   int cols, tables;    // columns of the page tables at a time, blocks of a group for them
 };
@@ -83,23 +83,26 @@ __global__ void __launch_bounds__(kThreads) k_reorder(const ReorderArgs a) {
   }
   __syncthreads();
   if (tid < a.beams && (s_from[s_parent[tid]] < 0 || s_to[tid] < 0)) set_device_error(a.err, SFFN_ERR_DEVICE);
+  // a thread takes the same 16 bytes of every page, reads all that go on and writes them after that
   const int per_head = 2 * tail * a.row_bytes + (tail + 7) / 8 * a.param_bytes;   // filled bytes
-  const int filled = per_head * (int)(a.page_bytes / a.head_bytes), begin = part * a.chunk;   // pages are at most 21 MB
-  const int words = min(filled - begin, a.chunk) / 16, per = a.chunk / 16;
-  for (int i = tid; i < words * a.beams; i += kThreads) {
-    const int s = i / words, w = i - s * words;
-    const int at = begin + w * 16, head = at / per_head, byte = filled_byte(a, tail, at - head * per_head);
-    if (s_from[s] >= 0)
-      stage[s * per + w] = __ldcg(reinterpret_cast<const uint4*>(a.pages[layer] + s_from[s] * a.page_bytes +
-                                                                 (size_t)head * a.head_bytes + byte));
+  const int at = part * a.chunk + tid * 16, head = at / per_head;
+  if (tid * 16 >= a.chunk || head >= a.heads) return;
+  uint8_t* base = a.pages[layer] + (size_t)head * a.head_bytes + filled_byte(a, tail, at - head * per_head);
+  uint4* own = stage + tid;
+  const int step = a.chunk / 16;
+  uint4 v[8];
+  for (int s0 = 0; s0 < a.beams; s0 += 8) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < a.beams && s_from[s0 + s] >= 0)
+        v[s] = __ldcg(reinterpret_cast<const uint4*>(base + s_from[s0 + s] * a.page_bytes));
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < a.beams && s_from[s0 + s] >= 0) own[(s0 + s) * step] = v[s];
   }
-  __syncthreads();
-  for (int i = tid; i < words * a.beams; i += kThreads) {
-    const int s = i / words, w = i - s * words, from = s_from[s_parent[s]];
-    const int at = begin + w * 16, head = at / per_head, byte = filled_byte(a, tail, at - head * per_head);
-    if (from >= 0 && s_to[s] >= 0 && s_to[s] != from)
-      *reinterpret_cast<uint4*>(a.pages[layer] + s_to[s] * a.page_bytes + (size_t)head * a.head_bytes + byte) =
-          stage[s_parent[s] * per + w];
+  for (int s = 0; s < a.beams; ++s) {
+    const int from = s_from[s_parent[s]], to = s_to[s];
+    if (from >= 0 && to >= 0 && to != from) *reinterpret_cast<uint4*>(base + to * a.page_bytes) = own[s_parent[s] * step];
   }
 }
 
@@ -114,7 +117,8 @@ cudaError_t launch_kv_reorder(const sffn_kv* const* kvs, int n_kv, const sffn_kv
   a.page_bytes = C.page_bytes, a.head_bytes = (int)C.head_bytes, a.page_size = C.desc.page_size;
   a.row_bytes = C.desc.head_dim / 2, a.param_bytes = C.desc.head_dim / C.desc.group * 64;
   a.beams = beams, a.out_stride = out_stride;
-  a.chunk = std::min(kStage / beams, 8192) / 16 * 16;
+  a.heads = C.desc.n_kv_heads;
+  a.chunk = std::min(kStage / beams, kThreads * 16) / 16 * 16;
   a.copies = (int)((C.page_bytes + a.chunk - 1) / a.chunk);
   a.cols = std::min(kThreads, kStage / 4 / beams);
   a.tables = (b.table_stride + kTableBlock - 1) / kTableBlock;
