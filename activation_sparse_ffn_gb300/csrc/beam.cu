@@ -310,19 +310,32 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) bound = min(bound, s_bound[w]);
     }
+    // the places of what reaches it; values are fetched again at the end. With no bound yet, of all that is not masked.
+    uint32_t hits = 0;
     if (best >= bound && best) {
-      // their places only: values are fetched again at the end. With no bound yet, what is not masked.
       const float from = bound ? value_of(bound) : lowest<T>();
-      uint32_t hits = 0;
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) hits |= which_reach<T>(v[r], from, 4 * r);
-      while (hits) {
-        const int bit = __ffs(hits) - 1, p = bit & 15;
-        hits &= hits - 1;
-        const int j = sizeof(T) == 4 ? p & 3 : 2 * (p & 3) + (bit >> 4);
-        const int n = atomicAdd(&s_count, 1);
-        if (n < kList) s_token[n] = c * kChunk + ((p >> 2) * kThreads + tid) * N + j;
+    }
+    int n = 0;
+    if (bound == 0) {   // many: one addition a warp
+      const int own = __popc(hits);
+      int upto = own;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int p = __shfl_up_sync(SFFN_FULL_MASK, upto, o);
+        if (lane >= o) upto += p;
       }
+      if (lane == 31) n = atomicAdd(&s_count, upto);
+      n = __shfl_sync(SFFN_FULL_MASK, n, 31) + upto - own;
+    }
+    while (hits) {
+      const int bit = __ffs(hits) - 1, p = bit & 15;
+      hits &= hits - 1;
+      const int j = sizeof(T) == 4 ? p & 3 : 2 * (p & 3) + (bit >> 4);
+      if (bound) n = atomicAdd(&s_count, 1);
+      if (n < kList) s_token[n] = c * kChunk + ((p >> 2) * kThreads + tid) * N + j;
+      ++n;
     }
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) v[r] = nv[r];

@@ -25,6 +25,7 @@
 // a tile leaves its sums in the workspace, and whichever comes last adds them:
 // whole numbers, so that the order does not matter.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear8.cuh"
 #include "rows_io.cuh"
@@ -36,7 +37,8 @@ namespace sffn {
 namespace {
 
 // Warps 0-3 widen even steps and 4-7 odd ones, 8-15 take the sums, and one thread each of 16 to 19 copies codes, copies
-// tokens, reports their arrival and issues products. Registers go where the sums are: 2 x 96 + 2 x 128 + 32 of the 5 x 96 a thread has at launch.
+// tokens, reports their arrival and issues products. Registers go where the sums are: 2 x 88 + 2 x 136 + 32 of
+// the 5 x 96 a thread has at launch.
 constexpr int kConvWarps = 4, kEpiWarps = 8, kEpiWarp0 = 8, kTcThreads = 640;
 constexpr int kWarpW = 16, kWarpX = 17, kWarpTold = 18, kWarpMma = 19;
 constexpr int kMaxTokens = 192;                          // of a tile
@@ -45,7 +47,7 @@ constexpr int kSlots = 2, kSlotCols = 64;                // of A in tensor memor
 constexpr int kAccCols = 192, kTmemCols = 512;           // accumulators at 0 and 192, A at 384
 constexpr int kStagesW = 6, kStagesX = 4;                // the first even: a set of warps keeps its own
 constexpr int kStepsExact = kL8Exact / kStep;
-constexpr int kLeastSteps = 4;                           // of a tile that a block takes a part of
+constexpr int kJoinSteps = 20;                           // that take as long as leaving and joining a tile's parts, 8 us
 constexpr int CG = 2;                                    // blocks of a cluster
 
 struct TcArgs {
@@ -213,13 +215,27 @@ __device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <typename T>
-__device__ __forceinline__ float as_float(T v) {
-  if (sizeof(T) == 4) return *reinterpret_cast<const float*>(&v);
-  const unsigned short u = *reinterpret_cast<const unsigned short*>(&v);
-  return std::is_same<T, __half>::value ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
+__device__ __forceinline__ T from_float(float v);
+// An element as its bits. The load stays where it is written: brought forward, all 96 of an output's residuals would want
+// registers at once.
+template <typename T>
+__device__ __forceinline__ uint32_t load_here(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t v;
+    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+  } else {
+    unsigned short v;
+    asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+  }
 }
 template <typename T>
-__device__ __forceinline__ T from_float(float v);
+__device__ __forceinline__ float as_float(uint32_t u) {
+  if constexpr (std::is_same<T, float>::value) return __uint_as_float(u);
+  if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)u));
+  return __uint_as_float(u << 16);
+}
 template <>
 __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <>
@@ -227,36 +243,32 @@ __device__ __forceinline__ __half from_float<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Outputs of row n and `tokens` tokens from token0 on (xs: their scales, one a lane). The type is settled outside: 96
-// times a choice of three types, code that no cache of instructions holds, took longer than a tile's products.
+// Outputs v of row n and `tokens` tokens from token0 on. The type is settled outside: 96 times a choice of three types, code
+// that no cache of instructions holds, took longer than a tile's products.
 template <typename T>
-__device__ __forceinline__ void put_outputs(const TcArgs& a, const int (&sum)[96], const float (&xs)[3], float scale,
-                                            float bias, int n, int token0, int tokens) {
-  const bool in = n < a.n;
+__device__ __forceinline__ void put_outputs(const TcArgs& a, const int (&v)[96], int n, int token0, int tokens) {
+  if (n >= a.n) tokens = 0;
   T* y = static_cast<T*>(a.y.ptr) + token0 * a.y.row_stride + n;
   if (a.residual.ptr) {
     const T* res = static_cast<const T*>(a.residual.ptr) + token0 * a.residual.row_stride + n;
+    uint32_t r[2][8];   // eight residuals on their way while eight outputs are written
+    auto load = [&](int b, uint32_t* to) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i, res += a.residual.row_stride)
+        if (b + i < tokens) to[i] = load_here(res);
+    };
+    load(0, r[0]);
 #pragma unroll
     for (int b = 0; b < 96; b += 8) {
-      T r[8];
+      if (b + 8 < 96) load(b + 8, r[(b / 8 + 1) & 1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (in && b + i < tokens) r[i] = __ldcg(res + i * a.residual.row_stride);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[(b + i) / 32], (b + i) % 32);
-        if (in && b + i < tokens) *y = from_float<T>(__fadd_rn(l8_value(sum[b + i], scale, x_scale, bias), as_float(r[i])));
-        y += a.y.row_stride;
-      }
-      res += 8 * a.residual.row_stride;
+      for (int i = 0; i < 8; ++i, y += a.y.row_stride)
+        if (b + i < tokens) *y = from_float<T>(__fadd_rn(__int_as_float(v[b + i]), as_float<T>(r[(b / 8) & 1][i])));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 96; ++i) {
-      const float x_scale = __shfl_sync(SFFN_FULL_MASK, xs[i / 32], i % 32);
-      if (in && i < tokens) *y = from_float<T>(l8_value(sum[i], scale, x_scale, bias));
-      y += a.y.row_stride;
-    }
+    for (int i = 0; i < 96; ++i, y += a.y.row_stride)
+      if (i < tokens) *y = from_float<T>(__int_as_float(v[i]));
   }
 }
 
@@ -300,7 +312,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 2 * kConvWarps) {
     // ------------------------------------------------------------ codes to halves
-    pdl_wait();   // keeps the registers it has
+    fewer_registers<88>();
+    pdl_wait();
     const int row = tid & 127, set = warp / kConvWarps;
     const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * kAccCols;
     Ring<kStagesW, 2> w(set);
@@ -338,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp < kEpiWarp0 + kEpiWarps) {
     // ------------------------------------------------------------ sums to whole numbers to outputs
-    more_registers<128>();
+    more_registers<136>();
     pdl_wait();
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2, blocks = a.nt / 16;
     const int b0 = half ? (blocks + 1) / 2 : 0, nb = half ? blocks - b0 : (blocks + 1) / 2;   // of 16 tokens, at most 6
@@ -412,12 +425,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < 3; ++i) xs[i] = token0 + 32 * i + lane < a.B ? __ldcg(a.x_scales + token0 + 32 * i + lane) : 0.f;
       const int tokens = min(nb * 16, a.B - token0);
+#pragma unroll
+      for (int i = 0; i < 96; ++i)   // the outputs but for the residual, in the registers of their sums
+        sum[i] = __float_as_int(l8_value(sum[i], scale, __shfl_sync(SFFN_FULL_MASK, xs[i / 32], i % 32), bias));
       if (a.dtype == SFFN_F32)
-        put_outputs<float>(a, sum, xs, scale, bias, n, token0, tokens);
+        put_outputs<float>(a, sum, n, token0, tokens);
       else if (a.dtype == SFFN_F16)
-        put_outputs<__half>(a, sum, xs, scale, bias, n, token0, tokens);
+        put_outputs<__half>(a, sum, n, token0, tokens);
       else
-        put_outputs<__nv_bfloat16>(a, sum, xs, scale, bias, n, token0, tokens);
+        put_outputs<__nv_bfloat16>(a, sum, n, token0, tokens);
       __syncwarp();
     }
   } else {
@@ -595,7 +611,9 @@ cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const f
   a.groups = L.num_sms / CG;
   const int tiles = L.tiles / CG * a.token_tiles;
   a.whole = tiles / a.groups, a.left = tiles % a.groups;
-  a.parted = a.left ? (int)std::min<long long>(a.groups, std::max<long long>(a.left, (long long)a.left * a.steps / kLeastSteps)) : 0;
+  // sharing the tiles left over makes them shorter by the clusters that would stand idle, and costs a join
+  const bool share = (long long)a.steps * (a.groups - a.left) > (long long)kJoinSteps * a.groups;
+  a.parted = a.left && share ? a.groups : a.left;
   const int runs = L.kp / 16;
   const unsigned threads = (unsigned)s.tokens * runs;
   cudaError_t e = launch_ex(k_lin8_widen, dim3((threads + 255) / 256), dim3(256), 0, st, true, 1, x, B, L.desc.in_features,

@@ -6,6 +6,7 @@
 // that is written has been read before: a thread takes the same 16 bytes of the
 // last page of every sequence of a group, through shared memory of its own.
 #include <algorithm>
+#include <climits>
 
 #include "kv_layout.cuh"
 #include "step.h"
@@ -123,7 +124,9 @@ cudaError_t launch_kv_reorder(const sffn_kv* const* kvs, int n_kv, const sffn_kv
   a.cols = std::min(kThreads, kStage / 4 / beams);
   a.tables = (b.table_stride + kTableBlock - 1) / kTableBlock;
   const int smem = std::max(a.chunk, a.cols * 4) * beams;
-  return launch_ex(k_reorder, dim3((unsigned)(a.copies + a.tables) * (b.n_seq / beams), 1, n_kv), dim3(kThreads), smem, st,
+  const long long blocks = (long long)(a.copies + a.tables) * (b.n_seq / beams);
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  return launch_ex(k_reorder, dim3((unsigned)blocks, 1, n_kv), dim3(kThreads), smem, st,
                    true, 1, a);
 }
 
