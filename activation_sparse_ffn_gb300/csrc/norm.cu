@@ -96,14 +96,29 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return top >= kInfBits ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
 }
 
-// y / scale rounded to the nearest whole number, ties to even, as the quotient rounded to fp32 gives it. The product
-// with 1 / scale is off by less than 2^-15 where the quotient is at most 128, so only near a tie is the quotient itself
-// looked at, which takes the division.
-__device__ __forceinline__ int code_of(float y, float scale, float inv) {
-  float q = __fmul_rn(y, inv);
-  float r = rintf(q);
-  if (!(fabsf(fabsf(q - r) - 0.5f) > 0x1p-14f)) r = rintf(__fdiv_rn(y, scale));
-  return (int)fminf(fmaxf(r, -127.f), 127.f);
+// N codes: y / scale rounded to the nearest whole number, ties to even, as the quotient rounded to fp32 gives it, four in a
+// word. The product with 1 / scale is off by less than 2^-15 where the quotient is at most 128, so only near a tie is the
+// quotient itself looked at, which takes the division. Added to 3 2^22 a quotient is rounded and its code stands in the
+// low byte, without a conversion (those issue at an eighth of the additions' rate).
+template <int N>
+__device__ __forceinline__ void codes_of(const float* y, float scale, float inv, uint32_t* w) {
+  constexpr float kShift = 12582912.f;
+  bool slow = !(scale >= 0x1p-120f);   // 0, no number, or too small for its reciprocal
+  uint32_t c[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float q = __fmul_rn(y[j], inv), m = __fadd_rn(q, kShift), off = __fsub_rn(q, __fsub_rn(m, kShift));
+    slow |= !(fabsf(__fsub_rn(fabsf(off), 0.5f)) > 0x1p-14f);
+    c[j] = __float_as_uint(m);
+  }
+  if (slow) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      c[j] = scale > 0.f ? (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(y[j], scale)), -127.f), 127.f) : 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < N; j += 4)
+    w[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
 }
 
 // Where rows may be read and written 16 bytes (codes: one run) at a time.
@@ -135,16 +150,7 @@ __device__ __forceinline__ void store_some(void* p, size_t i, int left, int dtyp
 template <int N>
 __device__ __forceinline__ void store_codes(int8_t* p, int left, bool vec, const float* y, float scale, float inv) {
   uint32_t w[N / 4];
-#pragma unroll
-  for (int j = 0; j < N; j += 4) {
-    uint32_t u = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = scale > 0.f ? code_of(y[j + e], scale, inv) : 0;
-      u |= (uint32_t)(c & 255) << (8 * e);
-    }
-    w[j / 4] = u;
-  }
+  codes_of<N>(y, scale, inv, w);
   if (vec && left >= N) {
     if (N == 4)
       *reinterpret_cast<uint32_t*>(p) = w[0];
@@ -165,15 +171,19 @@ constexpr int dtype_of() {
 // f of the block's row, of which each thread has EPT elements.
 template <int EPT>
 __device__ __forceinline__ float row_factor(const float* t, int width, double eps, double inv_width, float* red) {
-  float s = 0.f, c = 0.f;
+  // four sums, so that one addition need not wait for the one before
+  float part[4] = {0.f, 0.f, 0.f, 0.f}, rest[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < EPT; ++j) {
     const float p = __fmul_rn(t[j], t[j]);
-    two_sum(s, c, p);
-    c = __fadd_rn(c, __fmaf_rn(t[j], t[j], -p));
+    two_sum(part[j & 3], rest[j & 3], p);
+    rest[j & 3] = __fadd_rn(rest[j & 3], __fmaf_rn(t[j], t[j], -p));
     top = max(top, abs_bits(t[j]));
   }
+  float s = part[0], c = __fadd_rn(__fadd_rn(rest[0], rest[1]), __fadd_rn(rest[2], rest[3]));
+#pragma unroll
+  for (int i = 1; i < 4; ++i) two_sum(s, c, part[i]);
   block_reduce(s, c, top, red);
   double sum = (double)s + (double)c;
   if (top >= kInfBits) {
@@ -250,7 +260,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const No
     for (int j = 0; j < EPT; ++j) top = max(top, abs_bits(t[j]));
     top = block_max(top, red);
     const float scale = scale_of(top);
-    const float inv = __fdiv_rn(1.f, scale);   // infinite for a subnormal scale: code_of divides then
+    const float inv = __fdiv_rn(1.f, scale);
     if (threadIdx.x == 0) a.scales[row] = scale;
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
