@@ -205,69 +205,103 @@ __device__ __forceinline__ float row_factor(const float* t, int width, double ep
   return factor(sum, inv_width, eps, red);
 }
 
-// EPT elements a thread, in runs of 16 bytes: run r of thread t begins at (r * threads + t) * kRun.
-template <typename T, int EPT>
-__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, const NormVec vec, double inv_width) {
-  constexpr int N = kRun<T>, RUNS = EPT / N, D = dtype_of<T>();
+// EPT elements a thread: in runs of 16 bytes, run r of thread t from (r * threads + t) * kRun on, or, where some array is not
+// aligned to that (SPREAD), element k of thread t at k * threads + t, so that a warp reads what lies together (1671 rows of
+// 4839 halves with a residual: 58 us with runs).
+template <typename T, int EPT, bool SPREAD>
+__global__ void __launch_bounds__(kMaxThreads) k_norm(const NormArgs a, double inv_width) {
+  constexpr int N = kRun<T>, D = dtype_of<T>();
   __shared__ float red[97];
   pdl_launch_dependents();
   pdl_wait();
   const size_t row = blockIdx.x;
-  const int step = blockDim.x * N, at0 = threadIdx.x * N;
-  float t[EPT];
+  const int step = blockDim.x;
+  constexpr int G = 8;   // elements that are loaded together
+  auto load = [&](const void* p, size_t from, int dtype, int k0, float* o) {
+    if constexpr (SPREAD) {
 #pragma unroll
-  for (int r = 0; r < RUNS; ++r)
-    load_some<N>(a.x.ptr, row * a.x.row_stride + at0 + r * step, a.width - at0 - r * step, D, vec.x, t + r * N);
-  if (a.residual.ptr) {
+      for (int k = 0; k < G; ++k) {
+        const int at = (k0 + k) * step + threadIdx.x;
+        o[k] = at < a.width ? ld_elem(p, from + at, dtype) : 0.f;
+      }
+    } else {
 #pragma unroll
-    for (int r = 0; r < RUNS; ++r) {
-      float o[N];
-      load_some<N>(a.residual.ptr, row * a.residual.row_stride + at0 + r * step, a.width - at0 - r * step, D,
-                   vec.residual, o);
-#pragma unroll
-      for (int j = 0; j < N; ++j) t[r * N + j] = __fadd_rn(t[r * N + j], o[j]);
-    }
-  }
-  if (a.sum.ptr) {
-#pragma unroll
-    for (int r = 0; r < RUNS; ++r)
-      store_some<N>(a.sum.ptr, row * a.sum.row_stride + at0 + r * step, a.width - at0 - r * step, D, vec.sum, t + r * N);
-  }
-  if (a.norm) {
-    const float f = row_factor<EPT>(t, a.width, a.eps, inv_width, red);
-#pragma unroll
-    for (int r = 0; r < RUNS; ++r) {
-      const int at = at0 + r * step, left = a.width - at;
-      float w[N];
-      if (a.weight) load_some<N>(a.weight, at, left, SFFN_F32, vec.weight, w);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float v = __fmul_rn(t[r * N + j], f);
-        if (a.weight) v = __fmul_rn(v, w[j]);
-        t[r * N + j] = j < left ? v : 0.f;
+      for (int k = 0; k < G; k += N) {
+        const int at = (k0 + k) * step + threadIdx.x * N;
+        load_some<N>(p, from + at, a.width - at, dtype, true, o + k);
       }
     }
-    if (a.y.ptr) {
+  };
+  auto store = [&](void* p, size_t from, int dtype, const float* v) {
+    if constexpr (SPREAD) {
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r)
-        store_some<N>(a.y.ptr, row * a.y.row_stride + at0 + r * step, a.width - at0 - r * step, a.y_dtype, vec.y,
-                      t + r * N);
+      for (int k = 0; k < EPT; ++k) {
+        const int at = k * step + threadIdx.x;
+        if (at < a.width) st_elem(p, from + at, v[k], dtype);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPT; k += N) {
+        const int at = (k * step) + threadIdx.x * N;
+        store_some<N>(p, from + at, a.width - at, dtype, true, v + k);
+      }
     }
+  };
+  auto inside = [&](int k) { return (SPREAD ? k * step + (int)threadIdx.x : k / N * N * step + (int)threadIdx.x * N + k % N) < a.width; };
+  float t[EPT];
+#pragma unroll
+  for (int k0 = 0; k0 < EPT; k0 += G) load(a.x.ptr, row * a.x.row_stride, D, k0, t + k0);
+  if (a.residual.ptr) {
+#pragma unroll
+    for (int k0 = 0; k0 < EPT; k0 += G) {
+      float o[G];
+      load(a.residual.ptr, row * a.residual.row_stride, D, k0, o);
+#pragma unroll
+      for (int k = 0; k < G; ++k) t[k0 + k] = __fadd_rn(t[k0 + k], o[k]);
+    }
+  }
+  if (a.sum.ptr) store(a.sum.ptr, row * a.sum.row_stride, D, t);
+  if (a.norm) {
+    const float f = row_factor<EPT>(t, a.width, a.eps, inv_width, red);
+    if (a.weight) {
+#pragma unroll
+      for (int k0 = 0; k0 < EPT; k0 += G) {
+        float w[G];
+        load(a.weight, 0, SFFN_F32, k0, w);
+#pragma unroll
+        for (int k = 0; k < G; ++k) t[k0 + k] = __fmul_rn(__fmul_rn(t[k0 + k], f), w[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) t[k] = __fmul_rn(t[k], f);
+    }
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) t[k] = inside(k) ? t[k] : 0.f;   // of no element, whatever f is
+    if (a.y.ptr) store(a.y.ptr, row * a.y.row_stride, a.y_dtype, t);
   }
   if (a.codes.ptr) {
     uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) top = max(top, abs_bits(t[j]));
+    for (int k = 0; k < EPT; ++k) top = max(top, abs_bits(t[k]));
     top = block_max(top, red);
-    const float scale = scale_of(top);
-    const float inv = __fdiv_rn(1.f, scale);
+    const float scale = scale_of(top), inv = __fdiv_rn(1.f, scale);
     if (threadIdx.x == 0) a.scales[row] = scale;
+    int8_t* out = static_cast<int8_t*>(a.codes.ptr) + row * a.codes.row_stride;
+    if constexpr (SPREAD) {
 #pragma unroll
-    for (int r = 0; r < RUNS; ++r) {
-      const int at = at0 + r * step;
-      if (at < a.width)
-        store_codes<N>(static_cast<int8_t*>(a.codes.ptr) + row * a.codes.row_stride + at, a.width - at, vec.codes,
-                       t + r * N, scale, inv);
+      for (int k = 0; k < EPT; k += 4) {
+        uint32_t w;
+        codes_of<4>(t + k, scale, inv, &w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (inside(k + e)) out[(k + e) * step + threadIdx.x] = (int8_t)(w >> (8 * e));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPT; k += N) {
+        const int at = k * step + threadIdx.x * N;
+        if (at < a.width) store_codes<N>(out + at, a.width - at, true, t + k, scale, inv);
+      }
     }
   }
 }
@@ -417,11 +451,14 @@ cudaError_t launch_typed(const NormArgs& a, cudaStream_t st) {
   }
   // Few rows: as many threads as there are, for the shortest way through one row. Many: blocks of 256, so that an SM
   // holds several and one loads while another waits at its barriers.
+  const bool spread = !(vec.x && (!a.residual.ptr || vec.residual) && (!a.sum.ptr || vec.sum) && (!a.y.ptr || vec.y) &&
+                        (!a.codes.ptr || vec.codes) && vec.weight);
   int ept = 8;
-  while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > kManyRows && a.width > 256 * ept))) ept *= 2;
+  while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > kManyRows && a.width > (spread ? 512 : 256) * ept))) ept *= 2;
   const int threads = std::min(kMaxThreads, ((a.width + ept - 1) / ept + 31) / 32 * 32);
-  auto kern = ept == 8 ? k_norm<T, 8> : ept == 16 ? k_norm<T, 16> : k_norm<T, 32>;
-  return launch_ex(kern, dim3(a.rows), dim3(threads), 0, st, true, 1, a, vec, 1.0 / a.width);
+  auto kern = spread ? ept == 8 ? k_norm<T, 8, true> : ept == 16 ? k_norm<T, 16, true> : k_norm<T, 32, true>
+                     : ept == 8 ? k_norm<T, 8, false> : ept == 16 ? k_norm<T, 16, false> : k_norm<T, 32, false>;
+  return launch_ex(kern, dim3(a.rows), dim3(threads), 0, st, true, 1, a, 1.0 / a.width);
 }
 
 }  // namespace
