@@ -4,9 +4,15 @@
 // k_lin8_few: a cluster of blocks takes a run of rows (any number of them: equal
 // shares to a row) and its blocks split the inputs, as do the 16 warps of a
 // block, so that every code is read once, straight into the registers of the
-// lane that needs it, and a token's codes are held once. Sums leave the tensor
-// cores as whole numbers and meet in shared memory, where the order of
-// additions does not matter.
+// lane that needs it, and a token's codes are held once. A warp takes two or
+// three tiles of 16 rows at a time, so that it widens a token's codes once for
+// all of them. Sums leave the tensor cores as whole numbers and meet in shared
+// memory, where the order of additions does not matter.
+//
+// Measured: 10240 x 8192 for 16 tokens about 20 us, 4.2 TB/s of codes; widening and
+// address arithmetic (38% of issue slots) and the waits for codes that four warps a
+// scheduler do not cover. 4099 x 11008 for five 11 us, 4096 x 4096 for one 6 us, of
+// which a wave's beginning and end are five.
 #include <algorithm>
 
 #include "linear8.cuh"

@@ -343,6 +343,13 @@ def test_select_reports_what_has_no_distribution(sffn):
     check_select(sffn, z, bad, 8, fault=True)
 
 
+@pytest.mark.parametrize("batch,beams,vocab,n_out,dtype", [(40, 16, 60000, 32, "f32"), (77, 8, 70001, 64, "bf16"),
+                                                           (1, 16, 250001, 32, "f16"), (1, 64, 30000, 64, "f32")])
+def test_select_of_long_parts(sffn, batch, beams, vocab, n_out, dtype):
+    """Rows that a block or two take alone, with more that reaches the first chunk's bound than the list holds; many candidates."""
+    check_select(sffn, logits_of(batch * beams, vocab, dtype, 12), scores_of(batch, beams, 12), n_out)
+
+
 def test_select_of_logits_that_rise_and_fall(sffn):
     """Parts whose largest logits come late, or lie far below those before, and references between -2^22 and 2^22."""
     z = logits_of(6, 60000, "f32", 11)
