@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
     if (((c - c0) & 3) == 3) {   // a long list raises the bound: what reaches it of eight warps' entries, as above
       __syncthreads();
       const int listed = s_count;
+      __syncthreads();   // read by all before anything is added
       if (listed > kTighten && listed <= kList) tighten(a, base, listed, s_value, s_token, s_bound, &s_count, bound);
     }
 #pragma unroll

@@ -683,8 +683,8 @@ sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */
  *   weight [width] fp32; codes int8, scales [n_rows] fp32.
  * residual, weight, sum_out, y and (codes, scales) are optional (NULL), but
  * one of y and codes is required. x, residual and sum_out may be the same
- * rows; y may be x, residual or sum_out if it has their type and not both y
- * and sum_out are wanted there; rows must not overlap otherwise. A row whose
+ * rows; y may be x or residual if its elements have their size, but not
+ * sum_out; rows must not overlap otherwise. A row whose
  * y are all 0 has scale 0 and codes 0; a row with a y that is not finite has
  * scale NaN and codes 0. Pointers and strides need only be aligned to their
  * elements (rows on 16 bytes are faster).
