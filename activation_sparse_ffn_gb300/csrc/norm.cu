@@ -455,10 +455,11 @@ cudaError_t launch_typed(const NormArgs& a, cudaStream_t st) {
   }
   // Few rows: as many threads as there are, for the shortest way through one row. Many: blocks of 256, so that an SM
   // holds several and one loads while another waits at its barriers.
+  // Not aligned: 16 elements a thread while they reach, since 32 spill.
   const bool spread = !(vec.x && (!a.residual.ptr || vec.residual) && (!a.sum.ptr || vec.sum) && (!a.y.ptr || vec.y) &&
                         (!a.codes.ptr || vec.codes) && vec.weight);
   int ept = 8;
-  while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > kManyRows && a.width > (spread ? 512 : 256) * ept))) ept *= 2;
+  while (ept < 32 && (a.width > kMaxThreads * ept || (a.rows > kManyRows && a.width > (!spread ? 256 : ept == 8 ? 512 : kMaxThreads) * ept))) ept *= 2;
   const int threads = std::min(kMaxThreads, ((a.width + ept - 1) / ept + 31) / 32 * 32);
   auto kern = spread ? ept == 8 ? k_norm<T, 8, true> : ept == 16 ? k_norm<T, 16, true> : k_norm<T, 32, true>
                      : ept == 8 ? k_norm<T, 8, false> : ept == 16 ? k_norm<T, 16, false> : k_norm<T, 32, false>;
