@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "linear8.cuh"
+#include "linear8_split.h"
 #include "rows_io.cuh"
 #include "step.h"
 #include "tcgen05.cuh"
@@ -52,7 +53,6 @@ constexpr int kSlots = 2, kSlotCols = 64;                // of A in tensor memor
 constexpr int kAccCols = 192, kTmemCols = 512;           // accumulators at 0 and 192, A at 384
 constexpr int kStagesW = 6, kStagesX = 4;                // the first even: a set of warps keeps its own
 constexpr int kStepsExact = kL8Exact / kStep;
-constexpr int kJoinSteps = 20;                           // that take as long as leaving and joining a tile's parts, 8 us
 constexpr int CG = 2;                                    // blocks of a cluster
 
 struct TcArgs {
@@ -66,37 +66,7 @@ struct TcArgs {
   unsigned long long* tickets;   // [tiles left over][CG]
   uint32_t* err;
   int n, B, dtype, steps, nt, token_tiles, tokens;   // nt: tokens of a tile; tokens: token_tiles * nt
-  int groups;                                        // clusters
-  int whole, left, parted;                           // whole waves of tiles, tiles after them, clusters that share those
-};
-
-// What a cluster computes: tiles cluster + i * groups for i < whole, then its share [from, to) of the steps left over.
-struct Segment {
-  int tile, s0, s1;
-  bool part;    // others have the rest of the tile
-  int slot;     // of the workspace, for its sums
-};
-struct Segments {
-  int cluster, i = 0;
-  long long at, to;
-  __device__ Segments(const TcArgs& a, int c) : cluster(c) {
-    const long long units = (long long)a.left * a.steps;
-    at = c < a.parted ? units * c / a.parted : 0, to = c < a.parted ? units * (c + 1) / a.parted : 0;
-  }
-  __device__ bool next(const TcArgs& a, Segment& s) {
-    if (i < a.whole) {
-      s.tile = cluster + i * a.groups, s.s0 = 0, s.s1 = a.steps, s.part = false, s.slot = 0;
-      ++i;
-      return true;
-    }
-    if (at >= to) return false;
-    const int t = (int)(at / a.steps);
-    const long long begin = (long long)t * a.steps, end = min(begin + a.steps, to);
-    s.tile = a.whole * a.groups + t, s.s0 = (int)(at - begin), s.s1 = (int)(end - begin);
-    s.part = s.s1 - s.s0 < a.steps, s.slot = at == (long long)a.left * a.steps * cluster / a.parted ? 0 : 1;
-    at = end;
-    return true;
-  }
+  L8Split split;
 };
 
 // True in one lane of the warp, always the same. The warps that issue copies and products run their loops with every lane
@@ -312,8 +282,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     atomicExch(&s_abort, 1);
   };
   auto aborted = [&]() { return *(volatile int*)&s_abort != 0; };
-  Segments work(a, cluster);
-  Segment seg;
+  L8Segments work(a.split, cluster);
+  L8Segment seg;
 
   if (warp < 2 * kConvWarps) {
     // ------------------------------------------------------------ codes to halves
@@ -325,7 +295,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Ring<kSlots, 2> out(set);
     int it = 0;
     bool ok = true;
-    while (ok && work.next(a, seg)) {
+    while (ok && work.next(a.split, seg)) {
       const int len = seg.s1 - seg.s0;
       for (int k = (it ^ set) & 1; k < len; k += 2) {
         ok = wait_for(&wfull[w.at], w.phase);
@@ -364,7 +334,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int r = q * 32 + lane;
     int chunk = 0;
     bool ok = true;
-    while (ok && work.next(a, seg)) {
+    while (ok && work.next(a.split, seg)) {
       int sum[96];
 #pragma unroll
       for (int i = 0; i < 96; ++i) sum[i] = 0;
@@ -392,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int row_tile = seg.tile / a.token_tiles * CG + rank, token0 = seg.tile % a.token_tiles * a.nt + b0 * 16;
       if (seg.part) {
         // this block's sums to its place; the last to arrive adds the others'
-        const int left = seg.tile - a.whole * a.groups;
+        const int left = seg.tile - a.split.whole * a.split.groups;
         const size_t tile_ints = (size_t)a.nt * kL8Rows, at = (size_t)b0 * 16 * kL8Rows + r;
         int32_t* place = a.parts + ((size_t)blockIdx.x * 2 + seg.slot) * tile_ints + at;
 #pragma unroll
@@ -400,14 +370,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (i / 16 < nb) __stcg(place + (size_t)i * kL8Rows, sum[i]);
         __threadfence();
         epilogue_barrier();
-        // clusters that share the tile: those whose steps reach into it
-        const long long units = (long long)a.left * a.steps, begin = (long long)left * a.steps, end = begin + a.steps;
-        int from = cluster, to = cluster;   // a few each way
-        while (units * from / a.parted > begin) --from;
-        while (units * (to + 1) / a.parted < end) ++to;
+        const L8Sharers sharers = l8_sharers(a.split, left, cluster);
         if (warp == kEpiWarp0 && lane == 0) {
           unsigned long long* word = a.tickets + left * CG + rank;
-          s_last = take_ticket(word) == to - from;
+          s_last = take_ticket(word) == sharers.to - sharers.from;
           if (s_last) *word = kTicketMark;   // for the next call
         }
         epilogue_barrier();
@@ -415,10 +381,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         epilogue_barrier();   // read by all before it is written again
         if (!join) continue;
         __threadfence();
-        for (int c = from; c <= to; ++c) {
+        for (int c = sharers.from; c <= sharers.to; ++c) {
           if (c == cluster) continue;
-          const int slot = units * c / a.parted >= begin ? 0 : 1;   // its first steps are this tile's, or its last
-          const int32_t* other = a.parts + ((size_t)(c * CG + rank) * 2 + slot) * tile_ints + at;
+          const int32_t* other = a.parts + ((size_t)(c * CG + rank) * 2 + l8_slot(a.split, left, c)) * tile_ints + at;
 #pragma unroll
           for (int i = 0; i < 96; ++i)
             if (i / 16 < nb) sum[i] += __ldcg(other + (size_t)i * kL8Rows);
@@ -449,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       Ring<kStagesW, 1> w(0);
       int it = 0;
       bool ok = true;
-      while (ok && work.next(a, seg)) {
+      while (ok && work.next(a.split, seg)) {
         const int row_tile = seg.tile / a.token_tiles * CG + rank;
         const uint8_t* src = a.codes + ((size_t)row_tile * a.steps + seg.s0) * kStepW;
         for (int k = seg.s0; k < seg.s1; ++k, ++it, src += kStepW, w.next()) {
@@ -472,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       Ring<kStagesX, 1> x(0);
       int it = 0;
       bool ok = true;
-      while (ok && work.next(a, seg)) {
+      while (ok && work.next(a.split, seg)) {
         const int token0 = seg.tile % a.token_tiles * a.nt + rank * (a.nt / CG);
         const uint8_t* src = a.xh + ((size_t)seg.s0 * 2 * a.tokens + token0) * 128;
         for (int k = seg.s0; k < seg.s1; ++k, ++it, src += (size_t)a.tokens * 256, x.next()) {
@@ -494,7 +459,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       Ring<kStagesX, 1> x(0);
       Ring<kSlots, 1> slot(0);
       bool ok = true;
-      while (ok && work.next(a, seg))
+      while (ok && work.next(a.split, seg))
         for (int k = seg.s0; ok && k < seg.s1; ++k, x.next(), slot.next()) {
           // a slot's report counts for the product that comes next in it
           ok = wait_for(&xfull[x.at], x.phase) && wait_for(&freed[slot.at], slot.phase ^ 1);
@@ -511,7 +476,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Ring<kSlots, 1> slot(0);
         int chunk = 0;
         bool ok = true;
-        while (ok && work.next(a, seg)) {
+        while (ok && work.next(a.split, seg)) {
           for (int k = seg.s0; ok && k < seg.s1; ++chunk) {
             const int end = min(k + kStepsExact, seg.s1), buf = chunk & 1;
             ok = chunk < 2 || __all_sync(SFFN_FULL_MASK, wait_for(&accempty[buf], (uint32_t)((chunk / 2 - 1) & 1)));
@@ -613,19 +578,14 @@ cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const f
   a.parts = reinterpret_cast<int32_t*>(base + w.parts);
   a.err = L.err, a.n = L.desc.out_features, a.B = B, a.dtype = dtype, a.steps = L.kp / kStep;
   a.nt = s.nt, a.token_tiles = s.token_tiles, a.tokens = s.tokens;
-  a.groups = L.num_sms / CG;
-  const int tiles = L.tiles / CG * a.token_tiles;
-  a.whole = tiles / a.groups, a.left = tiles % a.groups;
-  // sharing the tiles left over makes them shorter by the clusters that would stand idle, and costs a join
-  const bool share = (long long)a.steps * (a.groups - a.left) > (long long)kJoinSteps * a.groups;
-  a.parted = a.left && share ? a.groups : a.left;
+  a.split = l8_split(L.tiles / CG * a.token_tiles, a.steps, L.num_sms / CG);
   const int runs = L.kp / 16;
   const unsigned threads = (unsigned)s.tokens * runs;
   cudaError_t e = launch_ex(k_lin8_widen, dim3((threads + 255) / 256), dim3(256), 0, st, true, 1, x, B, L.desc.in_features,
                             runs, s.tokens, reinterpret_cast<uint4*>(base + w.xh));
   if (e != cudaSuccess) return e;
   const int smem = 1024 + kStagesW * kStepW + kStagesX * (a.nt / CG * 256);
-  return launch_ex(k_lin8_tc, dim3((a.whole ? a.groups : a.parted) * CG), dim3(kTcThreads), smem, st, true, CG, a);
+  return launch_ex(k_lin8_tc, dim3((a.split.whole ? a.split.groups : a.split.parted) * CG), dim3(kTcThreads), smem, st, true, CG, a);
 }
 
 }  // namespace sffn

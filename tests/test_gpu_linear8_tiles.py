@@ -1,0 +1,60 @@
+"""8-bit linear layer for many tokens where few tiles are left over after whole waves: bits
+against a plain implementation."""
+
+import math
+
+import pytest
+import torch
+
+import step_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sffn():
+    import __graft_entry__
+    __graft_entry__.build()
+    from activation_sparse_ffn_gb300 import sffn
+    return sffn
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def layer(sffn, n, k, rows, seed=0):
+    """(layer, x, scales of x, its outputs in fp32, bit by bit)."""
+    g = gen(seed)
+    w = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    x = torch.randint(-128, 128, (rows, k), generator=g, device="cuda", dtype=torch.int8)
+    scales = (0.5 + torch.rand(n, generator=g, device="cuda")) / (5000 * math.sqrt(k))
+    xs, bias = 0.5 + torch.rand(rows, generator=g, device="cuda"), torch.randn(n, generator=g, device="cuda")
+    want = R.linear8(x, R.f32(xs), w, R.f32(scales), R.f32(bias), None, "f32").to("cuda")
+    return sffn.Linear8.from_weights(w, scales, bias, max_batch=rows), x, xs, want
+
+
+# (outputs, inputs, tokens): one to three tiles left over, alone or after whole waves (13 x 76 + 1 tiles)
+TILES = [(256, 4096, 64), (512, 4096, 100), (128, 8192, 192), (256, 8192, 33), (64, 8192, 100), (700, 2688, 150),
+         (256, 65536, 48), (1024, 8192, 64), (11008, 4096, 4300)]
+
+
+@pytest.mark.parametrize("n,k,rows", TILES)
+def test_few_tiles_left_over(sffn, n, k, rows):
+    """Four calls on one workspace, and a layer of another shape after them, whose tickets are the same words."""
+    L, x, xs, want = layer(sffn, n, k, rows)
+    other, x2, xs2, want2 = layer(sffn, 2560, 8192, 64, 1)
+    ws = max((L.workspace(rows), other.workspace(64)), key=len)
+    y, y2 = torch.empty_like(want), torch.empty_like(want2)
+    for _ in range(4):
+        y.fill_(7.0)
+        sffn.sffn_linear8_forward(L.handle, x, xs, y, None, ws)
+        assert torch.equal(y, want)
+    for _ in range(2):
+        y2.fill_(7.0)
+        sffn.sffn_linear8_forward(other.handle, x2, xs2, y2, None, ws)
+        assert torch.equal(y2, want2)
+    L.check_error()
+    other.check_error()

@@ -1,0 +1,78 @@
+"""How the 8-bit linear layer's kernel for many tokens shares its tiles out, without a GPU: the header's arithmetic, which
+the kernel runs too, compiled for the host."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "activation_sparse_ffn_gb300", "csrc")
+
+# Goes through what every cluster computes. Every step of every tile is done once; a tile that is done in parts is joined by
+# exactly the clusters that have some of it, each of which left its part where the others look for it; no cluster has more
+# than one part in a place; all tickets and places lie within the workspace.
+WALK = r"""
+#include <cstdio>
+#include <vector>
+#include "linear8_split.h"
+using namespace sffn;
+
+static long long bad(int tiles, int steps, int groups) {
+  const L8Split w = l8_split(tiles, steps, groups);
+  const int grid = w.whole ? w.groups : w.parted;
+  if (grid < 1 || grid > groups || w.left < 0 || w.left >= groups || w.parted < w.left || w.parted > groups) return 1;
+  std::vector<int> done(tiles), parts(tiles);
+  for (int c = 0; c < grid; ++c) {
+    L8Segments work(w, c);
+    L8Segment s;
+    int used[2] = {0, 0};
+    while (work.next(w, s)) {
+      if (s.tile < 0 || s.tile >= tiles || s.s0 < 0 || s.s1 <= s.s0 || s.s1 > steps) return 2;
+      if (s.s0 > done[s.tile] ) return 3;   // clusters follow each other
+      done[s.tile] += s.s1 - s.s0;
+      if (s.part != (s.s1 - s.s0 < steps)) return 4;
+      if (!s.part) continue;
+      if (s.slot < 0 || s.slot > 1 || used[s.slot]++) return 5;
+      const int left = s.tile - w.whole * w.groups;
+      if (left < 0 || left >= w.left) return 6;
+      const L8Sharers h = l8_sharers(w, left, c);
+      if (h.from < 0 || h.to >= w.parted || h.from > c || h.to < c || h.from == h.to) return 7;
+      ++parts[s.tile];
+      for (int o = h.from; o <= h.to; ++o) {   // each of them has a part of the tile, where this one would look
+        L8Segments other(w, o);
+        L8Segment t;
+        bool found = false;
+        while (other.next(w, t)) found |= t.tile == s.tile && t.part && t.slot == l8_slot(w, left, o);
+        if (!found) return 8;
+      }
+      if (c == h.to && parts[s.tile] != h.to - h.from + 1) return 9;   // arrivals that the last one has counted
+    }
+  }
+  for (int t = 0; t < tiles; ++t)
+    if (done[t] != steps) return 10;
+  return 0;
+}
+
+int main() {
+  long long wrong = 0;
+  const int many[] = {74, 76, 80};
+  for (int groups : many)
+    for (int tiles = 1; tiles <= 2 * groups + 3; ++tiles)
+      for (int steps = 1; steps <= 512; steps += steps < 128 ? 1 : 13) {
+        const long long why = bad(tiles, steps, groups);
+        if (why && ++wrong <= 5) printf("%d tiles of %d steps, %d clusters: %lld\n", tiles, steps, groups, why);
+      }
+  printf("%lld\n", wrong);
+  return wrong != 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
+def test_every_share_that_a_join_counts_has_steps(tmp_path):
+    src, exe = tmp_path / "walk.cpp", tmp_path / "walk"
+    src.write_text(WALK)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
