@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "linear8.cuh"
+#include "linear8_split.h"
 #include "q4mma.cuh"
 #include "rows_io.cuh"
 #include "step.h"
@@ -42,9 +43,6 @@ __global__ void k_pack_rows8(const float* in, float* out, int n, int np) {
 }
 
 constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
-constexpr int kFewTokens = 32;
-constexpr int kFewSmem = 200 * 1024;
-constexpr int kFewRows = 512;      // most rows of a cluster
 
 struct Lin8Args {
   const uint8_t* codes;
@@ -246,22 +244,12 @@ cudaError_t run_few(const Lin8Args& a, int cs, int smem, cudaStream_t st) {
 
 // Up to 32 tokens.
 cudaError_t launch_few(const sffn_linear8& L, Lin8Args a, cudaStream_t st) {
-  const int nt = a.B <= 8 ? 1 : a.B <= 16 ? 2 : 4;
-  // The smallest cluster whose blocks hold their share of the tokens' codes, and larger ones while rows are too few to
-  // give every SM a tile.
-  int cs = 1, smem = 0;
-  for (;; cs *= 2) {
-    const int own = (L.kp / kL8Inputs + cs - 1) / cs * kL8Inputs;
-    a.x_stride = own + (own % 128 ? 0 : 64);
-    a.clusters = std::max(std::min(L.num_sms / cs, (a.n + 15) / 16), (a.n + kFewRows - 1) / kFewRows);
-    const int rows = (a.n + a.clusters - 1) / a.clusters;
-    a.off_sum = 8 * nt * a.x_stride;
-    smem = a.off_sum + rows * 8 * nt * 4;
-    const bool spare = a.n < L.num_sms / cs * 16 && own > 1024;
-    if (cs == 8 || (smem <= kFewSmem && !spare)) break;
-  }
-  if (smem > kFewSmem) return cudaErrorInvalidConfiguration;
-  return nt == 1 ? run_few<1, 2>(a, cs, smem, st) : nt == 2 ? run_few<2, 3>(a, cs, smem, st) : run_few<4, 2>(a, cs, smem, st);
+  const L8Few p = l8_few(a.n, L.kp, a.B, L.num_sms);
+  if (p.smem > kL8FewSmem) return cudaErrorInvalidConfiguration;   // not with l8_few_tokens
+  a.clusters = p.clusters, a.x_stride = p.x_stride, a.off_sum = p.off_sum;
+  return p.nt == 1   ? run_few<1, 2>(a, p.cs, p.smem, st)
+         : p.nt == 2 ? run_few<2, 3>(a, p.cs, p.smem, st)
+                     : run_few<4, 2>(a, p.cs, p.smem, st);
 }
 
 }  // namespace
@@ -291,17 +279,16 @@ cudaError_t configure_linear8_kernels(sffn_linear8& L) {
   return e;
 }
 
-size_t linear8_ws_bytes(const sffn_linear8& L, int B) { return B > kFewTokens ? linear8_tc_ws_bytes(L, B) : 0; }
+size_t linear8_ws_bytes(const sffn_linear8& L, int B) { return B > kL8FewTokens ? linear8_tc_ws_bytes(L, B) : 0; }
 
 cudaError_t launch_linear8(const sffn_linear8& L, const sffn_rows& x, const float* x_scales, int B,
                            const sffn_rows& residual, const sffn_rows& y, int dtype, void* ws, cudaStream_t st) {
-  if (B > kFewTokens) return launch_linear8_tc(L, x, x_scales, B, residual, y, dtype, ws, st);
+  if (B > kL8FewTokens) return launch_linear8_tc(L, x, x_scales, B, residual, y, dtype, ws, st);
   Lin8Args a = {};
   a.codes = L.codes, a.scales = L.scales, a.bias = L.bias, a.n = L.desc.out_features, a.k = L.desc.in_features;
   a.kb = L.kp / kL8Inputs, a.dtype = dtype;
   const int elem = dtype == SFFN_F32 ? 4 : 2;
-  // tokens that a cluster of eight can hold the codes of
-  const int most = std::max(1, std::min(kFewTokens, kFewSmem * 5 / 8 * 8 / (L.kp + 64) / 8 * 8));
+  const int most = l8_few_tokens(a.n, L.kp, L.num_sms);
   for (int b = 0; b < B; b += most) {
     a.B = std::min(most, B - b);
     a.x = x, a.y = y, a.residual = residual, a.x_scales = x_scales + b;

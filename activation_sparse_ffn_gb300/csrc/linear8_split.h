@@ -1,6 +1,8 @@
-// How the 8-bit linear layer's kernel for many tokens shares its tiles out over
-// the clusters: whole waves of tiles first, then the steps of the tiles left
-// over. Plain arithmetic, for the host, the kernel and tests without a GPU.
+// How the 8-bit linear layer shares its work out over clusters of blocks. For
+// many tokens: whole waves of tiles first, then the steps of the tiles left
+// over. For few: rows to clusters, inputs to their blocks, and as many tokens a
+// launch as those hold. Plain arithmetic, for the host, the kernels and tests
+// without a GPU.
 #pragma once
 
 #ifdef __CUDACC__
@@ -74,6 +76,44 @@ SFFN_HD inline L8Sharers l8_sharers(const L8Split& w, int left, int cluster) {
 // Where sharer c of the tile has left its sums: its first steps are this tile's, or its last.
 SFFN_HD inline int l8_slot(const L8Split& w, int left, int c) {
   return (long long)w.left * w.steps * c / w.parted >= (long long)left * w.steps ? 0 : 1;
+}
+
+// ----------------------------------------------------------------- few tokens
+
+constexpr int kL8FewTokens = 32;            // of a launch, at most
+constexpr int kL8FewSmem = 200 * 1024;      // of a block: its inputs of every token, sums of its cluster's rows
+constexpr int kL8FewRows = 512;             // of a cluster, at most
+
+struct L8Few {
+  int nt;                  // column tiles of eight tokens: 1, 2 or 4
+  int cs, clusters;        // blocks of a cluster, clusters
+  int x_stride, off_sum;   // bytes of a token's codes held by a block, and where the sums begin
+  int smem;
+};
+
+// The smallest cluster whose blocks hold their share of the tokens' codes, and larger ones while rows are too few to give
+// every SM a tile. n outputs, kp inputs (a multiple of 128).
+inline L8Few l8_few(int n, int kp, int tokens, int num_sms) {
+  L8Few p = {};
+  p.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
+  for (p.cs = 1;; p.cs *= 2) {
+    const int own = (kp / 64 + p.cs - 1) / p.cs * 64, most = num_sms / p.cs, tiles = (n + 15) / 16;
+    const int least = (n + kL8FewRows - 1) / kL8FewRows;
+    p.x_stride = own + (own % 128 ? 0 : 64);
+    p.clusters = most < tiles ? most : tiles;
+    if (p.clusters < least) p.clusters = least;
+    p.off_sum = 8 * p.nt * p.x_stride;
+    p.smem = p.off_sum + (n + p.clusters - 1) / p.clusters * 8 * p.nt * 4;
+    const bool spare = n < most * 16 && own > 1024;
+    if (p.cs == 8 || (p.smem <= kL8FewSmem && !spare)) return p;
+  }
+}
+
+// Tokens of a launch: 32, 16 or 8, the most that a cluster of eight holds with their padding and the sums (eight always).
+inline int l8_few_tokens(int n, int kp, int num_sms) {
+  int t = kL8FewTokens;
+  while (t > 8 && l8_few(n, kp, t, num_sms).smem > kL8FewSmem) t /= 2;
+  return t;
 }
 
 }  // namespace sffn

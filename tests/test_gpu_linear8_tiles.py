@@ -1,5 +1,5 @@
-"""8-bit linear layer for many tokens where few tiles are left over after whole waves: bits
-against a plain implementation."""
+"""8-bit linear layer for many tokens where few tiles are left over after whole waves, and for
+few where their codes fill a block's shared memory: bits against a plain implementation."""
 
 import math
 
@@ -58,3 +58,16 @@ def test_few_tiles_left_over(sffn, n, k, rows):
         assert torch.equal(y2, want2)
     L.check_error()
     other.check_error()
+
+
+# wide layers whose clusters hold hundreds of rows, for 17 to 32 tokens, which count as 32; 16 of the widest
+@pytest.mark.parametrize("n,k,rows", [(8192, 40960, 24), (5200, 36864, 32), (4561, 42496, 17), (8192, 40960, 16),
+                                      (2000, 65536, 31), (200, 42560, 32), (2000, 65536, 16)])
+def test_few_tokens_of_wide_layers(sffn, n, k, rows):
+    L, x, xs, want = layer(sffn, n, k, rows)
+    y = torch.full((rows, n), 7.0, device="cuda")
+    sffn.sffn_linear8_forward(L.handle, x, xs, y, None, L.workspace(rows))
+    L.check_error()
+    assert torch.equal(y, want)
+    sffn.sffn_linear8_forward(L.handle, x, xs, y, y, L.workspace(rows))            # the residual in y's place
+    assert torch.equal(y, want + want)

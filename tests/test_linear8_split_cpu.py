@@ -1,5 +1,5 @@
-"""How the 8-bit linear layer's kernel for many tokens shares its tiles out, without a GPU: the header's arithmetic, which
-the kernel runs too, compiled for the host."""
+"""How the 8-bit linear layer shares its work out, without a GPU: the header's arithmetic, which the kernel for many tokens
+runs too, compiled for the host."""
 
 import os
 import shutil
@@ -69,10 +69,48 @@ int main() {
 """
 
 
-@pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
-def test_every_share_that_a_join_counts_has_steps(tmp_path):
-    src, exe = tmp_path / "walk.cpp", tmp_path / "walk"
-    src.write_text(WALK)
+def passes(program, tmp_path):
+    src, exe = tmp_path / "program.cpp", tmp_path / "program"
+    src.write_text(program)
     subprocess.run(["g++", "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
+def test_every_share_that_a_join_counts_has_steps(tmp_path):
+    passes(WALK, tmp_path)
+
+
+# Every number of outputs, inputs and tokens that a layer may have fits the blocks' shared memory.
+FIT = r"""
+#include <cstdio>
+#include "linear8_split.h"
+using namespace sffn;
+
+int main() {
+  long long wrong = 0;
+  const int many[] = {148, 152, 160};
+  for (int sms : many)
+    for (int kp = 128; kp <= 65536; kp += 128)
+      for (long long n = 1; n <= 1 << 20; n += n < 8192 ? 37 : n / 5) {
+        const int most = l8_few_tokens((int)n, kp, sms);
+        bool ok = most == 8 || most == 16 || most == 32;
+        for (int tokens = 1; ok && tokens <= most; ++tokens) {
+          const L8Few p = l8_few((int)n, kp, tokens, sms);
+          const int rows = (int)((n + p.clusters - 1) / p.clusters), own = (kp / 64 + p.cs - 1) / p.cs * 64;
+          ok = p.smem <= kL8FewSmem && p.clusters >= 1 && p.clusters <= n && rows <= kL8FewRows && 8 * p.nt >= tokens &&
+               p.x_stride >= own && p.off_sum >= 8 * p.nt * own && p.off_sum % 16 == 0 &&
+               p.smem >= p.off_sum + rows * 8 * p.nt * 4;
+        }
+        if (!ok && ++wrong <= 5) printf("%lld x %d, %d SMs, %d tokens a launch\n", n, kp, sms, most);
+      }
+  printf("%lld\n", wrong);
+  return wrong != 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
+def test_few_tokens_of_every_layer_fit(tmp_path):
+    passes(FIT, tmp_path)
