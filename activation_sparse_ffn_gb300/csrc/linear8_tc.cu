@@ -63,7 +63,7 @@ struct TcArgs {
   const float* x_scales;
   sffn_rows residual, y;
   int32_t* parts;         // [block][2][tokens of a tile][128]
-  unsigned long long* tickets;   // [tiles left over][CG]
+  uint32_t* tickets;      // [tiles left over][CG], zeros from k_lin8_widen: nothing stays of a call that gave up
   uint32_t* err;
   int n, B, dtype, steps, nt, token_tiles, tokens;   // nt: tokens of a tile; tokens: token_tiles * nt
   L8Split split;
@@ -371,11 +371,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __threadfence();
         epilogue_barrier();
         const L8Sharers sharers = l8_sharers(a.split, left, cluster);
-        if (warp == kEpiWarp0 && lane == 0) {
-          unsigned long long* word = a.tickets + left * CG + rank;
-          s_last = take_ticket(word) == sharers.to - sharers.from;
-          if (s_last) *word = kTicketMark;   // for the next call
-        }
+        if (warp == kEpiWarp0 && lane == 0)
+          s_last = (int)atomicAdd(a.tickets + left * CG + rank, 1u) == sharers.to - sharers.from;
         epilogue_barrier();
         const bool join = s_last;
         epilogue_barrier();   // read by all before it is written again
@@ -515,11 +512,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Tokens' codes as halves: inputs 64 k .., token b: 128 bytes at (k * tokens + b) * 128, their 16-byte chunk j (inputs 8 j ..) at
-// chunk position j ^ (b & 7). A thread widens 16 codes.
-__global__ void k_lin8_widen(sffn_rows x, int B, int k, int runs, int tokens, uint4* xh) {
+// chunk position j ^ (b & 7). A thread widens 16 codes. The first clear the tickets, at most 150.
+__global__ void k_lin8_widen(sffn_rows x, int B, int k, int runs, int tokens, uint4* xh, uint32_t* tickets, int n_tickets) {
   pdl_launch_dependents();
   pdl_wait();
   const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;   // at most 65536 tokens of 4096 runs, and a tile's padding
+  if (i < n_tickets) tickets[i] = 0;
   const int b = i / runs, c = i % runs, col = c * 16;
   if (b >= tokens) return;
   uint4 v = make_uint4(0, 0, 0, 0);
@@ -550,7 +548,7 @@ struct TcWs {
 };
 TcWs tc_ws(const sffn_linear8& L, const TcShape& s) {
   TcWs w;
-  w.xh = up256((size_t)L.num_sms * sizeof(unsigned long long));
+  w.xh = up256((size_t)L.num_sms * sizeof(uint32_t));
   w.parts = w.xh + up256((size_t)s.tokens * L.kp * 2);
   const int nt = s.token_tiles > 1 ? kMaxTokens : s.nt;   // the workspace of a batch serves every smaller one
   w.total = w.parts + (size_t)L.num_sms * 2 * nt * kL8Rows * 4;
@@ -574,7 +572,7 @@ cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const f
   uint8_t* base = static_cast<uint8_t*>(ws);
   TcArgs a = {};
   a.codes = L.codes, a.xh = base + w.xh, a.scales = L.scales, a.bias = L.bias, a.x_scales = x_scales;
-  a.residual = residual, a.y = y, a.tickets = static_cast<unsigned long long*>(ws);
+  a.residual = residual, a.y = y, a.tickets = static_cast<uint32_t*>(ws);
   a.parts = reinterpret_cast<int32_t*>(base + w.parts);
   a.err = L.err, a.n = L.desc.out_features, a.B = B, a.dtype = dtype, a.steps = L.kp / kStep;
   a.nt = s.nt, a.token_tiles = s.token_tiles, a.tokens = s.tokens;
@@ -582,7 +580,7 @@ cudaError_t launch_linear8_tc(const sffn_linear8& L, const sffn_rows& x, const f
   const int runs = L.kp / 16;
   const unsigned threads = (unsigned)s.tokens * runs;
   cudaError_t e = launch_ex(k_lin8_widen, dim3((threads + 255) / 256), dim3(256), 0, st, true, 1, x, B, L.desc.in_features,
-                            runs, s.tokens, reinterpret_cast<uint4*>(base + w.xh));
+                            runs, s.tokens, reinterpret_cast<uint4*>(base + w.xh), a.tickets, a.split.left * CG);
   if (e != cudaSuccess) return e;
   const int smem = 1024 + kStagesW * kStepW + kStagesX * (a.nt / CG * 256);
   return launch_ex(k_lin8_tc, dim3((a.split.whole ? a.split.groups : a.split.parted) * CG), dim3(kTcThreads), smem, st, true, CG, a);

@@ -71,3 +71,18 @@ def test_few_tokens_of_wide_layers(sffn, n, k, rows):
     assert torch.equal(y, want)
     sffn.sffn_linear8_forward(L.handle, x, xs, y, y, L.workspace(rows))            # the residual in y's place
     assert torch.equal(y, want + want)
+
+
+@pytest.mark.parametrize("pattern", [0, -1, 0x9e3779b900000000 - 2 ** 64, 0x9e3779b900000007 - 2 ** 64])
+def test_workspace_of_any_contents(sffn, pattern):
+    """A workspace needs no initialisation, whatever a call that gave up, or another operator, has left in it."""
+    for n, k, rows in ((1024, 8192, 64), (10240, 2048, 150), (2560, 8192, 64)):
+        L, x, xs, want = layer(sffn, n, k, rows, 2)
+        ws = L.workspace(rows)
+        y = torch.empty_like(want)
+        for _ in range(2):
+            y.fill_(7.0)
+            ws.view(torch.int64).fill_(pattern)
+            sffn.sffn_linear8_forward(L.handle, x, xs, y, None, ws)
+            assert torch.equal(y, want)
+        L.check_error()
