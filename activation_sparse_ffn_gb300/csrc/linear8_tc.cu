@@ -186,9 +186,6 @@ __device__ __forceinline__ void tmem_load16(uint32_t t, float* v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The barrier of the eight warps that take the sums.
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 template <typename T>
 __device__ __forceinline__ T from_float(float v);
 // An element as its bits. The load stays where it is written: brought forward, all 96 of an output's residuals would want
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* smem = dyn_smem + (1024 - (smem_u32(dyn_smem) & 1023)) % 1024;   // the swizzle counts from there
   __shared__ uint64_t wfull[kStagesW], wempty[kStagesW], xfull[kStagesX], xempty[kStagesX];
-  __shared__ uint64_t ready[kSlots], freed[kSlots], accfull[2], accempty[2], drain;
+  __shared__ uint64_t ready[kSlots], freed[kSlots], accfull[2], accempty[2], drain, meeting;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_last;
   const int tid = threadIdx.x, warp = __shfl_sync(SFFN_FULL_MASK, tid >> 5, 0), lane = tid & 31;
@@ -265,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int s = 0; s < kStagesX; ++s) mbar_init(&xfull[s], 1), mbar_init(&xempty[s], 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], (kConvWarps + 1) * CG), mbar_init(&freed[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&accfull[s], 1), mbar_init(&accempty[s], kEpiWarps * CG);
-    mbar_init(&drain, 1);
+    mbar_init(&drain, 1), mbar_init(&meeting, kEpiWarps);
     fence_mbar_init();
     s_abort = 0;
   }
@@ -332,8 +329,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int b0 = half ? (blocks + 1) / 2 : 0, nb = half ? blocks - b0 : (blocks + 1) / 2;   // of 16 tokens, at most 6
     const uint32_t mine = tmem + ((uint32_t)(q * 32) << 16) + b0 * 16;
     const int r = q * 32 + lane;
-    int chunk = 0;
+    int chunk = 0, met = 0;
     bool ok = true;
+    auto meet = [&]() {   // of the eight warps, one of which may have given up
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meeting);
+      return __all_sync(SFFN_FULL_MASK, wait_for(&meeting, (uint32_t)(met++ & 1)));
+    };
     while (ok && work.next(a.split, seg)) {
       int sum[96];
 #pragma unroll
@@ -369,13 +371,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 96; ++i)
           if (i / 16 < nb) __stcg(place + (size_t)i * kL8Rows, sum[i]);
         __threadfence();
-        epilogue_barrier();
+        ok = meet();
         const L8Sharers sharers = l8_sharers(a.split, left, cluster);
-        if (warp == kEpiWarp0 && lane == 0)
+        if (ok && warp == kEpiWarp0 && lane == 0)
           s_last = (int)atomicAdd(a.tickets + left * CG + rank, 1u) == sharers.to - sharers.from;
-        epilogue_barrier();
+        ok = ok && meet();
         const bool join = s_last;
-        epilogue_barrier();   // read by all before it is written again
+        ok = ok && meet();   // read by all before it is written again
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
         if (!join) continue;
         __threadfence();
         for (int c = sharers.from; c <= sharers.to; ++c) {

@@ -114,3 +114,15 @@ int main() {
 @pytest.mark.skipif(shutil.which("g++") is None, reason="no g++")
 def test_few_tokens_of_every_layer_fit(tmp_path):
     passes(FIT, tmp_path)
+
+
+def test_warps_that_may_give_up_alone_do_not_wait_for_each_other_without_a_limit():
+    """Between the kernel's first and last block barriers, which every thread meets, all waits are wait_for's."""
+    with open(os.path.join(CSRC, "linear8_tc.cu")) as f:
+        text = f.read()
+    kernel = text[text.index("k_lin8_tc(const __grid_constant__"):text.index("__global__ void k_lin8_widen")]
+    roles = kernel[kernel.index("fewer_registers<88>"):kernel.rindex("__syncwarp();")]
+    assert roles.count("wait_for(") >= 8
+    for name in ("__syncthreads", "cluster_sync_all", "_barrier(", "bar.sync", "mbar_try_wait", "while (true", "for (;;"):
+        assert name not in roles, name
+    assert "bar.sync" not in text
