@@ -494,17 +494,18 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
         }
         ref = top * kLn2 + peak * kLeftOver;
       } else {
-        // some part's own largest is its reference: in the measure of logits
+        // some part's own largest is its reference: all in the measure of logits, with what rounding log2 e left
+        auto reference = [](const float4& s) { return s.z == (float)kWhole ? s.x * kLn2 + s.w * kLeftOver : (double)s.x; };
         double most = -INFINITY;
         for (int c = lane; c < a.parts; c += 32) {
           const float4 s = c < 32 ? first : __ldcg(sums + c);
-          if (s.z != (float)kNothing) most = fmax(most, s.z == (float)kWhole ? s.x * kLn2 : (double)s.x);
+          if (s.z != (float)kNothing) most = fmax(most, reference(s));
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(SFFN_FULL_MASK, most, o));
         for (int c = lane; c < a.parts; c += 32) {
           const float4 s = c < 32 ? first : __ldcg(sums + c);
-          if (s.z != (float)kNothing) sum += s.y * exp((s.z == (float)kWhole ? s.x * kLn2 : (double)s.x) - most);
+          if (s.z != (float)kNothing) sum += s.y * exp(reference(s) - most);
         }
         ref = most;
       }

@@ -1,0 +1,47 @@
+"""Sums of exponentials of the choice of continuations where they are hard to keep exact."""
+
+import numpy as np
+import pytest
+import torch
+
+import step_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sffn():
+    import __graft_entry__
+    __graft_entry__.build()
+    from activation_sparse_ffn_gb300 import sffn
+    return sffn
+
+
+def select(sffn, logits, scores, n_out):
+    """(scores float64, parents, tokens) as numpy arrays."""
+    batch, beams = scores.shape
+    H = sffn.Beams(logits.shape[1], beams, n_out, max_batch=batch)
+    out = torch.empty(batch, n_out, device="cuda")
+    parents, tokens = torch.empty(2, batch, n_out, dtype=torch.int32, device="cuda")
+    sffn.sffn_beam_select(H.handle, logits, scores, out, parents, tokens, ws=H.workspace(batch))
+    H.check_error()
+    return out.double().cpu().numpy(), parents.cpu().numpy(), tokens.cpu().numpy()
+
+
+# masks that leave whole parts of a row far below every other logit: those parts take their own largest as reference
+@pytest.mark.parametrize("mask", [-1e9, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("at", [0.0, 1000.0, -2000.0, 4.0e6])
+def test_masked_parts_beside_large_logits(sffn, at, mask):
+    """Off by no more than a row without such parts. What rounding log2 e to a float left (1.3e-8 of each logit, 1.3e-5 at
+    1000) is put right in the other parts too."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    z = 2.5 * torch.randn(2, 60000, generator=g, device="cuda") + at
+    z[0, :40000] = mask
+    z[1, 20000:] = mask
+    scores = torch.tensor([[-0.5, -0.75]], device="cuda")
+    out, parents, tokens = select(sffn, z, scores, 8)
+    want, wp, wt = R.select(z.double().cpu().numpy(), scores[0].double().cpu().numpy(), 8)
+    np.testing.assert_array_equal(parents[0], wp)
+    np.testing.assert_array_equal(tokens[0], wt)
+    assert (np.abs(out[0] - want) <= R.LSE_OFF + 2.0 ** -24 * np.abs(want)).all()
