@@ -11,7 +11,10 @@
 // of itself, which a logit of 20 makes 2^-21; what the rounding left is put right
 // for the part's largest z at the end, by one product. Above |z| = 2^22 a
 // whole number no longer lies near enough: such a part is summed again, its
-// largest z the reference.
+// largest z the reference. A thread adds up a chunk's terms in a tree and the chunks
+// with what each addition rounds off (one running sum of a vocabulary of 2^20 was off
+// by 2^-16), so that a sum has at most 17 roundings: 5 + 2 of a thread, 2 of its
+// pair, 8 of the block.
 //
 // The n_out best. A bound that at least n_out elements of the first chunk reach,
 // and few others: the ceil(n_out / 8)-th largest of the lanes' own maxima, in
@@ -23,7 +26,7 @@
 // reach the bound for the list, a search over all bits and then over indices,
 // which reads the logits again, takes exactly the first of them.
 //
-// Measured: 32 x 8 rows of 131072 bf16 logits 28 us and the merge, 30 us of a graph;
+// Measured: 32 x 8 rows of 131072 bf16 logits 28 us and the merge, 29 us of a graph back to back;
 // half of the issue slots busy, the exponentials' unit a third of the time. Four
 // rows of 32000, one alive, 11 us: two launches and their dependent reads.
 #include <algorithm>
@@ -101,6 +104,7 @@ constexpr float kLog2eHi = 1.44269502f;           // log2(e) rounded
 constexpr double kLeftOver = 1.33497581575e-8;     // (log2(e) - kLog2eHi) * ln 2
 constexpr double kLn2 = 0.6931471805599453;
 constexpr float kWholeLimit = 0x1p22f;
+constexpr float kAbove = 8.f;   // how far above its reference a thread's logits go, times log2 e: arguments are rounded to 2^-21 there
 
 enum PartMode { kNothing = 0, kWhole = 1, kOwnMax = 2, kBad = 3 };
 
@@ -186,9 +190,19 @@ __device__ __forceinline__ float element(const uint4& v, int j) {
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Adds p to s, what the rounding left to `rest`, which goes into the next addition.
+__device__ __forceinline__ void add_with_rest(float& s, float& rest, float p) {
+  const float y = __fadd_rn(p, rest), t = __fadd_rn(s, y);
+  rest = __fadd_rn(__fsub_rn(s, t), y), s = t;
+}
+__device__ __forceinline__ void add_with_rest(float2& s, float2& rest, float2 p) {
+  const float2 y = __fadd2_rn(p, rest), t = __fadd2_rn(s, y);
+  rest = __fadd2_rn(__ffma2_rn(t, make_float2(-1.f, -1.f), s), y), s = t;
+}
+
 // Largest logit of a range and, relative to it, the sum of exponentials: for logits that are far from 0, or none.
 __device__ __noinline__ float2 far_sum(const Range c, float* red) {
-  float m = -INFINITY, sum = 0.f;
+  float m = -INFINITY, sum = 0.f, rest = 0.f;
   for (int i = c.from + threadIdx.x; i < c.to; i += kThreads) m = fmaxf(m, c.at(i));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(SFFN_FULL_MASK, m, o));
@@ -196,9 +210,9 @@ __device__ __noinline__ float2 far_sum(const Range c, float* red) {
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
   for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
-  for (int i = c.from + threadIdx.x; i < c.to; i += kThreads) sum += exp2_fast((c.at(i) - m) * kLog2eHi);
+  for (int i = c.from + threadIdx.x; i < c.to; i += kThreads) add_with_rest(sum, rest, exp2_fast((c.at(i) - m) * kLog2eHi));
   __syncthreads();
-  return make_float2(m, block_sum(sum, red));
+  return make_float2(m, block_sum(sum + rest, red));
 }
 
 // Largest element of 16 bytes; NaN aside.
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
   load(c0, v);
   // of this thread; until something is above -2^22 the reference is there, and nothing adds to the sum
   float ref = -kWholeLimit, most = -INFINITY;
-  float2 sum2 = make_float2(0.f, 0.f);
+  float2 sum2 = make_float2(0.f, 0.f), rest2 = sum2;
   uint32_t bound = 0;   // what an element has to reach
   for (int c = c0; c < c1; ++c) {
     uint4 nv[kRuns];
@@ -319,20 +333,27 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
     // -- sum of exponentials; a masked logit's is 0, that of no number is none
     if (top > most) {
       const float near = rintf(top * kLog2eHi);
-      if (top >= -kWholeLimit && (most < -kWholeLimit || near > ref + 64.f)) {
+      if (top >= -kWholeLimit && (most < -kWholeLimit || near > ref + kAbove)) {
         const float down = power_of_two(ref - near);
-        sum2.x *= down, sum2.y *= down, ref = near;
+        sum2.x *= down, sum2.y *= down, rest2.x *= down, rest2.y *= down, ref = near;
       }
       most = top;
     }
     const float2 hi = make_float2(kLog2eHi, kLog2eHi), off = make_float2(-ref, -ref);
+    auto term = [&](int r, int j) {
+      const float2 x = __ffma2_rn(make_float2(element<T>(v[r], j), element<T>(v[r], j + 1)), hi, off);
+      return make_float2(exp2_fast(x.x), exp2_fast(x.y));
+    };
+    float2 chunk = make_float2(0.f, 0.f), pair = chunk;
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r)
+    for (int r = 0; r < kRuns; ++r) {
+      float2 run = term(r, 0);
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 x = __ffma2_rn(make_float2(element<T>(v[r], j), element<T>(v[r], j + 1)), hi, off);
-        sum2 = __fadd2_rn(sum2, make_float2(exp2_fast(x.x), exp2_fast(x.y)));
-      }
+      for (int j = 2; j < N; j += 2) run = __fadd2_rn(run, term(r, j));
+      pair = r & 1 ? __fadd2_rn(pair, run) : run;
+      if (r & 1) chunk = r == 1 ? pair : __fadd2_rn(chunk, pair);
+    }
+    add_with_rest(sum2, rest2, chunk);
     // -- what may be among the best
     const uint32_t best = top > -INFINITY ? ordered(top) : 0u;
     if (bound == 0) {   // at the first chunk, and until one has enough elements; before that, everything goes
@@ -431,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) bref = fmaxf(bref, s_red[w]), bmost = fmaxf(bmost, s_red[kWarps + w]);
   __syncthreads();
-  float sum = block_sum((sum2.x + sum2.y) * power_of_two(ref - bref), s_red);
+  float sum = block_sum(((sum2.x + sum2.y) + (rest2.x + rest2.y)) * power_of_two(ref - bref), s_red);
   int mode = bmost == -INFINITY ? kNothing : kWhole;
   if (fabsf(bmost) > kWholeLimit && mode == kWhole) {
     const Range all = {a.logits.ptr, base, c0 * kChunk, min(c1 * kChunk, a.vocab), a.dtype};

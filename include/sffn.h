@@ -771,9 +771,9 @@ size_t sffn_beam_workspace_bytes(const sffn_beam* beam, int32_t batch);
  * +infinity, have none either and set the handle's device error word.
  * out_scores fp32, out_parents (j) and out_tokens (v) [batch][n_out]; places
  * that nothing is left for have score -infinity, parent 0 and token 0.
- * Exponentials are summed in fp32 (a logarithm of a sum is good to about
- * 2^-22), totals compared in 64 bits; the same arguments give the same bits
- * at every call.
+ * Exponentials are summed in fp32 with what additions round off (a logarithm
+ * of a sum is good to about 2^-22, and to 2^-18 whatever the logits), totals
+ * compared in 64 bits; the same arguments give the same bits at every call.
  * out_scores may be `scores` if n_out is `beams`. Errors: INVALID_ARG, CUDA. */
 sffn_status sffn_beam_select(const sffn_beam* beam, sffn_rows logits, const float* scores, const uint8_t* done,
                              int32_t end_token, int32_t batch, float* out_scores, int32_t* out_parents,

@@ -1,5 +1,7 @@
 """Sums of exponentials of the choice of continuations where they are hard to keep exact."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -45,3 +47,29 @@ def test_masked_parts_beside_large_logits(sffn, at, mask):
     np.testing.assert_array_equal(parents[0], wp)
     np.testing.assert_array_equal(tokens[0], wt)
     assert (np.abs(out[0] - want) <= R.LSE_OFF + 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("at", [0.02, -0.05, 0.12, -0.18])
+def test_equal_logits_over_a_long_row(sffn, dtype, at):
+    """64 rows that a block each takes alone. Equal terms are rounded the same way at every addition, so that one running
+    sum of a lane's 2048 was off by 2^-16. Now: 17 roundings of 2^-24, an argument below 8 rounded to 2^-22 (times log 2),
+    an exponential good to 2^-22: together below 2^-19."""
+    beams, vocab = 64, 1 << 20
+    z = torch.full((beams, vocab), at, dtype=R.TORCH[dtype], device="cuda")
+    out, parents, tokens = select(sffn, z, torch.full((1, beams), -1.0, device="cuda"), 64)
+    want = -1.0 - math.log(vocab)
+    assert (parents == 0).all() and (tokens == np.arange(64)).all()
+    assert np.abs(out - want).max() <= 2.0 ** -19 + 2.0 ** -24 * abs(want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_equal_logits_far_from_zero(sffn, dtype):
+    """The same beyond 2^22, where a part is summed again, its largest logit the reference."""
+    beams, vocab = 64, 1 << 20
+    z = torch.full((beams, vocab), -1e9, dtype=R.TORCH[dtype], device="cuda")
+    z[:, ::3] = z[:, ::3] * 2                                   # nothing beside the others
+    out, parents, tokens = select(sffn, z, torch.full((1, beams), -1.0, device="cuda"), 64)
+    want = -1.0 - math.log(vocab - len(range(0, vocab, 3)))
+    assert (parents == 0).all() and (tokens == [i for i in range(100) if i % 3][:64]).all()
+    assert np.abs(out - want).max() <= 2.0 ** -19 + 2.0 ** -24 * abs(want)
