@@ -463,6 +463,12 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
   if (tid == 0) a.sums[slot] = make_float4(bref, sum, (float)mode, bmost);
 }
 
+// What decides between equal totals, the smallest first: beam, logit (the largest first, where a large score swallows what
+// sets totals apart), token.
+__device__ __forceinline__ unsigned long long place_of(int j, int logit, int token) {
+  return (unsigned long long)j << 56 | (unsigned long long)~ordered(__int_as_float(logit)) << 24 | (unsigned)token;
+}
+
 __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) {
   constexpr int kWarps = kMergeThreads / 32;
   __shared__ double s_lse[kMaxBeams];      // log of the row's sum
@@ -472,8 +478,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   __shared__ int s_int[32], s_count;
   __shared__ float s_top[kWarps];
   __shared__ int s_steps[kSteps], s_step;
-  __shared__ unsigned long long s_key[kList];
-  __shared__ int s_place[kList][2];
+  __shared__ unsigned long long s_key[kList], s_place[kList];
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -565,22 +570,23 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
     keys[i] = candidate(tid + i * kMergeThreads, kept[i], j, token);
     values[i] = keys[i] ? (float)number(keys[i]) : -INFINITY;
   }
-  auto each = [&](auto&& take) {   // take(pattern, value, j, token)
+  auto each = [&](auto&& take) {   // take(pattern, value, place())
 #pragma unroll
     for (int i = 0; i < kKept; ++i)
       if (keys[i]) {
         const int j = (tid + i * kMergeThreads) / per_row;
-        take(keys[i], values[i], j, s_done[j] ? a.end_token : kept[i].y);
+        take(keys[i], values[i], [&] { return s_done[j] ? place_of(j, 0, a.end_token) : place_of(j, kept[i].x, kept[i].y); });
       }
     for (int e = tid + kKept * kMergeThreads; e < entries; e += kMergeThreads) {
       int j, token;
-      const unsigned long long o = candidate(e, fetch(e), j, token);
-      if (o) take(o, (float)number(o), j, token);
+      const int2 f = fetch(e);
+      const unsigned long long o = candidate(e, f, j, token);
+      if (o) take(o, (float)number(o), [&] { return place_of(j, s_done[j] ? 0 : f.x, token); });
     }
   };
   // a bound that n_out totals reach and few others: how many lie how far below the largest, in steps of 1/16
   float best = -INFINITY;
-  each([&](unsigned long long, float v, int, int) { best = fmaxf(best, v); });
+  each([&](unsigned long long, float v, auto) { best = fmaxf(best, v); });
 #pragma unroll
   for (int o = 16; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(SFFN_FULL_MASK, best, o));
   if (lane == 0) s_top[warp] = best;
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) best = fmaxf(best, s_top[w]);
   auto step_of = [&](float v) { return (int)fminf((best - v) * 16.f, kSteps - 1.f); };
-  each([&](unsigned long long, float v, int, int) { atomicAdd(&s_steps[step_of(v)], 1); });
+  each([&](unsigned long long, float v, auto) { atomicAdd(&s_steps[step_of(v)], 1); });
   __syncthreads();
   if (warp == 0) {
     int n = 0, at = kSteps - 1;
@@ -610,34 +616,33 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   }
   __syncthreads();
   const int last_step = s_step;   // the last of all has no end
-  each([&](unsigned long long o, float v, int j, int token) {
+  each([&](unsigned long long o, float v, auto place) {
     if (step_of(v) <= last_step) {
       const int n = atomicAdd(&s_count, 1);
-      if (n < kList) s_key[n] = o, s_place[n][0] = j, s_place[n][1] = token;
+      if (n < kList) s_key[n] = o, s_place[n] = place();
     }
   });
   __syncthreads();
   int n = s_count;
   if (n > kList) {
-    auto reach = [&](unsigned long long t, long long last) {
+    auto reach = [&](unsigned long long t, unsigned long long last) {
       int c = 0;
-      each([&](unsigned long long o, float, int j, int token) {
-        c += o > t || (o == t && (long long)j * a.vocab + token <= last);
-      });
+      each([&](unsigned long long o, float, auto place) { c += o > t || (o == t && place() <= last); });
       return block_sum(c, s_int);
     };
     unsigned long long t = 0;
     for (int i = 63; i >= 0; --i)
-      if (reach(t | 1ull << i, LLONG_MAX) >= a.n_out) t |= 1ull << i;
-    long long last = 0;
-    for (int i = 32; i >= 0; --i)
-      if (reach(t, last + (1ll << i) - 1) < a.n_out) last += 1ll << i;
+      if (reach(t | 1ull << i, ~0ull) >= a.n_out) t |= 1ull << i;
+    unsigned long long last = 0;   // the smallest place with which there are enough
+    for (int i = 61; i >= 0; --i)
+      if (reach(t, last + (1ull << i) - 1) < a.n_out) last += 1ull << i;
     if (tid == 0) s_count = 0;
     __syncthreads();
-    each([&](unsigned long long o, float, int j, int token) {
-      if (o > t || (o == t && (long long)j * a.vocab + token <= last)) {
+    each([&](unsigned long long o, float, auto place) {
+      const unsigned long long p = place();
+      if (o > t || (o == t && p <= last)) {
         const int k = atomicAdd(&s_count, 1);
-        if (k < kList) s_key[k] = o, s_place[k][0] = j, s_place[k][1] = token;
+        if (k < kList) s_key[k] = o, s_place[k] = p;
       }
     });
     __syncthreads();
@@ -645,15 +650,16 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) 
   }
   const size_t out = (size_t)b * a.n_out;
   for (int i = tid; i < n; i += kMergeThreads) {
-    const unsigned long long v = s_key[i];
-    const int pj = s_place[i][0], pt = s_place[i][1];
+    const unsigned long long v = s_key[i], p = s_place[i];
     int ahead = 0;
     for (int k = 0; k < n; ++k) {
       const unsigned long long o = s_key[k];
-      ahead += o > v || (o == v && (s_place[k][0] < pj || (s_place[k][0] == pj && s_place[k][1] < pt)));
+      ahead += o > v || (o == v && s_place[k] < p);
     }
-    if (ahead < a.n_out)
-      a.out_scores[out + ahead] = (float)number(v), a.out_parents[out + ahead] = pj, a.out_tokens[out + ahead] = pt;
+    if (ahead < a.n_out) {
+      a.out_scores[out + ahead] = (float)number(v);
+      a.out_parents[out + ahead] = (int)(p >> 56), a.out_tokens[out + ahead] = (int)(p & 0xffffff);
+    }
   }
   for (int i = n + tid; i < a.n_out; i += kMergeThreads)
     a.out_scores[out + i] = -INFINITY, a.out_parents[out + i] = 0, a.out_tokens[out + i] = 0;

@@ -745,7 +745,9 @@ void sffn_linear8_destroy(sffn_linear8* linear);
 /* The n_out best continuations of each of `batch` searches with `beams`
  * sequences each, over a vocabulary: with z = logits[b * beams + j],
  *   total[j][v] = scores[b][j] + z[v] - log sum_u exp(z[u]),
- * the n_out largest by (total, then lowest j * vocab + v), largest first.
+ * the n_out largest by (total, then lowest j * vocab + v), largest first. Of
+ * one sequence a larger logit goes first also where its score is so large that
+ * totals in 64 bits are equal.
  *   vocab: 1 .. 2^24.  beams: 1 .. 64.  n_out: 1 .. 64.
  *   max_batch: largest batch the handle will be called with, at least 1, max_batch * beams at most 65535. */
 typedef struct {
@@ -770,7 +772,8 @@ size_t sffn_beam_workspace_bytes(const sffn_beam* beam, int32_t batch);
  * chosen). Logits with a NaN or +infinity, or a score that is NaN or
  * +infinity, have none either and set the handle's device error word.
  * out_scores fp32, out_parents (j) and out_tokens (v) [batch][n_out]; places
- * that nothing is left for have score -infinity, parent 0 and token 0.
+ * that nothing is left for have score -infinity, parent 0 and token 0 (a total
+ * below fp32's range has score -infinity too, but its parent and token).
  * Exponentials are summed in fp32 with what additions round off (a logarithm
  * of a sum is good to about 2^-22, and to 2^-18 whatever the logits), totals
  * compared in 64 bits; the same arguments give the same bits at every call.

@@ -73,3 +73,32 @@ def test_equal_logits_far_from_zero(sffn, dtype):
     want = -1.0 - math.log(vocab - len(range(0, vocab, 3)))
     assert (parents == 0).all() and (tokens == [i for i in range(100) if i % 3][:64]).all()
     assert np.abs(out - want).max() <= 2.0 ** -19 + 2.0 ** -24 * abs(want)
+
+
+@pytest.mark.parametrize("score", [-1e9, -1e30, torch.finfo(torch.float32).min, 1e30])
+@pytest.mark.parametrize("vocab,n_out", [(60000, 12), (3000, 64)])
+def test_scores_that_swallow_the_logits(sffn, score, vocab, n_out):
+    """Of one sequence the largest logits go on, in their order, whatever its score and however many parts its row has."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    z = 1e-3 * torch.randn(6, vocab, generator=g, device="cuda")
+    z[0, ::7] = z[0, 5]                                         # ties of logits go to the lowest token
+    order = [np.lexsort((np.arange(vocab), -r))[:n_out] for r in z.double().cpu().numpy()]
+    alone = torch.full((6, 1), score, device="cuda")
+    for batch in (6, 1):
+        out, parents, tokens = select(sffn, z[:batch], alone[:batch], n_out)
+        assert (parents == 0).all() and (out[np.isfinite(out)] == alone[0].item()).all()
+        np.testing.assert_array_equal(tokens, order[:batch])
+    out, parents, tokens = select(sffn, z, alone.view(1, 6), n_out)
+    if score != -1e9:                                           # whose totals differ by sequence
+        assert (parents == 0).all()
+        np.testing.assert_array_equal(tokens[0], order[0])
+
+
+def test_many_candidates_of_one_total(sffn):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    z = torch.randn(16, 60000, generator=g, device="cuda")
+    out, parents, tokens = select(sffn, z, torch.full((1, 16), -1e30, device="cuda"), 32)
+    assert (parents == 0).all()
+    np.testing.assert_array_equal(tokens[0], np.argsort(-z[0].cpu().numpy(), kind="stable")[:32])
