@@ -322,7 +322,7 @@ __device__ __forceinline__ void unpack16(const uint4& v, float* o) {
 template <typename T, int EPT>
 __global__ void __launch_bounds__(256, EPT == 32 ? 2 : 4) k_norm_many(const NormArgs a, double inv_width) {
   constexpr int N = kRun<T>, RUNS = EPT / N;
-  extern __shared__ float weights[];
+  extern __shared__ __align__(16) float weights[];
   __shared__ float red[97];
   pdl_launch_dependents();
   pdl_wait();
