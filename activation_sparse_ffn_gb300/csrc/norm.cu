@@ -46,8 +46,8 @@ __device__ __forceinline__ void block_reduce(float& s, float& c, uint32_t& top, 
   // lanes may differ in the last bits of c: the block goes by the first's
   s = __shfl_sync(SFFN_FULL_MASK, s, 0), c = __shfl_sync(SFFN_FULL_MASK, c, 0);
   top = __reduce_max_sync(SFFN_FULL_MASK, top);
-  if (warps == 1) return;
-  __syncthreads();   // red may still be read from an earlier call
+  if (warps == 1) return __syncwarp();   // red may still be read from an earlier row, here and below
+  __syncthreads();
   if (lane == 0) red[warp] = s, red[32 + warp] = c, red[64 + warp] = __uint_as_float(top);
   __syncthreads();
   s = lane < warps ? red[lane] : 0.f;
