@@ -896,6 +896,8 @@ def sffn_kv_reorder(caches: "KvCaches", batch: "KvBatch", parents, beams, table_
     """Reorder the caches (KvCaches) by parents (n_seq,) int32: page ids of batch.table go to table_out (the table itself if None),
     the filled part of every sequence's last page to the page it keeps."""
     n_seq, out, stride = batch.c.n_seq, batch.table, batch.c.table_stride
+    if None in [c.handle for c in caches.caches]:
+        raise ValueError("caches: one of them is closed")
     if table_out is not None and table_out is not out:
         out = table_out
         if out.dtype is not torch.int32 or out.shape != batch.table.shape or out.shape[1] > 1 and out.stride(1) != 1:
