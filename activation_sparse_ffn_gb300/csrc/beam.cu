@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) k_beam_rows(const BeamAr
   __syncthreads();
   float sum = block_sum(((sum2.x + sum2.y) + (rest2.x + rest2.y)) * power_of_two(ref - bref), s_red);
   int mode = bmost == -INFINITY ? kNothing : kWhole;
-  if (fabsf(bmost) > kWholeLimit && mode == kWhole) {
+  // below -2^22 a thread has no reference, so that its logits count for nothing: 256 above it they do
+  if ((bmost > kWholeLimit || bmost < 256.f - kWholeLimit) && mode == kWhole) {
     const Range all = {a.logits.ptr, base, c0 * kChunk, min(c1 * kChunk, a.vocab), a.dtype};
     const float2 f = far_sum(all, s_red);
     bref = bmost = f.x, sum = f.y, mode = kOwnMax;

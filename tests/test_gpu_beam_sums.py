@@ -102,3 +102,17 @@ def test_many_candidates_of_one_total(sffn):
     out, parents, tokens = select(sffn, z, torch.full((1, 16), -1e30, device="cuda"), 32)
     assert (parents == 0).all()
     np.testing.assert_array_equal(tokens[0], np.argsort(-z[0].cpu().numpy(), kind="stable")[:32])
+
+
+@pytest.mark.parametrize("above", [0.5, 8.0, 255.0, 300.0])
+@pytest.mark.parametrize("limit", [-2.0 ** 22, 2.0 ** 22])
+def test_logits_around_the_last_whole_reference(sffn, above, limit):
+    """One logit on one side of 2^22 in size, all others on the other, 1.5 below it."""
+    z = torch.full((2, 5000), limit + above - 1.5, device="cuda")
+    z[:, 777] = limit + above
+    z[1, 1000:] = limit - 2.0
+    out, parents, tokens = select(sffn, z, torch.tensor([[-1.0, -1.5]], device="cuda"), 3)
+    want, wp, wt = R.select(z.double().cpu().numpy(), np.array([-1.0, -1.5]), 3)
+    np.testing.assert_array_equal(parents[0], wp)
+    np.testing.assert_array_equal(tokens[0], wt)
+    assert (np.abs(out[0] - want) <= R.LSE_OFF + 2.0 ** -24 * np.abs(want)).all()
