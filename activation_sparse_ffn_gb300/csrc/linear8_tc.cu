@@ -25,10 +25,10 @@
 // a tile leaves its sums in the workspace, and whichever comes last adds them:
 // whole numbers, so that the order does not matter.
 //
-// Measured: 10240 x 8192 for 4096 tokens 375 us, 1.83 PFLOP/s of halves, the tensor
+// Measured: 10240 x 8192 for 4096 tokens 370 us, 1.86 PFLOP/s of halves, the tensor
 // cores active 80% of the time (a step takes 845 cycles, its products 768); for 150
-// tokens 33 us, of which the steps are 16, and leaving, joining and writing the
-// parts of tiles up to 14.
+// tokens 33 us (42 from cold caches), of which the steps are 16, and leaving, joining
+// and writing the parts of tiles up to 14.
 #include <algorithm>
 #include <type_traits>
 

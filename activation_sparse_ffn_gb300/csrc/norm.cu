@@ -3,14 +3,16 @@
 // One block per row, which stays in registers from the one read to the one
 // write. The codes have to be defined, so every step but the mean is one fp32
 // rounding, and the mean, whose order of summation differs from block to
-// block, is carried far enough that its rounding to f does not depend on it:
+// block, is carried far enough that its rounding to f hardly ever depends on it:
 // squares and sums as two floats each (the second has what the first's
 // rounding left, by fma(t, t, -t^2) and by Knuth's two-sum), 2^-44 or better
-// after all additions, and the root in 64 bits.
+// after all additions, and the root in 64 bits. One row in some 2^20 lies so near
+// a rounding's border that f may be its other neighbour.
 //
-// Measured: 8192 rows of 8192 bf16 elements with a residual 106 us, 5.1 TB/s; the sums' ten operations an element keep
-// 54% of the issue slots busy, and two blocks an SM wait for each other's barriers. One fp32 row of 8192 5.0 us, a
-// block's way through it: load, sum, root, store.
+// Measured: 8192 rows of 8192 bf16 elements with a residual 106 us, 5.1 TB/s; 34 instructions an element, ten of them the
+// sums', keep 55% of the issue slots busy, and two blocks an SM wait for each other's barriers. 4096 rows of 8192 to codes
+// alone 82 us (45 instructions an element), their codes without a norm 40 (22). One fp32 row of 8192 5.0 us, a block's way
+// through it: load, sum, root, store.
 #include <algorithm>
 
 #include "rows_io.cuh"

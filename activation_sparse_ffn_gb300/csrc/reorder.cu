@@ -6,8 +6,9 @@
 // that is written has been read before: a thread takes the same 16 bytes of the
 // last page of every sequence of a group, through shared memory of its own.
 //
-// Measured: 64 x 8 sequences with pages of 64, half filled (18.7 MB read and written)
-// 12 us; one group of four 3.5 us, four dependent reads: lengths, tables, pages.
+// Measured: 64 x 8 sequences with pages of 64, half filled: 32 caches (570 MB read and as
+// much written) 193 us, 5.9 TB/s; one cache 12 us, of which the bytes are 5 and the
+// dependent reads (lengths, tables, pages) 3.5, as for one group of four.
 #include <algorithm>
 #include <climits>
 

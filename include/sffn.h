@@ -678,7 +678,9 @@ sffn_status sffn_attend(const sffn_kv* kv, const sffn_kv_batch* batch /* host */
  *   y = (t * f) * weight                     (y = t * f without one)
  *   scale = max |y| / 127,  code = y / scale rounded to the nearest whole
  *                                            number, ties to even
- * in fp32, one rounding per operation, so that codes and scales are defined.
+ * in fp32, one rounding per operation, so that codes and scales are defined
+ * (the mean is good to 2^-44: f is its rounding but for one row in some 2^20,
+ * where it may be the next number).
  *   x, residual, sum_out (t, rounded once) in `dtype`; y in `y_dtype`;
  *   weight [width] fp32; codes int8, scales [n_rows] fp32.
  * residual, weight, sum_out, y and (codes, scales) are optional (NULL), but
